@@ -22,6 +22,7 @@ ASF_ACT_RELU = 0
 ASF_ACT_REGLU = 1
 ASF_MAX_BATCH = 32
 ASF_NOALLOC_SCRATCH_BYTES = 32 << 20
+ASF_W4_MAX_K = 65536
 ASF_INJECT_NONE = 0
 ASF_INJECT_WITHHOLD_FFN_COPIES = 1
 
@@ -44,6 +45,15 @@ ASF_MAX_PEERS = 8
 class asf_peer_group(ctypes.Structure):
     _fields_ = [("world", c_int32), ("rank", c_int32), ("max_batch", c_int32), ("d", c_int32),
                 ("pub", c_void_p * ASF_MAX_PEERS), ("flag", c_void_p * ASF_MAX_PEERS), ("epoch", c_void_p)]
+
+
+class asf_w4_matrix(ctypes.Structure):
+    _fields_ = [("rows", c_int32), ("k", c_int32), ("group", c_int32), ("data", c_void_p), ("row_stride", c_int64)]
+
+
+class asf_w4_ffn(ctypes.Structure):
+    _fields_ = [("d", c_int32), ("n", c_int32), ("group", c_int32), ("act", c_int), ("data", c_void_p),
+                ("neuron_stride", c_int64), ("bias", c_void_p)]
 
 
 # name -> (restype, argtypes), exactly the declarations of include/asffn.h
@@ -78,6 +88,14 @@ PROTOTYPES = {
                                 c_void_p]),
     "asf_sparse_ffn_noalloc": (c_int, [POINTER(asf_ffn), c_void_p, c_int32, c_void_p, c_void_p, c_void_p,
                                        c_void_p, c_void_p]),
+    "asf_w4_row_bytes": (c_int64, [c_int32, c_int32]),
+    "asf_w4_workspace_bytes": (c_size_t, [POINTER(asf_w4_matrix), POINTER(asf_w4_ffn), c_int32]),
+    "asf_w4_quantize": (c_int, [c_void_p, c_int, POINTER(asf_w4_matrix), c_void_p]),
+    "asf_w4_dequantize": (c_int, [POINTER(asf_w4_matrix), c_void_p, c_int, c_void_p]),
+    "asf_w4_matmul": (c_int, [POINTER(asf_w4_matrix), c_void_p, c_int, c_int32, c_void_p, c_int32, c_void_p,
+                              c_void_p, c_size_t, c_void_p]),
+    "asf_w4_sparse_ffn": (c_int, [POINTER(asf_w4_ffn), c_void_p, c_int, c_int32, c_void_p, c_void_p, c_void_p,
+                                  c_void_p, c_size_t, c_void_p]),
     "asf_read_error": (c_int, [c_void_p, POINTER(c_int32), c_void_p]),
     "asf_status_string": (c_char_p, [c_int]),
     "asf_version": (c_int32, []),

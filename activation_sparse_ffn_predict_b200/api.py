@@ -38,6 +38,38 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _arg(t: torch.Tensor, name: str, device, dtype=None) -> int:
+    """Address of a contiguous tensor on ``device``."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+class _on:
+    """The raw stream of a call whose tensors are on ``device``: the given one,
+    or that device's current stream; the device is current inside."""
+    __slots__ = ("device", "stream", "guard")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guard = device, stream, None
+
+    def __enter__(self) -> int:
+        if self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        if self.stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        return self.stream.cuda_stream if isinstance(self.stream, torch.cuda.Stream) else int(self.stream)
+
+    def __exit__(self, *exc) -> None:
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
 class Predictor:
     """Descriptor of the two-layer predictor: W1 [r,d], b1 [r], W2 [n,r], b2 [n]."""
 
@@ -138,6 +170,28 @@ class Workspace:
         self.buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         self.nbytes = nbytes
         asf_workspace_init(self, stream)
+
+    @classmethod
+    def _sized(cls, nbytes: int, device, stream, where: str) -> "Workspace":
+        if nbytes == 0:
+            raise AsfError(L.ASF_ERR_INVALID_ARG, where)
+        self = cls.__new__(cls)
+        self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.nbytes = nbytes
+        with _on(self.buf.device, stream) as st:
+            asf_workspace_init(self, st)
+        return self
+
+    @classmethod
+    def for_w4(cls, op, max_batch: int, stream=None) -> "Workspace":
+        """Scratch of asf_w4_matmul (op a W4Matrix) or asf_w4_sparse_ffn (a W4FFN)."""
+        return cls._sized(op.workspace_bytes(max_batch), op.device, stream, "asf_w4_workspace_bytes")
+
+    def on(self, device) -> int:
+        """Its address, for a call on ``device``."""
+        if self.buf.device != device:
+            raise ValueError(f"the workspace must be on {device}")
+        return self.buf.data_ptr()
 
     @property
     def ptr(self) -> ctypes.c_void_p:

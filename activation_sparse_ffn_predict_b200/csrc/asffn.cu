@@ -36,11 +36,11 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
-#include <mutex>
 #include <vector>
 
 #include "asffn.h"
 #include "common.cuh"
+#include "host.cuh"
 
 using namespace asf;
 
@@ -2283,57 +2283,9 @@ __global__ void __launch_bounds__(kThreads)
 // host side                                                                //
 // ======================================================================== //
 
-struct DevCache {
-  int sms = 0;
-};
-std::mutex g_mu;
-DevCache g_dev[64];
-
-int sm_count() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (g_dev[dev].sms == 0) {
-    int v = 0;
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) v = 148;
-    g_dev[dev].sms = v;
-  }
-  return g_dev[dev].sms;
-}
-
 // Process-wide test hook (asf_set_fault_injection): 0 = off.
 std::atomic<int> g_inject{0};
-template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                   Args... args) {
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute((const void *)kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  // Every kernel prefers the largest shared-memory carveout: an SM then never
-  // has to be reconfigured between the chained kernels, and a kernel can start
-  // beside one that uses less than all of it (the layer-2 predictor beside the
-  // layer-1 slice kernel: +1.7% tokens/s at the 70B shape).
-  cudaFuncSetAttribute((const void *)kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                       (int)cudaSharedmemCarveoutMaxShared);
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
-}
 
-inline bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline bool al4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-inline size_t r256(size_t v) { return (v + 255) & ~size_t(255); }
 inline int vec_of(asf_dtype t) { return t == ASF_F16 ? 8 : 4; }
 inline int esize(asf_dtype t) { return t == ASF_F16 ? 2 : 4; }
 
@@ -2442,14 +2394,6 @@ asf_status check_ffn(const asf_ffn *f) {
   if (!al16(f->Wu) || !al16(f->WdT) || (f->Wg && !al16(f->Wg)) || !al4(f->bias)) return ASF_ERR_MISALIGNED;
   return ASF_OK;
 }
-
-asf_status check_ws(void *ws, size_t ws_bytes, size_t need) {
-  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return ASF_ERR_WORKSPACE;
-  if (ws_bytes < need) return ASF_ERR_WORKSPACE;
-  return ASF_OK;
-}
-
-inline asf_status cuda_status(cudaError_t e) { return e == cudaSuccess ? ASF_OK : ASF_ERR_CUDA; }
 
 // largest token group in {1, 2, 4, 8} not above B whose staging fits
 int pick_nb(int B, size_t bytes_per_token) {

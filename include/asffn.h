@@ -251,6 +251,80 @@ ASF_API asf_status asf_sparse_ffn_noalloc(const asf_ffn *ffn, const void *x, int
                                           const int32_t *count, float *y, int32_t *fault, asf_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * 4-bit weights with group scales.
+ *
+ * The pages run their models at 4 bits ("PowerInfer Guide", the hardware
+ * sizing table); these calls are the sparse FFN, a dense product and the
+ * format between them.  A row of k weights is stored as
+ *
+ *   kp / 2 bytes of codes (kp = k rounded up to a multiple of 128), then one
+ *   fp16 scale per group of 32, 64 or 128 weights, zero padded:
+ *   asf_w4_row_bytes(k, group) bytes, a multiple of 16.
+ *
+ * Weight i is (code_i - 8) * scale[i / group], 0 <= code_i <= 15; weights past
+ * k have code 8.  In each block of 128 weights (16 little-endian 32-bit words)
+ * word 4t+j (t, j in 0..3) holds weights 32j+8t .. 32j+8t+7, and weight 2p+h of
+ * a word is the nibble at bit 16h+4p.  Rows are plain bytes: asf_gather_rows
+ * and asf_permute_rows move them.
+ *
+ * No weight is rounded on its way through a product: sums run in fp32, scales
+ * multiply fp32 sums.  x is fp16 or fp32 (an fp32 x enters exactly), y fp32. */
+#define ASF_W4_MAX_K 65536
+
+typedef struct {
+  int32_t rows, k;      /* weights are [rows][k]; k a multiple of 8, at most ASF_W4_MAX_K */
+  int32_t group;        /* 32, 64 or 128 */
+  const void *data;     /* device, 16-byte aligned; written by asf_w4_quantize only */
+  int64_t row_stride;   /* bytes between rows: a multiple of 16, >= asf_w4_row_bytes(k, group) */
+} asf_w4_matrix;
+
+/* One FFN layer of 4-bit rows, neuron by neuron: gate | up | down rows (REGLU)
+ * or up | down rows (RELU) of a neuron one after the other, each
+ * asf_w4_row_bytes(d, group) bytes, the down row being a column of W_down. */
+typedef struct {
+  int32_t d, n;
+  int32_t group;
+  asf_act act;
+  const void *data;        /* device, 16-byte aligned */
+  int64_t neuron_stride;   /* bytes between neurons: a multiple of 16, >= 3 (REGLU) or 2 (RELU) rows */
+  const float *bias;       /* device [n] */
+} asf_w4_ffn;
+
+/* Bytes of one row, or 0 for a k or group that the format does not have. */
+ASF_API int64_t asf_w4_row_bytes(int32_t k, int32_t group);
+
+/* Rows [rows][k] (fp16 or fp32, contiguous, 16-byte aligned) to 4 bits, into
+ * mat->data: per group scale = fp16(max |w| / 7), code = clamp(round half to
+ * even(w / scale), -8, 7) + 8, evaluated in fp32; a group of scale 0 gets code
+ * 8.  A group with a NaN, an infinity or a maximum past fp16's range gets the
+ * scale NaN, so that no product over it looks sound. */
+ASF_API asf_status asf_w4_quantize(const void *src, asf_dtype dtype, const asf_w4_matrix *mat, asf_stream_t stream);
+
+/* The weights back as contiguous [rows][k] fp16 (rounded once) or fp32 (exact). */
+ASF_API asf_status asf_w4_dequantize(const asf_w4_matrix *mat, void *dst, asf_dtype dtype, asf_stream_t stream);
+
+/* Workspace bytes of asf_w4_matmul / asf_w4_sparse_ffn for batches up to
+ * max_batch (either descriptor may be NULL; with both, enough for each of the
+ * calls in turn).  0 on invalid arguments.  asf_workspace_init zeroes it once. */
+ASF_API size_t asf_w4_workspace_bytes(const asf_w4_matrix *mat, const asf_w4_ffn *ffn, int32_t max_batch);
+
+/* y[b][i] = act(sum_k w[i][k] x[b][k] + bias[i]) for 1 <= B <= ASF_MAX_BATCH tokens.
+ *   x     device [B][k] in xdtype, 16-byte aligned (an fp32 x must be finite)
+ *   bias  device fp32 [rows], or NULL
+ *   relu  0: none, 1: max(., 0)
+ *   y     device fp32 [B][rows], overwritten */
+ASF_API asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dtype xdtype, int32_t B,
+                                 const float *bias, int32_t relu, float *y, void *ws, size_t ws_bytes,
+                                 asf_stream_t stream);
+
+/* asf_sparse_ffn over 4-bit rows: x [B][d] in xdtype, idx/count/y as there;
+ * idx and count both NULL runs all n neurons (asf_dense_ffn).  The activations
+ * between the two products stay fp32. */
+ASF_API asf_status asf_w4_sparse_ffn(const asf_w4_ffn *ffn, const void *x, asf_dtype xdtype, int32_t B,
+                                     const int32_t *idx, const int32_t *count, float *y, void *ws, size_t ws_bytes,
+                                     asf_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Neuron-sharded layer across GPUs (the layer + neuron partitioning of the
  * "PowerInfer_x64" page's multi-GPU coordination): rank r holds the predictor
  * rows and FFN rows of its own neurons, and the ranks' partial outputs are

@@ -1,0 +1,248 @@
+"""4-bit rows on the GPU against the float64 oracle: the format byte by byte,
+the dense product and the sparse FFN.
+
+Tolerances.  Products of a code and an operand are exact, and so are a group's
+(c - 8) x terms; what rounds is the fp32 accumulation: a chain of at most 3 x 8
+tensor-core steps inside a group (2^-23 of the partial sum each, truncated),
+then one fused multiply-add per group (2^-24), then the sums of the splits.
+Against sum |w x| =: M, elementwise, |error| <= (24 + groups + 256) 2^-23 M.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import w4 as O
+from tests.gpu_util import ensure_built
+
+import activation_sparse_ffn_predict_b200 as A
+from activation_sparse_ffn_predict_b200 import _lib as L
+
+pytestmark = pytest.mark.gpu
+DT = {"f16": torch.float16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    ensure_built()
+
+
+def _weights(m, k, seed, std=1.0):
+    return (np.random.default_rng(seed).standard_normal((m, k)) * std / np.sqrt(k)).astype(np.float32)
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("m,k,group", [(1, 8, 32), (5, 128, 128), (3, 136, 64), (17, 512, 32), (9, 1000, 32),
+                                       (4, 1096, 128), (33, 4096, 64)])
+def test_quantize_is_the_definition(m, k, group, dt):
+    W = _weights(m, k, k + group)
+    W[0] *= 1e-9                                            # scales underflow: zeros
+    if m > 2:
+        W[1, :k // 2] = 0
+        W[2, 0], W[2, k - 1] = 6e4 if dt == "f16" else 4e5, np.nan
+    src = torch.from_numpy(W).to(DT[dt]).cuda()
+    data = torch.full((m, O.row_bytes(k, group) + 16), 0xAB, dtype=torch.uint8, device="cuda")   # a wider stride
+    mat = A.W4Matrix(data, k, group)
+    A.asf_w4_quantize(src, mat)
+    want = O.w4_pack(src.float().cpu().numpy(), group)
+    got = data.cpu().numpy()
+    rb = O.row_bytes(k, group)
+    nan = np.isnan(want[:, O.padded(k) // 2:].copy().view(np.float16))
+    sc = got[:, O.padded(k) // 2:rb].copy().view(np.float16)
+    assert np.array_equal(np.isnan(sc), nan)                # a NaN scale may have any NaN's bits
+    same = got[:, :rb] == want
+    same[:, O.padded(k) // 2:] |= np.repeat(nan, 2, axis=1)
+    assert same.all()
+    assert (got[:, rb:] == 0xAB).all()                      # behind the row: untouched
+    back = torch.empty(m, k, dtype=DT[dt], device="cuda")
+    A.asf_w4_dequantize(mat, back)
+    ref = O.w4_unpack(got[:, :rb], k, group)
+    with np.errstate(over="ignore"):
+        assert np.array_equal(back.cpu().numpy(), ref.astype(back.cpu().numpy().dtype), equal_nan=True)
+
+
+def _check(y, ref, mass, groups):
+    y = y.cpu().numpy().astype(np.float64)
+    assert np.isfinite(y).all()
+    over = np.abs(y - ref) - (24 + groups + 256) * 2.0 ** -23 * mass
+    assert over.max() <= 0, (over.max(), np.abs(y - ref).max(), np.abs(ref).max())
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("m,k,group,B", [
+    (1, 8, 32, 1), (16, 128, 128, 1), (17, 136, 64, 2), (31, 520, 32, 8), (1003, 1376, 32, 3), (64, 4096, 128, 1),
+    (256, 8192, 64, 9), (40, 12288, 128, 17), (129, 2760, 64, 32), (5000, 512, 128, 5), (24, 49152, 128, 32),
+    (2500, 4096, 64, 24)])
+def test_matmul(m, k, group, B, dt):
+    rng = np.random.default_rng(m * k + B)
+    rows = O.w4_pack(_weights(m, k, m + k), group)
+    x = torch.from_numpy(rng.standard_normal((B, k)).astype(np.float32)).to(DT[dt])
+    bias = rng.standard_normal(m).astype(np.float32)
+    mat = A.W4Matrix(torch.from_numpy(rows).cuda(), k, group)
+    ws = A.Workspace.for_w4(mat, B)
+    W = O.w4_unpack(rows, k, group)
+    xn = x.double().numpy()
+    mass = np.abs(xn) @ np.abs(W).T + np.abs(bias)
+    for use_bias, relu in ((False, False), (True, True)):
+        y = torch.full((B, m), float("nan"), device="cuda")
+        A.asf_w4_matmul(mat, x.cuda(), y, ws, bias=torch.from_numpy(bias).cuda() if use_bias else None, relu=relu)
+        ref = xn @ W.T + (bias if use_bias else 0)
+        _check(y, np.maximum(ref, 0) if relu else ref, mass, k // group + 1)
+        again = torch.full((B, m), float("nan"), device="cuda")
+        A.asf_w4_matmul(mat, x.cuda(), again, ws, bias=torch.from_numpy(bias).cuda() if use_bias else None, relu=relu)
+        assert torch.equal(y, again)                        # fixed summation order
+    assert A.asf_read_error(ws) == 0
+
+
+def _layer(act, n, d, group, seed):
+    mats = 3 if act == "reglu" else 2
+    data = np.stack([O.w4_pack(_weights(n, d, seed + i), group) for i in range(mats)], 1)
+    bias = (np.random.default_rng(seed).standard_normal(n) * 0.3).astype(np.float32)
+    return data, bias
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("act,n,d,group,B,active", [
+    ("reglu", 1376, 512, 32, 1, 140), ("relu", 1376, 512, 32, 2, 1), ("reglu", 300, 1096, 64, 8, 0),
+    ("relu", 500, 136, 128, 9, 500), ("reglu", 700, 2048, 128, 17, 333), ("relu", 260, 4096, 64, 32, 100),
+    ("reglu", 64, 8, 32, 4, 17), ("reglu", 200, 8192, 128, 3, 77), ("relu", 120, 12288, 32, 16, 120)])
+def test_sparse_ffn(act, n, d, group, B, active, dt):
+    rng = np.random.default_rng(n + d)
+    data, bias = _layer(act, n, d, group, n)
+    x = torch.from_numpy(rng.standard_normal((B, d)).astype(np.float32)).to(DT[dt])
+    ids = np.sort(rng.choice(n, active, replace=False)).astype(np.int32)
+    ffn = A.W4FFN(act, torch.from_numpy(data).cuda(), torch.from_numpy(bias).cuda(), d, group)
+    ws = A.Workspace.for_w4(ffn, B)
+    idx = torch.full((n,), 1 << 30, dtype=torch.int32, device="cuda")       # past the count: never read
+    idx[:active] = torch.from_numpy(ids).cuda()
+    cnt = torch.tensor([active], dtype=torch.int32, device="cuda")
+    y = torch.full((B, d), float("nan"), device="cuda")
+    A.asf_w4_sparse_ffn(ffn, x.cuda(), idx, cnt, y, ws)
+    _check_ffn(y, act, data, bias, d, group, x.double().numpy(), ids)
+    y2 = torch.full((B, d), float("nan"), device="cuda")
+    A.asf_w4_sparse_ffn(ffn, x.cuda(), idx, cnt, y2, ws)
+    assert torch.equal(y, y2)
+    if active == n:                                                           # all neurons: the dense form
+        A.asf_w4_sparse_ffn(ffn, x.cuda(), None, None, y2, ws)
+        assert torch.equal(y, y2)
+    assert A.asf_read_error(ws) == 0
+
+
+def _check_ffn(y, act, data, bias, d, group, xn, ids):
+    """Error of an activation, by the product's bound, then of the sum over them."""
+    ref = O.w4_ffn(act, data, bias, d, group, xn, ids)
+    y = y.cpu().numpy().astype(np.float64)
+    if len(ids) == 0:
+        assert (y == 0).all()
+        return
+    W = O.w4_unpack(data[ids], d, group)
+    u = (24 + d // group + 1 + 256) * 2.0 ** -23
+    z = [xn @ W[:, i].T + (bias[ids] if i == 0 else 0) for i in range(W.shape[1] - 1)]
+    m = [np.abs(xn) @ np.abs(W[:, i]).T + (np.abs(bias[ids]) if i == 0 else 0) for i in range(W.shape[1] - 1)]
+    a = np.maximum(z[0], 0)
+    da = u * m[0]
+    if act == "reglu":
+        da = da * np.abs(z[1]) + np.abs(a) * u * m[1] + da * u * m[1]
+        a = a * z[1]
+    # down: three tensor-core steps of 2^-23 per 16 neurons, and the sums of warps and splits
+    v = (3 * len(ids) / 16 + 3 + 300) * 2.0 ** -23
+    tol = (da + v * (np.abs(a) + da)) @ np.abs(W[:, -1])
+    assert np.isfinite(y).all()
+    assert (np.abs(y - ref) - tol).max() <= 0, (np.abs(y - ref).max(), np.abs(ref).max())
+
+
+def test_errors_of_the_list_are_flagged_and_skipped():
+    n, d, group, B = 96, 256, 64, 3
+    data, bias = _layer("reglu", n, d, group, 5)
+    x = torch.randn(B, d).half()
+    ffn = A.W4FFN("reglu", torch.from_numpy(data).cuda(), torch.from_numpy(bias).cuda(), d, group)
+    ws = A.Workspace.for_w4(ffn, B)
+    ids = np.array([3, 90, 17, 17, 5], np.int32)                              # any order, one twice
+    bad = np.array([3, 90, n, 17, 17, -1, 5], np.int32)
+    ys = []
+    for lst in (ids, bad):
+        idx = torch.zeros(n, dtype=torch.int32, device="cuda")
+        idx[:len(lst)] = torch.from_numpy(lst).cuda()
+        y = torch.empty(B, d, device="cuda")
+        A.asf_w4_sparse_ffn(ffn, x.cuda(), idx, torch.tensor([len(lst)], dtype=torch.int32, device="cuda"), y, ws)
+        assert A.asf_read_error(ws) == (0 if lst is ids else L.ASF_ERR_DEVICE_INDEX)
+        _check_ffn(y, "reglu", data, bias, d, group, x.double().numpy(), ids)
+        ys.append(y)
+    idx = torch.arange(n, dtype=torch.int32, device="cuda")
+    for count, ref in ((n + 7, np.arange(n)), (-3, np.arange(0))):
+        y = torch.empty(B, d, device="cuda")
+        A.asf_w4_sparse_ffn(ffn, x.cuda(), idx, torch.tensor([count], dtype=torch.int32, device="cuda"), y, ws)
+        assert A.asf_read_error(ws) == L.ASF_ERR_DEVICE_INDEX
+        _check_ffn(y, "reglu", data, bias, d, group, x.double().numpy(), ref)
+
+
+def test_a_nan_group_reaches_only_its_rows():
+    W = _weights(40, 512, 1)
+    W[7, 300] = np.inf
+    mat = A.W4Matrix.quantize(torch.from_numpy(W).cuda(), 64)
+    y = torch.empty(2, 40, device="cuda")
+    A.asf_w4_matmul(mat, torch.randn(2, 512, device="cuda").half(), y, A.Workspace.for_w4(mat, 2))
+    assert torch.isnan(y[:, 7]).all() and torch.isfinite(torch.cat([y[:, :7], y[:, 8:]], 1)).all()
+
+
+def test_matrix_ffn_quantize_and_row_moves():
+    """W4FFN.quantize lays rows as described; asf_gather_rows permutes packed neurons."""
+    n, d, group = 50, 264, 32
+    mats = [_weights(n, d, i) for i in range(3)]
+    dev = [torch.from_numpy(m).cuda() for m in mats]
+    bias = torch.zeros(n, device="cuda")
+    ffn = A.W4FFN.quantize("reglu", *dev, bias, group)
+    want = np.stack([O.w4_pack(m, group) for m in mats], 1)
+    assert np.array_equal(ffn.data.cpu().numpy(), want)
+    perm = torch.randperm(n).int().cuda()
+    out = torch.empty_like(ffn.data)
+    A.asf_gather_rows(ffn.data, out, perm)
+    assert np.array_equal(out.cpu().numpy(), want[perm.cpu().numpy()])
+
+
+def test_graph_streams_and_shared_workspace():
+    """A captured call, replayed with new inputs; two shapes in turn on one workspace; a side stream."""
+    a = A.W4Matrix.quantize(torch.from_numpy(_weights(300, 4096, 1)).cuda(), 128)
+    b = A.W4Matrix.quantize(torch.from_numpy(_weights(4096, 304, 2)).cuda(), 32)
+    ws = max((A.Workspace.for_w4(m, 8) for m in (a, b)), key=lambda w: w.nbytes)
+    x = torch.zeros(8, 4096, device="cuda", dtype=torch.float16)
+    h, y = torch.empty(8, 300, device="cuda"), torch.empty(8, 4096, device="cuda")
+    hp = torch.zeros(8, 304, device="cuda")
+
+    def both():
+        A.asf_w4_matmul(a, x, h, ws, relu=True)
+        hp[:, :300].copy_(h)
+        A.asf_w4_matmul(b, hp, y, ws)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for seed in range(3):
+        torch.manual_seed(seed)
+        x.copy_(torch.randn(8, 4096))
+        graph.replay()
+        got = y.clone()
+        y.zero_()
+        both()
+        assert torch.equal(got, y) and float(got.abs().max()) > 0
+
+
+def test_python_refusals():
+    mat = A.W4Matrix.quantize(torch.randn(32, 256, device="cuda"), 64)
+    ws = A.Workspace.for_w4(mat, 2)
+    x, y = torch.randn(2, 256, device="cuda"), torch.empty(2, 32, device="cuda")
+    for bad in (lambda: A.asf_w4_matmul(mat, x.cpu(), y, ws), lambda: A.asf_w4_matmul(mat, x, y.cpu(), ws),
+                lambda: A.asf_w4_matmul(mat, x.bfloat16(), y, ws), lambda: A.asf_w4_matmul(mat, x[:, :128], y, ws),
+                lambda: A.asf_w4_matmul(mat, x.t().contiguous().t(), y, ws), lambda: A.asf_w4_matmul(mat, x, y.half(), ws),
+                lambda: A.asf_w4_matmul(mat, x, y[:1], ws), lambda: A.asf_w4_matmul(mat, x, y, ws, bias=y[0, :5]),
+                lambda: A.W4Matrix(mat.data.int(), 256, 64), lambda: A.W4Matrix(mat.data, 1024, 64),
+                lambda: A.W4Matrix.quantize(x.bfloat16(), 64), lambda: A.asf_w4_dequantize(mat, y),
+                lambda: A.W4FFN("reglu", mat.data[None], y[0], 256, 64)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(A.AsfError):
+        A.asf_w4_matmul(mat, torch.randn(33, 256, device="cuda"), torch.empty(33, 32, device="cuda"), ws)
