@@ -23,6 +23,9 @@ ASF_ACT_REGLU = 1
 ASF_MAX_BATCH = 32
 ASF_NOALLOC_SCRATCH_BYTES = 32 << 20
 ASF_W4_MAX_K = 65536
+ASF_MAX_KV_HEADS = 1024
+ASF_MAX_HEAD_GROUP = 128
+ASF_MAX_KEYS = 1 << 30
 ASF_INJECT_NONE = 0
 ASF_INJECT_WITHHOLD_FFN_COPIES = 1
 
@@ -54,6 +57,11 @@ class asf_w4_matrix(ctypes.Structure):
 class asf_w4_ffn(ctypes.Structure):
     _fields_ = [("d", c_int32), ("n", c_int32), ("group", c_int32), ("act", c_int), ("data", c_void_p),
                 ("neuron_stride", c_int64), ("bias", c_void_p)]
+
+
+class asf_kv_cache(ctypes.Structure):
+    _fields_ = [("pages", c_int32), ("page", c_int32), ("heads", c_int32), ("head_dim", c_int32), ("k", c_void_p),
+                ("v", c_void_p), ("page_stride", c_int64), ("token_stride", c_int64), ("head_stride", c_int64)]
 
 
 # name -> (restype, argtypes), exactly the declarations of include/asffn.h
@@ -96,6 +104,11 @@ PROTOTYPES = {
                               c_void_p, c_size_t, c_void_p]),
     "asf_w4_sparse_ffn": (c_int, [POINTER(asf_w4_ffn), c_void_p, c_int, c_int32, c_void_p, c_void_p, c_void_p,
                                   c_void_p, c_size_t, c_void_p]),
+    "asf_attention_workspace_bytes": (c_size_t, [POINTER(asf_kv_cache), c_int32, c_int32, c_int32]),
+    "asf_kv_append": (c_int, [POINTER(asf_kv_cache), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32, c_void_p,
+                              c_void_p, c_void_p, c_size_t, c_void_p]),
+    "asf_tree_attention": (c_int, [POINTER(asf_kv_cache), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32,
+                                   c_int32, c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
     "asf_read_error": (c_int, [c_void_p, POINTER(c_int32), c_void_p]),
     "asf_status_string": (c_char_p, [c_int]),
     "asf_version": (c_int32, []),

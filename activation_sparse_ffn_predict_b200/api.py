@@ -187,6 +187,12 @@ class Workspace:
         """Scratch of asf_w4_matmul (op a W4Matrix) or asf_w4_sparse_ffn (a W4FFN)."""
         return cls._sized(op.workspace_bytes(max_batch), op.device, stream, "asf_w4_workspace_bytes")
 
+    @classmethod
+    def for_attention(cls, cache, q_heads: int, requests: int, tokens: int, stream=None) -> "Workspace":
+        """Scratch of asf_kv_append and asf_tree_attention over a KVCache, up to that many requests and tokens."""
+        return cls._sized(cache.workspace_bytes(q_heads, requests, tokens), cache.device, stream,
+                          "asf_attention_workspace_bytes")
+
     def on(self, device) -> int:
         """Its address, for a call on ``device``."""
         if self.buf.device != device:

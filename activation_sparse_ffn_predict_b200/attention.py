@@ -1,0 +1,79 @@
+"""Tree attention over a paged key/value cache: tensor-level binding of
+asf_kv_append and asf_tree_attention (include/asffn.h, "Tree attention")."""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _lib as L
+from ._lib import check
+from .api import Workspace, _arg, _on
+
+
+class KVCache:
+    """A layer's keys and values, fp16 [pages, page, heads, head_dim] each; any
+    strides (multiples of 8 elements) with a contiguous last dimension."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        for name, x in (("k", k), ("v", v)):
+            if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != torch.float16 or x.dim() != 4:
+                raise ValueError(f"{name} must be a float16 CUDA tensor [pages, page, heads, head_dim]")
+            if x.numel() == 0 or x.stride(3) != 1:
+                raise ValueError(f"{name} must not be empty, and its last dimension contiguous")
+        if k.shape != v.shape or k.stride() != v.stride() or k.device != v.device:
+            raise ValueError("k and v must have one shape, layout and device")
+        self.k, self.v, self.device = k, v, k.device
+        self.pages, self.page, self.heads, self.head_dim = (int(n) for n in k.shape)
+        self.desc = L.asf_kv_cache(self.pages, self.page, self.heads, self.head_dim, k.data_ptr(), v.data_ptr(),
+                                   *(int(n) for n in k.stride()[:3]))
+        self._ref = ctypes.byref(self.desc)
+
+    def workspace_bytes(self, q_heads: int, requests: int, tokens: int) -> int:
+        return int(L.load().asf_attention_workspace_bytes(self._ref, int(q_heads), int(requests), int(tokens)))
+
+
+def _requests(cache: KVCache, table, lens, begin):
+    dev = cache.device
+    if table.dim() != 2 or lens.dim() != 1 or lens.shape[0] != table.shape[0]:
+        raise ValueError("table must be [R, max_pages] and lens [R]")
+    R = lens.shape[0]
+    if begin.dim() != 1 or begin.shape[0] != R + 1:
+        raise ValueError("begin must be [R + 1]")
+    return (_arg(table, "table", dev, torch.int32), int(table.shape[1]), R, _arg(lens, "lens", dev, torch.int32),
+            _arg(begin, "begin", dev, torch.int32))
+
+
+def asf_kv_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin: torch.Tensor, k: torch.Tensor,
+                  v: torch.Tensor, ws: Workspace, stream=None) -> None:
+    """Write the tokens' k and v [T, heads, head_dim] at positions lens[r] + i of their requests."""
+    if k.dim() != 3 or k.shape[1] != cache.heads or k.shape[2] != cache.head_dim or v.shape != k.shape:
+        raise ValueError("k and v must be [T, heads, head_dim]")
+    dev = cache.device
+    req = _requests(cache, table, lens, begin)
+    kp, vp = _arg(k, "k", dev, torch.float16), _arg(v, "v", dev, torch.float16)
+    with _on(dev, stream) as st:
+        check(L.load().asf_kv_append(cache._ref, *req, k.shape[0], kp, vp, ws.on(dev), ws.nbytes, st), "asf_kv_append")
+
+
+def asf_tree_attention(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin: torch.Tensor, q: torch.Tensor,
+                       anc: torch.Tensor, o: torch.Tensor, ws: Workspace, scale: Optional[float] = None,
+                       stream=None) -> None:
+    """o [T, q_heads, head_dim] = attention of the call's tokens over their requests' keys.
+
+    table int32 [R, max_pages], lens int32 [R], begin int32 [R + 1]; anc int32 [T]: which of the call's
+    tokens each token sees, beside every key before lens.  scale: head_dim ** -0.5 unless given."""
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or o.shape != q.shape:
+        raise ValueError("q and o must be [T, q_heads, head_dim]")
+    if anc.dim() != 1 or anc.shape[0] != q.shape[0]:
+        raise ValueError("anc must be [T]")
+    dev = cache.device
+    req = _requests(cache, table, lens, begin)
+    qp, op = _arg(q, "q", dev, torch.float16), _arg(o, "o", dev, torch.float16)
+    ap = _arg(anc, "anc", dev, torch.int32)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    with _on(dev, stream) as st:
+        check(L.load().asf_tree_attention(cache._ref, *req, q.shape[0], q.shape[1], qp, ap, scale, op, ws.on(dev),
+                                          ws.nbytes, st), "asf_tree_attention")

@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libasffn.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("asffn.cu", "w4.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("asffn.cu", "w4.cu", "attention.cu")]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "host.cuh"), os.path.join(INCLUDE, "asffn.h")]
 DEPS = SOURCES + HEADERS
 

@@ -325,6 +325,59 @@ ASF_API asf_status asf_w4_sparse_ffn(const asf_w4_ffn *ffn, const void *x, asf_d
                                      asf_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Tree attention: the attention step in front of the predictor (PowerInfer_x64
+ * page: attention, then predictor, then the sparse operators) for the tokens
+ * of one call, over a paged key/value cache in fp16.
+ *
+ * R requests share the call's T tokens (1 <= R, T <= ASF_MAX_BATCH): tokens
+ * begin[r] .. begin[r+1]-1 are request r's (none is allowed), tokens outside
+ * every range take no part.  Request r has lens[r] keys in the cache; its i-th
+ * token of the call is at position lens[r] + i.  With one token a request this
+ * is plain decoding; several are a tree of drafted tokens, of which token t
+ * sees every key before lens[r] and, of the call's tokens, those of its own
+ * request whose bit is set in anc[t] (bit j: token j of the call; a token sees
+ * itself only through its own bit).  A token that sees nothing gets zeros, and
+ * what it does not see, NaN or not, does not reach it.
+ *
+ * Position p of request r is row p % page of page table[r * max_pages + p / page].
+ * After a tree is verified, its accepted tokens are appended again, in order,
+ * with lens unchanged; then lens grows.
+ *
+ * table, lens and begin are device memory.  What the host cannot check (a page
+ * outside [0, pages), begin not ascending within 0..T, a negative length, a
+ * position past max_pages * page) is skipped, as a key that nobody sees or a
+ * row that is not written, and recorded in the workspace error word. */
+#define ASF_MAX_KV_HEADS 1024
+#define ASF_MAX_HEAD_GROUP 128       /* query heads of a kv head */
+#define ASF_MAX_KEYS (1 << 30)       /* most of max_pages * page */
+
+typedef struct {
+  int32_t pages, page;               /* pages, and tokens in each */
+  int32_t heads, head_dim;           /* kv heads; head_dim a multiple of 8, at most 128 */
+  void *k, *v;                       /* device fp16, 16-byte aligned, one layout for both */
+  int64_t page_stride, token_stride, head_stride;   /* elements, multiples of 8 */
+} asf_kv_cache;
+
+/* Workspace bytes of asf_tree_attention for up to R requests and T tokens with
+ * q_heads query heads.  0 on invalid arguments. */
+ASF_API size_t asf_attention_workspace_bytes(const asf_kv_cache *cache, int32_t q_heads, int32_t R, int32_t T);
+
+/* Writes the tokens' keys and values (device fp16 [T][heads][head_dim], 16-byte
+ * aligned) at their positions.  ws: at least 4096 bytes, for the error word. */
+ASF_API asf_status asf_kv_append(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
+                                 const int32_t *lens, const int32_t *begin, int32_t T, const void *k, const void *v,
+                                 void *ws, size_t ws_bytes, asf_stream_t stream);
+
+/* o[t][h] = sum over the keys p that t sees of softmax_p(scale q[t][h] . k_p) v_p,
+ * query head h reading kv head h / (q_heads / heads).
+ *   q, o  device fp16 [T][q_heads][head_dim], 16-byte aligned
+ *   anc   device 32-bit masks [T] */
+ASF_API asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
+                                      const int32_t *lens, const int32_t *begin, int32_t T, int32_t q_heads,
+                                      const void *q, const int32_t *anc, float scale, void *o, void *ws,
+                                      size_t ws_bytes, asf_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Neuron-sharded layer across GPUs (the layer + neuron partitioning of the
  * "PowerInfer_x64" page's multi-GPU coordination): rank r holds the predictor
  * rows and FFN rows of its own neurons, and the ranks' partial outputs are

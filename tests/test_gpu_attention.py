@@ -1,0 +1,266 @@
+"""Tree attention and the append on the GPU against the float64 oracle.
+
+Tolerance, elementwise, with M = sum_p p |v|: the output's rounding 2^-11 |o|,
+the weights' rounding to fp16 2^-11 M (their sum stays fp32), and twice the
+relative error of a weight, which is the absolute error of its score: (D + 16)
+2^-23 max_p scale sum |q k| of fp32 accumulation and scaling, plus 2^-20 for
+the exponential and the merges; 2^-24 below fp16's normal range.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention as O
+from tests.gpu_util import ensure_built
+
+import activation_sparse_ffn_predict_b200 as A
+from activation_sparse_ffn_predict_b200 import _lib as L
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    ensure_built()
+
+
+class Case:
+    """Requests of given lengths and tokens, with a random tree each, over shuffled pages."""
+
+    def __init__(self, lens, toks, hkv=2, grp=2, D=64, page=16, seed=0, spread=1.5):
+        rng = np.random.default_rng(seed)
+        self.rng, self.lens, self.D, self.page, self.hkv, self.grp = rng, list(lens), D, page, hkv, grp
+        self.begin = np.concatenate([[0], np.cumsum(toks)]).astype(int)
+        T = self.T = int(self.begin[-1])
+        need = [-(-(n + m) // page) for n, m in zip(lens, toks)]
+        pages = max(1, sum(need)) + 2
+        order = rng.permutation(pages)
+        self.table = np.zeros((len(lens), max(1, max(need))), int)
+        at = 0
+        for r, n in enumerate(need):
+            self.table[r, :n] = order[at:at + n]
+            at += n
+        f16 = lambda *s: rng.standard_normal(s).astype(np.float16)  # noqa: E731
+        self.k, self.v = f16(pages, page, hkv, D), f16(pages, page, hkv, D)
+        self.kn, self.vn = f16(T, hkv, D), f16(T, hkv, D)
+        self.q = (rng.standard_normal((T, hkv * grp, D)) * spread).astype(np.float16)
+        self.anc = np.zeros(T, np.int64)
+        for r in range(len(lens)):
+            for t in range(self.begin[r], self.begin[r + 1]):
+                up = rng.integers(self.begin[r] - 1, t) if t > self.begin[r] else -1
+                self.anc[t] = (1 << t) | (self.anc[up] if up >= self.begin[r] else 0)
+
+    def device(self):
+        i32 = lambda a: torch.from_numpy(np.asarray(a).astype(np.uint32).view(np.int32)).cuda()  # noqa: E731
+        d = dict(cache=A.KVCache(torch.from_numpy(self.k.copy()).cuda(), torch.from_numpy(self.v.copy()).cuda()),
+                 table=i32(self.table), lens=i32(self.lens), begin=i32(self.begin), anc=i32(self.anc))
+        for n in ("kn", "vn", "q"):
+            d[n] = torch.from_numpy(getattr(self, n)).cuda()
+        d["o"] = torch.full_like(d["q"], 7.0)
+        d["ws"] = A.Workspace.for_attention(d["cache"], self.hkv * self.grp, len(self.lens), self.T)
+        return d
+
+    def run(self, d=None, scale=None, append=True):
+        d = d or self.device()
+        if append:
+            A.asf_kv_append(d["cache"], d["table"], d["lens"], d["begin"], d["kn"], d["vn"], d["ws"])
+        A.asf_tree_attention(d["cache"], d["table"], d["lens"], d["begin"], d["q"], d["anc"], d["o"], d["ws"], scale=scale)
+        return d
+
+    def check(self, d, scale=None, error=0):
+        scale = self.D ** -0.5 if scale is None else scale
+        k, v = self.k.copy(), self.v.copy()
+        O.append(k, v, self.table, self.lens, self.begin, self.kn, self.vn)
+        assert np.array_equal(d["cache"].k.cpu().numpy(), k, equal_nan=True)
+        assert np.array_equal(d["cache"].v.cpu().numpy(), v, equal_nan=True)
+        o, mass, big = O.tree_attention(k, v, self.table, self.lens, self.begin, self.q, self.anc, scale)
+        tol = 2.0 ** -11 * np.abs(o) + (2.0 ** -11 + 2 * (self.D + 16) * 2.0 ** -23 * big + 2.0 ** -20) * mass + 2.0 ** -24
+        got = d["o"].cpu().numpy().astype(np.float64)
+        assert np.isfinite(got).all()
+        off = np.abs(got - o) - tol
+        assert off.max() <= 0, (off.max(), np.unravel_index(off.argmax(), off.shape))
+        assert A.asf_read_error(d["ws"]) == error
+
+
+@pytest.mark.parametrize("lens,toks,kw", [
+    ([0], [1], {}), ([1], [1], dict(D=8, page=1)), ([0], [32], dict(grp=1)), ([63], [1], dict(D=128)),
+    ([64], [1], dict(D=128, hkv=1, grp=1)), ([65, 0, 130], [3, 2, 1], dict(D=80, page=20)),
+    ([500], [16], dict(D=128, grp=8)), ([1000, 7], [1, 31], dict(grp=5, page=64)),
+    ([3000, 1, 0, 2047, 2048], [8, 8, 8, 4, 4], dict(hkv=4, grp=4, D=128)),
+    ([5000], [32], dict(hkv=1, grp=16, D=96, page=256)), ([12345], [1], dict(hkv=3, grp=7, D=72, page=7)),
+    (list(range(0, 640, 20)), [1] * 32, dict(hkv=2, grp=1, D=128)),
+    ([20000], [2], dict(hkv=1, grp=4, D=128, page=33)), ([300, 400, 500], [0, 5, 0], dict(D=40))])
+def test_against_the_definition(lens, toks, kw):
+    c = Case(lens, toks, seed=sum(lens) + len(toks), **kw)
+    d = c.run()
+    c.check(d)
+    first = d["o"].clone()
+    d["o"].fill_(0)
+    c.run(d)
+    assert torch.equal(d["o"], first)                       # no order depends on timing
+
+
+def test_large_scores_and_scale():
+    c = Case([700], [4], D=64, spread=40.0, seed=3)         # one key takes nearly all of the weight
+    c.check(c.run(scale=0.5), scale=0.5)
+    c.check(c.run(scale=-0.25), scale=-0.25)
+
+
+def test_rows_that_see_nothing_and_rows_behind():
+    c = Case([0, 40], [6, 5], grp=3, seed=4)
+    c.anc[2] = 0                                            # no prefix and no own bit
+    c.anc[8] = 0                                            # only the prefix
+    c.anc[1] |= 1 << 9                                      # a bit of another request: not its token
+    c.anc[4] = 1 << 31
+    d = c.device()
+    pad = torch.full((4,) + d["q"].shape[1:], 5.0, dtype=torch.float16, device="cuda")
+    d["q"] = torch.cat([d["q"], pad])
+    for n in ("kn", "vn"):
+        d[n] = torch.cat([d[n], torch.full((4,) + d[n].shape[1:], 9.0, dtype=torch.float16, device="cuda")])
+    d["anc"] = torch.cat([d["anc"], torch.full((4,), -1, dtype=torch.int32, device="cuda")])
+    d["o"] = torch.full_like(d["q"], 7.0)
+    d["ws"] = A.Workspace.for_attention(d["cache"], 6, 2, 15)
+    c.run(d)
+    assert (d["o"][11:] == 7.0).all()                       # tokens behind the last request
+    assert (d["o"][2] == 0).all() and (d["o"][4] == 0).all()
+    c.anc[1] &= ~(1 << 9)
+    c.anc[4] = 0
+    d["o"] = d["o"][:11]
+    c.check(d)
+
+
+@pytest.mark.parametrize("n", [0, 50, 61])
+def test_what_a_row_does_not_see_does_not_reach_it(n):
+    """NaN and infinities in drafted tokens' keys and values, and behind the last key."""
+    c = Case([n], [8], grp=4, seed=n)
+    c.anc[:] = [1, 3, 5, 9, 19, 32, 64, 128]
+    for t, val in ((5, np.nan), (6, np.inf), (7, -np.inf)):
+        c.kn[t], c.vn[t] = val, val
+    c.vn[4, 0, 3] = np.nan
+    behind = (c.table[0][(n + 8) // 16] if (n + 8) // 16 < c.table.shape[1] else None, (n + 8) % 16)
+    if behind[0] is not None and behind[1]:
+        c.k[behind], c.v[behind] = np.nan, np.nan
+    d = c.run()
+    got = d["o"].cpu().numpy()
+    k, v = c.k.copy(), c.v.copy()
+    O.append(k, v, c.table, c.lens, c.begin, c.kn, c.vn)
+    o, _, _ = O.tree_attention(k[..., :], v, c.table, c.lens, c.begin, c.q, np.where(np.arange(8) < 4, c.anc, 1), c.D ** -0.5)
+    assert np.isfinite(got[:4]).all() and np.allclose(got[:4], o[:4], rtol=4e-3, atol=4e-3)
+    assert np.isnan(got[5:]).all()                          # rows that see them
+    assert np.isnan(got[4, :4, 3]).all() and np.isfinite(got[4, 4:]).all()
+
+
+def test_strided_caches():
+    """Pages laid out head by head, and keys and values side by side in one tensor."""
+    c = Case([200, 30], [3, 4], hkv=4, D=64, seed=6)
+    for make in (lambda a: torch.from_numpy(a).cuda().permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3), None):
+        d = c.device()
+        if make is not None:
+            d["cache"] = A.KVCache(make(c.k), make(c.v))
+        else:
+            both = torch.stack([torch.from_numpy(c.k), torch.from_numpy(c.v)], 3).cuda()
+            d["cache"] = A.KVCache(both[:, :, :, 0], both[:, :, :, 1])
+        c.check(c.run(d))
+
+
+def test_offsets_past_32_bits():
+    page, D, pages = 64, 128, 2 ** 31 // (64 * 128) + 3     # elements behind 2^31
+    k = torch.zeros(pages, page, 1, D, dtype=torch.float16, device="cuda")
+    v = torch.zeros_like(k)
+    c = Case([100], [2], hkv=1, grp=2, D=D, page=page, seed=8)
+    where = torch.tensor([pages - 1, pages - 3, 0, 1], device="cuda")
+    c.table = c.table * 0 + np.arange(c.table.shape[1])
+    k[where[:2]], v[where[:2]] = torch.from_numpy(c.k[:2]).cuda(), torch.from_numpy(c.v[:2]).cuda()
+    d = c.device()
+    small = d["cache"]
+    d["cache"], d["table"] = A.KVCache(k, v), where[:2].int()[None].contiguous()
+    c.run(d)
+    small.k[:2], small.v[:2] = k[where[:2]], v[where[:2]]
+    d["cache"] = small
+    c.check(d)
+
+
+def test_bad_tables_are_flagged_and_skipped():
+    c = Case([40, 30], [2, 3], seed=9)
+    d = c.device()
+    d["table"][0, 1] = c.k.shape[0] + 5                     # positions 16..31 of request 0
+    d["table"][1, 0] = -1
+    c.run(d)
+    assert A.asf_read_error(d["ws"]) == L.ASF_ERR_DEVICE_INDEX
+    o = d["o"].clone()
+    # the same with those keys masked by hand: request 0 without 16 keys, request 1 without its first 16
+    short = Case([40, 30], [2, 3], seed=9)
+    keep = [np.r_[0:16, 32:40], np.r_[16:30]]
+    ks, vs = c.k.copy(), c.v.copy()
+    O.append(ks, vs, c.table, c.lens, c.begin, c.kn, c.vn)
+    for r in range(2):
+        pg, sl = O.positions(c.table[r], 16, c.lens[r] + c.begin[r + 1] - c.begin[r])
+        idx = np.concatenate([keep[r], np.arange(c.lens[r], len(pg))])
+        kk, vv = ks[pg[idx], sl[idx]][None], vs[pg[idx], sl[idx]][None]
+        t = slice(c.begin[r], c.begin[r + 1])
+        ref, _, _ = O.tree_attention(kk, vv, [[0]], [len(keep[r])], [0, t.stop - t.start], short.q[t],
+                                     short.anc[t] >> t.start, 0.125)
+        assert np.allclose(o[t].cpu().numpy(), ref, rtol=4e-3, atol=4e-3)
+    # lengths and ranges that cannot be: clamped, flagged, nothing written outside
+    for lens, begin in (([-5, 30], [0, 2, 5]), ([40, 10 ** 9], [0, 2, 5]), ([40, 30], [0, 7, 3]), ([40, 30], [3, 1, 99]),
+                        ([2 ** 31 - 1, 2 ** 31 - 1], [-4, 2, 5])):
+        d = c.device()
+        d["lens"], d["begin"] = (torch.tensor(x, dtype=torch.int64).int().cuda() for x in (lens, begin))
+        c.run(d)
+        assert A.asf_read_error(d["ws"]) == L.ASF_ERR_DEVICE_INDEX
+    c2 = Case([40, 30], [2, 3], seed=9)
+    c2.check(c2.run())                                      # and the next call is sound
+
+
+def test_accepted_tokens_are_appended_again():
+    c = Case([37], [6], seed=10)
+    d = c.run()
+    keep = [0, 2, 5]                                        # a path of the tree
+    d["begin"] = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    A.asf_kv_append(d["cache"], d["table"], d["lens"], d["begin"], d["kn"][keep], d["vn"][keep], d["ws"])
+    d["lens"] += 3
+    got = d["cache"].k.cpu().numpy()
+    pg, sl = O.positions(c.table[0], 16, 40)
+    assert np.array_equal(got[pg[37:], sl[37:]], c.kn[keep])
+
+
+def test_graph_replays_with_other_lengths():
+    c = Case([900, 0], [4, 4], seed=11)
+    d = c.device()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c.run(d)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(d)
+    for lens in ([900, 0], [10, 0], [333, 0]):
+        c.lens = lens
+        d["cache"].k.copy_(torch.from_numpy(c.k))
+        d["cache"].v.copy_(torch.from_numpy(c.v))
+        d["lens"].copy_(torch.tensor(lens))
+        graph.replay()
+        c.check(d)
+
+
+def test_python_refusals():
+    c = Case([20], [2])
+    d = c.device()
+    k = d["cache"].k
+
+    def att(**kw):
+        a = dict(d, **kw)
+        A.asf_tree_attention(a["cache"], a["table"], a["lens"], a["begin"], a["q"], a["anc"], a["o"], a["ws"])
+
+    for bad in (lambda: A.KVCache(k.float(), k.float()), lambda: A.KVCache(k, k[:1]), lambda: A.KVCache(k.cpu(), k.cpu()),
+                lambda: A.KVCache(k[..., ::2], k[..., ::2]), lambda: att(q=d["q"].float()), lambda: att(o=d["o"][:1]),
+                lambda: att(anc=d["anc"].long()), lambda: att(anc=d["anc"][:1]), lambda: att(lens=d["lens"].cpu()),
+                lambda: att(begin=d["begin"][:1]), lambda: att(table=d["table"][0]),
+                lambda: A.asf_kv_append(d["cache"], d["table"], d["lens"], d["begin"], d["kn"][:, :1], d["vn"], d["ws"])):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: att(q=d["q"][:, :3].contiguous(), o=d["o"][:, :3].contiguous()),
+                lambda: att(ws=A.Workspace.for_w4(A.W4Matrix.quantize(torch.ones(8, 8, device="cuda"), 32), 1))):
+        with pytest.raises(A.AsfError):
+            bad()
