@@ -14,7 +14,7 @@ from .api import (FFN, AsfError, Predictor, Workspace, asf_activation_counts,  #
                   asf_predict_sparse_ffn, asf_predict_sparse_ffn_begin, asf_predict_sparse_ffn_end,
                   asf_predict_sparse_ffn_exchange, asf_read_error, asf_reduce_exchange, asf_set_fault_injection, asf_sparse_ffn, asf_sparse_ffn_noalloc,
                   asf_status_string, asf_version, asf_workspace_bytes, asf_workspace_init, pack_layer)
-from .stack import LayerStack  # noqa: F401
+from .stack import AttentionStage, LayerStack  # noqa: F401
 from .attention import KVCache, asf_kv_append, asf_tree_attention  # noqa: F401
 from .w4 import (W4FFN, W4Matrix, asf_w4_dequantize, asf_w4_matmul, asf_w4_quantize, asf_w4_row_bytes,  # noqa: F401
                  asf_w4_sparse_ffn)

@@ -100,7 +100,7 @@ PROTOTYPES = {
     "asf_w4_workspace_bytes": (c_size_t, [POINTER(asf_w4_matrix), POINTER(asf_w4_ffn), c_int32]),
     "asf_w4_quantize": (c_int, [c_void_p, c_int, POINTER(asf_w4_matrix), c_void_p]),
     "asf_w4_dequantize": (c_int, [POINTER(asf_w4_matrix), c_void_p, c_int, c_void_p]),
-    "asf_w4_matmul": (c_int, [POINTER(asf_w4_matrix), c_void_p, c_int, c_int32, c_void_p, c_int32, c_void_p,
+    "asf_w4_matmul": (c_int, [POINTER(asf_w4_matrix), c_void_p, c_int, c_int32, c_void_p, c_int32, c_void_p, c_int,
                               c_void_p, c_size_t, c_void_p]),
     "asf_w4_sparse_ffn": (c_int, [POINTER(asf_w4_ffn), c_void_p, c_int, c_int32, c_void_p, c_void_p, c_void_p,
                                   c_void_p, c_size_t, c_void_p]),

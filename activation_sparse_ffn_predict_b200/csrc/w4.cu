@@ -213,6 +213,7 @@ struct DotArgs {
   int relu;
   const int32_t *idx, *count;  // list form; null count: all rows
   float *y;                    // dense: [B][rows]; list form: a [positions][8 * NT]
+  int y16;                     // dense: y is fp16
   float *part;                 // partial tiles of a split k
   int smin;
   Header *hdr;
@@ -398,7 +399,9 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
             const int b = 8 * n + 2 * t + c;
             float v = tot[n][2 * h + c] + bias;
             if (A.relu) v = v > 0.f ? v : (v != v ? v : 0.f);
-            if (b < A.B) A.y[(int64_t)b * A.rows + r] = v;
+            if (b >= A.B) continue;
+            if (A.y16) reinterpret_cast<__half *>(A.y)[(int64_t)b * A.rows + r] = __float2half_rn(v);
+            else A.y[(int64_t)b * A.rows + r] = v;
           }
       }
       return;
@@ -785,11 +788,12 @@ asf_status asf_w4_dequantize(const asf_w4_matrix *mat, void *dst, asf_dtype dtyp
 }
 
 asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dtype xdtype, int32_t B, const float *bias,
-                         int32_t relu, float *y, void *ws, size_t ws_bytes, asf_stream_t stream) {
+                         int32_t relu, void *y, asf_dtype ydtype, void *ws, size_t ws_bytes, asf_stream_t stream) {
   asf_status s = check_w4(mat);
   if (s != ASF_OK) return s;
   if (!x || !y || B < 1 || B > ASF_MAX_BATCH || (relu != 0 && relu != 1)) return ASF_ERR_INVALID_ARG;
   if (xdtype != ASF_F16 && xdtype != ASF_F32) return ASF_ERR_UNSUPPORTED;
+  if (ydtype != ASF_F16 && ydtype != ASF_F32) return ASF_ERR_UNSUPPORTED;
   if (!al16(x) || !al4(y) || !al4(bias)) return ASF_ERR_MISALIGNED;
   s = check_ws(ws, ws_bytes, kHeaderBytes + dot_part_bytes(ceil_div(mat->rows, 16), mat->k, B));
   if (s != ASF_OK) return s;
@@ -803,7 +807,8 @@ asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dtype xdty
   a.B = B;
   a.bias = bias;
   a.relu = relu;
-  a.y = y;
+  a.y = static_cast<float *>(y);
+  a.y16 = ydtype == ASF_F16;
   a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kHeaderBytes);
   a.smin = dot_smin(mat->k, B, xdtype == ASF_F32 ? 3 : 1);
   a.hdr = static_cast<Header *>(ws);

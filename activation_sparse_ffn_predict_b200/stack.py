@@ -9,21 +9,71 @@ dependent launch (each waits for its predecessor before reading its inputs).
 """
 from __future__ import annotations
 
-from typing import List, Optional, Sequence
+from typing import List, Optional, Sequence, Union
 
 import torch
 
-from .api import (FFN, Predictor, Workspace, asf_dense_ffn, asf_predict, asf_predict_sparse_ffn,
+from .api import (FFN, Predictor, Workspace, asf_dense_ffn, asf_predict, asf_predict_sparse_ffn, asf_read_error,
                   asf_sparse_ffn)
+from .attention import KVCache, asf_kv_append, asf_tree_attention
+from .w4 import W4FFN, W4Matrix, asf_w4_matmul, asf_w4_sparse_ffn
+
+
+class AttentionStage:
+    """The attention in front of a stack's FFN layers, for the stack's B tokens.
+
+    Layer l appends k[l], v[l] [B, heads, head_dim] to caches[l], runs the
+    tokens' tree attention with q[l] [B, q_heads, head_dim], and leaves the
+    layer's FFN input in the stack's x[l]: the attention output itself (then
+    q_heads * head_dim is the hidden size), or its product with the 4-bit
+    projection out[l] [hidden, q_heads * head_dim].  The caller fills q, k, v
+    and, for all layers alike, table [R, max_pages], lens [R], begin [R + 1]
+    and anc [B]."""
+
+    def __init__(self, caches: Sequence[KVCache], q_heads: int, requests: int, max_pages: int, batch: int,
+                 out: Optional[Sequence[W4Matrix]] = None):
+        c0, n = caches[0], len(caches)
+        if any((c.heads, c.head_dim, c.device) != (c0.heads, c0.head_dim, c0.device) for c in caches):
+            raise ValueError("the layers' caches must have one head layout and device")
+        if out is not None and (len(out) != n or any(m.k != q_heads * c0.head_dim for m in out)):
+            raise ValueError("one projection of q_heads * head_dim columns per layer")
+        self.caches, self.out, self.R, self.max_pages = list(caches), out, int(requests), int(max_pages)
+        half = lambda *s: torch.zeros(*s, dtype=torch.float16, device=c0.device)  # noqa: E731
+        ints = lambda *s: torch.zeros(*s, dtype=torch.int32, device=c0.device)  # noqa: E731
+        self.q = half(n, batch, q_heads, c0.head_dim)
+        self.k, self.v = half(n, batch, c0.heads, c0.head_dim), half(n, batch, c0.heads, c0.head_dim)
+        self.o = half(batch, q_heads, c0.head_dim)
+        self.table, self.lens, self.begin, self.anc = ints(requests, max_pages), ints(requests), ints(requests + 1), ints(batch)
+        self.ws = Workspace.for_attention(c0, q_heads, requests, batch)
+        self.ws_out = Workspace.for_w4(out[0], batch) if out is not None else None
+        self.width = out[0].rows if out is not None else q_heads * c0.head_dim
+
+    def launches(self) -> int:
+        """Kernels per layer: append, attention, the merge of split keys unless the table is too
+        short for a split, and the projection."""
+        split = self.max_pages * self.caches[0].page > 256
+        return 2 + int(split) + int(self.out is not None)
+
+    def enqueue(self, l: int, x: torch.Tensor, stream=None) -> None:
+        o = self.o if self.out is not None else x.view(self.o.shape)
+        asf_kv_append(self.caches[l], self.table, self.lens, self.begin, self.k[l], self.v[l], self.ws, stream)
+        asf_tree_attention(self.caches[l], self.table, self.lens, self.begin, self.q[l], self.anc, o, self.ws,
+                           stream=stream)
+        if self.out is not None:
+            asf_w4_matmul(self.out[l], o.view(x.shape[0], -1), x, self.ws_out, stream=stream)
 
 
 class LayerStack:
-    def __init__(self, preds: Sequence[Optional[Predictor]], ffns: Sequence[FFN], batch: int,
-                 tau: float = 0.5, mode: str = "predict", device=None, combined: bool = True):
+    def __init__(self, preds: Sequence[Optional[Predictor]], ffns: Sequence[Union[FFN, W4FFN]], batch: int,
+                 tau: float = 0.5, mode: str = "predict", device=None, combined: bool = True,
+                 attention: Optional[AttentionStage] = None):
         """mode: "predict" (predictor + sparse FFN), "sparse" (sparse FFN over
         caller-filled idx/count), or "dense" (all neurons).  combined: in
         predict mode, one asf_predict_sparse_ffn call per layer instead of
-        asf_predict followed by asf_sparse_ffn (same results)."""
+        asf_predict followed by asf_sparse_ffn (same results).  FFNs of 4-bit
+        rows (all layers or none) take the predicted list from asf_predict.
+        attention: what computes x[l] before each layer; without it the caller
+        fills x."""
         if mode not in ("predict", "sparse", "dense"):
             raise ValueError("mode must be predict, sparse or dense")
         self.preds = list(preds)
@@ -35,13 +85,25 @@ class LayerStack:
         self.combined = bool(combined)
         f0 = self.ffns[0]
         dev = device if device is not None else f0.tensors[1].device
-        self.d, self.n, self.dtype = f0.d, f0.n, f0.dtype
+        self.w4 = isinstance(f0, W4FFN)
+        if any(isinstance(f, W4FFN) != self.w4 for f in self.ffns):
+            raise ValueError("4-bit FFNs: all layers or none")
+        if self.w4:
+            self.combined = False
+        p0 = self.preds[0] if (self.preds and mode == "predict") else None
+        self.d, self.n = f0.d, f0.n
+        self.dtype = (p0.dtype if p0 is not None else torch.float16) if self.w4 else f0.dtype
+        self.attention = attention
+        if attention is not None and (attention.width != self.d or attention.q.shape[:2] != (self.L, self.B)
+                                      or self.dtype != torch.float16):
+            raise ValueError("the attention stage must have the stack's layers and batch and give its fp16 input")
         self.x = torch.zeros(self.L, self.B, self.d, dtype=self.dtype, device=dev)
         self.y = torch.zeros(self.L, self.B, self.d, dtype=torch.float32, device=dev)
         self.idx = torch.zeros(self.L, self.n, dtype=torch.int32, device=dev)
         self.count = torch.zeros(self.L, dtype=torch.int32, device=dev)
-        p0 = self.preds[0] if (self.preds and mode == "predict") else None
-        self.ws = Workspace(p0, f0, self.B, device=dev)
+        self.ws = Workspace(p0, f0, self.B, device=dev) if not self.w4 else (
+            Workspace(p0, None, self.B, device=dev) if p0 is not None else None)
+        self.ws_w4 = Workspace.for_w4(f0, self.B) if self.w4 else None
         self.graph: Optional[torch.cuda.CUDAGraph] = None
 
     def launches_per_step(self) -> int:
@@ -54,7 +116,12 @@ class LayerStack:
         the batch; otherwise, for 5-32 tokens with fp16 weights, the
         tensor-core gate/up kernel once per 16 tokens, the tensor-core down
         projection and the reduction of its splits; else gate/up and down on
-        the CUDA cores."""
+        the CUDA cores; gate/up and down for 4-bit rows.  The attention stage
+        adds its own."""
+        attention = getattr(self, "attention", None)
+        before = attention.launches() if attention is not None else 0
+        if getattr(self, "w4", False):
+            return self.L * (before + 2 + (2 + -(-self.B // 8) if self.mode == "predict" else 0))
         fused = _fused_sparse_ffn(self.d, self.dtype, self.B)
         if fused:
             ffn = 2
@@ -63,14 +130,24 @@ class LayerStack:
         else:
             ffn = 2
         if self.mode != "predict":
-            return self.L * ffn
+            return self.L * (before + ffn)
         pred = 1 + -(-self.B // 8)
         compact = 0 if (self.combined and fused) else 1
-        return self.L * (pred + compact + ffn)
+        return self.L * (before + pred + compact + ffn)
 
     def enqueue(self, stream=None) -> None:
         for l in range(self.L):
             x, y = self.x[l], self.y[l]
+            if self.attention is not None:
+                self.attention.enqueue(l, x, stream)
+            if self.w4:
+                cnt = self.count[l:l + 1]
+                if self.mode == "predict":
+                    asf_predict(self.preds[l], x, self.tau, self.idx[l], cnt, self.ws, stream)
+                dense = self.mode == "dense"
+                asf_w4_sparse_ffn(self.ffns[l], x, None if dense else self.idx[l], None if dense else cnt, y, self.ws_w4,
+                                  stream)
+                continue
             if self.mode == "dense":
                 asf_dense_ffn(self.ffns[l], x, y, self.ws, stream)
                 continue
@@ -82,6 +159,12 @@ class LayerStack:
             if self.mode == "predict":
                 asf_predict(self.preds[l], x, self.tau, self.idx[l], cnt, self.ws, stream)
             asf_sparse_ffn(self.ffns[l], x, self.idx[l], cnt, y, self.ws, stream)
+
+    def read_error(self, stream=None) -> int:
+        """asf_read_error over all of the stack's workspaces: the first error, or 0."""
+        stage = self.attention
+        spaces = [self.ws, self.ws_w4] + ([stage.ws, stage.ws_out] if stage is not None else [])
+        return next((e for e in [asf_read_error(w, stream) for w in spaces if w is not None] if e), 0)
 
     def capture(self, warmup: int = 2) -> None:
         s = torch.cuda.Stream()

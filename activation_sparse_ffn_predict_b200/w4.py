@@ -121,22 +121,22 @@ def asf_w4_dequantize(mat: W4Matrix, dst: torch.Tensor, stream=None) -> None:
 
 def asf_w4_matmul(mat: W4Matrix, x: torch.Tensor, y: torch.Tensor, ws: Workspace,
                   bias: Optional[torch.Tensor] = None, relu: bool = False, stream=None) -> None:
-    """y [B, m] fp32 = x [B, k] (fp16 or fp32) times the 4-bit rows (+ bias [m], then ReLU)."""
+    """y [B, m] = x [B, k] times the 4-bit rows (+ bias [m], then ReLU); x and y fp16 or fp32."""
     if x.dtype not in _DT or x.dim() != 2 or x.shape[1] != mat.k:
         raise ValueError("x must be [B, k], float16 or float32")
     B = x.shape[0]
-    if y.dim() != 2 or y.shape[0] != B or y.shape[1] != mat.rows:
-        raise ValueError("y must be [B, rows]")
+    if y.dtype not in _DT or y.dim() != 2 or y.shape[0] != B or y.shape[1] != mat.rows:
+        raise ValueError("y must be [B, rows], float16 or float32")
     dev = mat.device
     bp = None
     if bias is not None:
         if bias.shape != (mat.rows,):
             raise ValueError("bias must be [rows]")
         bp = _arg(bias, "bias", dev, torch.float32)
-    xp, yp = _arg(x, "x", dev), _arg(y, "y", dev, torch.float32)
+    xp, yp = _arg(x, "x", dev), _arg(y, "y", dev)
     with _on(dev, stream) as st:
-        check(L.load().asf_w4_matmul(mat._ref, xp, _DT[x.dtype], B, bp, int(bool(relu)), yp, ws.on(dev), ws.nbytes, st),
-              "asf_w4_matmul")
+        check(L.load().asf_w4_matmul(mat._ref, xp, _DT[x.dtype], B, bp, int(bool(relu)), yp, _DT[y.dtype], ws.on(dev),
+                                     ws.nbytes, st), "asf_w4_matmul")
 
 
 def asf_w4_sparse_ffn(ffn: W4FFN, x: torch.Tensor, idx: Optional[torch.Tensor], count: Optional[torch.Tensor],

@@ -268,7 +268,7 @@ ASF_API asf_status asf_sparse_ffn_noalloc(const asf_ffn *ffn, const void *x, int
  * and asf_permute_rows move them.
  *
  * No weight is rounded on its way through a product: sums run in fp32, scales
- * multiply fp32 sums.  x is fp16 or fp32 (an fp32 x enters exactly), y fp32. */
+ * multiply fp32 sums.  x is fp16 or fp32 (an fp32 x enters exactly). */
 #define ASF_W4_MAX_K 65536
 
 typedef struct {
@@ -312,10 +312,10 @@ ASF_API size_t asf_w4_workspace_bytes(const asf_w4_matrix *mat, const asf_w4_ffn
  *   x     device [B][k] in xdtype, 16-byte aligned (an fp32 x must be finite)
  *   bias  device fp32 [rows], or NULL
  *   relu  0: none, 1: max(., 0)
- *   y     device fp32 [B][rows], overwritten */
+ *   y     device [B][rows] in ydtype (fp16: the fp32 sum rounded once), overwritten */
 ASF_API asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dtype xdtype, int32_t B,
-                                 const float *bias, int32_t relu, float *y, void *ws, size_t ws_bytes,
-                                 asf_stream_t stream);
+                                 const float *bias, int32_t relu, void *y, asf_dtype ydtype, void *ws,
+                                 size_t ws_bytes, asf_stream_t stream);
 
 /* asf_sparse_ffn over 4-bit rows: x [B][d] in xdtype, idx/count/y as there;
  * idx and count both NULL runs all n neurons (asf_dense_ffn).  The activations

@@ -90,6 +90,9 @@ def test_matmul(m, k, group, B, dt):
         again = torch.full((B, m), float("nan"), device="cuda")
         A.asf_w4_matmul(mat, x.cuda(), again, ws, bias=torch.from_numpy(bias).cuda() if use_bias else None, relu=relu)
         assert torch.equal(y, again)                        # fixed summation order
+        half = torch.empty(B, m, device="cuda", dtype=torch.float16)
+        A.asf_w4_matmul(mat, x.cuda(), half, ws, bias=torch.from_numpy(bias).cuda() if use_bias else None, relu=relu)
+        assert torch.equal(half, y.half())                  # the same sum, rounded once
     assert A.asf_read_error(ws) == 0
 
 
@@ -237,7 +240,7 @@ def test_python_refusals():
     x, y = torch.randn(2, 256, device="cuda"), torch.empty(2, 32, device="cuda")
     for bad in (lambda: A.asf_w4_matmul(mat, x.cpu(), y, ws), lambda: A.asf_w4_matmul(mat, x, y.cpu(), ws),
                 lambda: A.asf_w4_matmul(mat, x.bfloat16(), y, ws), lambda: A.asf_w4_matmul(mat, x[:, :128], y, ws),
-                lambda: A.asf_w4_matmul(mat, x.t().contiguous().t(), y, ws), lambda: A.asf_w4_matmul(mat, x, y.half(), ws),
+                lambda: A.asf_w4_matmul(mat, x.t().contiguous().t(), y, ws), lambda: A.asf_w4_matmul(mat, x, y.double(), ws),
                 lambda: A.asf_w4_matmul(mat, x, y[:1], ws), lambda: A.asf_w4_matmul(mat, x, y, ws, bias=y[0, :5]),
                 lambda: A.W4Matrix(mat.data.int(), 256, 64), lambda: A.W4Matrix(mat.data, 1024, 64),
                 lambda: A.W4Matrix.quantize(x.bfloat16(), 64), lambda: A.asf_w4_dequantize(mat, y),

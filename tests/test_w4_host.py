@@ -62,7 +62,7 @@ def test_matrix_descriptors_refused(lib, kw, status):
     m = ctypes.byref(_mat(**kw))
     assert lib.asf_w4_quantize(FAKE, L.ASF_F16, m, None) == status
     assert lib.asf_w4_dequantize(m, FAKE, L.ASF_F16, None) == status
-    assert lib.asf_w4_matmul(m, FAKE, L.ASF_F16, 1, None, 0, FAKE, FAKE, 1 << 40, None) == status
+    assert lib.asf_w4_matmul(m, FAKE, L.ASF_F16, 1, None, 0, FAKE, L.ASF_F32, FAKE, 1 << 40, None) == status
     assert lib.asf_w4_workspace_bytes(m, None, 1) == 0
 
 
@@ -71,16 +71,16 @@ def test_matmul_refuses(lib):
     need = lib.asf_w4_workspace_bytes(ctypes.byref(m), None, 4)
     assert need > 4096
 
-    def call(x=FAKE, dt=L.ASF_F16, B=4, bias=None, relu=0, y=FAKE, ws=FAKE, wsb=need - 1):
-        return lib.asf_w4_matmul(ctypes.byref(m), x, dt, B, bias, relu, y, ws, wsb, None)
+    def call(x=FAKE, dt=L.ASF_F16, B=4, bias=None, relu=0, y=FAKE, ydt=L.ASF_F32, ws=FAKE, wsb=need - 1):
+        return lib.asf_w4_matmul(ctypes.byref(m), x, dt, B, bias, relu, y, ydt, ws, wsb, None)
 
     assert call() == L.ASF_ERR_WORKSPACE
     assert call(ws=0, wsb=need) == L.ASF_ERR_WORKSPACE
     assert call(ws=FAKE + 16, wsb=need) == L.ASF_ERR_WORKSPACE
     assert call(x=0) == call(y=0) == call(B=0) == call(B=33) == call(relu=2) == L.ASF_ERR_INVALID_ARG
-    assert call(dt=7) == L.ASF_ERR_UNSUPPORTED
+    assert call(dt=7) == call(ydt=3) == L.ASF_ERR_UNSUPPORTED
     assert call(x=FAKE + 8) == call(y=FAKE + 2) == call(bias=FAKE + 2) == L.ASF_ERR_MISALIGNED
-    assert lib.asf_w4_matmul(None, FAKE, 1, 1, None, 0, FAKE, FAKE, 1 << 40, None) == L.ASF_ERR_INVALID_ARG
+    assert lib.asf_w4_matmul(None, FAKE, 1, 1, None, 0, FAKE, L.ASF_F32, FAKE, 1 << 40, None) == L.ASF_ERR_INVALID_ARG
     assert lib.asf_w4_quantize(0, L.ASF_F16, ctypes.byref(m), None) == L.ASF_ERR_INVALID_ARG
     assert lib.asf_w4_quantize(FAKE + 2, L.ASF_F16, ctypes.byref(m), None) == L.ASF_ERR_MISALIGNED
     assert lib.asf_w4_quantize(FAKE, 9, ctypes.byref(m), None) == L.ASF_ERR_UNSUPPORTED
