@@ -35,7 +35,7 @@ constexpr int kDotWarps = 16;
 constexpr int kDownWarps = 8;
 constexpr int kDownCols = 256;         // columns per down-projection CTA (two blocks)
 constexpr int kTicketBytes = kMaxTiles * 4;   // one byte a ticket: more than the splits a row tile has
-constexpr size_t kDotSmem = 200 * 1024;
+constexpr size_t kDotSmem = 226 * 1024;
 constexpr float kFp16Max = 65504.f;
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -183,6 +183,20 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// one of the two fp16 values of a word
+__device__ __forceinline__ float half_of(uint32_t w, int hi) {
+  return __half2float(__ushort_as_half((unsigned short)(hi ? w >> 16 : w & 0xffffu)));
+}
+// 4-, 8- or 16-byte asynchronous copy global -> shared
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(void *dst, const void *src, bool in = true) {
+  if constexpr (BYTES == 16)
+    cp_async16(dst, src, in ? 16u : 0u);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES),
+                 "r"(in ? BYTES : 0)
+                 : "memory");
+}
 __device__ __forceinline__ float trunc_bf16(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
 // the upper halves of two floats as one pair (lo first)
 __device__ __forceinline__ uint32_t upper2(float lo, float hi) {
@@ -190,76 +204,165 @@ __device__ __forceinline__ uint32_t upper2(float lo, float hi) {
 }
 
 // ------------------------------------------------------- row products --
-// Splits S of k (in superblocks) such that tiles * S fills the warps that keep
-// enough loads in flight (8 an SM); smin splits at least, so that a CTA's part
-// of x fits its shared memory.  Even shares.
-__host__ __device__ inline int w4_splits(int tiles, int nsb, int smin, int ctas) {
-  int S = ceil_div(8 * ctas, tiles > 0 ? tiles : 1);
-  if (S < smin) S = smin;
-  if (S > nsb) S = nsb;
-  if (S > ctas) S = ctas;
-  return ceil_div(nsb, ceil_div(nsb, S));
-}
-
 struct DotArgs {
   const unsigned char *data;   // first row (gate rows of the list form)
   int64_t stride;              // bytes from row to row (neuron to neuron)
   int64_t up;                  // bytes from a neuron's gate row to its up row (REGLU), else 0
   int rows;                    // rows, or neurons the list may name
-  int k, group;
+  int k;
   const void *x;
   int B;
   const float *bias;           // per row, or null
   int relu;
-  const int32_t *idx, *count;  // list form; null count: all rows
+  const int32_t *idx, *count;  // list form; null: all rows
   float *y;                    // dense: [B][rows]; list form: a [positions][8 * NT]
   int y16;                     // dense: y is fp16
   float *part;                 // partial tiles of a split k
-  int smin;
+  int most;                    // superblocks of k whose x fits a CTA
   Header *hdr;
 };
 
 enum { kDense = 0, kListUp = 1, kListGated = 2 };
 
+// Stages of two blocks (256 weights of 16 rows, and their scales) that a warp
+// keeps in shared memory, all but one of them in flight.
+__host__ __device__ constexpr int dot_stages(int NT) { return NT == 1 ? 4 : 3; }
+__host__ __device__ constexpr int dot_stage_bytes(int GS) { return 2048 + 16 * (4 << GS); }
+__host__ __device__ constexpr size_t dot_ring_bytes(int NT, int GS) { return (size_t)kDotWarps * dot_stages(NT) * dot_stage_bytes(GS); }
+
+// Superblocks of k per CTA (k is split into ceil(nsb / per) parts): the least
+// of (row tiles of a CTA, or 8 where it has fewer: about what keeps enough
+// loads in flight) x per, where a split costs as much as 20 superblocks for its
+// partial sums and ticket.  More than 16 tile parts an SM are never made by
+// choice, which bounds the workspace.
+__device__ __forceinline__ int dot_per(int tiles, int nsb, int most, int ctas, int lane) {
+  uint32_t best = 0xffffffffu;
+  for (int p0 = 0; p0 < most; p0 += 32) {
+    const int per = p0 + lane + 1;
+    uint32_t key = 0xffffffffu;
+    if (per <= most) {
+      const int S = ceil_div(nsb, per);
+      if (per == most || (int64_t)tiles * S <= 16 * ctas) {
+        const int u = max(8, ceil_div(tiles, ctas / S));
+        const int64_t cost = (int64_t)u * per + (S > 1 ? 20 + S : 0);
+        key = (uint32_t)min(cost, (int64_t)(1 << 23)) * 256u + (uint32_t)(255 - per);
+      }
+    }
+    best = min(best, __reduce_min_sync(0xffffffffu, key));
+  }
+  return 255 - (int)(best & 255u);
+}
+
 // Each warp owns row tiles of 16 rows (8 neurons' gate rows over their 8 up
 // rows in the gated form: a thread then holds a neuron's gate and up sums of
-// the same tokens side by side) over its CTA's part of k.  A stage is UB
-// blocks of 128 weights of each row, loaded one stage ahead into registers
-// (16-byte loads; four lanes share a row, so 64 bytes of a row in a row), also
-// across the tile's end.  x's part sits in shared memory for the CTA's life.
-// With k split, a tile's partial sums meet in the workspace and the warp that
-// takes the tile's last ticket adds them in the order of the splits.
-template <bool BF, int NT, int UB>
+// the same tokens side by side) over its CTA's part of k.  It streams them
+// through a ring of its own in shared memory by 16-byte cp.async, whole
+// 128-byte lines of a row, across tile ends, without meeting the other warps.
+// x's part sits in shared memory for the CTA's life.  With k split, a tile's
+// partial sums meet in the workspace and the warp that takes the tile's last
+// ticket adds them in the order of the splits.
+template <bool BF, int NT, int GS>
 __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mode) {
-  extern __shared__ __align__(16) unsigned char sm[];
+  extern __shared__ __align__(128) unsigned char sm[];
   constexpr int P = BF ? 3 : 1;                    // parts of x
+  constexpr int NS = dot_stages(NT), SB = dot_stage_bytes(GS), SCB = 4 << GS;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   int total = A.rows;
-  if (mode != kDense) {
-    if (A.count) {
-      total = ld_cg_i32(A.count);
-      if (total < 0 || total > A.rows) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) flag_error(&A.hdr->err, kErrIndex);
-        total = total < 0 ? 0 : A.rows;
-      }
+  if (A.count) {
+    total = ld_cg_i32(A.count);
+    if (total < 0 || total > A.rows) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) flag_error(&A.hdr->err, kErrIndex);
+      total = total < 0 ? 0 : A.rows;
     }
   }
   const int per = mode == kListGated ? 8 : 16;
   const int tiles = ceil_div(total, per);
   const int nblk = w4_kp(A.k) / kBlk, nsb = ceil_div(nblk, 4);
-  const int S = w4_splits(tiles, nsb, A.smin, gridDim.x);
+  const int sb_per = dot_per(tiles, nsb, A.most, gridDim.x, lane);
+  const int S = ceil_div(nsb, sb_per);
   const int ctas = gridDim.x / S;                  // CTAs of one part of k
   const int s = blockIdx.x / ctas, p = blockIdx.x % ctas;
   if (s >= S) return;
-  const int sb_per = ceil_div(nsb, S);
   const int b0 = s * sb_per * 4, b1 = min(nblk, b0 + sb_per * 4);   // blocks of this part
   // a warp's unit: tpu consecutive tiles under one ticket
   const int tpu = S > 1 ? ceil_div(tiles, kTicketBytes) : 1;
   const int units = ceil_div(tiles, tpu);
   if (p >= units) return;
+
+  unsigned char *ring = sm + (size_t)warp * NS * SB;
+  unsigned char *sx = sm + dot_ring_bytes(NT, GS);
+  const int stages = ceil_div(b1 - b0, 2);
+  const int step = ctas * kDotWarps;
+
+  // ---- the copying side, ahead of the computing side
+  struct {
+    int unit, tile, stage;
+  } pr{p + ctas * warp, 0, 0}, co;
+  pr.tile = pr.unit * tpu;
+  co = pr;
+  auto advance = [&](auto &c) {                    // to the next stage; true at a tile's end
+    if (++c.stage < stages) return false;
+    c.stage = 0;
+    if (++c.tile >= min(tiles, (c.unit + 1) * tpu)) {
+      c.unit += step;
+      c.tile = c.unit * tpu;
+    }
+    return true;
+  };
+  const int mine = lane & (per - 1);               // this lane's place in a tile's list
+  auto id_of = [&](int tile) {
+    const int pos = min(tile * per + mine, total - 1);
+    return A.idx ? ld_cg_i32(A.idx + pos) : pos;
+  };
+  const unsigned char *rp[4], *sp;
+  int next_id = 0;
+  auto point = [&]() {                             // at pr.tile's rows; next_id holds its list entry
+    int id = next_id;
+    if ((unsigned)id >= (unsigned)A.rows) {
+      flag_error(&A.hdr->err, kErrIndex);
+      id = 0;
+    }
+    {                                              // the entry of the tile after this one
+      int nu = pr.unit, nt = pr.tile + 1;
+      if (nt >= min(tiles, (nu + 1) * tpu)) nt = (nu + step) * tpu;
+      if (nt < tiles) next_id = id_of(nt);
+    }
+    const int part = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const unsigned char *row = A.data + (int64_t)__shfl_sync(0xffffffffu, id, r & (per - 1)) * A.stride;
+      if (mode == kListGated && r >= 8) row += A.up;
+      rp[i] = row + (int64_t)b0 * 64 + part * 16;
+    }
+    sp = A.data + (int64_t)id * A.stride + (mode == kListGated && (lane & 8) ? A.up : 0) + w4_kp(A.k) / 2 +
+         (int64_t)b0 * (2 << GS);
+  };
+  const uint64_t pol = l2_evict_first();
+  auto copy = [&](int slot) {                      // stage pr.stage of pr.tile
+    if (pr.unit < units) {
+      unsigned char *to = ring + slot * SB;
+      const int part = lane & 7;
+      const bool in = b0 + pr.stage * 2 + (part >> 2) < b1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        cp_async16(to + (part >> 2) * 1024 + (4 * i + (lane >> 3)) * 64 + (part & 3) * 16,
+                   in ? rp[i] + pr.stage * 128 : A.data, in ? 16u : 0u, pol);
+      // the scale area is padded to whole superblocks: a stage's scales are inside it
+      if (lane < 16) cp_async_small<SCB>(to + 2048 + lane * SCB, sp + pr.stage * SCB);
+      if (advance(pr) && pr.unit < units) point();
+    }
+    cp_async_commit();
+  };
+  if (pr.unit < units) {
+    next_id = id_of(pr.tile);
+    point();
+  }
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i) copy(i);
 
   // x's part: [P][B][b1-b0 blocks], rows 64 bytes past a multiple of 128 apart
   // (eight lanes of a 16-byte read then touch every bank once)
@@ -270,7 +373,7 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
     if constexpr (!BF) {
       uint4 v = make_uint4(0, 0, 0, 0);
       if (kk < A.k) v = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(A.x) + (int64_t)b * A.k + kk);
-      *reinterpret_cast<uint4 *>(sm + (size_t)b * xrow + c * 2) = v;
+      *reinterpret_cast<uint4 *>(sx + (size_t)b * xrow + c * 2) = v;
     } else {
       float f[8] = {};
       if (kk < A.k) {
@@ -282,7 +385,7 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
       for (int q = 0; q < 3; ++q) {
         uint4 v;
         v.x = upper2(f[0], f[1]); v.y = upper2(f[2], f[3]); v.z = upper2(f[4], f[5]); v.w = upper2(f[6], f[7]);
-        *reinterpret_cast<uint4 *>(sm + ((size_t)q * A.B + b) * xrow + c * 2) = v;
+        *reinterpret_cast<uint4 *>(sx + ((size_t)q * A.B + b) * xrow + c * 2) = v;
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] -= trunc_bf16(f[e]);
       }
@@ -290,96 +393,56 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
   }
   __syncthreads();
 
-  const int stages = ceil_div(b1 - b0, UB);
-  const int kp2 = w4_kp(A.k) / 2;
-  const int gsh = A.group == 32 ? 2 : A.group == 64 ? 1 : 0;         // log2 of the groups of a block
-  constexpr int SB = UB * 4;                                         // most scales of a stage
-
-  // rows of a tile: this lane's two row pointers
-  auto rows_of = [&](int tile, const unsigned char *&ra, const unsigned char *&rb) {
-    int pa = tile * per + g, pb = pa + 8;
-    if (mode == kListGated) pb = pa;
-    pa = min(pa, total - 1);
-    pb = min(pb, total - 1);
-    if (mode != kDense && A.idx) {
-      pa = ld_cg_i32(A.idx + pa);
-      pb = ld_cg_i32(A.idx + pb);
-      if ((unsigned)pa >= (unsigned)A.rows) { flag_error(&A.hdr->err, kErrIndex); pa = 0; }
-      if ((unsigned)pb >= (unsigned)A.rows) { flag_error(&A.hdr->err, kErrIndex); pb = 0; }
-    }
-    ra = A.data + (int64_t)pa * A.stride;
-    rb = A.data + (int64_t)pb * A.stride + (mode == kListGated ? A.up : 0);
-  };
-  struct Stage {
-    uint4 c[UB][2];
-    uint32_t sc[2][SB / 2];
-  };
-  auto load = [&](Stage &st, const unsigned char *ra, const unsigned char *rb, int stage) {
-    const int b = b0 + stage * UB;
-#pragma unroll
-    for (int u = 0; u < UB; ++u) {
-      const bool in = b + u < b1;
-      st.c[u][0] = in ? ld_stream(ra + (int64_t)(b + u) * 64 + t * 16) : make_uint4(0, 0, 0, 0);
-      st.c[u][1] = in ? ld_stream(rb + (int64_t)(b + u) * 64 + t * 16) : make_uint4(0, 0, 0, 0);
-    }
-    // UB << gsh scales of each row; the scale area is padded to whole
-    // superblocks, so the reads past the last block stay inside it
-    const unsigned char *pa = ra + kp2 + ((b << gsh) * 2), *pb = rb + kp2 + ((b << gsh) * 2);
-#pragma unroll
-    for (int q = 0; q < SB / 2; ++q) {
-      const bool in = 2 * q < (UB << gsh);
-      st.sc[0][q] = in ? __ldg(reinterpret_cast<const uint32_t *>(pa) + q) : 0u;
-      st.sc[1][q] = in ? __ldg(reinterpret_cast<const uint32_t *>(pb) + q) : 0u;
-    }
-  };
-
+  // ---- the computing side
   float tot[NT][4];
-  auto compute = [&](const Stage &st, int stage) {
+  auto clear = [&]() {
 #pragma unroll
-    for (int u = 0; u < UB; ++u) {
-      if (b0 + stage * UB + u >= b1) break;
+    for (int n = 0; n < NT; ++n) tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.f;
+  };
+  const unsigned char *xl = sx + (size_t)g * xrow + t * 16;            // this lane's token of tile 0
+  auto compute = [&](const unsigned char *st, int stage) {
+    uint32_t sa[1 << GS], sb[1 << GS];             // scales of rows g and g + 8
+#pragma unroll
+    for (int i = 0; i < (1 << GS); ++i) {
+      sa[i] = *reinterpret_cast<const uint32_t *>(st + 2048 + g * SCB + 4 * i);
+      sb[i] = *reinterpret_cast<const uint32_t *>(st + 2048 + (g + 8) * SCB + 4 * i);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (b0 + stage * 2 + u >= b1) break;
+      const uint4 ca = *reinterpret_cast<const uint4 *>(st + u * 1024 + g * 64 + t * 16);
+      const uint4 cb = *reinterpret_cast<const uint4 *>(st + u * 1024 + (g + 8) * 64 + t * 16);
+      const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
+      const unsigned char *xb = xl + (stage * 2 + u) * 256;
       float acc[NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-      const unsigned char *xb = sm + (size_t)(stage * UB + u) * 256 + t * 16;
-      const uint32_t wa[4] = {st.c[u][0].x, st.c[u][0].y, st.c[u][0].z, st.c[u][0].w};
-      const uint32_t wb[4] = {st.c[u][1].x, st.c[u][1].y, st.c[u][1].z, st.c[u][1].w};
-#pragma unroll
       for (int j = 0; j < 4; ++j) {
+        const bool fresh = j % (4 >> GS) == 0, last = (j + 1) % (4 >> GS) == 0;   // of a group
         uint32_t ha[4], hb[4];
         unpack8<BF>(wa[j], ha);
         unpack8<BF>(wb[j], hb);
+        if (fresh) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int b = 8 * n + g;
+          for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int q = 0; q < P; ++q) {
             uint4 xv = make_uint4(0, 0, 0, 0);
-            if (b < A.B) xv = *reinterpret_cast<const uint4 *>(xb + ((size_t)q * A.B + b) * xrow + j * 64);
+            if (8 * n + g < A.B) xv = *reinterpret_cast<const uint4 *>(xb + ((size_t)q * A.B + 8 * n) * xrow + j * 64);
             mma16816<BF>(acc[n], ha[0], hb[0], ha[1], hb[1], xv.x, xv.y);
             mma16816<BF>(acc[n], ha[2], hb[2], ha[3], hb[3], xv.z, xv.w);
           }
-        }
-        // end of a group: scale its sum (all lanes alike)
-        if (j == 3 || gsh == 2 || (gsh == 1 && j == 1)) {
-          const int i = (u << gsh) + (j >> (2 - gsh));
-          float sa, sb;
-          {
-            // i is not a constant: pick the half without indexing registers
-            uint32_t va = 0, vb = 0;
-#pragma unroll
-            for (int q = 0; q < SB / 2; ++q)
-              if (q == (i >> 1)) { va = st.sc[0][q]; vb = st.sc[1][q]; }
-            sa = __half2float(__ushort_as_half((unsigned short)((i & 1) ? va >> 16 : va & 0xffffu)));
-            sb = __half2float(__ushort_as_half((unsigned short)((i & 1) ? vb >> 16 : vb & 0xffffu)));
-          }
+        if (last) {                                // scale the group's sum
+          const int i = (u << GS) + (j >> (2 - GS));
+          const float fa = half_of(sa[i >> 1], i & 1), fb = half_of(sb[i >> 1], i & 1);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            tot[n][0] = fmaf(sa, acc[n][0], tot[n][0]);
-            tot[n][1] = fmaf(sa, acc[n][1], tot[n][1]);
-            tot[n][2] = fmaf(sb, acc[n][2], tot[n][2]);
-            tot[n][3] = fmaf(sb, acc[n][3], tot[n][3]);
-            acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+            tot[n][0] = fmaf(fa, acc[n][0], tot[n][0]);
+            tot[n][1] = fmaf(fa, acc[n][1], tot[n][1]);
+            tot[n][2] = fmaf(fb, acc[n][2], tot[n][2]);
+            tot[n][3] = fmaf(fb, acc[n][3], tot[n][3]);
           }
         }
       }
@@ -407,7 +470,8 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
       return;
     }
 #pragma unroll
-    for (int h = 0; h < (mode == kListGated ? 1 : 2); ++h) {
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1 && mode == kListGated) continue;
       const int pos = tile * per + g + 8 * h;
       if (pos >= total) continue;
       const int nrn = A.idx ? ld_cg_i32(A.idx + pos) : pos;
@@ -415,91 +479,62 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
       const float bias = ok ? __ldg(A.bias + nrn) : 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float2 v;
-        float *pv = &v.x;
+        float v[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float a = tot[n][2 * h + c] + bias;
           a = a > 0.f ? a : (a != a ? a : 0.f);
           if (mode == kListGated) a *= tot[n][2 + c];
-          pv[c] = ok && 8 * n + 2 * t + c < A.B ? a : 0.f;
+          v[c] = ok && 8 * n + 2 * t + c < A.B ? a : 0.f;
         }
-        *reinterpret_cast<float2 *>(A.y + ((int64_t)pos * NT + n) * 8 + 2 * t) = v;
+        *reinterpret_cast<float2 *>(A.y + ((int64_t)pos * NT + n) * 8 + 2 * t) = make_float2(v[0], v[1]);
       }
     }
   };
-
-  const int step = ctas * kDotWarps;
-  Stage cur, nxt;
-  int unit = p + ctas * warp;
-  if (unit >= units) return;
-  int tile = unit * tpu, stage = 0;
-  const unsigned char *ra, *rb;
-  rows_of(tile, ra, rb);
-  load(cur, ra, rb, 0);
+  // the tile's partial sums, and with the unit's last ticket its whole sums
+  auto share = [&](int tile, int unit) {
+    float4 *to = reinterpret_cast<float4 *>(A.part) + ((int64_t)tile * S + s) * NT * 32 + lane;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.f;
-  while (true) {
-    // where the next stage is
-    int nu = unit, nt = tile, ns = stage + 1;
-    if (ns == stages) {
-      ns = 0;
-      nt = tile + 1;
-      if (nt == min(tiles, (unit + 1) * tpu)) {
-        nu = unit + step;
-        nt = nu * tpu;
-      }
+    for (int n = 0; n < NT; ++n) __stcg(to + n * 32, make_float4(tot[n][0], tot[n][1], tot[n][2], tot[n][3]));
+    if (tile + 1 < min(tiles, (unit + 1) * tpu)) return;
+    __threadfence();
+    __syncwarp();
+    const int sh = 8 * (unit & 3);
+    uint32_t *word = &A.hdr->tile_done[unit >> 2];
+    uint32_t old = 0;
+    if (lane == 0) {
+      old = (atomicAdd(word, 1u << sh) >> sh) & 255u;
+      __threadfence();
     }
-    const bool more = nu < units;
-    if (more) {
-      if (ns == 0) rows_of(nt, ra, rb);
-      load(nxt, ra, rb, ns);
-    }
-    compute(cur, stage);
-    if (stage == stages - 1) {
-      if (S == 1) {
-        finish(tile);
-      } else {
-        float4 *to = reinterpret_cast<float4 *>(A.part) + ((int64_t)tile * S + s) * NT * 32 + lane;
+    old = __shfl_sync(0xffffffffu, old, 0);
+    if (old != (uint32_t)(S - 1)) return;
+    for (int tl = unit * tpu; tl <= tile; ++tl) {
+      clear();
+      const float4 *from = reinterpret_cast<const float4 *>(A.part) + (int64_t)tl * S * NT * 32 + lane;
+#pragma unroll 4
+      for (int q = 0; q < S; ++q)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) __stcg(to + n * 32, make_float4(tot[n][0], tot[n][1], tot[n][2], tot[n][3]));
-        if (nu != unit) {                          // the unit's last tile
-          __syncwarp();
-          uint32_t old = 0;
-          const int sh = 8 * (unit & 3);
-          uint32_t *word = &A.hdr->tile_done[unit >> 2];
-          if (lane == 0) {
-            __threadfence();
-            old = (atomicAdd(word, 1u << sh) >> sh) & 255u;
-            __threadfence();
-          }
-          old = __shfl_sync(0xffffffffu, old, 0);
-          if (old == (uint32_t)(S - 1)) {
-            for (int tl = unit * tpu; tl < min(tiles, (unit + 1) * tpu); ++tl) {
-#pragma unroll
-              for (int n = 0; n < NT; ++n) tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.f;
-              for (int q = 0; q < S; ++q) {
-                const float4 *from = reinterpret_cast<const float4 *>(A.part) + ((int64_t)tl * S + q) * NT * 32 + lane;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  const float4 v = __ldcg(from + n * 32);
-                  tot[n][0] += v.x; tot[n][1] += v.y; tot[n][2] += v.z; tot[n][3] += v.w;
-                }
-              }
-              finish(tl);
-            }
-            if (lane == 0) atomicSub(word, (uint32_t)S << sh);       // the ticket is zero again for the next call
-          }
+        for (int n = 0; n < NT; ++n) {
+          const float4 v = __ldcg(from + (q * NT + n) * 32);
+          tot[n][0] += v.x; tot[n][1] += v.y; tot[n][2] += v.z; tot[n][3] += v.w;
         }
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.f;
+      finish(tl);
     }
-    if (!more) break;
-    cur = nxt;
-    unit = nu;
-    tile = nt;
-    stage = ns;
+    if (lane == 0) atomicSub(word, (uint32_t)S << sh);                 // the ticket is zero again for the next call
+  };
+
+  clear();
+  for (int i = 0; co.unit < units; i = i + 1 == NS ? 0 : i + 1) {
+    cp_async_wait<NS - 2>();
+    __syncwarp();
+    copy(i == 0 ? NS - 1 : i - 1);                 // the slot that the last step has read
+    compute(ring + i * SB, co.stage);
+    const int unit = co.unit, tile = co.tile;
+    if (advance(co)) {
+      if (S == 1) finish(tile);
+      else share(tile, unit);
+      clear();
+    }
   }
 }
 
@@ -513,7 +548,7 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
 struct DownArgs {
   const unsigned char *data;   // first down row
   int64_t stride;
-  int n, d, group;
+  int n, d;
   const int32_t *idx, *count;
   const float *a;              // [positions][8 * NT]
   int B, R;                    // tokens, list splits
@@ -522,13 +557,33 @@ struct DownArgs {
   Header *hdr;
 };
 
-template <int NT>
+// A warp's stage: 16 neurons' codes of one block of 128 columns, their scales
+// and their activations.
+__host__ __device__ constexpr int down_stages(int NT) { return NT == 2 ? 5 : 6; }
+__host__ __device__ constexpr int down_scale_bytes(int GS) { return GS == 2 ? 8 : 4; }
+__host__ __device__ constexpr int down_stage_bytes(int NT, int GS) { return 1024 + 16 * down_scale_bytes(GS) + 512 * NT; }
+__host__ __device__ constexpr size_t down_smem(int NT, int GS) {
+  const size_t ring = (size_t)kDownWarps * down_stages(NT) * down_stage_bytes(NT, GS);
+  const size_t red = (size_t)(kDownWarps / 2) * kDownCols * (8 * NT + 1) * 4;
+  return ring > red ? ring : red;
+}
+
+// A CTA is 256 columns x a share of the list: four shares of neurons, two
+// blocks of columns, a warp each with its own ring of cp.async stages.  The
+// 64 bytes of codes of neurons 2i and 2i+1 share 128 bytes of shared memory,
+// chunk (part, odd) at (2 part + odd) ^ x(i), so that the eight lanes of a
+// 16-byte read touch every bank once.  Codes and scales do not depend on the
+// gate/up kernel: the first stages are on their way while it still runs (it
+// passed its own wait before this grid could start, so the list and the rows
+// are complete).  With PC (one or two tokens) the three parts of an activation
+// are three columns of one product instead of three products.
+template <int NT, int GS, bool PC>
 __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(DownArgs A) {
-  extern __shared__ __align__(16) float red[];     // [256 columns][8 * NT + 1]
+  extern __shared__ __align__(128) unsigned char sm[];
+  constexpr int NS = down_stages(NT), SB = down_stage_bytes(NT, GS), SCB = down_scale_bytes(GS);
   constexpr int RS = 8 * NT + 1;
+  constexpr int P = PC ? 1 : 3;
   __shared__ uint32_t s_last;
-  pdl_wait();
-  pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   int total = A.n;
@@ -539,122 +594,168 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
   if (r >= R) return;
   const int kp = w4_kp(A.d);
   const int col0 = cu * kDownCols + (warp & 1) * kBlk;         // this warp's block
-  const bool live = col0 < kp;
-  const int gsh = A.group == 32 ? 2 : A.group == 64 ? 1 : 0;
   const int sub = g & 3;                                       // word column of this lane's rows
   const uint32_t sel = (g >> 2) ? 0x7632u : 0x5410u;           // odd or even weights of two words
+
+  unsigned char *ring = sm + (size_t)warp * NS * SB;
+  const int first = r * (kDownWarps / 2) + (warp >> 1), step = R * (kDownWarps / 2);
+  const int tiles = col0 < kp && first < ntile ? (ntile - first + step - 1) / step : 0;
+  const uint64_t pol = l2_evict_first();
+  auto id_of = [&](int i) {
+    const int pos = (first + i * step) * 16 + (lane & 15);
+    int id = -1;
+    if (pos < total) id = A.idx ? ld_cg_i32(A.idx + pos) : pos;
+    return (unsigned)id < (unsigned)A.n ? id : -1;
+  };
+  int id = tiles > 0 ? id_of(0) : -1;
+  auto copy_rows = [&](int i) {                                // stage i's codes and scales
+    if (i >= tiles) return;
+    const int now = id;
+    if (i + 1 < tiles) id = id_of(i + 1);
+    unsigned char *to = ring + (i % NS) * SB;
+    const int part = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = h * 8 + (lane >> 2);
+      const int nrn = __shfl_sync(0xffffffffu, now, row);
+      const int x = ((row >> 1) & 1) | ((row & 4));
+      cp_async16(to + (row >> 1) * 128 + (((part * 2 + (row & 1)) ^ x) * 16),
+                 A.data + (int64_t)max(nrn, 0) * A.stride + col0 / 2 + part * 16, nrn >= 0 ? 16u : 0u, pol);
+    }
+    if (lane < 16) {
+      // one block's scales; a single one comes with its neighbour (4 bytes at least)
+      const int at = GS == 0 ? (col0 / kBlk) & ~1 : (col0 / kBlk) << GS;
+      cp_async_small<SCB>(to + 1024 + lane * SCB, A.data + (int64_t)max(now, 0) * A.stride + kp / 2 + at * 2, now >= 0);
+    }
+  };
+  auto copy_act = [&](int i) {
+    if (i < tiles) {
+      unsigned char *to = ring + (i % NS) * SB + 1024 + 16 * SCB;
+      const int64_t pos0 = (int64_t)(first + i * step) * 16;
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        const int c = q * 32 + lane;
+        const bool in = pos0 + c / (2 * NT) < total;
+        cp_async16(to + c * 16, in ? A.a + pos0 * 8 * NT + c * 4 : A.a, in ? 16u : 0u);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i) copy_rows(i);
+  pdl_wait();
+  pdl_trigger();
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i) copy_act(i);
 
   float acc[8][NT][4];                             // [group of 32][half] x tokens
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
+  // PC: column g is part g % 3 of token g / 3
+  const uint32_t cut1 = PC && g % 3 >= 1 ? 0xffff0000u : 0u, cut2 = PC && g % 3 == 2 ? 0xffff0000u : 0u;
+  const int act0 = PC ? g / 3 : g;
+  const int hi0 = GS == 0 ? (col0 / kBlk) & 1 : 0;
 
-  struct Stage {
+  for (int i = 0; i < tiles; ++i) {
+    cp_async_wait<NS - 2>();
+    __syncwarp();
+    copy_rows(i + NS - 1);                         // into the slot that the last step has read
+    copy_act(i + NS - 1);
+    const unsigned char *st = ring + (i % NS) * SB;
     uint4 c[4];
-    uint2 sc[4];
-    int pos[4];                                    // -1: no such position, or not a neuron
-  };
-  // the four neurons of this lane: 2t, 2t+1, 2t+8, 2t+9 of the tile
-  auto load = [&](Stage &st, int tile) {
+    uint32_t sc[4][GS == 2 ? 2 : 1];
+    float av[4][NT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int pos = tile * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
-      int nrn = -1;
-      if (pos < total) nrn = A.idx ? ld_cg_i32(A.idx + pos) : pos;
-      const bool ok = (unsigned)nrn < (unsigned)A.n;
-      st.pos[i] = ok ? pos : -1;
-      const unsigned char *row = A.data + (int64_t)(ok ? nrn : 0) * A.stride;
-      st.c[i] = ok ? ld_stream(row + col0 / 2 + sub * 16) : make_uint4(0, 0, 0, 0);
-      st.sc[i] = make_uint2(0, 0);
-      if (ok) {
-        const unsigned char *ps = row + kp / 2 + (((col0 / kBlk) << gsh) * 2);
-        if (gsh == 0) st.sc[i].x = __ldg(reinterpret_cast<const unsigned short *>(ps));
-        else if (gsh == 1) st.sc[i].x = __ldg(reinterpret_cast<const uint32_t *>(ps));
-        else st.sc[i] = __ldg(reinterpret_cast<const uint2 *>(ps));
-      }
+    for (int q = 0; q < 4; ++q) {                  // this lane's neurons: 2t, 2t+1, 2t+8, 2t+9
+      const int row = 2 * t + (q & 1) + 8 * (q >> 1);
+      const int x = (t & 1) | ((t & 2) << 1);
+      c[q] = *reinterpret_cast<const uint4 *>(st + (row >> 1) * 128 + (((sub * 2 + (q & 1)) ^ x) * 16));
+#pragma unroll
+      for (int w = 0; w < (GS == 2 ? 2 : 1); ++w) sc[q][w] = *reinterpret_cast<const uint32_t *>(st + 1024 + row * SCB + 4 * w);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) av[q][n] = *reinterpret_cast<const float *>(st + 1024 + 16 * SCB + ((row * NT + n) * 8 + act0) * 4);
     }
-  };
-  auto compute = [&](const Stage &st) {
-    uint32_t bp[NT][3][2];
+    uint32_t bp[NT][P][2];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (j == 0 || gsh == 2 || (gsh == 1 && j == 2)) {        // a new group of columns: a * s
+      if (j % (4 >> GS) == 0) {                    // a new group of columns: a * s
         float s[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w = (gsh == 2 && j >= 2) ? st.sc[i].y : st.sc[i].x;
-          const bool hi = gsh == 2 ? (j & 1) : (gsh == 1 && j == 2);
-          s[i] = __half2float(__ushort_as_half((unsigned short)(hi ? w >> 16 : w & 0xffffu)));
-        }
+        for (int q = 0; q < 4; ++q) s[q] = half_of(sc[q][GS == 2 ? j >> 1 : 0], GS == 2 ? j & 1 : GS == 1 ? j >> 1 : hi0);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i] = st.pos[i] >= 0 ? ld_cg_f32(A.a + ((int64_t)st.pos[i] * NT + n) * 8 + g) * s[i] : 0.f;
+          for (int q = 0; q < 4; ++q) v[q] = av[q][n] * s[q];
+          if constexpr (PC) {
 #pragma unroll
-          for (int q = 0; q < 3; ++q) {
-            bp[n][q][0] = upper2(v[0], v[1]);
-            bp[n][q][1] = upper2(v[2], v[3]);
+            for (int q = 0; q < 4; ++q) {
+              v[q] -= __uint_as_float(__float_as_uint(v[q]) & cut1);
+              v[q] -= __uint_as_float(__float_as_uint(v[q]) & cut2);
+            }
+            bp[n][0][0] = upper2(v[0], v[1]);
+            bp[n][0][1] = upper2(v[2], v[3]);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] -= trunc_bf16(v[i]);
+            for (int q = 0; q < 3; ++q) {
+              bp[n][q][0] = upper2(v[0], v[1]);
+              bp[n][q][1] = upper2(v[2], v[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] -= trunc_bf16(v[e]);
+            }
           }
         }
       }
-      const uint32_t w[4] = {(&st.c[0].x)[j], (&st.c[1].x)[j], (&st.c[2].x)[j], (&st.c[3].x)[j]};
+      const uint32_t w[4] = {j == 0 ? c[0].x : j == 1 ? c[0].y : j == 2 ? c[0].z : c[0].w,
+                             j == 0 ? c[1].x : j == 1 ? c[1].y : j == 2 ? c[1].z : c[1].w,
+                             j == 0 ? c[2].x : j == 1 ? c[2].y : j == 2 ? c[2].z : c[2].w,
+                             j == 0 ? c[3].x : j == 1 ? c[3].y : j == 2 ? c[3].z : c[3].w};
       uint32_t lo[4], hi[4];
       unpack8<true>(__byte_perm(w[0], w[1], sel), lo);         // [p] = weight 2p + (g >> 2) of neurons 2t, 2t+1
       unpack8<true>(__byte_perm(w[2], w[3], sel), hi);         // of neurons 2t+8, 2t+9
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int q = 0; q < 3; ++q) {
+        for (int q = 0; q < P; ++q) {
           mma16816<true>(acc[2 * j][n], lo[0], lo[1], hi[0], hi[1], bp[n][q][0], bp[n][q][1]);
           mma16816<true>(acc[2 * j + 1][n], lo[2], lo[3], hi[2], hi[3], bp[n][q][0], bp[n][q][1]);
         }
     }
-  };
-  const int first = r * (kDownWarps / 2) + (warp >> 1), stride = R * (kDownWarps / 2);
-  if (live && first < ntile) {
-    Stage cur, nxt;
-    load(cur, first);
-    for (int tile = first; tile < ntile; tile += stride) {
-      if (tile + stride < ntile) load(nxt, tile + stride);
-      compute(cur);
-      cur = nxt;
-    }
   }
-  // sum the four warps of a column block, in order
-  for (int q = 0; q < kDownWarps / 2; ++q) {
-    if ((warp >> 1) == q) {
+  // the four shares of a column, added in order
+  cp_async_wait<0>();
+  __syncthreads();
+  float *red = reinterpret_cast<float *>(sm);                  // [share][256 columns][8 * NT + 1]
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            // row g of half h is weight 2p + (g >> 2) of word 4j + (g & 3), p = 2h (+1 for row g + 8)
-            const int p = 2 * (i & 1) + (c >> 1);
-            const int col = (warp & 1) * kBlk + (i >> 1) * 32 + sub * 8 + 2 * p + (g >> 2);
-            float *to = red + col * RS + 8 * n + 2 * t + (c & 1);
-            *to = q == 0 ? acc[i][n][c] : *to + acc[i][n][c];
-          }
-    }
-    __syncthreads();
-  }
-  float *out = R == 1 ? A.y : A.part + (int64_t)r * A.B * A.d;
+      for (int e = 0; e < 4; ++e) {
+        // row g of half h is weight 2p + (g >> 2) of word 4j + (g & 3), p = 2h (+1 for row g + 8)
+        const int p = 2 * (i & 1) + (e >> 1);
+        const int col = (warp & 1) * kBlk + (i >> 1) * 32 + sub * 8 + 2 * p + (g >> 2);
+        red[((warp >> 1) * kDownCols + col) * RS + 8 * n + 2 * t + (e & 1)] = acc[i][n][e];
+      }
+  __syncthreads();
   for (int i = threadIdx.x; i < A.B * kDownCols; i += blockDim.x) {
     const int b = i / kDownCols, c = cu * kDownCols + i % kDownCols;
-    if (c < A.d) {
-      if (R == 1) out[(int64_t)b * A.d + c] = red[(i % kDownCols) * RS + b];
-      else __stcg(out + (int64_t)b * A.d + c, red[(i % kDownCols) * RS + b]);
+    if (c >= A.d) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < kDownWarps / 2; ++q) {
+      const float *from = red + (q * kDownCols + i % kDownCols) * RS;
+      v += PC ? (from[3 * b + 2] + from[3 * b + 1]) + from[3 * b] : from[b];
     }
+    if (R == 1) A.y[(int64_t)b * A.d + c] = v;
+    else __stcg(A.part + ((int64_t)r * A.B + b) * A.d + c, v);
   }
   if (R == 1) return;
+  __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
     s_last = ticket_acq_rel(&A.hdr->tile_done[cu]);
     __threadfence();
   }
@@ -664,6 +765,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
     const int b = i / kDownCols, c = cu * kDownCols + i % kDownCols;
     if (c >= A.d) continue;
     float v = 0.f;
+#pragma unroll 8
     for (int q = 0; q < R; ++q) v += __ldcg(A.part + ((int64_t)q * A.B + b) * A.d + c);
     A.y[(int64_t)b * A.d + c] = v;
   }
@@ -692,20 +794,23 @@ asf_status check_w4_ffn(const asf_w4_ffn *f) {
   return ASF_OK;
 }
 
-// superblocks of x that fit a CTA, for B tokens
-int dot_smin(int k, int B, int parts) {
-  const int nsb = ceil_div(w4_kp(k), kSuper);
-  const size_t row = (size_t)B * parts;
-  const int fit = (int)std::max<size_t>(1, (kDotSmem - row * 64) / (row * kSuper * 2));
-  return ceil_div(nsb, fit);
-}
-int dot_ctas() { return sm_count(); }
 int nt_of(int B) { return B <= 8 ? 1 : B <= 16 ? 2 : 4; }
-
-// partial sums of a split k: at most max(8 CTAs-worth of tiles + tiles, tiles * smin) row tiles
-size_t dot_part_bytes(int tiles, int k, int B) {
-  const size_t most = std::max<size_t>((size_t)8 * dot_ctas() + tiles, (size_t)tiles * (dot_smin(k, B, 3) + 1));
-  return r256(most * nt_of(B) * 512);
+int gs_of(int group) { return group == 32 ? 2 : group == 64 ? 1 : 0; }
+int dot_ctas() { return sm_count(); }
+size_t x_bytes(int B, int parts, int superblocks) { return (size_t)B * parts * ((size_t)superblocks * kSuper * 2 + 64); }
+// superblocks of k whose x fits a CTA beside the rings
+int dot_most(int k, int group, int B, int parts) {
+  const int nsb = ceil_div(w4_kp(k), kSuper);
+  const size_t room = kDotSmem - dot_ring_bytes(nt_of(B), gs_of(group));
+  int n = nsb;
+  while (n > 1 && x_bytes(B, parts, n) > room) --n;
+  return n;
+}
+// partial sums of a split k (the most that dot_per makes of it)
+size_t dot_part_bytes(int tiles, int k, int group, int B) {
+  const int nsb = ceil_div(w4_kp(k), kSuper);
+  const size_t forced = (size_t)tiles * ceil_div(nsb, dot_most(k, group, B, 3));
+  return r256(std::max<size_t>((size_t)16 * dot_ctas(), forced) * nt_of(B) * 512);
 }
 int down_units(int d) { return ceil_div(w4_kp(d), kDownCols); }
 int down_w4_splits(int d, int B) {
@@ -714,21 +819,36 @@ int down_w4_splits(int d, int B) {
 }
 size_t ffn_w4_scratch(const asf_w4_ffn *f, int B) {
   const int tiles = ceil_div(f->n, f->act == ASF_ACT_REGLU ? 8 : 16);
-  return r256((size_t)f->n * nt_of(B) * 32) + dot_part_bytes(tiles, f->d, B) +
+  return r256((size_t)f->n * nt_of(B) * 32) + dot_part_bytes(tiles, f->d, f->group, B) +
          r256((size_t)down_w4_splits(f->d, B) * B * f->d * 4);
 }
 
-template <bool BF>
-cudaError_t run_dot(const DotArgs &a, int mode, cudaStream_t st) {
-  const int parts = BF ? 3 : 1;
-  const int nsb = ceil_div(w4_kp(a.k), kSuper);
-  const int sb = ceil_div(nsb, a.smin);
-  const size_t smem = (size_t)a.B * parts * ((size_t)sb * kSuper * 2 + 64);
+template <bool BF, int NT>
+cudaError_t run_dot_nt(const DotArgs &a, int group, int mode, cudaStream_t st) {
+  const size_t smem = dot_ring_bytes(NT, gs_of(group)) + x_bytes(a.B, BF ? 3 : 1, a.most);
   const dim3 grid(dot_ctas()), block(kDotWarps * 32);
+  return group == 128  ? launch(k_w4_dot<BF, NT, 0>, grid, block, smem, st, a, mode)
+         : group == 64 ? launch(k_w4_dot<BF, NT, 1>, grid, block, smem, st, a, mode)
+                       : launch(k_w4_dot<BF, NT, 2>, grid, block, smem, st, a, mode);
+}
+cudaError_t run_dot(DotArgs a, int group, asf_dtype xdtype, int mode, cudaStream_t st) {
+  const bool bf = xdtype == ASF_F32;
+  a.most = dot_most(a.k, group, a.B, bf ? 3 : 1);
   switch (nt_of(a.B)) {
-    case 1: return launch(k_w4_dot<BF, 1, 2>, grid, block, smem, st, a, mode);
-    case 2: return launch(k_w4_dot<BF, 2, 2>, grid, block, smem, st, a, mode);
-    default: return launch(k_w4_dot<BF, 4, 2>, grid, block, smem, st, a, mode);
+    case 1: return bf ? run_dot_nt<true, 1>(a, group, mode, st) : run_dot_nt<false, 1>(a, group, mode, st);
+    case 2: return bf ? run_dot_nt<true, 2>(a, group, mode, st) : run_dot_nt<false, 2>(a, group, mode, st);
+    default: return bf ? run_dot_nt<true, 4>(a, group, mode, st) : run_dot_nt<false, 4>(a, group, mode, st);
+  }
+}
+
+template <int GS>
+cudaError_t run_down(const DownArgs &a, cudaStream_t st) {
+  const dim3 grid(down_units(a.d) * a.R), block(kDownWarps * 32);
+  if (a.B <= 2) return launch(k_w4_down<1, GS, true>, grid, block, down_smem(1, GS), st, a);
+  switch (nt_of(a.B)) {
+    case 1: return launch(k_w4_down<1, GS, false>, grid, block, down_smem(1, GS), st, a);
+    case 2: return launch(k_w4_down<2, GS, false>, grid, block, down_smem(2, GS), st, a);
+    default: return launch(k_w4_down<4, GS, false>, grid, block, down_smem(4, GS), st, a);
   }
 }
 
@@ -748,7 +868,7 @@ size_t asf_w4_workspace_bytes(const asf_w4_matrix *mat, const asf_w4_ffn *ffn, i
   size_t need = 0;
   for (int b : {1, 8, 16, 32}) {                   // the need grows with each of the token tiles, and within one
     const int B = std::min<int>(b, max_batch);
-    if (mat) need = std::max(need, dot_part_bytes(ceil_div(mat->rows, 16), mat->k, B));
+    if (mat) need = std::max(need, dot_part_bytes(ceil_div(mat->rows, 16), mat->k, mat->group, B));
     if (ffn) need = std::max(need, ffn_w4_scratch(ffn, B));
   }
   return kHeaderBytes + need;
@@ -795,14 +915,13 @@ asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dtype xdty
   if (xdtype != ASF_F16 && xdtype != ASF_F32) return ASF_ERR_UNSUPPORTED;
   if (ydtype != ASF_F16 && ydtype != ASF_F32) return ASF_ERR_UNSUPPORTED;
   if (!al16(x) || !al4(y) || !al4(bias)) return ASF_ERR_MISALIGNED;
-  s = check_ws(ws, ws_bytes, kHeaderBytes + dot_part_bytes(ceil_div(mat->rows, 16), mat->k, B));
+  s = check_ws(ws, ws_bytes, kHeaderBytes + dot_part_bytes(ceil_div(mat->rows, 16), mat->k, mat->group, B));
   if (s != ASF_OK) return s;
   DotArgs a{};
   a.data = static_cast<const unsigned char *>(mat->data);
   a.stride = mat->row_stride;
   a.rows = mat->rows;
   a.k = mat->k;
-  a.group = mat->group;
   a.x = x;
   a.B = B;
   a.bias = bias;
@@ -810,10 +929,8 @@ asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dtype xdty
   a.y = static_cast<float *>(y);
   a.y16 = ydtype == ASF_F16;
   a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kHeaderBytes);
-  a.smin = dot_smin(mat->k, B, xdtype == ASF_F32 ? 3 : 1);
   a.hdr = static_cast<Header *>(ws);
-  return cuda_status(xdtype == ASF_F32 ? run_dot<true>(a, kDense, (cudaStream_t)stream)
-                                       : run_dot<false>(a, kDense, (cudaStream_t)stream));
+  return cuda_status(run_dot(a, mat->group, xdtype, kDense, (cudaStream_t)stream));
 }
 
 asf_status asf_w4_sparse_ffn(const asf_w4_ffn *f, const void *x, asf_dtype xdtype, int32_t B, const int32_t *idx,
@@ -834,7 +951,6 @@ asf_status asf_w4_sparse_ffn(const asf_w4_ffn *f, const void *x, asf_dtype xdtyp
   a.up = gated ? rb : 0;
   a.rows = f->n;
   a.k = f->d;
-  a.group = f->group;
   a.x = x;
   a.B = B;
   a.bias = f->bias;
@@ -843,19 +959,16 @@ asf_status asf_w4_sparse_ffn(const asf_w4_ffn *f, const void *x, asf_dtype xdtyp
   a.y = reinterpret_cast<float *>(base);
   base += r256((size_t)f->n * nt_of(B) * 32);
   a.part = reinterpret_cast<float *>(base);
-  base += dot_part_bytes(ceil_div(f->n, gated ? 8 : 16), f->d, B);
-  a.smin = dot_smin(f->d, B, xdtype == ASF_F32 ? 3 : 1);
+  base += dot_part_bytes(ceil_div(f->n, gated ? 8 : 16), f->d, f->group, B);
   a.hdr = static_cast<Header *>(ws);
-  const int mode = gated ? kListGated : kListUp;
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = xdtype == ASF_F32 ? run_dot<true>(a, mode, st) : run_dot<false>(a, mode, st);
+  const cudaError_t e = run_dot(a, f->group, xdtype, gated ? kListGated : kListUp, st);
   if (e != cudaSuccess) return ASF_ERR_CUDA;
   DownArgs w{};
   w.data = a.data + (ffn_mats(f) - 1) * rb;
   w.stride = f->neuron_stride;
   w.n = f->n;
   w.d = f->d;
-  w.group = f->group;
   w.idx = idx;
   w.count = count;
   w.a = a.y;
@@ -864,12 +977,9 @@ asf_status asf_w4_sparse_ffn(const asf_w4_ffn *f, const void *x, asf_dtype xdtyp
   w.part = reinterpret_cast<float *>(base);
   w.y = y;
   w.hdr = a.hdr;
-  const dim3 grid(down_units(f->d) * w.R), block(kDownWarps * 32);
-  const int nt = nt_of(B);
-  const size_t smem = (size_t)kDownCols * (8 * nt + 1) * 4;
-  return cuda_status(nt == 1   ? launch(k_w4_down<1>, grid, block, smem, st, w)
-                     : nt == 2 ? launch(k_w4_down<2>, grid, block, smem, st, w)
-                               : launch(k_w4_down<4>, grid, block, smem, st, w));
+  return cuda_status(f->group == 128  ? run_down<0>(w, st)
+                     : f->group == 64 ? run_down<1>(w, st)
+                                      : run_down<2>(w, st));
 }
 
 }  // extern "C"
