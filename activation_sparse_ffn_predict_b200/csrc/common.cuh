@@ -158,9 +158,9 @@ __device__ __forceinline__ void named_arrive(int id, int nthreads) {
 // Ticket for "last CTA to finish" patterns: callers __syncthreads() first so
 // the whole CTA's writes precede thread 0's release; the acquire half lets the
 // last arriver read every other CTA's writes after a following __syncthreads().
-__device__ __forceinline__ uint32_t ticket_acq_rel(uint32_t *p) {
+__device__ __forceinline__ uint32_t ticket_acq_rel(uint32_t *p, uint32_t add = 1) {
   uint32_t old;
-  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(add) : "memory");
   return old;
 }
 

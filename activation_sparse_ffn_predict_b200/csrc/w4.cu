@@ -36,6 +36,7 @@ constexpr int kDownWarps = 8;
 constexpr int kDownCols = 256;         // columns per down-projection CTA (two blocks)
 constexpr int kTicketBytes = kMaxTiles * 4;   // one byte a ticket: more than the splits a row tile has
 constexpr size_t kDotSmem = 226 * 1024;
+constexpr int kPartsPerCta = 64;       // see dot_per
 constexpr float kFp16Max = 65504.f;
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -46,92 +47,102 @@ __host__ __device__ inline int w4_scale_bytes(int k, int group) {
 inline int64_t w4_row_bytes(int k, int group) { return (int64_t)w4_kp(k) / 2 + w4_scale_bytes(k, group); }
 
 // ------------------------------------------------------------- quantize --
-// One warp per superblock of 512 weights of a row, 8 weights a lane at a
-// time: the group maximum over group / 8 neighbouring lanes, one division per
-// weight (IEEE, so that codes are the formula's own), one word of codes.
+// A CTA takes 1, 2, 4 or 8 rows, so that its eight warps have a superblock of
+// 512 weights each; a lane has 8 weights of each half of it, the group maximum
+// comes from group / 8 neighbouring lanes.  A code is the rounding of the IEEE
+// quotient v / s.  v (1/s) is within 2^-22 of it, relatively, and |v / s| < 16,
+// so wherever that product is 1e-5 or more off a half its rounding is the same;
+// the few others divide.  (Dividing always: 72 us for 11008 x 4096 in fp16.)
+__device__ __forceinline__ void rows_of_cta(int nsb, int warp, int &lsh, int &sb, int64_t &row) {
+  lsh = nsb > 4 ? 3 : nsb > 2 ? 2 : nsb > 1 ? 1 : 0;           // log2 of the warps of a row
+  sb = warp & ((1 << lsh) - 1);
+  row = (int64_t)blockIdx.x * (8 >> lsh) + (warp >> lsh);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_w4_quantize(const T *__restrict__ src, int rows, int k, int group, unsigned char *__restrict__ dst, int64_t stride) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int nsb = ceil_div(k, kSuper), kp = w4_kp(k);
-  const int64_t unit = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-  if (unit >= (int64_t)rows * nsb) return;
-  const int64_t row = unit / nsb;
-  const int sb = (int)(unit % nsb);
+  int lsh, sb0;
+  int64_t row;
+  rows_of_cta(nsb, threadIdx.x >> 5, lsh, sb0, row);
+  if (row >= rows) return;
   const T *in = src + row * k;
   unsigned char *out = dst + row * stride;
-  const int per = group / 8;                       // lanes of a group
+  const int gsh = group == 32 ? 2 : group == 64 ? 3 : 4;       // log2 of a group's lanes
+  for (int sb = sb0; sb < nsb; sb += 1 << lsh) {
+    uint4 raw[2][sizeof(T) / 2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i0 = sb * kSuper + h * 256 + lane * 8;
-    float v[8] = {};
-    if (i0 < k) {                                  // k is a multiple of 8
+    for (int h = 0; h < 2; ++h) {
+      const int i0 = sb * kSuper + h * 256 + lane * 8;
+#pragma unroll
+      for (int q = 0; q < (int)sizeof(T) / 2; ++q)
+        raw[h][q] = i0 < k ? __ldcs(reinterpret_cast<const uint4 *>(in + i0) + q) : make_uint4(0, 0, 0, 0);   // k % 8 == 0
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i0 = sb * kSuper + h * 256 + lane * 8;
+      float v[8];
+      // the largest magnitude by its bits: a NaN counts as more than an infinity
+      uint32_t m = 0;
       if constexpr (sizeof(T) == 2) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(in + i0);
-        Vec<__half>::to_float(u, v);
+        Vec<__half>::to_float(raw[h][0], v);
+        const uint32_t w[4] = {raw[h][0].x, raw[h][0].y, raw[h][0].z, raw[h][0].w};
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, w[i] & 0x7fff7fffu);
+        m = max(m2 >> 16, m2 & 0xffffu);
       } else {
-        const float4 a = *reinterpret_cast<const float4 *>(in + i0), b = *reinterpret_cast<const float4 *>(in + i0 + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        const uint32_t w[8] = {raw[h][0].x, raw[h][0].y, raw[h][0].z, raw[h][0].w,
+                               raw[h][sizeof(T) / 2 - 1].x, raw[h][sizeof(T) / 2 - 1].y, raw[h][sizeof(T) / 2 - 1].z,
+                               raw[h][sizeof(T) / 2 - 1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = __uint_as_float(w[i]);
+          m = max(m, w[i] & 0x7fffffffu);
+        }
       }
-    }
-    // NaN counts as infinite: the maximum of fmaxf would drop it
-    float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i] != v[i] ? INFINITY : fabsf(v[i]));
-    for (int o = 1; o < per; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const __half sh = __float2half_rn(__fdiv_rn(m, 7.f));
-    const float s = __half2float(sh);
-    const bool good = s <= kFp16Max;               // a group that fp16 scales cannot hold reads back as NaN
-    uint32_t word = 0;
+      for (int o = 0; o < 4; ++o)
+        if (o < gsh) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1 << o));
+      float top;
+      if constexpr (sizeof(T) == 2) top = __half2float(__ushort_as_half((unsigned short)m));
+      else top = __uint_as_float(m);
+      const __half sh = __float2half_rn(__fdiv_rn(top, 7.f));
+      const float s = __half2float(sh);
+      const bool good = s <= kFp16Max;             // a group that fp16 scales cannot hold reads back as NaN
+      const float r = good && s > 0.f ? __frcp_rn(s) : 0.f;
+      uint32_t word = 0;
+      float off = 0.f;
+      constexpr float kMagic = 12582912.f;         // 1.5 * 2^23: adding it rounds to whole numbers, half to even
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float c = good && s > 0.f ? rintf(__fdiv_rn(v[i], s)) : 0.f;
-      c = fminf(fmaxf(c, -8.f), 7.f);
-      word |= (uint32_t)((int)c + 8) << (16 * (i & 1) + 4 * (i >> 1));
-    }
-    const int wi = (i0 % kBlk) / 8;                // word j*4 + t of the block is stored at t*4 + j
-    if (i0 < kp) *reinterpret_cast<uint32_t *>(out + (i0 / kBlk) * 64 + ((wi & 3) * 4 + (wi >> 2)) * 4) = word;
-    if (lane % per == 0) {                         // past kp the maximum is 0: zero padding
-      __half w = good ? sh : __ushort_as_half((unsigned short)0x7fff);
-      *reinterpret_cast<__half *>(out + kp / 2 + (i0 / group) * 2) = w;
+      for (int i = 0; i < 8; ++i) {
+        const float q = good ? v[i] * r : 0.f;
+        const float t = fminf(fmaxf(q, -8.f), 7.f) + (kMagic + 8.f);
+        off = fmaxf(off, fabsf(q - (t - (kMagic + 8.f))));     // a clamped one is far off: it divides
+        word |= (__float_as_uint(t) & 15u) << (16 * (i & 1) + 4 * (i >> 1));
+      }
+      if (off > 0.5f - 1e-5f && r > 0.f) {
+        word = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float c = fminf(fmaxf(rintf(__fdiv_rn(v[i], s)), -8.f), 7.f);
+          word |= (uint32_t)((int)c + 8) << (16 * (i & 1) + 4 * (i >> 1));
+        }
+      }
+      const int wi = (i0 % kBlk) / 8;              // word j*4 + t of the block is stored at t*4 + j
+      if (i0 < kp) *reinterpret_cast<uint32_t *>(out + (i0 / kBlk) * 64 + ((wi & 3) * 4 + (wi >> 2)) * 4) = word;
+      if ((lane & ((1 << gsh) - 1)) == 0) {        // past kp the maximum is 0: zero padding
+        const __half w = good ? sh : __ushort_as_half((unsigned short)0x7fff);
+        *reinterpret_cast<__half *>(out + kp / 2 + (i0 >> (gsh + 3)) * 2) = w;
+      }
     }
   }
   const int used = nsb * (kSuper / group) * 2;     // rest of the scale area, up to 16 bytes
-  if (sb == nsb - 1 && lane * 2 < w4_scale_bytes(k, group) - used)
+  if (sb0 == 0 && lane * 2 < w4_scale_bytes(k, group) - used)
     *reinterpret_cast<uint16_t *>(out + kp / 2 + used + lane * 2) = 0;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256)
-k_w4_dequantize(const unsigned char *__restrict__ src, int64_t stride, int rows, int k, int group, T *__restrict__ dst) {
-  pdl_wait();
-  const int words = k / 8;
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (int64_t)rows * words) return;
-  const int64_t row = i / words;
-  const int at = (int)(i % words) * 8;
-  const unsigned char *in = src + row * stride;
-  const int wi = (at % kBlk) / 8;
-  const uint32_t w = *reinterpret_cast<const uint32_t *>(in + (at / kBlk) * 64 + ((wi & 3) * 4 + (wi >> 2)) * 4);
-  const float s = __half2float(*reinterpret_cast<const __half *>(in + w4_kp(k) / 2 + (at / group) * 2));
-  float v[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = (float)((int)((w >> (16 * (e & 1) + 4 * (e >> 1))) & 15u) - 8) * s;
-  T *out = dst + row * k + at;
-  if constexpr (sizeof(T) == 2) {
-    uint4 u;
-    uint32_t *p = &u.x;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const __half2 h2 = __floats2half2_rn(v[2 * q], v[2 * q + 1]);
-      p[q] = *reinterpret_cast<const uint32_t *>(&h2);
-    }
-    *reinterpret_cast<uint4 *>(out) = u;
-  } else {
-    *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  }
 }
 
 // ---------------------------------------------------- codes to operands --
@@ -197,10 +208,75 @@ __device__ __forceinline__ void cp_async_small(void *dst, const void *src, bool 
                  "r"(in ? BYTES : 0)
                  : "memory");
 }
+// D = A B
+template <bool BF>
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  if constexpr (BF)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ float trunc_bf16(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
 // the upper halves of two floats as one pair (lo first)
 __device__ __forceinline__ uint32_t upper2(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+
+// ----------------------------------------------------------- dequantize --
+// fp16: (c - 8) is exact in fp16, and its product with the scale rounds once.
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_w4_dequantize(const unsigned char *__restrict__ src, int64_t stride, int rows, int k, int group, T *__restrict__ dst) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int nsb = ceil_div(k, kSuper);
+  int lsh, sb0;
+  int64_t row;
+  rows_of_cta(nsb, threadIdx.x >> 5, lsh, sb0, row);
+  if (row >= rows) return;
+  const unsigned char *in = src + row * stride;
+  const __half *sc = reinterpret_cast<const __half *>(in + w4_kp(k) / 2);
+  T *out = dst + row * k;
+  const int gsh = group == 32 ? 5 : group == 64 ? 6 : 7;
+  for (int sb = sb0; sb < nsb; sb += 1 << lsh) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = sb * kSuper + h * 256 + lane * 8;
+      if (at >= k) continue;
+      const int wi = (at % kBlk) / 8;
+      const uint32_t w = *reinterpret_cast<const uint32_t *>(in + (at / kBlk) * 64 + ((wi & 3) * 4 + (wi >> 2)) * 4);
+      uint32_t c[4];
+      unpack8<false>(w, c);
+      if constexpr (sizeof(T) == 2) {
+        const __half2 s = __half2half2(sc[at >> gsh]);
+        uint4 u;
+        uint32_t *p = &u.x;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&c[q]), s);
+          p[q] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        __stcs(reinterpret_cast<uint4 *>(out + at), u);
+      } else {
+        const float s = __half2float(sc[at >> gsh]);
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&c[q]));
+          v[2 * q] = f.x * s;
+          v[2 * q + 1] = f.y * s;
+        }
+        __stcs(reinterpret_cast<float4 *>(out + at), make_float4(v[0], v[1], v[2], v[3]));
+        __stcs(reinterpret_cast<float4 *>(out + at) + 1, make_float4(v[4], v[5], v[6], v[7]));
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------- row products --
@@ -231,20 +307,22 @@ __host__ __device__ constexpr int dot_stage_bytes(int GS) { return 2048 + 16 * (
 __host__ __device__ constexpr size_t dot_ring_bytes(int NT, int GS) { return (size_t)kDotWarps * dot_stages(NT) * dot_stage_bytes(GS); }
 
 // Superblocks of k per CTA (k is split into ceil(nsb / per) parts): the least
-// of (row tiles of a CTA, or 8 where it has fewer: about what keeps enough
-// loads in flight) x per, where a split costs as much as 20 superblocks for its
-// partial sums and ticket.  More than 16 tile parts an SM are never made by
-// choice, which bounds the workspace.
-__device__ __forceinline__ int dot_per(int tiles, int nsb, int most, int ctas, int lane) {
+// of (row tiles of a CTA, in whole rounds of its four schedulers, and 8 at
+// least, about what keeps enough loads in flight) x per, where a split costs a
+// CTA as much as 12 superblocks for its last ticket and an eighth of one per
+// tile and 8 tokens for the partial sums.  At most 64 tile parts an SM, or
+// twice the parts that x forces, are made, which bounds the workspace.
+__device__ __forceinline__ int dot_per(int tiles, int nsb, int most, int ctas, int NT, int lane) {
+  const int64_t room = max((int64_t)kPartsPerCta * ctas, 2 * (int64_t)tiles * ceil_div(nsb, most));
   uint32_t best = 0xffffffffu;
   for (int p0 = 0; p0 < most; p0 += 32) {
     const int per = p0 + lane + 1;
     uint32_t key = 0xffffffffu;
     if (per <= most) {
       const int S = ceil_div(nsb, per);
-      if (per == most || (int64_t)tiles * S <= 16 * ctas) {
-        const int u = max(8, ceil_div(tiles, ctas / S));
-        const int64_t cost = (int64_t)u * per + (S > 1 ? 20 + S : 0);
+      if (per == most || (int64_t)tiles * S <= room) {
+        const int u = max(8, ceil_div(ceil_div(tiles, ctas / S), 4) * 4);
+        const int64_t cost = 8 * (int64_t)u * per + (S > 1 ? 8 * (12 + S) + (int64_t)u * NT : 0);
         key = (uint32_t)min(cost, (int64_t)(1 << 23)) * 256u + (uint32_t)(255 - per);
       }
     }
@@ -265,6 +343,7 @@ template <bool BF, int NT, int GS>
 __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mode) {
   extern __shared__ __align__(128) unsigned char sm[];
   constexpr int P = BF ? 3 : 1;                    // parts of x
+  constexpr int AC = NT == 1 ? 2 : 1;              // accumulators of a group: a shorter chain where one token tile is all
   constexpr int NS = dot_stages(NT), SB = dot_stage_bytes(GS), SCB = 4 << GS;
   pdl_wait();
   pdl_trigger();
@@ -281,7 +360,7 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
   const int per = mode == kListGated ? 8 : 16;
   const int tiles = ceil_div(total, per);
   const int nblk = w4_kp(A.k) / kBlk, nsb = ceil_div(nblk, 4);
-  const int sb_per = dot_per(tiles, nsb, A.most, gridDim.x, lane);
+  const int sb_per = dot_per(tiles, nsb, A.most, gridDim.x, NT, lane);
   const int S = ceil_div(nsb, sb_per);
   const int ctas = gridDim.x / S;                  // CTAs of one part of k
   const int s = blockIdx.x / ctas, p = blockIdx.x % ctas;
@@ -349,10 +428,13 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
       const bool in = b0 + pr.stage * 2 + (part >> 2) < b1;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        cp_async16(to + (part >> 2) * 1024 + (4 * i + (lane >> 3)) * 64 + (part & 3) * 16,
-                   in ? rp[i] + pr.stage * 128 : A.data, in ? 16u : 0u, pol);
+      {
+        cp_async16(to + (part >> 2) * 1024 + (4 * i + (lane >> 3)) * 64 + (part & 3) * 16, rp[i], in ? 16u : 0u, pol);
+        rp[i] += 128;
+      }
       // the scale area is padded to whole superblocks: a stage's scales are inside it
-      if (lane < 16) cp_async_small<SCB>(to + 2048 + lane * SCB, sp + pr.stage * SCB);
+      if (lane < 16) cp_async_small<SCB>(to + 2048 + lane * SCB, sp);
+      sp += SCB;
       if (advance(pr) && pr.unit < units) point();
     }
     cp_async_commit();
@@ -366,8 +448,10 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
 
   // x's part: [P][B][b1-b0 blocks], rows 64 bytes past a multiple of 128 apart
   // (eight lanes of a 16-byte read then touch every bank once)
-  const int kw = (b1 - b0) * kBlk;
+  const int kw = stages * 2 * kBlk;                // a last stage of one block multiplies zeros
   const int xrow = kw * 2 + 64;
+  for (int i = threadIdx.x; i < kw / 8; i += blockDim.x)
+    *reinterpret_cast<uint4 *>(sx + (size_t)P * A.B * xrow + i * 16) = make_uint4(0, 0, 0, 0);
   for (int i = threadIdx.x; i < A.B * (kw / 8); i += blockDim.x) {
     const int b = i / (kw / 8), c = (i % (kw / 8)) * 8, kk = b0 * kBlk + c;
     if constexpr (!BF) {
@@ -399,7 +483,13 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
 #pragma unroll
     for (int n = 0; n < NT; ++n) tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.f;
   };
-  const unsigned char *xl = sx + (size_t)g * xrow + t * 16;            // this lane's token of tile 0
+  // this lane's token of each tile; columns past the batch read a row of zeros
+  uint32_t xo[NT], xpart[NT];                      // and from part to part
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    xo[n] = (8 * n + g < A.B ? 8 * n + g : P * A.B) * xrow;
+    xpart[n] = 8 * n + g < A.B ? A.B * xrow : 0;
+  }
   auto compute = [&](const unsigned char *st, int stage) {
     uint32_t sa[1 << GS], sb[1 << GS];             // scales of rows g and g + 8
 #pragma unroll
@@ -407,43 +497,41 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
       sa[i] = *reinterpret_cast<const uint32_t *>(st + 2048 + g * SCB + 4 * i);
       sb[i] = *reinterpret_cast<const uint32_t *>(st + 2048 + (g + 8) * SCB + 4 * i);
     }
+    uint4 ca[2], cb[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      if (b0 + stage * 2 + u >= b1) break;
-      const uint4 ca = *reinterpret_cast<const uint4 *>(st + u * 1024 + g * 64 + t * 16);
-      const uint4 cb = *reinterpret_cast<const uint4 *>(st + u * 1024 + (g + 8) * 64 + t * 16);
-      const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
-      const unsigned char *xb = xl + (stage * 2 + u) * 256;
-      float acc[NT][4];
+      ca[u] = *reinterpret_cast<const uint4 *>(st + u * 1024 + g * 64 + t * 16);
+      cb[u] = *reinterpret_cast<const uint4 *>(st + u * 1024 + (g + 8) * 64 + t * 16);
+    }
+    const unsigned char *xb = sx + t * 16 + stage * 512;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t wa[4] = {ca[u].x, ca[u].y, ca[u].z, ca[u].w}, wb[4] = {cb[u].x, cb[u].y, cb[u].z, cb[u].w};
+      float acc[NT][AC][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bool fresh = j % (4 >> GS) == 0, last = (j + 1) % (4 >> GS) == 0;   // of a group
         uint32_t ha[4], hb[4];
         unpack8<BF>(wa[j], ha);
         unpack8<BF>(wb[j], hb);
-        if (fresh) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int q = 0; q < P; ++q) {
-            uint4 xv = make_uint4(0, 0, 0, 0);
-            if (8 * n + g < A.B) xv = *reinterpret_cast<const uint4 *>(xb + ((size_t)q * A.B + 8 * n) * xrow + j * 64);
-            mma16816<BF>(acc[n], ha[0], hb[0], ha[1], hb[1], xv.x, xv.y);
-            mma16816<BF>(acc[n], ha[2], hb[2], ha[3], hb[3], xv.z, xv.w);
+            const uint4 xv = *reinterpret_cast<const uint4 *>(xb + xo[n] + q * xpart[n] + u * 256 + j * 64);
+            if (fresh && q == 0) mma16816_first<BF>(acc[n][0], ha[0], hb[0], ha[1], hb[1], xv.x, xv.y);
+            else mma16816<BF>(acc[n][0], ha[0], hb[0], ha[1], hb[1], xv.x, xv.y);
+            if (fresh && q == 0 && AC == 2) mma16816_first<BF>(acc[n][AC - 1], ha[2], hb[2], ha[3], hb[3], xv.z, xv.w);
+            else mma16816<BF>(acc[n][AC - 1], ha[2], hb[2], ha[3], hb[3], xv.z, xv.w);
           }
         if (last) {                                // scale the group's sum
           const int i = (u << GS) + (j >> (2 - GS));
           const float fa = half_of(sa[i >> 1], i & 1), fb = half_of(sb[i >> 1], i & 1);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            tot[n][0] = fmaf(fa, acc[n][0], tot[n][0]);
-            tot[n][1] = fmaf(fa, acc[n][1], tot[n][1]);
-            tot[n][2] = fmaf(fb, acc[n][2], tot[n][2]);
-            tot[n][3] = fmaf(fb, acc[n][3], tot[n][3]);
-          }
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              tot[n][e] = fmaf(e < 2 ? fa : fb, AC == 2 ? acc[n][0][e] + acc[n][AC - 1][e] : acc[n][0][e], tot[n][e]);
         }
       }
     }
@@ -497,15 +585,11 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
 #pragma unroll
     for (int n = 0; n < NT; ++n) __stcg(to + n * 32, make_float4(tot[n][0], tot[n][1], tot[n][2], tot[n][3]));
     if (tile + 1 < min(tiles, (unit + 1) * tpu)) return;
-    __threadfence();
-    __syncwarp();
+    __syncwarp();                                  // the warp's sums, then lane 0's release
     const int sh = 8 * (unit & 3);
     uint32_t *word = &A.hdr->tile_done[unit >> 2];
     uint32_t old = 0;
-    if (lane == 0) {
-      old = (atomicAdd(word, 1u << sh) >> sh) & 255u;
-      __threadfence();
-    }
+    if (lane == 0) old = (ticket_acq_rel(word, 1u << sh) >> sh) & 255u;
     old = __shfl_sync(0xffffffffu, old, 0);
     if (old != (uint32_t)(S - 1)) return;
     for (int tl = unit * tpu; tl <= tile; ++tl) {
@@ -753,12 +837,8 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
     else __stcg(A.part + ((int64_t)r * A.B + b) * A.d + c, v);
   }
   if (R == 1) return;
-  __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) {
-    s_last = ticket_acq_rel(&A.hdr->tile_done[cu]);
-    __threadfence();
-  }
+  if (threadIdx.x == 0) s_last = ticket_acq_rel(&A.hdr->tile_done[cu]);
   __syncthreads();
   if (s_last != (uint32_t)(R - 1)) return;
   for (int i = threadIdx.x; i < A.B * kDownCols; i += blockDim.x) {
@@ -782,6 +862,11 @@ asf_status check_w4(const asf_w4_matrix *m) {
   if (m->row_stride < w4_row_bytes(m->k, m->group)) return ASF_ERR_INVALID_ARG;
   return ASF_OK;
 }
+// CTAs of the row-wise kernels (rows_of_cta)
+unsigned row_ctas(const asf_w4_matrix *m) {
+  const int nsb = ceil_div(m->k, kSuper), per = nsb > 4 ? 1 : nsb > 2 ? 2 : nsb > 1 ? 4 : 8;
+  return (unsigned)ceil_div(m->rows, per);
+}
 int ffn_mats(const asf_w4_ffn *f) { return f->act == ASF_ACT_REGLU ? 3 : 2; }
 asf_status check_w4_ffn(const asf_w4_ffn *f) {
   if (!f || !f->data || !f->bias) return ASF_ERR_INVALID_ARG;
@@ -797,7 +882,7 @@ asf_status check_w4_ffn(const asf_w4_ffn *f) {
 int nt_of(int B) { return B <= 8 ? 1 : B <= 16 ? 2 : 4; }
 int gs_of(int group) { return group == 32 ? 2 : group == 64 ? 1 : 0; }
 int dot_ctas() { return sm_count(); }
-size_t x_bytes(int B, int parts, int superblocks) { return (size_t)B * parts * ((size_t)superblocks * kSuper * 2 + 64); }
+size_t x_bytes(int B, int parts, int superblocks) { return ((size_t)B * parts + 1) * ((size_t)superblocks * kSuper * 2 + 64); }
 // superblocks of k whose x fits a CTA beside the rings
 int dot_most(int k, int group, int B, int parts) {
   const int nsb = ceil_div(w4_kp(k), kSuper);
@@ -810,7 +895,7 @@ int dot_most(int k, int group, int B, int parts) {
 size_t dot_part_bytes(int tiles, int k, int group, int B) {
   const int nsb = ceil_div(w4_kp(k), kSuper);
   const size_t forced = (size_t)tiles * ceil_div(nsb, dot_most(k, group, B, 3));
-  return r256(std::max<size_t>((size_t)16 * dot_ctas(), forced) * nt_of(B) * 512);
+  return r256(std::max<size_t>((size_t)kPartsPerCta * dot_ctas(), 2 * forced) * nt_of(B) * 512);
 }
 int down_units(int d) { return ceil_div(w4_kp(d), kDownCols); }
 int down_w4_splits(int d, int B) {
@@ -880,8 +965,7 @@ asf_status asf_w4_quantize(const void *src, asf_dtype dtype, const asf_w4_matrix
   if (!src) return ASF_ERR_INVALID_ARG;
   if (dtype != ASF_F16 && dtype != ASF_F32) return ASF_ERR_UNSUPPORTED;
   if (!al16(src)) return ASF_ERR_MISALIGNED;
-  const int64_t units = (int64_t)mat->rows * ceil_div(mat->k, kSuper);
-  const dim3 grid((unsigned)((units + 7) / 8)), block(256);
+  const dim3 grid(row_ctas(mat)), block(256);
   unsigned char *dst = static_cast<unsigned char *>(const_cast<void *>(mat->data));
   cudaStream_t st = (cudaStream_t)stream;
   return cuda_status(dtype == ASF_F16
@@ -897,8 +981,7 @@ asf_status asf_w4_dequantize(const asf_w4_matrix *mat, void *dst, asf_dtype dtyp
   if (!dst) return ASF_ERR_INVALID_ARG;
   if (dtype != ASF_F16 && dtype != ASF_F32) return ASF_ERR_UNSUPPORTED;
   if (!al16(dst)) return ASF_ERR_MISALIGNED;
-  const int64_t words = (int64_t)mat->rows * (mat->k / 8);
-  const dim3 grid((unsigned)((words + 255) / 256)), block(256);
+  const dim3 grid(row_ctas(mat)), block(256);
   const unsigned char *src = static_cast<const unsigned char *>(mat->data);
   cudaStream_t st = (cudaStream_t)stream;
   return cuda_status(dtype == ASF_F16 ? launch(k_w4_dequantize<__half>, grid, block, 0, st, src, mat->row_stride,

@@ -261,6 +261,6 @@ def test_python_refusals():
         with pytest.raises(ValueError):
             bad()
     for bad in (lambda: att(q=d["q"][:, :3].contiguous(), o=d["o"][:, :3].contiguous()),
-                lambda: att(ws=A.Workspace.for_w4(A.W4Matrix.quantize(torch.ones(8, 8, device="cuda"), 32), 1))):
+                lambda: att(ws=A.Workspace._sized(4096, d["q"].device, None, "test"))):
         with pytest.raises(A.AsfError):
             bad()

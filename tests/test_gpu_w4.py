@@ -71,7 +71,8 @@ def _check(y, ref, mass, groups):
 @pytest.mark.parametrize("m,k,group,B", [
     (1, 8, 32, 1), (16, 128, 128, 1), (17, 136, 64, 2), (31, 520, 32, 8), (1003, 1376, 32, 3), (64, 4096, 128, 1),
     (256, 8192, 64, 9), (40, 12288, 128, 17), (129, 2760, 64, 32), (5000, 512, 128, 5), (24, 49152, 128, 32),
-    (2500, 4096, 64, 24)])
+    (2500, 4096, 64, 24), (48, 1024, 128, 18),
+    (33, 640, 32, 25)])
 def test_matmul(m, k, group, B, dt):
     rng = np.random.default_rng(m * k + B)
     rows = O.w4_pack(_weights(m, k, m + k), group)
