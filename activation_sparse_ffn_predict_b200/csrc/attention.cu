@@ -29,6 +29,7 @@ namespace {
 constexpr int kTile = 64;              // keys per tile
 constexpr int kStages = 3;             // tiles in shared memory
 constexpr int kMinChunk = 4;           // key tiles per split, at least
+constexpr int kWhole = 8;              // key tiles up to which nothing is split (no merge to launch)
 
 struct AttnArgs {
   const __half *k, *v;
@@ -43,6 +44,7 @@ struct AttnArgs {
   __half *o;
   float *part;                         // [unit][MT][DP]
   float2 *ml;                          // [unit][MT]: maximum (log2) and sum
+  int4 *plan;                          // per request, for the merge: first token, tokens, splits, first unit
   int target;                          // CTAs to aim at
   int32_t *err;
 };
@@ -97,7 +99,7 @@ __device__ __forceinline__ Req plan_lane(const AttnArgs &A, int MT, int lane, in
     W += __shfl_xor_sync(0xffffffffu, W, o);
     most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
   }
-  C = max(kMinChunk, (int)((W * A.hkv + A.target - 1) / A.target));
+  C = max(most <= kWhole ? kWhole : kMinChunk, (int)((W * A.hkv + A.target - 1) / A.target));
   while (true) {
     q.splits = (q.nkt + C - 1) / C;
     int u = q.rt * q.splits * A.hkv;
@@ -110,7 +112,7 @@ __device__ __forceinline__ Req plan_lane(const AttnArgs &A, int MT, int lane, in
     q.base = u - own;
     units = __shfl_sync(0xffffffffu, u, 31);
     if (units <= A.target || C >= most) break;
-    C += max(1, C / 32);
+    C += max(1, C / 16);
   }
   return q;
 }
@@ -142,12 +144,15 @@ __device__ __forceinline__ float exp2_fast(float v) {
   return r;
 }
 
+// CTAs of an SM: what their stages (48 or 96 KB) and registers leave.
+__host__ __device__ constexpr int attn_resident(int DP, int WM) { return DP == 64 ? (WM == 8 ? 2 : 3) : (WM == 8 ? 1 : 2); }
+
 // A CTA is one unit: WM groups of 16 query rows x KG groups of keys, a warp
 // each.  Keys and values of a tile go to shared memory by 16-byte cp.async, two
 // tiles ahead; 16-byte chunk c of row i sits at c ^ (i & 7), so that the
 // 8 x 8 matrix loads touch every bank once.
 template <int DP, int WM>
-__global__ void __launch_bounds__((WM > 4 ? WM : 4) * 32) k_tree_attn(AttnArgs A) {
+__global__ void __launch_bounds__((WM > 4 ? WM : 4) * 32, attn_resident(DP, WM)) k_tree_attn(AttnArgs A) {
   constexpr int NW = WM > 4 ? WM : 4;
   constexpr int KG = NW / WM;          // key groups
   constexpr int KW = kTile / KG;       // keys of a warp
@@ -167,6 +172,7 @@ __global__ void __launch_bounds__((WM > 4 ? WM : 4) * 32) k_tree_attn(AttnArgs A
     bool bad;
     const Req q = plan_lane(A, MT, lane, C, units, bad);
     if (bad && blockIdx.x == 0) flag_error(A.err, kErrIndex);
+    if (blockIdx.x == 0) A.plan[lane] = make_int4(q.t0, q.n, q.splits, q.base);
     const int mine = q.rt * q.splits * A.hkv, u = (int)blockIdx.x - q.base;
     if (lane == 0) s_unit[0] = -1;
     __syncwarp();
@@ -471,18 +477,15 @@ __global__ void __launch_bounds__(128) k_tree_merge(AttnArgs A, int MT) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  int C, units;
-  bool bad;
-  const Req q = plan_lane(A, MT, lane, C, units, bad);
+  const int4 q = __ldcg(A.plan + lane);
   const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
   const int hq = A.hkv * A.grp, tok = row / hq, hd = row % hq;
   if (tok >= A.T) return;
-  // a token belongs to the first request whose range holds it
-  const uint32_t who = __ballot_sync(0xffffffffu, lane < A.R && tok >= q.t0 && tok < q.t0 + q.n);
+  const uint32_t who = __ballot_sync(0xffffffffu, tok >= q.x && tok < q.x + q.y);   // ranges do not overlap
   if (!who) return;
   const int r = __ffs(who) - 1;
-  const int t0 = __shfl_sync(0xffffffffu, q.t0, r), rt = __shfl_sync(0xffffffffu, q.rt, r);
-  const int splits = __shfl_sync(0xffffffffu, q.splits, r), base = __shfl_sync(0xffffffffu, q.base, r);
+  const int t0 = __shfl_sync(0xffffffffu, q.x, r), rt = (__shfl_sync(0xffffffffu, q.y, r) * A.grp + MT - 1) / MT;
+  const int splits = __shfl_sync(0xffffffffu, q.z, r), base = __shfl_sync(0xffffffffu, q.w, r);
   if (splits == 1) return;
   const int m = (tok - t0) * A.grp + hd % A.grp, head = hd / A.grp;
   const int64_t first = ((int64_t)base + (int64_t)head * splits * rt + m / MT) * MT + m % MT, step = (int64_t)rt * MT;
@@ -492,7 +495,7 @@ __global__ void __launch_bounds__(128) k_tree_merge(AttnArgs A, int MT) {
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float ref = M == -INFINITY ? 0.f : M;
   float l = 0.f, o[V] = {};
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < splits; ++s) {
     const int64_t at = first + s * step;
     const float2 ml = __ldcg(A.ml + at);
@@ -535,12 +538,12 @@ __global__ void __launch_bounds__(128) k_kv_append(AppendArgs A) {
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= A.T * per) return;
   const int tok = i / per, head = i % per / (A.D / 8), c = i % (A.D / 8);
-  int r = -1, t0 = 0;                  // the first request whose range holds the token
-  for (int q = 0; q < A.R && r < 0; ++q) {
-    t0 = ld_cg_i32(A.begin + q);
-    if (tok >= t0 && tok < ld_cg_i32(A.begin + q + 1)) r = q;
-  }
-  if (r < 0) return;                   // behind the last range: nothing is written
+  int r = 0;                           // the request whose range holds the token
+#pragma unroll 8
+  for (int q = 1; q <= A.R; ++q) r += tok >= ld_cg_i32(A.begin + q);
+  if (r >= A.R) return;                // behind the last range: nothing is written
+  const int t0 = ld_cg_i32(A.begin + r);
+  if (tok < t0) return;
   const int len = ld_cg_i32(A.lens + r);
   const int64_t pos = (int64_t)len + (tok - t0);
   const int64_t pi = pos / A.page;
@@ -585,17 +588,16 @@ int row_groups(int grp, int R, int T) {
   const int rows = (T + R - 1) / R * grp;
   return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8;
 }
-// Resident CTAs to aim at: two an SM (shared memory), one of 8 warps.
-int attn_target(int wm) { return sm_count() * (wm == 8 ? 1 : 2); }
 int row_tiles_most(int grp, int R, int T, int wm) { return T * grp / (16 * wm) + R; }
-int attn_units_most(const asf_kv_cache *c, int grp, int R, int T, int wm) {
-  return attn_target(wm) + c->heads * row_tiles_most(grp, R, T, wm);
-}
 int attn_dp(const asf_kv_cache *c) { return c->head_dim <= 64 ? 64 : 128; }
+int attn_target(const asf_kv_cache *c, int wm) { return sm_count() * attn_resident(attn_dp(c), wm); }
+int attn_units_most(const asf_kv_cache *c, int grp, int R, int T, int wm) {
+  return attn_target(c, wm) + c->heads * row_tiles_most(grp, R, T, wm);
+}
 size_t attn_scratch(const asf_kv_cache *c, int grp, int R, int T) {
   const int wm = row_groups(grp, R, T);
   const size_t rows = (size_t)attn_units_most(c, grp, R, T, wm) * 16 * wm;
-  return r256(rows * attn_dp(c) * 4) + r256(rows * 8);
+  return 512 + r256(rows * attn_dp(c) * 4) + r256(rows * 8);
 }
 
 template <int DP, int WM>
@@ -611,8 +613,7 @@ cudaError_t run_attn_any(const AttnArgs &a, int wm, int units, cudaStream_t st) 
                   : wm == 4 ? run_attn<DP, 4>(a, units, st)
                             : run_attn<DP, 8>(a, units, st);
   if (e != cudaSuccess) return e;
-  // a table of at most kMinChunk key tiles is never split
-  if ((int64_t)a.max_pages * a.page <= kMinChunk * kTile) return e;
+  if ((int64_t)a.max_pages * a.page <= kWhole * kTile) return e;
   const int rows = a.T * a.hkv * a.grp;
   return launch(k_tree_merge<DP>, dim3((rows + 3) / 4), dim3(128), 0, st, a, 16 * wm);
 }
@@ -685,9 +686,11 @@ asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *table, i
   a.anc = anc;
   a.scale = (float)((double)scale * 1.4426950408889634);
   a.o = static_cast<__half *>(o);
+  a.plan = reinterpret_cast<int4 *>(base);
+  base += 512;
   a.part = reinterpret_cast<float *>(base);
   a.ml = reinterpret_cast<float2 *>(base + r256((size_t)units * 16 * wm * attn_dp(cache) * 4));
-  a.target = attn_target(wm);
+  a.target = attn_target(cache, wm);
   a.err = &static_cast<Header *>(ws)->err;
   cudaStream_t st = (cudaStream_t)stream;
   return cuda_status(attn_dp(cache) == 64 ? run_attn_any<64>(a, wm, units, st) : run_attn_any<128>(a, wm, units, st));

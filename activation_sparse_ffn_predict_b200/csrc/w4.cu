@@ -420,7 +420,6 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
     sp = A.data + (int64_t)id * A.stride + (mode == kListGated && (lane & 8) ? A.up : 0) + w4_kp(A.k) / 2 +
          (int64_t)b0 * (2 << GS);
   };
-  const uint64_t pol = l2_evict_first();
   auto copy = [&](int slot) {                      // stage pr.stage of pr.tile
     if (pr.unit < units) {
       unsigned char *to = ring + slot * SB;
@@ -429,7 +428,7 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
 #pragma unroll
       for (int i = 0; i < 4; ++i)
       {
-        cp_async16(to + (part >> 2) * 1024 + (4 * i + (lane >> 3)) * 64 + (part & 3) * 16, rp[i], in ? 16u : 0u, pol);
+        cp_async16(to + (part >> 2) * 1024 + (4 * i + (lane >> 3)) * 64 + (part & 3) * 16, rp[i], in ? 16u : 0u);
         rp[i] += 128;
       }
       // the scale area is padded to whole superblocks: a stage's scales are inside it
@@ -684,7 +683,6 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
   unsigned char *ring = sm + (size_t)warp * NS * SB;
   const int first = r * (kDownWarps / 2) + (warp >> 1), step = R * (kDownWarps / 2);
   const int tiles = col0 < kp && first < ntile ? (ntile - first + step - 1) / step : 0;
-  const uint64_t pol = l2_evict_first();
   auto id_of = [&](int i) {
     const int pos = (first + i * step) * 16 + (lane & 15);
     int id = -1;
@@ -704,7 +702,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
       const int nrn = __shfl_sync(0xffffffffu, now, row);
       const int x = ((row >> 1) & 1) | ((row & 4));
       cp_async16(to + (row >> 1) * 128 + (((part * 2 + (row & 1)) ^ x) * 16),
-                 A.data + (int64_t)max(nrn, 0) * A.stride + col0 / 2 + part * 16, nrn >= 0 ? 16u : 0u, pol);
+                 A.data + (int64_t)max(nrn, 0) * A.stride + col0 / 2 + part * 16, nrn >= 0 ? 16u : 0u);
     }
     if (lane < 16) {
       // one block's scales; a single one comes with its neighbour (4 bytes at least)

@@ -51,7 +51,7 @@ class AttentionStage:
     def launches(self) -> int:
         """Kernels per layer: append, attention, the merge of split keys unless the table is too
         short for a split, and the projection."""
-        split = self.max_pages * self.caches[0].page > 256
+        split = self.max_pages * self.caches[0].page > 512
         return 2 + int(split) + int(self.out is not None)
 
     def enqueue(self, l: int, x: torch.Tensor, stream=None) -> None:
