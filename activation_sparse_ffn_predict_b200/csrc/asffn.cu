@@ -2693,23 +2693,6 @@ cudaError_t launch_final_reduce(const float *part, int G, int B, int d, float *y
 // CUDA-core pair measured about twice as fast there.
 bool tc_ok(const asf_ffn *f, int B) { return f->wdtype == ASF_F16 && B > 4 && B <= ASF_MAX_BATCH; }
 
-// cuTensorMapEncodeTiled, from the driver through the runtime (no link to the
-// driver library).
-using TmapEncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-TmapEncodeFn tmap_encoder() {
-  static TmapEncodeFn fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return (TmapEncodeFn) nullptr;
-    return reinterpret_cast<TmapEncodeFn>(p);
-  }();
-  return fn;
-}
-
 // Map of `rows` fp16 rows of d elements, `stride` elements apart, read in boxes
 // of box_cols columns x box_rows rows (box_cols * 2 bytes = the swizzle span:
 // the 128-byte swizzle for 64 columns, the 64-byte one for 32); out-of-range

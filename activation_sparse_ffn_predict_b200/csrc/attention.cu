@@ -12,11 +12,13 @@
 // All of it in fp32 in units of log2 (scale log2(e) joins the score); the
 // weights e^(z - m) are rounded to fp16 for the product with v, half a step of
 // 2^-11 each, as much as the output's own rounding and averaged over the keys.
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "asffn.h"
 #include "common.cuh"
@@ -46,6 +48,7 @@ struct AttnArgs {
   float2 *ml;                          // [unit][MT]: maximum (log2) and sum
   int4 *plan;                          // per request, for the merge: first token, tokens, splits, first unit
   int target;                          // CTAs to aim at
+  int box;                             // keys of a TMA load, or 0
   int32_t *err;
 };
 
@@ -144,8 +147,9 @@ __device__ __forceinline__ float exp2_fast(float v) {
   return r;
 }
 
-// CTAs of an SM: what their stages (48 or 96 KB) and registers leave.
-__host__ __device__ constexpr int attn_resident(int DP, int WM) { return DP == 64 ? (WM == 8 ? 2 : 3) : (WM == 8 ? 1 : 2); }
+// CTAs of an SM: what their stages (48 or 96 KB), registers and, for tiles of
+// 8 x 16 rows, tensor memory leave.
+__host__ __device__ constexpr int attn_resident(int DP, int WM) { return DP == 64 && WM < 8 ? 3 : 2; }
 
 // A CTA is one unit: WM groups of 16 query rows x KG groups of keys, a warp
 // each.  Keys and values of a tile go to shared memory by 16-byte cp.async, two
@@ -296,7 +300,8 @@ __global__ void __launch_bounds__((WM > 4 ? WM : 4) * 32, attn_resident(DP, WM))
       nonfin[1] = s_nonfin[1];
       if (nonfin[0] | nonfin[1]) {
         for (int i = tid; i < kTile * CH; i += NW * 32)
-          if (((i / CH & 32 ? nonfin[1] : nonfin[0]) >> (i / CH % 32)) & 1u) *reinterpret_cast<uint4 *>(vp + i * 16) = make_uint4(0, 0, 0, 0);
+          if (((i / CH & 32 ? nonfin[1] : nonfin[0]) >> (i / CH % 32)) & 1u)
+            *reinterpret_cast<uint4 *>(vp + i * 16) = make_uint4(0, 0, 0, 0);
         __syncthreads();
       }
     }
@@ -470,6 +475,600 @@ __global__ void __launch_bounds__((WM > 4 ? WM : 4) * 32, attn_resident(DP, WM))
   }
 }
 
+// ------------------------------------------- many rows: tcgen05 ----------
+// For tiles of more than 32 query rows mma.sync's rate (a quarter of
+// tcgen05's) bounds the kernel above, not HBM.  Here a CTA takes 128 rows:
+//   warps 4, 5 copy Q once, then tiles of 64 keys (warp 4) and of their values
+//              (warp 5), into the 128-byte swizzled layout that the MMA reads;
+//   warp 6     one thread issues S = Q K^T (M 128, N 64) into one of two
+//              accumulators in tensor memory, and O += P V with P read from
+//              tensor memory (V as it lies: keys are its K, so it is MN-major);
+//   warps 0-3  a thread per row reads S, masks it, takes the running maximum
+//              and sum, and writes P in fp16 over the accumulator it has read.
+// S of the next tile is computed while this one's weights are, and keys and
+// values have slots of their own: the keys' are free as soon as S is there, so
+// only their copy has to be ahead, and a tile's values arrive under its
+// exponentials (one slot for both: 1.6 times the time).  O is rescaled
+// only when some row of a warp has outgrown its reference by 2^8: any reference
+// is right as long as the weights (up to 2^8 here) and their sums stay finite,
+// and it spares a pass over O in tensor memory per tile.  Two CTAs share an SM,
+// one's products under the other's exponentials.
+template <int DP>
+struct TreeTc {
+  static constexpr int Q = 128 * DP * 2;
+  static constexpr int KV = kTile * DP * 2;        // keys, or values, of a tile
+  static constexpr int NS = DP == 128 ? 2 : 4;     // slots of keys, and of values
+  static constexpr int BAR = 1024;
+  static constexpr size_t SMEM = 1024 + BAR + Q + (size_t)NS * 2 * KV;
+  static constexpr uint32_t COLS = 256;            // O: DP columns at 0; S and P: 64 each at 128 and 192
+};
+constexpr int kTcThreads = 7 * 32;
+constexpr uint64_t kTcWaitNs = 200ull * 1000 * 1000;   // bound on any mbarrier wait
+
+// Whether a phase is over, without waiting (try_wait sleeps for microseconds).
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// The bounded wait for a whole warp: one lane polls, and looks at the clock
+// only now and then (the timer is read over the chip, not on the SM).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
+      if ((i & 63u) == 0) {
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kTcWaitNs) {
+          ok = false;
+          break;
+        }
+      }
+  }
+  return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+}
+
+__device__ __forceinline__ unsigned char *align_1024(unsigned char *p) {
+  const uint32_t a = smem_u32(p);
+  return p + (((a + 1023u) & ~1023u) - a);
+}
+// D (tensor memory) += A (tensor memory, fp16 pairs) B (shared memory)
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accum)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+// 16 or 64 columns of this thread's lane, and the wait that makes them usable:
+// in one statement, so that no use can slip between the two.
+__device__ __forceinline__ void tmem_ld16w(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  float v;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v)
+      : "r"(taddr)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]),
+        "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]),
+        "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]),
+        "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]),
+        "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+//
+// Copies: where a tile is whole pages or lies in one (pages of 8, 16, 32 or a
+// multiple of 64 tokens), one TMA load per page and 64 columns; else 16-byte
+// cp.async, whose rate is what an SM's load path takes (about 25 bytes a
+// clock).
+template <int DP, bool TMA>
+__global__ void __launch_bounds__(kTcThreads, 2)
+    k_tree_tc(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, AttnArgs A) {
+  using Lc = TreeTc<DP>;
+  constexpr int NS = Lc::NS, MT = 128, CH = DP / 8;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ int s_unit[10];
+  __shared__ int64_t s_off[2][2][kTile];           // of keys, of values: element offset of a row, -1: no such key
+  __shared__ uint32_t s_valid[8][2];               // keys of a tile that exist
+  __shared__ uint32_t s_nonfin[NS][kTile];         // 16-byte chunks of drafted values left out of the product
+  __shared__ int s_any[NS];
+  unsigned char *smem = align_1024(smem_raw);
+  uint64_t *full_k = reinterpret_cast<uint64_t *>(smem), *empty_k = full_k + NS;
+  uint64_t *full_v = empty_k + NS, *empty_v = full_v + NS;
+  uint64_t *bs = empty_v + NS, *bp = bs + 2, *bo = bp + 2, *bq = bo + 2, *land = bq + 1;
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(land + 1);
+  unsigned char *sq = smem + Lc::BAR, *sk = sq + Lc::Q, *sv = sk + NS * Lc::KV;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full_k[i], TMA ? 1 : 32);
+      mbar_init(&full_v[i], TMA ? 1 : 32);
+      mbar_init(&empty_k[i], 1);
+      mbar_init(&empty_v[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bs[i], 2);                        // the products, and the thread that issued them
+      mbar_init(&bp[i], 4 * 32);
+      mbar_init(&bo[i], 1);
+    }
+    mbar_init(bq, 64);
+    mbar_init(land, 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 0) {
+    int C, units;
+    bool bad;
+    const Req q = plan_lane(A, MT, lane, C, units, bad);
+    if (bad && blockIdx.x == 0) flag_error(A.err, kErrIndex);
+    if (blockIdx.x == 0) A.plan[lane] = make_int4(q.t0, q.n, q.splits, q.base);
+    const int mine = q.rt * q.splits * A.hkv, u = (int)blockIdx.x - q.base;
+    if (lane == 0) s_unit[0] = -1;
+    __syncwarp();
+    if (u >= 0 && u < mine) {
+      const int tile = u % q.rt, s = u / q.rt % q.splits;
+      s_unit[0] = lane;
+      s_unit[1] = u / q.rt / q.splits;
+      s_unit[2] = tile;
+      s_unit[3] = s * C;
+      s_unit[4] = min(q.nkt, (s + 1) * C);
+      s_unit[5] = q.t0;
+      s_unit[6] = q.n;
+      s_unit[7] = q.len;
+      s_unit[8] = q.L;
+      s_unit[9] = q.splits;
+    }
+  }
+  __syncthreads();
+  const int req = s_unit[0];
+  if (req < 0) return;
+  if (warp == 6) {
+    tmem_alloc(tslot, Lc::COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tslot;
+  const int head = s_unit[1], row0 = s_unit[2] * MT, kt0 = s_unit[3], tiles = s_unit[4] - kt0;
+  const int t0 = s_unit[5], n = s_unit[6], len = s_unit[7], L = s_unit[8], splits = s_unit[9];
+  const int rows = n * A.grp;
+
+  if (warp == 4 || warp == 5) {
+    // ---------------------------------------------------------------- copies --
+    const bool is_k = warp == 4;
+    const __half *base = is_k ? A.k : A.v;
+    unsigned char *slots = is_k ? sk : sv;
+    uint64_t *full = is_k ? full_k : full_v, *empty = is_k ? empty_k : empty_v;
+    int64_t(*off)[kTile] = s_off[warp - 4];
+    auto offsets = [&](int j) {                    // two keys a lane
+      if (TMA || j >= tiles) return;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int pos = (kt0 + j) * kTile + 32 * h + lane;
+        int64_t o = -1;
+        if (pos < L) {
+          const int pi = pos / A.page;
+          const int id = __ldg(A.table + (int64_t)req * A.max_pages + pi);
+          if ((unsigned)id < (unsigned)A.pages)
+            o = (int64_t)id * A.page_stride + (int64_t)(pos - pi * A.page) * A.token_stride + (int64_t)head * A.head_stride;
+          else
+            flag_error(A.err, kErrIndex);
+        }
+        off[j & 1][32 * h + lane] = o;
+        const uint32_t have = __ballot_sync(0xffffffffu, o >= 0);
+        if (is_k && lane == 0) s_valid[j & 7][h] = have;
+      }
+    };
+    // this lane's 16-byte chunk of every RP-th row
+    constexpr int RP = 32 / CH, ROWS = kTile / RP;
+    const int r0 = lane / CH, c = lane % CH;
+    const bool col = c * 8 < A.D;
+    offsets(0);
+    // half of Q each; rows past the request's as zeros
+#pragma unroll 8
+    for (int i = 0; i < 64 / RP; ++i) {
+      const int r = (warp - 4) * 64 + r0 + i * RP, m = row0 + r;
+      const bool in = m < rows && col;
+      const __half *src = A.q;
+      if (in) src += ((int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp) * A.D + c * 8;
+      cp_async16(sq + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, in ? 16u : 0u);
+    }
+    cp_async_commit();
+    // tile j has landed; drafted values are looked over first
+    auto hand_on = [&](int j) {
+      const int sl = j % NS, pos0 = (kt0 + j) * kTile;
+      if (!is_k && pos0 + kTile > len) {
+#pragma unroll 4
+        for (int i = 0; i < ROWS; ++i) {           // (cp.async: the chunks that this lane has copied)
+          const int r = r0 + i * RP;
+          uint4 *at = reinterpret_cast<uint4 *>(slots + (size_t)sl * Lc::KV + (c >> 3) * (kTile * 128) + r * 128 +
+                                                (((c & 7) ^ (r & 7)) << 4));
+          const uint4 u = *at;
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          bool bad = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) bad |= (w[e] & 0x7c00u) == 0x7c00u || (w[e] & 0x7c000000u) == 0x7c000000u;
+          if (TMA && pos0 + r >= L) {
+            *at = make_uint4(0, 0, 0, 0);          // what lies behind the last key
+          } else if (bad && pos0 + r >= len) {
+            // 0 * NaN would reach rows that do not see the key: out of the
+            // product, added by the rows that do
+            *at = make_uint4(0, 0, 0, 0);
+            atomicOr(&s_nonfin[sl][r], 1u << c);
+            s_any[sl] = 1;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      if (TMA) __syncwarp();
+      if (!TMA || lane == 0) mbar_arrive(&full[sl]);
+    };
+    bool ok = true;
+    int marked = 0;                                // tiles that had to be looked over
+    if (TMA) {
+      const int nb = kTile / A.box;
+      // lane b: box b of tile j, as a page and a token of it
+      auto page_of = [&](int j, int &tok) {
+        const int pos = (kt0 + j) * kTile + lane * A.box;
+        int id = -1;
+        tok = 0;
+        if (j < tiles && lane < nb && pos < L) {
+          const int pi = pos / A.page;
+          tok = pos - pi * A.page;
+          id = __ldg(A.table + (int64_t)req * A.max_pages + pi);
+          if ((unsigned)id >= (unsigned)A.pages) {
+            flag_error(A.err, kErrIndex);
+            id = -1;
+          }
+        }
+        return id;
+      };
+      int tok, id = page_of(0, tok);
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      mbar_arrive(bq);
+      const uint32_t bytes = kTile * DP * 2;
+      for (int j = 0; j < tiles; ++j) {
+        const int sl = j % NS, pos0 = (kt0 + j) * kTile;
+        const int now = id, at = tok;
+        id = page_of(j + 1, tok);
+        if (j >= NS) {
+          ok = warp_wait(&empty[sl], (uint32_t)((j / NS) - 1) & 1u);
+          if (!ok) {
+            // what is on its way lands before the shared memory is given back
+            for (int e = j - NS; e < j; ++e) warp_wait(&full[e % NS], (uint32_t)(e / NS) & 1u);
+            break;
+          }
+        }
+        if (is_k) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key = 32 * h + lane;
+            const bool there = __shfl_sync(0xffffffffu, now, key / A.box) >= 0 && pos0 + key < L;
+            const uint32_t have = __ballot_sync(0xffffffffu, there);
+            if (lane == 0) s_valid[j & 7][h] = have;
+          }
+        } else {
+          s_nonfin[sl][lane] = s_nonfin[sl][32 + lane] = 0;
+          if (lane == 0) s_any[sl] = 0;
+        }
+        const bool look = !is_k && pos0 + kTile > len;
+        uint64_t *bar = look ? land : &full[sl];
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+        __syncwarp();
+        if (lane < nb) {
+          // a page that is not there: outside the map, zeros
+#pragma unroll
+          for (int h = 0; h < DP / 64; ++h)
+            tma_load_4d(slots + (size_t)sl * Lc::KV + h * (kTile * 128) + lane * A.box * 128, is_k ? &map_k : &map_v, 64 * h,
+                        now >= 0 ? at : 0, head, now >= 0 ? now : A.pages, bar);
+        }
+        __syncwarp();
+        if (look) {
+          ok = warp_wait(land, (uint32_t)(marked++) & 1u);
+          __syncwarp();
+          if (!ok) break;
+          hand_on(j);
+        }
+      }
+      if (!ok) flag_error(A.err, kErrTimeout);
+    }
+    for (int j = 0; j < (TMA ? 0 : tiles); ++j) {
+      const int sl = j % NS;
+      bool behind = j > 0;                         // tile j - 1 is not handed on yet
+      __syncwarp();                                // off[j & 1] is written
+      if (j >= NS) {
+        const uint32_t parity = (uint32_t)((j / NS) - 1) & 1u;
+        if (!__all_sync(0xffffffffu, mbar_test(&empty[sl], parity))) {
+          cp_async_wait<0>();                      // the slot may need tile j - 1
+          hand_on(j - 1);
+          behind = false;
+          ok = warp_wait(&empty[sl], parity);
+          if (!ok) break;
+        }
+      }
+      if (!is_k) {
+        s_nonfin[sl][lane] = s_nonfin[sl][32 + lane] = 0;
+        if (lane == 0) s_any[sl] = 0;
+        __syncwarp();
+      }
+      unsigned char *to = slots + (size_t)sl * Lc::KV + (c >> 3) * (kTile * 128);
+#pragma unroll
+      for (int i0 = 0; i0 < ROWS; i0 += 16) {
+        int64_t o[16];                             // read ahead: a copy is a barrier to the compiler
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = off[j & 1][r0 + (i0 + i) * RP];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = r0 + (i0 + i) * RP;
+          const bool in = o[i] >= 0 && col;
+          cp_async16(to + r * 128 + (((c & 7) ^ (r & 7)) << 4), in ? base + o[i] + c * 8 : base, in ? 16u : 0u);
+        }
+      }
+      cp_async_commit();
+      if (j == 0) {
+        offsets(1);
+        cp_async_wait<1>();
+        fence_proxy_async_smem();
+        mbar_arrive(bq);
+      } else {
+        if (behind) {
+          cp_async_wait<1>();
+          hand_on(j - 1);
+        }
+        offsets(j + 1);
+      }
+    }
+    if (!TMA) {
+      cp_async_wait<0>();                          // nothing lands in shared memory that is given back
+      if (ok) hand_on(tiles - 1);
+      else flag_error(A.err, kErrTimeout);
+    }
+  } else if (warp == 6) {
+    // ------------------------------------------------------------------- MMA --
+    if (lane == 0) {
+      constexpr uint32_t id_s = umma_idesc_f16(128, kTile, 0, 0), id_o = umma_idesc_f16(128, DP, 0, 1);
+      const uint64_t dq = umma_desc(sq, 16, 1024, kSwz128), dk = umma_desc(sk, 16, 1024, kSwz128);
+      // 16 keys of V: two groups of 8 rows (1024 apart), 64-column atoms a slot's half apart
+      const uint64_t dv = umma_desc(sv, kTile * 128, 1024, kSwz128);
+      bool ok = mbar_wait(bq, 0, kTcWaitNs);
+      auto pv = [&](int i) {
+        const int sl = i % NS;
+        if (!mbar_wait(&bp[i & 1], (uint32_t)(i >> 1) & 1u, kTcWaitNs)) return false;
+        if (!mbar_wait(&full_v[sl], (uint32_t)(i / NS) & 1u, kTcWaitNs)) return false;
+        tc_fence_after();
+        const uint64_t d = dv + (uint64_t)(sl * (Lc::KV >> 4));
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          umma_f16_ta(tbase, tbase + 128 + 64 * (i & 1) + 8 * k, d + k * (2048 >> 4), id_o, 1);
+        umma_commit(&empty_v[sl]);
+        umma_commit(&bo[i & 1]);
+        return true;
+      };
+      for (int j = 0; j < tiles && ok; ++j) {
+        const int sl = j % NS;
+        if (!(ok = mbar_wait(&full_k[sl], (uint32_t)(j / NS) & 1u, kTcWaitNs))) break;
+        tc_fence_after();
+        const uint64_t d = dk + (uint64_t)(sl * (Lc::KV >> 4));
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)
+          umma_f16(tbase + 128 + 64 * (j & 1), dq + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16,
+                   d + ((k >> 2) * (kTile * 128) + (k & 3) * 32) / 16, id_s, k != 0);
+        umma_commit(&empty_k[sl]);
+        umma_commit(&bs[j & 1]);
+        mbar_arrive(&bs[j & 1]);                   // passes on what the copying threads have written
+        if (j > 0) ok = pv(j - 1);
+      }
+      if (ok) ok = pv(tiles - 1);
+      if (!ok) flag_error(A.err, kErrTimeout);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax --
+    const int m = row0 + tid;
+    const bool live = m < rows;
+    const int tok = t0 + (live ? m / A.grp : 0);
+    // drafted tokens that the row sees, by their place in the request
+    const uint32_t see = live ? ((uint32_t)__ldg(A.anc + tok) >> t0) & (n >= 32 ? 0xffffffffu : (1u << n) - 1u) : 0u;
+    const uint32_t tl = tbase + ((uint32_t)(32 * warp) << 16);
+    {
+      float zero[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) zero[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < DP; c += 16) tmem_st16(tl + c, zero);
+      tmem_wait_st();
+    }
+    float ref = 0.f, sum = 0.f;
+    bool any = false, ok = true;                   // a key seen so far
+    for (int j = 0; j < tiles; ++j) {
+      const uint32_t sc = tl + 128 + 64 * (j & 1);
+      const int pos0 = (kt0 + j) * kTile, sl = j % NS;
+      ok = warp_wait(&bs[j & 1], (uint32_t)(j >> 1) & 1u);
+      if (ok && pos0 + kTile > len) ok = warp_wait(&full_v[sl], (uint32_t)(j / NS) & 1u);   // the marks of its values
+      if (!ok) break;
+      tc_fence_after();
+      __syncwarp();                                // tensor-memory accesses are warp-synchronous
+      // which of the tile's keys the row sees
+      uint64_t sees = (uint64_t)s_valid[j & 7][0] | (uint64_t)s_valid[j & 7][1] << 32;
+      const int d = len - pos0;                    // keys of the tile in front of the drafted ones
+      if (d < kTile) {
+        uint64_t w = 0;
+        if (d > 0) w = ((uint64_t)1 << d) - 1 | (uint64_t)see << d;
+        else if (d > -32) w = (uint64_t)(see >> -d);
+        sees &= w;
+      }
+      float top = -INFINITY;
+      const bool all = __all_sync(0xffffffffu, sees == ~(uint64_t)0);
+      float z[kTile];
+      tmem_ld64(sc, z);
+      if (!all) {
+#pragma unroll
+        for (int i = 0; i < kTile; ++i) z[i] = (sees >> i) & 1 ? z[i] * A.scale : -INFINITY;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kTile; ++i) z[i] *= A.scale;
+      }
+#pragma unroll
+      for (int i = 0; i < kTile; ++i) top = fmaxf(top, z[i]);
+      // a new reference for the warp's rows where some row needs one
+      const bool grow = top != -INFINITY && (!any || top > ref + 8.f);
+      const bool redo = __any_sync(0xffffffffu, grow);
+      const bool extra = d < kTile && s_any[sl];
+      if ((redo || extra) && j > 0) {              // O must rest: the product of the last tile is done
+        ok = warp_wait(&bo[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+        __syncwarp();
+      }
+      if (redo) {
+        const float now = grow ? top : ref;
+        const float f = any ? exp2_fast(ref - now) : 0.f;
+        if (j > 0) {
+#pragma unroll
+          for (int c = 0; c < DP; c += 16) {
+            float o[16];
+            tmem_ld16w(tl + c, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = any ? o[i] * f : 0.f;
+            tmem_st16(tl + c, o);
+          }
+          tmem_wait_st();
+        }
+        sum = any ? sum * f : 0.f;
+        ref = now;
+      }
+      any |= top != -INFINITY;
+      if (extra) {
+        // the chunks of v left out, for the rows that see their keys
+#pragma unroll 1
+        for (int i = max(0, d); i < kTile && pos0 + i < L; ++i) {
+          const uint32_t bad = s_nonfin[sl][i];
+          if (!bad) continue;                      // the same for every lane
+          const int pos = pos0 + i, pi = pos / A.page, id = __ldg(A.table + (int64_t)req * A.max_pages + pi);
+          const __half *v = A.v + (int64_t)id * A.page_stride + (int64_t)(pos - pi * A.page) * A.token_stride +
+                            (int64_t)head * A.head_stride;
+          const bool on = (sees >> i) & 1;
+          const float w = exp2_fast(tmem_ld1(sc + i) * A.scale - ref);
+#pragma unroll 1
+          for (int h = 0; h < CH; h += 2) {
+            if (!((bad >> h) & 3u)) continue;
+            float o[16];
+            __syncwarp();
+            tmem_ld16w(tl + 8 * h, o);
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              if (on && ((bad >> (h + (q >> 3))) & 1u)) o[q] = fmaf(w, __half2float(__ldg(v + 8 * h + q)), o[q]);
+            __syncwarp();
+            tmem_st16(tl + 8 * h, o);
+            tmem_wait_st();
+          }
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int i = 0; i < kTile; ++i) {
+        z[i] = exp2_fast(z[i] - ref);
+        sum += z[i];
+      }
+#pragma unroll
+      for (int c = 0; c < kTile; c += 16) {        // over scores that are in registers
+        uint32_t p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = pack_h2(z[c + 2 * i], z[c + 2 * i + 1]);
+        tmem_st8(sc + c / 2, p);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bp[j & 1]);
+    }
+    if (ok) {
+      ok = warp_wait(&bo[(tiles - 1) & 1], (uint32_t)((tiles - 1) >> 1) & 1u);
+      tc_fence_after();
+    }
+    if (!ok && lane == 0) flag_error(A.err, kErrTimeout);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;                      // nothing seen: zeros
+    const int64_t at = (int64_t)blockIdx.x * MT + tid;
+    if (splits > 1 && live) __stcg(A.ml + at, make_float2(any ? ref : -INFINITY, sum));
+    __half *op = A.o + ((int64_t)tok * A.hkv * A.grp + head * A.grp + (live ? m % A.grp : 0)) * A.D;
+#pragma unroll
+    for (int c = 0; c < DP; c += 16) {
+      float o[16];
+      __syncwarp();
+      tmem_ld16w(tl + c, o);
+      if (live && splits == 1) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (c + 8 * h < A.D) {
+            uint4 u;
+            u.x = pack_h2(o[8 * h] * inv, o[8 * h + 1] * inv);
+            u.y = pack_h2(o[8 * h + 2] * inv, o[8 * h + 3] * inv);
+            u.z = pack_h2(o[8 * h + 4] * inv, o[8 * h + 5] * inv);
+            u.w = pack_h2(o[8 * h + 6] * inv, o[8 * h + 7] * inv);
+            *reinterpret_cast<uint4 *>(op + c + 8 * h) = u;
+          }
+      } else if (live) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          __stcg(reinterpret_cast<float4 *>(A.part + at * DP + c) + q, make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 6) {
+    tc_fence_after();
+    tmem_dealloc(tbase, Lc::COLS);
+  }
+}
+
 // The splits of a row, in order: one warp per (token, query head).
 template <int DP>
 __global__ void __launch_bounds__(128) k_tree_merge(AttnArgs A, int MT) {
@@ -586,7 +1185,7 @@ asf_status check_tables(const int32_t *table, int max_pages, int page, const int
 // are shared out evenly (any number is right, the rest become row tiles).
 int row_groups(int grp, int R, int T) {
   const int rows = (T + R - 1) / R * grp;
-  return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8;
+  return rows <= 16 ? 1 : rows <= 32 ? 2 : 8;
 }
 int row_tiles_most(int grp, int R, int T, int wm) { return T * grp / (16 * wm) + R; }
 int attn_dp(const asf_kv_cache *c) { return c->head_dim <= 64 ? 64 : 128; }
@@ -606,12 +1205,38 @@ cudaError_t run_attn(const AttnArgs &a, int units, cudaStream_t st) {
   const size_t smem = (size_t)kStages * 2 * kTile * DP * 2;
   return launch(k_tree_attn<DP, WM>, dim3(units), dim3(NW * 32), smem, st, a);
 }
+// Map of a cache's keys or values: columns, tokens of a page, heads, pages; a
+// box is `box` tokens of one head and page by 64 columns, swizzled as the MMA
+// reads it.  Columns past head_dim and pages past the last read as zeros.
+bool cache_map(CUtensorMap *tm, const void *base, const AttnArgs &a) {
+  TmapEncodeFn enc = tmap_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.page, (cuuint64_t)a.hkv, (cuuint64_t)a.pages};
+  // the stride of a dimension of one is never used, but has to be legal
+  const cuuint64_t strides[3] = {(cuuint64_t)a.token_stride * 2, (cuuint64_t)std::max<int64_t>(a.head_stride, 8) * 2,
+                                 (cuuint64_t)std::max<int64_t>(a.page_stride, 8) * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)a.box, 1, 1}, one[4] = {1, 1, 1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP>
+cudaError_t run_tc(AttnArgs a, int units, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  std::memset(&mk, 0, sizeof(mk));
+  std::memset(&mv, 0, sizeof(mv));
+  a.box = a.page >= kTile ? (a.page % kTile ? 0 : kTile) : a.page >= 8 && kTile % a.page == 0 ? a.page : 0;
+  if (a.box && cache_map(&mk, a.k, a) && cache_map(&mv, a.v, a))
+    return launch(k_tree_tc<DP, true>, dim3(units), dim3(kTcThreads), TreeTc<DP>::SMEM, st, mk, mv, a);
+  return launch(k_tree_tc<DP, false>, dim3(units), dim3(kTcThreads), TreeTc<DP>::SMEM, st, mk, mv, a);
+}
+
 template <int DP>
 cudaError_t run_attn_any(const AttnArgs &a, int wm, int units, cudaStream_t st) {
-  cudaError_t e = wm == 1   ? run_attn<DP, 1>(a, units, st)
-                  : wm == 2 ? run_attn<DP, 2>(a, units, st)
-                  : wm == 4 ? run_attn<DP, 4>(a, units, st)
-                            : run_attn<DP, 8>(a, units, st);
+  const cudaError_t e = wm == 1   ? run_attn<DP, 1>(a, units, st)
+                        : wm == 2 ? run_attn<DP, 2>(a, units, st)
+                                  : run_tc<DP>(a, units, st);
   if (e != cudaSuccess) return e;
   if ((int64_t)a.max_pages * a.page <= kWhole * kTile) return e;
   const int rows = a.T * a.hkv * a.grp;

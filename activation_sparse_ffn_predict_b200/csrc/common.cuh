@@ -228,6 +228,14 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int x, 
       "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
+// The same of a 4-D map.
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+          "r"(smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
 // Four rows (y0..y3, any order) of a map whose box is one row high, columns
 // x.. of the box width, written as four consecutive box rows at dst (the
 // swizzle follows the shared-memory address).

@@ -2,6 +2,7 @@
 // kernel goes through, the device's SM count, and the argument checks.
 #pragma once
 
+#include <cuda.h>            // CUtensorMap and its encoder's types (the encoder comes from the runtime)
 #include <cuda_runtime.h>
 
 #include <cstring>
@@ -68,5 +69,22 @@ inline asf_status check_ws(void *ws, size_t ws_bytes, size_t need) {
 }
 
 inline asf_status cuda_status(cudaError_t e) { return e == cudaSuccess ? ASF_OK : ASF_ERR_CUDA; }
+
+// cuTensorMapEncodeTiled, from the driver through the runtime (no link to the
+// driver library).
+using TmapEncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline TmapEncodeFn tmap_encoder() {
+  static TmapEncodeFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return (TmapEncodeFn) nullptr;
+    return reinterpret_cast<TmapEncodeFn>(p);
+  }();
+  return fn;
+}
 
 }  // namespace asf

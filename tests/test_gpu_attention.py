@@ -89,7 +89,10 @@ class Case:
     ([3000, 1, 0, 2047, 2048], [8, 8, 8, 4, 4], dict(hkv=4, grp=4, D=128)),
     ([5000], [32], dict(hkv=1, grp=16, D=96, page=256)), ([12345], [1], dict(hkv=3, grp=7, D=72, page=7)),
     (list(range(0, 640, 20)), [1] * 32, dict(hkv=2, grp=1, D=128)),
-    ([20000], [2], dict(hkv=1, grp=4, D=128, page=33)), ([300, 400, 500], [0, 5, 0], dict(D=40))])
+    ([20000], [2], dict(hkv=1, grp=4, D=128, page=33)), ([9000], [3], dict(hkv=2, grp=11, D=64)),
+    ([4000, 100, 0], [16, 8, 8], dict(hkv=2, grp=128, D=80, page=48)), ([1], [32], dict(hkv=1, grp=71, D=64)),
+    ([777, 3], [5, 6], dict(grp=16, D=128, page=8)), ([2000], [9], dict(grp=8, D=56, page=128)),
+    ([640], [8], dict(hkv=1, grp=9, D=128, page=640)), ([300, 400, 500], [0, 5, 0], dict(D=40))])
 def test_against_the_definition(lens, toks, kw):
     c = Case(lens, toks, seed=sum(lens) + len(toks), **kw)
     d = c.run()
@@ -100,14 +103,16 @@ def test_against_the_definition(lens, toks, kw):
     assert torch.equal(d["o"], first)                       # no order depends on timing
 
 
-def test_large_scores_and_scale():
-    c = Case([700], [4], D=64, spread=40.0, seed=3)         # one key takes nearly all of the weight
+@pytest.mark.parametrize("grp,D", [(2, 64), (8, 64), (16, 64), (40, 128)])
+def test_large_scores_and_scale(grp, D):
+    c = Case([700], [4], grp=grp, D=D, spread=40.0, seed=3)  # one key takes nearly all of the weight
     c.check(c.run(scale=0.5), scale=0.5)
     c.check(c.run(scale=-0.25), scale=-0.25)
 
 
-def test_rows_that_see_nothing_and_rows_behind():
-    c = Case([0, 40], [6, 5], grp=3, seed=4)
+@pytest.mark.parametrize("grp", [3, 12])
+def test_rows_that_see_nothing_and_rows_behind(grp):
+    c = Case([0, 40], [6, 5], grp=grp, seed=4)
     c.anc[2] = 0                                            # no prefix and no own bit
     c.anc[8] = 0                                            # only the prefix
     c.anc[1] |= 1 << 9                                      # a bit of another request: not its token
@@ -119,7 +124,7 @@ def test_rows_that_see_nothing_and_rows_behind():
         d[n] = torch.cat([d[n], torch.full((4,) + d[n].shape[1:], 9.0, dtype=torch.float16, device="cuda")])
     d["anc"] = torch.cat([d["anc"], torch.full((4,), -1, dtype=torch.int32, device="cuda")])
     d["o"] = torch.full_like(d["q"], 7.0)
-    d["ws"] = A.Workspace.for_attention(d["cache"], 6, 2, 15)
+    d["ws"] = A.Workspace.for_attention(d["cache"], 2 * grp, 2, 15)
     c.run(d)
     assert (d["o"][11:] == 7.0).all()                       # tokens behind the last request
     assert (d["o"][2] == 0).all() and (d["o"][4] == 0).all()
@@ -129,17 +134,19 @@ def test_rows_that_see_nothing_and_rows_behind():
     c.check(d)
 
 
-@pytest.mark.parametrize("n", [0, 50, 61])
-def test_what_a_row_does_not_see_does_not_reach_it(n):
+@pytest.mark.parametrize("grp,D", [(1, 64), (4, 64), (8, 64), (9, 128)])
+@pytest.mark.parametrize("page", [16, 20, 64])
+@pytest.mark.parametrize("n", [0, 50, 61, 700])
+def test_what_a_row_does_not_see_does_not_reach_it(n, grp, D, page):
     """NaN and infinities in drafted tokens' keys and values, and behind the last key."""
-    c = Case([n], [8], grp=4, seed=n)
+    c = Case([n], [8], grp=grp, D=D, page=page, seed=n)
     c.anc[:] = [1, 3, 5, 9, 19, 32, 64, 128]
     for t, val in ((5, np.nan), (6, np.inf), (7, -np.inf)):
         c.kn[t], c.vn[t] = val, val
     c.vn[4, 0, 3] = np.nan
-    behind = (c.table[0][(n + 8) // 16] if (n + 8) // 16 < c.table.shape[1] else None, (n + 8) % 16)
-    if behind[0] is not None and behind[1]:
-        c.k[behind], c.v[behind] = np.nan, np.nan
+    if (n + 8) % page:                                      # the rest of the last page
+        c.k[c.table[0][(n + 8) // page], (n + 8) % page:] = np.nan
+        c.v[c.table[0][(n + 8) // page], (n + 8) % page:] = np.inf
     d = c.run()
     got = d["o"].cpu().numpy()
     k, v = c.k.copy(), c.v.copy()
@@ -147,12 +154,13 @@ def test_what_a_row_does_not_see_does_not_reach_it(n):
     o, _, _ = O.tree_attention(k[..., :], v, c.table, c.lens, c.begin, c.q, np.where(np.arange(8) < 4, c.anc, 1), c.D ** -0.5)
     assert np.isfinite(got[:4]).all() and np.allclose(got[:4], o[:4], rtol=4e-3, atol=4e-3)
     assert np.isnan(got[5:]).all()                          # rows that see them
-    assert np.isnan(got[4, :4, 3]).all() and np.isfinite(got[4, 4:]).all()
+    assert np.isnan(got[4, :grp, 3]).all() and np.isfinite(got[4, grp:]).all()
 
 
-def test_strided_caches():
+@pytest.mark.parametrize("grp,D", [(2, 64), (16, 64), (12, 104)])
+def test_strided_caches(grp, D):
     """Pages laid out head by head, and keys and values side by side in one tensor."""
-    c = Case([200, 30], [3, 4], hkv=4, D=64, seed=6)
+    c = Case([200, 30], [3, 4], hkv=4, grp=grp, D=D, seed=6)
     for make in (lambda a: torch.from_numpy(a).cuda().permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3), None):
         d = c.device()
         if make is not None:
@@ -163,11 +171,12 @@ def test_strided_caches():
         c.check(c.run(d))
 
 
-def test_offsets_past_32_bits():
+@pytest.mark.parametrize("grp", [2, 40])
+def test_offsets_past_32_bits(grp):
     page, D, pages = 64, 128, 2 ** 31 // (64 * 128) + 3     # elements behind 2^31
     k = torch.zeros(pages, page, 1, D, dtype=torch.float16, device="cuda")
     v = torch.zeros_like(k)
-    c = Case([100], [2], hkv=1, grp=2, D=D, page=page, seed=8)
+    c = Case([100], [2], hkv=1, grp=grp, D=D, page=page, seed=8)
     where = torch.tensor([pages - 1, pages - 3, 0, 1], device="cuda")
     c.table = c.table * 0 + np.arange(c.table.shape[1])
     k[where[:2]], v[where[:2]] = torch.from_numpy(c.k[:2]).cuda(), torch.from_numpy(c.v[:2]).cuda()
@@ -180,8 +189,9 @@ def test_offsets_past_32_bits():
     c.check(d)
 
 
-def test_bad_tables_are_flagged_and_skipped():
-    c = Case([40, 30], [2, 3], seed=9)
+@pytest.mark.parametrize("grp", [2, 30])
+def test_bad_tables_are_flagged_and_skipped(grp):
+    c = Case([40, 30], [2, 3], grp=grp, seed=9)
     d = c.device()
     d["table"][0, 1] = c.k.shape[0] + 5                     # positions 16..31 of request 0
     d["table"][1, 0] = -1
@@ -189,7 +199,7 @@ def test_bad_tables_are_flagged_and_skipped():
     assert A.asf_read_error(d["ws"]) == L.ASF_ERR_DEVICE_INDEX
     o = d["o"].clone()
     # the same with those keys masked by hand: request 0 without 16 keys, request 1 without its first 16
-    short = Case([40, 30], [2, 3], seed=9)
+    short = Case([40, 30], [2, 3], grp=grp, seed=9)
     keep = [np.r_[0:16, 32:40], np.r_[16:30]]
     ks, vs = c.k.copy(), c.v.copy()
     O.append(ks, vs, c.table, c.lens, c.begin, c.kn, c.vn)
@@ -208,7 +218,7 @@ def test_bad_tables_are_flagged_and_skipped():
         d["lens"], d["begin"] = (torch.tensor(x, dtype=torch.int64).int().cuda() for x in (lens, begin))
         c.run(d)
         assert A.asf_read_error(d["ws"]) == L.ASF_ERR_DEVICE_INDEX
-    c2 = Case([40, 30], [2, 3], seed=9)
+    c2 = Case([40, 30], [2, 3], grp=grp, seed=9)
     c2.check(c2.run())                                      # and the next call is sound
 
 
@@ -224,8 +234,9 @@ def test_accepted_tokens_are_appended_again():
     assert np.array_equal(got[pg[37:], sl[37:]], c.kn[keep])
 
 
-def test_graph_replays_with_other_lengths():
-    c = Case([900, 0], [4, 4], seed=11)
+@pytest.mark.parametrize("grp", [2, 20])
+def test_graph_replays_with_other_lengths(grp):
+    c = Case([900, 0], [4, 4], grp=grp, seed=11)
     d = c.device()
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
