@@ -478,12 +478,12 @@ __global__ void __launch_bounds__((WM > 4 ? WM : 4) * 32, attn_resident(DP, WM))
 // ------------------------------------------- many rows: tcgen05 ----------
 // For tiles of more than 32 query rows mma.sync's rate (a quarter of
 // tcgen05's) bounds the kernel above, not HBM.  Here a CTA takes 128 rows:
-//   warps 4, 5 copy Q once, then tiles of 64 keys (warp 4) and of their values
-//              (warp 5), into the 128-byte swizzled layout that the MMA reads;
+//   warps 4, 5 copy tiles of 64 keys (warp 4) and of their values (warp 5) into
+//              the 128-byte swizzled layout that the MMA reads;
 //   warp 6     one thread issues S = Q K^T (M 128, N 64) into one of two
 //              accumulators in tensor memory, and O += P V with P read from
 //              tensor memory (V as it lies: keys are its K, so it is MN-major);
-//   warps 0-3  a thread per row reads S, masks it, takes the running maximum
+//   warps 0-3  a thread per row copies its row of Q, then per tile reads S, masks it, takes the running maximum
 //              and sum, and writes P in fp16 over the accumulator it has read.
 // S of the next tile is computed while this one's weights are, and keys and
 // values have slots of their own: the keys' are free as soon as S is there, so
@@ -635,9 +635,17 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       mbar_init(&bp[i], 4 * 32);
       mbar_init(&bo[i], 1);
     }
-    mbar_init(bq, 64);
+    mbar_init(bq, 128);
     mbar_init(land, 1);
     fence_mbar_init();
+    if (TMA) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+    }
+  }
+  if (warp == 6) {
+    tmem_alloc(tslot, Lc::COLS);
+    tmem_relinquish();
   }
   pdl_wait();
   pdl_trigger();
@@ -664,17 +672,15 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       s_unit[9] = q.splits;
     }
   }
-  __syncthreads();
-  const int req = s_unit[0];
-  if (req < 0) return;
-  if (warp == 6) {
-    tmem_alloc(tslot, Lc::COLS);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tslot;
+  const int req = s_unit[0];
+  if (req < 0) {
+    if (warp == 6) tmem_dealloc(tbase, Lc::COLS);
+    return;
+  }
   const int head = s_unit[1], row0 = s_unit[2] * MT, kt0 = s_unit[3], tiles = s_unit[4] - kt0;
   const int t0 = s_unit[5], n = s_unit[6], len = s_unit[7], L = s_unit[8], splits = s_unit[9];
   const int rows = n * A.grp;
@@ -710,16 +716,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const int r0 = lane / CH, c = lane % CH;
     const bool col = c * 8 < A.D;
     offsets(0);
-    // half of Q each; rows past the request's as zeros
-#pragma unroll 8
-    for (int i = 0; i < 64 / RP; ++i) {
-      const int r = (warp - 4) * 64 + r0 + i * RP, m = row0 + r;
-      const bool in = m < rows && col;
-      const __half *src = A.q;
-      if (in) src += ((int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp) * A.D + c * 8;
-      cp_async16(sq + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), src, in ? 16u : 0u);
-    }
-    cp_async_commit();
     // tile j has landed; drafted values are looked over first
     auto hand_on = [&](int j) {
       const int sl = j % NS, pos0 = (kt0 + j) * kTile;
@@ -770,9 +766,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         return id;
       };
       int tok, id = page_of(0, tok);
-      cp_async_wait<0>();
-      fence_proxy_async_smem();
-      mbar_arrive(bq);
       const uint32_t bytes = kTile * DP * 2;
       for (int j = 0; j < tiles; ++j) {
         const int sl = j % NS, pos0 = (kt0 + j) * kTile;
@@ -853,18 +846,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
       }
       cp_async_commit();
-      if (j == 0) {
-        offsets(1);
+      if (behind) {
         cp_async_wait<1>();
-        fence_proxy_async_smem();
-        mbar_arrive(bq);
-      } else {
-        if (behind) {
-          cp_async_wait<1>();
-          hand_on(j - 1);
-        }
-        offsets(j + 1);
+        hand_on(j - 1);
       }
+      offsets(j + 1);
     }
     if (!TMA) {
       cp_async_wait<0>();                          // nothing lands in shared memory that is given back
@@ -919,12 +905,22 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const uint32_t see = live ? ((uint32_t)__ldg(A.anc + tok) >> t0) & (n >= 32 ? 0xffffffffu : (1u << n) - 1u) : 0u;
     const uint32_t tl = tbase + ((uint32_t)(32 * warp) << 16);
     {
+      // the row of Q; a row past the request's is zeros
+      const __half *src = live ? A.q + ((int64_t)tok * A.hkv * A.grp + head * A.grp + m % A.grp) * A.D : A.q;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        cp_async16(sq + (c >> 3) * (128 * 128) + tid * 128 + (((c & 7) ^ (tid & 7)) << 4), live && c * 8 < A.D ? src + c * 8 : A.q,
+                   live && c * 8 < A.D ? 16u : 0u);
+      cp_async_commit();
       float zero[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) zero[i] = 0.f;
 #pragma unroll
       for (int c = 0; c < DP; c += 16) tmem_st16(tl + c, zero);
       tmem_wait_st();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      mbar_arrive(bq);
     }
     float ref = 0.f, sum = 0.f;
     bool any = false, ok = true;                   // a key seen so far
