@@ -505,49 +505,6 @@ struct TreeTc {
 constexpr int kTcThreads = 7 * 32;
 constexpr uint64_t kTcWaitNs = 200ull * 1000 * 1000;   // bound on any mbarrier wait
 
-// Whether a phase is over, without waiting (try_wait sleeps for microseconds).
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// The bounded wait for a whole warp: one lane polls, and looks at the clock
-// only now and then (the timer is read over the chip, not on the SM).
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) {
-    uint64_t t0 = 0;
-    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
-      if ((i & 63u) == 0) {
-        const uint64_t now = global_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > kTcWaitNs) {
-          ok = false;
-          break;
-        }
-      }
-  }
-  return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-}
-
-__device__ __forceinline__ unsigned char *align_1024(unsigned char *p) {
-  const uint32_t a = smem_u32(p);
-  return p + (((a + 1023u) & ~1023u) - a);
-}
-// D (tensor memory) += A (tensor memory, fp16 pairs) B (shared memory)
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accum)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -560,45 +517,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
       "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
       : "memory");
 }
-// 16 or 64 columns of this thread's lane, and the wait that makes them usable:
-// in one statement, so that no use can slip between the two.
-__device__ __forceinline__ void tmem_ld16w(uint32_t taddr, float (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
-  float v;
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v)
-      : "r"(taddr)
-      : "memory");
-  return v;
-}
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]),
-        "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]),
-        "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]),
-        "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]),
-        "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 //
 // Copies: where a tile is whole pages or lies in one (pages of 8, 16, 32 or a
@@ -639,8 +557,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     mbar_init(land, 1);
     fence_mbar_init();
     if (TMA) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+      prefetch_map(&map_k);
+      prefetch_map(&map_v);
     }
   }
   if (warp == 6) {
@@ -772,10 +690,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const int now = id, at = tok;
         id = page_of(j + 1, tok);
         if (j >= NS) {
-          ok = warp_wait(&empty[sl], (uint32_t)((j / NS) - 1) & 1u);
+          ok = warp_wait(&empty[sl], (uint32_t)((j / NS) - 1) & 1u, kTcWaitNs);
           if (!ok) {
             // what is on its way lands before the shared memory is given back
-            for (int e = j - NS; e < j; ++e) warp_wait(&full[e % NS], (uint32_t)(e / NS) & 1u);
+            for (int e = j - NS; e < j; ++e) warp_wait(&full[e % NS], (uint32_t)(e / NS) & 1u, kTcWaitNs);
             break;
           }
         }
@@ -805,7 +723,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
         __syncwarp();
         if (look) {
-          ok = warp_wait(land, (uint32_t)(marked++) & 1u);
+          ok = warp_wait(land, (uint32_t)(marked++) & 1u, kTcWaitNs);
           __syncwarp();
           if (!ok) break;
           hand_on(j);
@@ -823,7 +741,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           cp_async_wait<0>();                      // the slot may need tile j - 1
           hand_on(j - 1);
           behind = false;
-          ok = warp_wait(&empty[sl], parity);
+          ok = warp_wait(&empty[sl], parity, kTcWaitNs);
           if (!ok) break;
         }
       }
@@ -927,8 +845,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     for (int j = 0; j < tiles; ++j) {
       const uint32_t sc = tl + 128 + 64 * (j & 1);
       const int pos0 = (kt0 + j) * kTile, sl = j % NS;
-      ok = warp_wait(&bs[j & 1], (uint32_t)(j >> 1) & 1u);
-      if (ok && pos0 + kTile > len) ok = warp_wait(&full_v[sl], (uint32_t)(j / NS) & 1u);   // the marks of its values
+      ok = warp_wait(&bs[j & 1], (uint32_t)(j >> 1) & 1u, kTcWaitNs);
+      if (ok && pos0 + kTile > len) ok = warp_wait(&full_v[sl], (uint32_t)(j / NS) & 1u, kTcWaitNs);   // the marks of its values
       if (!ok) break;
       tc_fence_after();
       __syncwarp();                                // tensor-memory accesses are warp-synchronous
@@ -959,7 +877,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       const bool redo = __any_sync(0xffffffffu, grow);
       const bool extra = d < kTile && s_any[sl];
       if ((redo || extra) && j > 0) {              // O must rest: the product of the last tile is done
-        ok = warp_wait(&bo[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u);
+        ok = warp_wait(&bo[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u, kTcWaitNs);
         if (!ok) break;
         tc_fence_after();
         __syncwarp();
@@ -1026,7 +944,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       mbar_arrive(&bp[j & 1]);
     }
     if (ok) {
-      ok = warp_wait(&bo[(tiles - 1) & 1], (uint32_t)((tiles - 1) >> 1) & 1u);
+      ok = warp_wait(&bo[(tiles - 1) & 1], (uint32_t)((tiles - 1) >> 1) & 1u, kTcWaitNs);
       tc_fence_after();
     }
     if (!ok && lane == 0) flag_error(A.err, kErrTimeout);

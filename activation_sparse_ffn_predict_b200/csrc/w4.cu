@@ -15,6 +15,7 @@
 // other operand as it is; x in fp32 is the exact sum of three bf16 parts
 // (8 + 8 + 8 mantissa bits, by truncation), multiplied in three instructions
 // into the same accumulators.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -621,6 +622,332 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
   }
 }
 
+// ------------------------------------------------ fp16 x: tcgen05 -------
+// The dense product for fp16 x.  A row of the tile is a lane of tensor memory:
+// its thread reads the row's codes from shared memory, turns them into fp16
+// whole numbers and stores them to tensor memory as the MMA's A operand (M 128,
+// K 16); x is the B operand, N = 16 or 32 tokens.  What is left per weight is
+// the unpacking: nothing is read again for the tokens, and the products cost no
+// issue slots.  Each group's product has an accumulator of its own, which the
+// row's thread scales into its fp32 totals.
+//   warp 8      one lane loads stages of 256 weights of 128 rows, their scales
+//               and x's columns by TMA (rows and columns past the end as zeros)
+//   warps 0-3   unpack the first 128 weights of a stage, warps 4-7 the others;
+//               two A operands and (up to) two accumulators each, so that they
+//               unpack a block while the one before is multiplied
+//   warp 9      one thread issues the MMAs
+// The (row tile, stage) pairs are dealt out in one run of equal lengths per
+// CTA; tiles that fall to several CTAs meet in the workspace, where the one that
+// takes a tile's last ticket adds the parts in the order of the CTAs.
+constexpr int kTcStageK = 256;
+template <int N, int GS>
+struct MatTc {
+  static constexpr int W = 128 * kTcStageK / 2;
+  static constexpr int SC = 128 * 16;              // a 16-byte piece of each row's scales
+  static constexpr int X = N * kTcStageK * 2;
+  static constexpr int STAGE = W + SC + X;
+  static constexpr int NS = N == 16 ? 7 : 6;
+  static constexpr int BAR = 1024;
+  static constexpr int RED = 128 * (N + 1) * 4;
+  static constexpr size_t SMEM = 1024 + BAR + RED + 1024 + (size_t)NS * STAGE;
+  static constexpr int DB = (N << GS) <= 64 ? 2 : 1;           // accumulators of each half of the stage
+  static constexpr uint32_t COLS = 512;            // A: 2 x 2 x 64 columns, then D: 2 x DB x (N << GS)
+  static_assert(STAGE % 1024 == 0, "stages must keep the 1024-byte swizzle alignment");
+  static_assert(256 + 2 * DB * (N << GS) <= 512, "tensor memory");
+};
+constexpr int kMatTcThreads = 10 * 32;
+constexpr uint64_t kTcWaitNs = 200ull * 1000 * 1000;           // bound on any mbarrier wait
+
+struct MatTcArgs {
+  int rows, k, nst;            // weights [rows][k]; stages of a row
+  int B;
+  const float *bias;
+  int relu;
+  void *y;
+  int y16;
+  float *part;                 // [CTA][2][N][128]
+  Header *hdr;
+};
+
+// columns c .. c+31 of this lane
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+template <int N, int GS>
+__global__ void __launch_bounds__(kMatTcThreads, 1)
+    k_w4_matmul_tc(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_s,
+                   const __grid_constant__ CUtensorMap map_x, MatTcArgs A) {
+  using Lc = MatTc<N, GS>;
+  constexpr int NS = Lc::NS, DB = Lc::DB, DC = N << GS;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint32_t s_last;
+  unsigned char *smem = align_1024(smem_raw);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + NS;
+  uint64_t *a_full = empty + NS, *d_full = a_full + 4;         // [half][buffer]
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(d_full + 4);
+  float *red = reinterpret_cast<float *>(smem + Lc::BAR);      // [128][N + 1]
+  unsigned char *stages = align_1024(smem + Lc::BAR + Lc::RED);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 8 + 1);                 // the unpacking warps, and the products
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&a_full[i], 128);
+      mbar_init(&d_full[i], 1);
+    }
+    fence_mbar_init();
+    prefetch_map(&map_w);
+    prefetch_map(&map_s);
+    prefetch_map(&map_x);
+  }
+  if (warp == 9) {
+    tmem_alloc(tslot, Lc::COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tslot;
+  pdl_wait();
+  pdl_trigger();
+
+  const int tiles = ceil_div(A.rows, 128);
+  const int64_t total = (int64_t)tiles * A.nst;
+  const int G = (int)min((int64_t)gridDim.x, total);           // a stage at least for each CTA that takes part
+  auto start_of = [&](int c) { return total * min(c, G) / G; };
+  const int64_t u0 = start_of(blockIdx.x), u1 = start_of(blockIdx.x + 1);
+  const int n = (int)(u1 - u0);                    // this CTA's stages
+  int32_t *err = &A.hdr->err;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------------ loads --
+    if (lane == 0) {
+      int tile = (int)(u0 / A.nst), st = (int)(u0 % A.nst);
+      for (int i = 0; i < n; ++i) {
+        const int sl = i % NS;
+        if (i >= NS && !mbar_wait(&empty[sl], (uint32_t)((i / NS) - 1) & 1u, kTcWaitNs)) {
+          flag_error(err, kErrTimeout);
+          // what is on its way lands before the shared memory is given back
+          for (int e = i - NS; e < i; ++e) mbar_wait(&full[e % NS], (uint32_t)(e / NS) & 1u, kTcWaitNs);
+          break;
+        }
+        unsigned char *to = stages + (size_t)sl * Lc::STAGE;
+        mbar_arrive_expect_tx(&full[sl], Lc::STAGE);
+        tma_load_2d(to, &map_w, st * (kTcStageK / 2), tile * 128, &full[sl]);
+        tma_load_2d(to + Lc::W, &map_s, (st * (4 << GS)) & ~15, tile * 128, &full[sl]);
+#pragma unroll
+        for (int q = 0; q < kTcStageK / 64; ++q)
+          tma_load_2d(to + Lc::W + Lc::SC + q * (N * 128), &map_x, st * kTcStageK + 64 * q, 0, &full[sl]);
+        if (++st == A.nst) {
+          st = 0;
+          ++tile;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // -------------------------------------------------------------------- MMA --
+    if (lane == 0) {
+      constexpr uint32_t idesc = umma_idesc_f16(128, N, 0, 0);
+      const uint64_t dx = umma_desc(stages + Lc::W + Lc::SC, 16, 1024, kSwz128);
+      bool ok = true;
+      for (int i = 0; i < n && ok; ++i) {
+        const int sl = i % NS;
+        const uint64_t d = dx + (uint64_t)(sl * (Lc::STAGE >> 4));
+        ok = mbar_wait(&full[sl], (uint32_t)(i / NS) & 1u, kTcWaitNs);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (ok) ok = mbar_wait(&a_full[2 * e + (i & 1)], (uint32_t)(i >> 1) & 1u, kTcWaitNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = tbase + (2 * e + (i & 1)) * 64;
+          const uint32_t acc = tbase + 256 + (e * DB + i % DB) * DC;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)              // 16 weights; a group's first product starts its accumulator
+            umma_f16_ta(acc + (k >> (3 - GS)) * N, a + 8 * k, d + (uint64_t)((((2 * e + (k >> 2)) * (N * 128)) + (k & 3) * 32) >> 4),
+                        idesc, (k & ((8 >> GS) - 1)) != 0);
+          umma_commit(&d_full[2 * e + (i & 1)]);
+        }
+        if (ok) umma_commit(&empty[sl]);
+      }
+      if (!ok) flag_error(err, kErrTimeout);
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------------- unpack --
+    const int e = warp >> 2, row = tid & 127;
+    const uint32_t tl = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
+    float tot[N];
+#pragma unroll
+    for (int b = 0; b < N; ++b) tot[b] = 0.f;
+    uint32_t sc[2][2];                             // a block's scales, kept until its products are there
+    int tile = (int)(u0 / A.nst), st = (int)(u0 % A.nst);      // of the products taken next
+    const int first_tile = tile;
+    int here = st;                                 // stage within its row tile, of the one unpacked
+    bool ok = true;
+
+    // whole or partial sums of `tile` (its stages up to this CTA's last, from its first)
+    auto finish = [&](bool whole) {
+      if (e == 1) {
+        named_sync(3, 256);                        // the buffer is free
+#pragma unroll
+        for (int b = 0; b < N; ++b) red[row * (N + 1) + b] = tot[b];
+        named_arrive(2, 256);
+      } else {
+        named_arrive(3, 256);
+        named_sync(2, 256);
+#pragma unroll
+        for (int b = 0; b < N; ++b) tot[b] += red[row * (N + 1) + b];
+        bool mine = whole;
+        if (!whole) {
+          const int64_t t0 = (int64_t)tile * A.nst;
+          const int c0 = (int)(((t0 + 1) * G - 1) / total), c1 = (int)(((t0 + A.nst) * G - 1) / total);
+          float *to = A.part + ((int64_t)blockIdx.x * 2 + (tile != first_tile)) * (N * 128) + row;
+#pragma unroll
+          for (int b = 0; b < N; ++b)
+            if (b < A.B) __stcg(to + b * 128, tot[b]);
+          named_sync(4, 128);
+          if (tid == 0) s_last = ticket_acq_rel(&A.hdr->tile_done[c0]);
+          named_sync(4, 128);
+          mine = s_last == (uint32_t)(c1 - c0);
+          if (mine) {
+#pragma unroll
+            for (int b = 0; b < N; ++b) tot[b] = 0.f;
+            for (int c = c0; c <= c1; ++c) {
+              const float *from = A.part + ((int64_t)c * 2 + (start_of(c) / A.nst != tile)) * (N * 128) + row;
+#pragma unroll
+              for (int b = 0; b < N; ++b)
+                if (b < A.B) tot[b] += __ldcg(from + b * 128);
+            }
+            if (tid == 0) A.hdr->tile_done[c0] = 0;            // zero again for the next call
+          }
+        }
+        const int r = tile * 128 + row;
+        if (mine && r < A.rows) {
+          const float bias = A.bias ? __ldg(A.bias + r) : 0.f;
+#pragma unroll
+          for (int b = 0; b < N; ++b) {
+            float v = tot[b] + bias;
+            if (A.relu) v = v > 0.f ? v : (v != v ? v : 0.f);
+            if (b >= A.B) continue;
+            if (A.y16) static_cast<__half *>(A.y)[(int64_t)b * A.rows + r] = __float2half_rn(v);
+            else static_cast<float *>(A.y)[(int64_t)b * A.rows + r] = v;
+          }
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < N; ++b) tot[b] = 0.f;
+    };
+    int begun = st;                                // first stage of the tile in this CTA
+    // products of stage q: scaled into the totals
+    auto take = [&](int q) {
+      if (ok) ok = warp_wait(&d_full[2 * e + (q & 1)], (uint32_t)(q >> 1) & 1u, kTcWaitNs);
+      if (ok) {
+        tc_fence_after();
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < (1 << GS); ++g) {
+          const float s = half_of(q & 1 ? sc[1][g >> 1] : sc[0][g >> 1], g & 1);
+#pragma unroll
+          for (int c = 0; c < N; c += 16) {
+            if (c >= A.B) continue;
+            float v[16];
+            tmem_ld16w(tl + 256 + (e * DB + q % DB) * DC + g * N + c, v);
+#pragma unroll
+            for (int b = 0; b < 16; ++b) tot[c + b] = fmaf(s, v[b], tot[c + b]);
+          }
+        }
+        tc_fence_before();
+      }
+      if (++st == A.nst || q == n - 1) {
+        finish(begun == 0 && st == A.nst);
+        if (st == A.nst) {
+          st = 0;
+          ++tile;
+        }
+        begun = st;
+      }
+    };
+    for (int i = 0; i < n; ++i) {
+      const int sl = i % NS;
+      if (DB == 2 && i >= 2) take(i - 2);
+      if (ok) ok = warp_wait(&full[sl], (uint32_t)(i / NS) & 1u, kTcWaitNs);
+      if (ok) {
+        __syncwarp();
+        const unsigned char *w = stages + (size_t)sl * Lc::STAGE;
+        uint32_t word[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(w + row * 128 + (((4 * e + t) ^ (row & 7)) << 4));
+          word[t][0] = v.x;
+          word[t][1] = v.y;
+          word[t][2] = v.z;
+          word[t][3] = v.w;
+        }
+        // the 2 << GS bytes of this block in the 16-byte piece of its row
+        const unsigned char *ps = w + Lc::W + row * 16 + (((here * (4 << GS)) & 15) + e * (2 << GS));
+        uint32_t s0, s1 = 0;
+        if constexpr (GS == 0) {
+          s0 = *reinterpret_cast<const unsigned short *>(ps);
+        } else {
+          s0 = *reinterpret_cast<const uint32_t *>(ps);
+          if constexpr (GS == 2) s1 = *reinterpret_cast<const uint32_t *>(ps + 4);
+        }
+        if (i & 1) {
+          sc[1][0] = s0;
+          sc[1][1] = s1;
+        } else {
+          sc[0][0] = s0;
+          sc[0][1] = s1;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {              // weights 64 h .. 64 h + 63: words j = 2h, 2h + 1
+          uint32_t r[32];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              uint32_t p[4];
+              unpack8<false>(word[t][2 * h + j], p);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) r[16 * j + 4 * t + q] = p[q];
+            }
+          __syncwarp();
+          tmem_st32(tl + (2 * e + (i & 1)) * 64 + 32 * h, r);
+        }
+        tmem_wait_st();
+      }
+      if (DB == 1 && i >= 1) take(i - 1);          // its accumulator is the next one's too
+      if (ok) {
+        tc_fence_before();
+        mbar_arrive(&a_full[2 * e + (i & 1)]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[sl]);
+      }
+      if (++here == A.nst) here = 0;
+    }
+    if (DB == 2 && n >= 2) take(n - 2);
+    if (n >= 1) take(n - 1);
+    if (!ok && lane == 0) flag_error(err, kErrTimeout);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tbase, Lc::COLS);
+  }
+}
+
 // ---------------------------------------------------- down projection --
 // y[b][c] = sum_j a[j][b] s[j][c / group] (q[j][c] - 8): the neurons are the
 // contracted dimension, so the scale, which changes with the neuron, joins the
@@ -893,6 +1220,7 @@ int dot_most(int k, int group, int B, int parts) {
 size_t dot_part_bytes(int tiles, int k, int group, int B) {
   const int nsb = ceil_div(w4_kp(k), kSuper);
   const size_t forced = (size_t)tiles * ceil_div(nsb, dot_most(k, group, B, 3));
+  // (the tensor-memory product needs two parts of 16 or 32 x 512 bytes a CTA: less)
   return r256(std::max<size_t>((size_t)kPartsPerCta * dot_ctas(), 2 * forced) * nt_of(B) * 512);
 }
 int down_units(int d) { return ceil_div(w4_kp(d), kDownCols); }
@@ -924,6 +1252,48 @@ cudaError_t run_dot(DotArgs a, int group, asf_dtype xdtype, int mode, cudaStream
   }
 }
 
+// Byte map of `rows` rows `stride` apart, in boxes of cols x box_rows bytes.
+bool byte_map(CUtensorMap *tm, const void *base, int64_t width, int64_t rows, int64_t stride, int cols, int box_rows,
+              CUtensorMapSwizzle swz) {
+  TmapEncodeFn enc = tmap_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride};
+  const cuuint32_t box[2] = {(cuuint32_t)cols, (cuuint32_t)box_rows}, one[2] = {1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool x_map(CUtensorMap *tm, const void *x, int k, int B, int box_rows) {
+  TmapEncodeFn enc = tmap_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)B}, strides[1] = {(cuuint64_t)k * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(x), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int N>
+cudaError_t run_matmul_tc_n(const asf_w4_matrix *m, const CUtensorMap &w, const CUtensorMap &s, const CUtensorMap &x,
+                            const MatTcArgs &a, cudaStream_t st) {
+  const dim3 grid(dot_ctas()), block(kMatTcThreads);
+  return m->group == 128  ? launch(k_w4_matmul_tc<N, 0>, grid, block, MatTc<N, 0>::SMEM, st, w, s, x, a)
+         : m->group == 64 ? launch(k_w4_matmul_tc<N, 1>, grid, block, MatTc<N, 1>::SMEM, st, w, s, x, a)
+                          : launch(k_w4_matmul_tc<N, 2>, grid, block, MatTc<N, 2>::SMEM, st, w, s, x, a);
+}
+// false: no maps for these operands
+bool run_matmul_tc(const asf_w4_matrix *m, const void *x, MatTcArgs a, cudaStream_t st, cudaError_t &e) {
+  CUtensorMap mw, ms, mx;
+  const int N = a.B <= 16 ? 16 : 32, half = w4_kp(m->k) / 2;
+  a.nst = ceil_div(w4_kp(m->k), kTcStageK);
+  if (!byte_map(&mw, m->data, half, m->rows, m->row_stride, kTcStageK / 2, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !byte_map(&ms, static_cast<const unsigned char *>(m->data) + half, w4_scale_bytes(m->k, m->group), m->rows,
+                m->row_stride, 16, 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !x_map(&mx, x, m->k, a.B, N))
+    return false;
+  e = N == 16 ? run_matmul_tc_n<16>(m, mw, ms, mx, a, st) : run_matmul_tc_n<32>(m, mw, ms, mx, a, st);
+  return true;
+}
 template <int GS>
 cudaError_t run_down(const DownArgs &a, cudaStream_t st) {
   const dim3 grid(down_units(a.d) * a.R), block(kDownWarps * 32);
@@ -998,6 +1368,20 @@ asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dtype xdty
   if (!al16(x) || !al4(y) || !al4(bias)) return ASF_ERR_MISALIGNED;
   s = check_ws(ws, ws_bytes, kHeaderBytes + dot_part_bytes(ceil_div(mat->rows, 16), mat->k, mat->group, B));
   if (s != ASF_OK) return s;
+  if (xdtype == ASF_F16) {
+    MatTcArgs t{};
+    t.rows = mat->rows;
+    t.k = mat->k;
+    t.B = B;
+    t.bias = bias;
+    t.relu = relu;
+    t.y = y;
+    t.y16 = ydtype == ASF_F16;
+    t.part = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kHeaderBytes);
+    t.hdr = static_cast<Header *>(ws);
+    cudaError_t e = cudaSuccess;
+    if (run_matmul_tc(mat, x, t, (cudaStream_t)stream, e)) return cuda_status(e);
+  }
   DotArgs a{};
   a.data = static_cast<const unsigned char *>(mat->data);
   a.stride = mat->row_stride;
