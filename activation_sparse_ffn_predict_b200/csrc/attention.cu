@@ -777,43 +777,47 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     }
   } else if (warp == 6) {
     // ------------------------------------------------------------------- MMA --
-    if (lane == 0) {
-      constexpr uint32_t id_s = umma_idesc_f16(128, kTile, 0, 0), id_o = umma_idesc_f16(128, DP, 0, 1);
-      const uint64_t dq = umma_desc(sq, 16, 1024, kSwz128), dk = umma_desc(sk, 16, 1024, kSwz128);
-      // 16 keys of V: two groups of 8 rows (1024 apart), 64-column atoms a slot's half apart
-      const uint64_t dv = umma_desc(sv, kTile * 128, 1024, kSwz128);
-      bool ok = mbar_wait(bq, 0, kTcWaitNs);
-      auto pv = [&](int i) {
-        const int sl = i % NS;
-        if (!mbar_wait(&bp[i & 1], (uint32_t)(i >> 1) & 1u, kTcWaitNs)) return false;
-        if (!mbar_wait(&full_v[sl], (uint32_t)(i / NS) & 1u, kTcWaitNs)) return false;
-        tc_fence_after();
-        const uint64_t d = dv + (uint64_t)(sl * (Lc::KV >> 4));
+    constexpr uint32_t id_s = umma_idesc_f16(128, kTile, 0, 0), id_o = umma_idesc_f16(128, DP, 0, 1);
+    const uint64_t dq = umma_desc(sq, 16, 1024, kSwz128), dk = umma_desc(sk, 16, 1024, kSwz128);
+    // 16 keys of V: two groups of 8 rows (1024 apart), 64-column atoms half a slot apart
+    const uint64_t dv = umma_desc(sv, kTile * 128, 1024, kSwz128);
+    bool ok = warp_wait(bq, 0, kTcWaitNs);
+    auto pv = [&](int i) {
+      const int sl = i % NS;
+      if (!warp_wait(&bp[i & 1], (uint32_t)(i >> 1) & 1u, kTcWaitNs)) return false;
+      if (!warp_wait(&full_v[sl], (uint32_t)(i / NS) & 1u, kTcWaitNs)) return false;
+      tc_fence_after();
+      const uint64_t d = dv + (uint64_t)(sl * (Lc::KV >> 4));
+      const uint32_t p = tbase + 128 + 64 * (i & 1);
+      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          umma_f16_ta(tbase, tbase + 128 + 64 * (i & 1) + 8 * k, d + k * (2048 >> 4), id_o, 1);
+        for (int k = 0; k < kTile / 16; ++k) umma_f16_ta(tbase, p + 8 * k, d + k * (2048 >> 4), id_o, 1);
         umma_commit(&empty_v[sl]);
         umma_commit(&bo[i & 1]);
-        return true;
-      };
-      for (int j = 0; j < tiles && ok; ++j) {
-        const int sl = j % NS;
-        if (!(ok = mbar_wait(&full_k[sl], (uint32_t)(j / NS) & 1u, kTcWaitNs))) break;
-        tc_fence_after();
-        const uint64_t d = dk + (uint64_t)(sl * (Lc::KV >> 4));
+      }
+      __syncwarp();
+      return true;
+    };
+    for (int j = 0; j < tiles && ok; ++j) {
+      const int sl = j % NS;
+      if (!(ok = warp_wait(&full_k[sl], (uint32_t)(j / NS) & 1u, kTcWaitNs))) break;
+      tc_fence_after();
+      const uint64_t d = dk + (uint64_t)(sl * (Lc::KV >> 4));
+      const uint32_t z = tbase + 128 + 64 * (j & 1);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k)
-          umma_f16(tbase + 128 + 64 * (j & 1), dq + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16,
-                   d + ((k >> 2) * (kTile * 128) + (k & 3) * 32) / 16, id_s, k != 0);
+          umma_f16(z, dq + ((k >> 2) * (128 * 128) + (k & 3) * 32) / 16, d + ((k >> 2) * (kTile * 128) + (k & 3) * 32) / 16, id_s,
+                   k != 0);
         umma_commit(&empty_k[sl]);
         umma_commit(&bs[j & 1]);
-        mbar_arrive(&bs[j & 1]);                   // passes on what the copying threads have written
-        if (j > 0) ok = pv(j - 1);
       }
-      if (ok) ok = pv(tiles - 1);
-      if (!ok) flag_error(A.err, kErrTimeout);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bs[j & 1]);      // passes on what the copying threads have written
+      if (j > 0) ok = pv(j - 1);
     }
-    __syncwarp();
+    if (ok) ok = pv(tiles - 1);
+    if (!ok && lane == 0) flag_error(A.err, kErrTimeout);
   } else {
     // ---------------------------------------------------------------- softmax --
     const int m = row0 + tid;

@@ -331,28 +331,38 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// The bounded wait for a whole warp: one lane polls, and looks at the clock
-// only now and then (the timer is read over the chip, not on the SM).
+// The bounded wait for a whole warp, every lane polling; the clock is read now
+// and then only, since the timer is not on the SM.  One answer for the warp.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
     uint64_t t0 = 0;
-    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
+    for (uint32_t i = 1; !(ok = mbar_try_wait(bar, parity)); ++i)
       if ((i & 63u) == 0) {
         const uint64_t now = global_ns();
         if (t0 == 0) t0 = now;
-        if (now - t0 > limit_ns) {
-          ok = false;
-          break;
-        }
+        if (now - t0 > limit_ns) break;
       }
   }
-  return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+  return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ unsigned char *align_1024(unsigned char *p) {
   const uint32_t a = smem_u32(p);
   return p + (((a + 1023u) & ~1023u) - a);
+}
+// One lane of a converged warp.  Issue loops are run by the whole warp with this
+// around the instruction: under a branch on the lane index the operands of each
+// tcgen05.mma have to be moved to uniform registers one by one (80 cycles an
+// instruction instead of 30).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void prefetch_map(const void *tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");

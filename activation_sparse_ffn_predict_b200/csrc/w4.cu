@@ -757,32 +757,32 @@ __global__ void __launch_bounds__(kMatTcThreads, 1)
     __syncwarp();
   } else if (warp == 9) {
     // -------------------------------------------------------------------- MMA --
-    if (lane == 0) {
-      constexpr uint32_t idesc = umma_idesc_f16(128, N, 0, 0);
-      const uint64_t dx = umma_desc(stages + Lc::W + Lc::SC, 16, 1024, kSwz128);
-      bool ok = true;
-      for (int i = 0; i < n && ok; ++i) {
-        const int sl = i % NS;
-        const uint64_t d = dx + (uint64_t)(sl * (Lc::STAGE >> 4));
-        ok = mbar_wait(&full[sl], (uint32_t)(i / NS) & 1u, kTcWaitNs);
+    constexpr uint32_t idesc = umma_idesc_f16(128, N, 0, 0);
+    const uint64_t dx = umma_desc(stages + Lc::W + Lc::SC, 16, 1024, kSwz128);
+    bool ok = true;
+    for (int i = 0; i < n && ok; ++i) {
+      const int sl = i % NS;
+      const uint64_t d = dx + (uint64_t)(sl * (Lc::STAGE >> 4));
+      ok = warp_wait(&full[sl], (uint32_t)(i / NS) & 1u, kTcWaitNs);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (ok) ok = mbar_wait(&a_full[2 * e + (i & 1)], (uint32_t)(i >> 1) & 1u, kTcWaitNs);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = tbase + (2 * e + (i & 1)) * 64;
-          const uint32_t acc = tbase + 256 + (e * DB + i % DB) * DC;
+      for (int e = 0; e < 2; ++e) {
+        if (ok) ok = warp_wait(&a_full[2 * e + (i & 1)], (uint32_t)(i >> 1) & 1u, kTcWaitNs);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = tbase + (2 * e + (i & 1)) * 64;
+        const uint32_t acc = tbase + 256 + (e * DB + i % DB) * DC;
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)              // 16 weights; a group's first product starts its accumulator
-            umma_f16_ta(acc + (k >> (3 - GS)) * N, a + 8 * k, d + (uint64_t)((((2 * e + (k >> 2)) * (N * 128)) + (k & 3) * 32) >> 4),
-                        idesc, (k & ((8 >> GS) - 1)) != 0);
+            umma_f16_ta(acc + (k >> (3 - GS)) * N, a + 8 * k,
+                        d + (uint64_t)((((2 * e + (k >> 2)) * (N * 128)) + (k & 3) * 32) >> 4), idesc, (k & ((8 >> GS) - 1)) != 0);
           umma_commit(&d_full[2 * e + (i & 1)]);
+          if (e == 1) umma_commit(&empty[sl]);
         }
-        if (ok) umma_commit(&empty[sl]);
+        __syncwarp();
       }
-      if (!ok) flag_error(err, kErrTimeout);
     }
-    __syncwarp();
+    if (!ok && lane == 0) flag_error(err, kErrTimeout);
   } else {
     // ----------------------------------------------------------------- unpack --
     const int e = warp >> 2, row = tid & 127;
