@@ -630,12 +630,14 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
 // the unpacking: nothing is read again for the tokens, and the products cost no
 // issue slots.  Each group's product has an accumulator of its own, which the
 // row's thread scales into its fp32 totals.
-//   warp 8      one lane loads stages of 256 weights of 128 rows, their scales
+//   one warp    loads stages of 256 weights of 128 rows, their scales
 //               and x's columns by TMA (rows and columns past the end as zeros)
-//   warps 0-3   unpack the first 128 weights of a stage, warps 4-7 the others;
-//               two A operands and (up to) two accumulators each, so that they
-//               unpack a block while the one before is multiplied
-//   warp 9      one thread issues the MMAs
+//   four sets of four warps unpack, each one half of every other stage into an A
+//               operand of its own, so that a set unpacks while the others'
+//               blocks are multiplied (two sets, each with two operands and one
+//               half of every stage, where 32 tokens x 4 groups of 32 weights
+//               leave room for two accumulators only)
+//   two warps   issue the MMAs, one for each half of a stage
 // The (row tile, stage) pairs are dealt out in one run of equal lengths per
 // CTA; tiles that fall to several CTAs meet in the workspace, where the one that
 // takes a tile's last ticket adds the parts in the order of the CTAs.
@@ -646,16 +648,17 @@ struct MatTc {
   static constexpr int SC = 128 * 16;              // a 16-byte piece of each row's scales
   static constexpr int X = N * kTcStageK * 2;
   static constexpr int STAGE = W + SC + X;
-  static constexpr int NS = N == 16 ? 7 : 6;
+  static constexpr int SETS = (N << GS) <= 64 ? 4 : 2;
+  static constexpr int NS = N == 16 ? 7 : SETS == 4 ? 5 : 6;
+  static constexpr int THREADS = SETS * 128 + 96;
   static constexpr int BAR = 1024;
-  static constexpr int RED = 128 * (N + 1) * 4;
+  static constexpr int RED = (SETS - 1) * 128 * (N + 1) * 4;
   static constexpr size_t SMEM = 1024 + BAR + RED + 1024 + (size_t)NS * STAGE;
-  static constexpr int DB = (N << GS) <= 64 ? 2 : 1;           // accumulators of each half of the stage
-  static constexpr uint32_t COLS = 512;            // A: 2 x 2 x 64 columns, then D: 2 x DB x (N << GS)
+  static constexpr uint32_t COLS = 512;            // A: 4 x 64 columns, then D: SETS x (N << GS)
   static_assert(STAGE % 1024 == 0, "stages must keep the 1024-byte swizzle alignment");
-  static_assert(256 + 2 * DB * (N << GS) <= 512, "tensor memory");
+  static_assert(256 + SETS * (N << GS) <= 512, "tensor memory");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
 };
-constexpr int kMatTcThreads = 10 * 32;
 constexpr uint64_t kTcWaitNs = 200ull * 1000 * 1000;           // bound on any mbarrier wait
 
 struct MatTcArgs {
@@ -682,16 +685,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 
 template <int N, int GS>
-__global__ void __launch_bounds__(kMatTcThreads, 1)
+__global__ void __launch_bounds__(MatTc<N, GS>::THREADS, 1)
     k_w4_matmul_tc(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_s,
                    const __grid_constant__ CUtensorMap map_x, MatTcArgs A) {
   using Lc = MatTc<N, GS>;
-  constexpr int NS = Lc::NS, DB = Lc::DB, DC = N << GS;
+  constexpr int NS = Lc::NS, SETS = Lc::SETS, DC = N << GS, kLoad = 4 * SETS, kMma = 4 * SETS + 1;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint32_t s_last;
   unsigned char *smem = align_1024(smem_raw);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem), *empty = full + NS;
-  uint64_t *a_full = empty + NS, *d_full = a_full + 4;         // [half][buffer]
+  uint64_t *a_full = empty + NS, *d_full = a_full + 4;         // of the A operands
   uint32_t *tslot = reinterpret_cast<uint32_t *>(d_full + 4);
   float *red = reinterpret_cast<float *>(smem + Lc::BAR);      // [128][N + 1]
   unsigned char *stages = align_1024(smem + Lc::BAR + Lc::RED);
@@ -699,7 +702,7 @@ __global__ void __launch_bounds__(kMatTcThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 8 + 1);                 // the unpacking warps, and the products
+      mbar_init(&empty[i], 8 + 2);                 // the warps that unpack it, and its halves' products
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&a_full[i], 128);
@@ -710,7 +713,7 @@ __global__ void __launch_bounds__(kMatTcThreads, 1)
     prefetch_map(&map_s);
     prefetch_map(&map_x);
   }
-  if (warp == 9) {
+  if (warp == kMma) {
     tmem_alloc(tslot, Lc::COLS);
     tmem_relinquish();
   }
@@ -729,7 +732,7 @@ __global__ void __launch_bounds__(kMatTcThreads, 1)
   const int n = (int)(u1 - u0);                    // this CTA's stages
   int32_t *err = &A.hdr->err;
 
-  if (warp == 8) {
+  if (warp == kLoad) {
     // ------------------------------------------------------------------ loads --
     if (lane == 0) {
       int tile = (int)(u0 / A.nst), st = (int)(u0 % A.nst);
@@ -755,59 +758,60 @@ __global__ void __launch_bounds__(kMatTcThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp >= kMma) {
     // -------------------------------------------------------------------- MMA --
     constexpr uint32_t idesc = umma_idesc_f16(128, N, 0, 0);
-    const uint64_t dx = umma_desc(stages + Lc::W + Lc::SC, 16, 1024, kSwz128);
+    const int e = warp - kMma;                     // half of the stages
+    const uint64_t dx = umma_desc(stages + Lc::W + Lc::SC + e * (2 * N * 128), 16, 1024, kSwz128);
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
-      const int sl = i % NS;
+      const int sl = i % NS, op = 2 * (i & 1) + e; // A operand (and set, where there are four)
       const uint64_t d = dx + (uint64_t)(sl * (Lc::STAGE >> 4));
-      ok = warp_wait(&full[sl], (uint32_t)(i / NS) & 1u, kTcWaitNs);
+      const uint32_t a = tbase + op * 64, acc = tbase + 256 + (SETS == 4 ? op : e) * DC;
+      ok = warp_wait(&full[sl], (uint32_t)(i / NS) & 1u, kTcWaitNs) && warp_wait(&a_full[op], (uint32_t)(i >> 1) & 1u, kTcWaitNs);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (ok) ok = warp_wait(&a_full[2 * e + (i & 1)], (uint32_t)(i >> 1) & 1u, kTcWaitNs);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t a = tbase + (2 * e + (i & 1)) * 64;
-        const uint32_t acc = tbase + 256 + (e * DB + i % DB) * DC;
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)              // 16 weights; a group's first product starts its accumulator
-            umma_f16_ta(acc + (k >> (3 - GS)) * N, a + 8 * k,
-                        d + (uint64_t)((((2 * e + (k >> 2)) * (N * 128)) + (k & 3) * 32) >> 4), idesc, (k & ((8 >> GS) - 1)) != 0);
-          umma_commit(&d_full[2 * e + (i & 1)]);
-          if (e == 1) umma_commit(&empty[sl]);
-        }
-        __syncwarp();
+        for (int k = 0; k < 8; ++k)                // 16 weights; a group's first product starts its accumulator
+          umma_f16_ta(acc + (k >> (3 - GS)) * N, a + 8 * k, d + (uint64_t)(((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), idesc,
+                      (k & ((8 >> GS) - 1)) != 0);
+        umma_commit(&d_full[op]);
+        umma_commit(&empty[sl]);
       }
+      __syncwarp();
     }
     if (!ok && lane == 0) flag_error(err, kErrTimeout);
   } else {
     // ----------------------------------------------------------------- unpack --
-    const int e = warp >> 2, row = tid & 127;
+    const int set = warp >> 2, e = set & 1, par = set >> 1, row = tid & 127;
     const uint32_t tl = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t acc = tl + 256 + set * DC;
     float tot[N];
 #pragma unroll
     for (int b = 0; b < N; ++b) tot[b] = 0.f;
-    uint32_t sc[2][2];                             // a block's scales, kept until its products are there
-    int tile = (int)(u0 / A.nst), st = (int)(u0 % A.nst);      // of the products taken next
+    uint32_t sc[2] = {0, 0};                       // a block's scales, kept until its products are there
+    int tile = (int)(u0 / A.nst), st = (int)(u0 % A.nst);      // of the stage settled next
     const int first_tile = tile;
+    int begun = st;                                // first stage of the tile in this CTA
     int here = st;                                 // stage within its row tile, of the one unpacked
     bool ok = true;
 
-    // whole or partial sums of `tile` (its stages up to this CTA's last, from its first)
+    // the sets' sums of `tile` meet in set 0, whole or this CTA's part
     auto finish = [&](bool whole) {
-      if (e == 1) {
-        named_sync(3, 256);                        // the buffer is free
+      if (set != 0) {
+        float *to = red + ((set - 1) * 128 + row) * (N + 1);
+        named_sync(3, SETS * 128);                 // the buffer is free
 #pragma unroll
-        for (int b = 0; b < N; ++b) red[row * (N + 1) + b] = tot[b];
-        named_arrive(2, 256);
+        for (int b = 0; b < N; ++b) to[b] = tot[b];
+        named_arrive(2, SETS * 128);
       } else {
-        named_arrive(3, 256);
-        named_sync(2, 256);
+        named_arrive(3, SETS * 128);
+        named_sync(2, SETS * 128);
 #pragma unroll
-        for (int b = 0; b < N; ++b) tot[b] += red[row * (N + 1) + b];
+        for (int q = 0; q < SETS - 1; ++q)
+#pragma unroll
+          for (int b = 0; b < N; ++b) tot[b] += red[(q * 128 + row) * (N + 1) + b];
         bool mine = whole;
         if (!whole) {
           const int64_t t0 = (int64_t)tile * A.nst;
@@ -848,26 +852,27 @@ __global__ void __launch_bounds__(kMatTcThreads, 1)
 #pragma unroll
       for (int b = 0; b < N; ++b) tot[b] = 0.f;
     };
-    int begun = st;                                // first stage of the tile in this CTA
-    // products of stage q: scaled into the totals
-    auto take = [&](int q) {
-      if (ok) ok = warp_wait(&d_full[2 * e + (q & 1)], (uint32_t)(q >> 1) & 1u, kTcWaitNs);
-      if (ok) {
-        tc_fence_after();
-        __syncwarp();
+    // the products of stage q, if they are this set's, into its sums; at a tile's end they meet
+    auto settle = [&](int q) {
+      if (SETS == 2 || (q & 1) == par) {
+        const int op = 2 * (q & 1) + e;
+        if (ok) ok = warp_wait(&d_full[op], (uint32_t)(q >> 1) & 1u, kTcWaitNs);
+        if (ok) {
+          tc_fence_after();
 #pragma unroll
-        for (int g = 0; g < (1 << GS); ++g) {
-          const float s = half_of(q & 1 ? sc[1][g >> 1] : sc[0][g >> 1], g & 1);
+          for (int g = 0; g < (1 << GS); ++g) {
+            const float s = half_of(sc[g >> 1], g & 1);
 #pragma unroll
-          for (int c = 0; c < N; c += 16) {
-            if (c >= A.B) continue;
-            float v[16];
-            tmem_ld16w(tl + 256 + (e * DB + q % DB) * DC + g * N + c, v);
+            for (int c = 0; c < N; c += 16) {
+              if (c >= A.B) continue;
+              float v[16];
+              tmem_ld16w(acc + g * N + c, v);
 #pragma unroll
-            for (int b = 0; b < 16; ++b) tot[c + b] = fmaf(s, v[b], tot[c + b]);
+              for (int b = 0; b < 16; ++b) tot[c + b] = fmaf(s, v[b], tot[c + b]);
+            }
           }
+          tc_fence_before();
         }
-        tc_fence_before();
       }
       if (++st == A.nst || q == n - 1) {
         finish(begun == 0 && st == A.nst);
@@ -878,71 +883,62 @@ __global__ void __launch_bounds__(kMatTcThreads, 1)
         begun = st;
       }
     };
+    int settled = 0;
     for (int i = 0; i < n; ++i) {
-      const int sl = i % NS;
-      if (DB == 2 && i >= 2) take(i - 2);
-      if (ok) ok = warp_wait(&full[sl], (uint32_t)(i / NS) & 1u, kTcWaitNs);
-      if (ok) {
-        __syncwarp();
-        const unsigned char *w = stages + (size_t)sl * Lc::STAGE;
-        uint32_t word[4][4];
+      if (SETS == 2 || (i & 1) == par) {
+        const int sl = i % NS, op = 2 * (i & 1) + e;
+        if (SETS == 4)
+          while (settled < i) settle(settled++);   // frees the set's operand and accumulator
+        if (ok) ok = warp_wait(&full[sl], (uint32_t)(i / NS) & 1u, kTcWaitNs);
+        uint32_t next[2] = {0, 0};
+        if (ok) {
+          const unsigned char *w = stages + (size_t)sl * Lc::STAGE;
+          // the 2 << GS bytes of this block in the 16-byte piece of its row
+          const unsigned char *ps = w + Lc::W + row * 16 + (((here * (4 << GS)) & 15) + e * (2 << GS));
+          if constexpr (GS == 0) {
+            next[0] = *reinterpret_cast<const unsigned short *>(ps);
+          } else {
+            next[0] = *reinterpret_cast<const uint32_t *>(ps);
+            if constexpr (GS == 2) next[1] = *reinterpret_cast<const uint32_t *>(ps + 4);
+          }
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(w + row * 128 + (((4 * e + t) ^ (row & 7)) << 4));
-          word[t][0] = v.x;
-          word[t][1] = v.y;
-          word[t][2] = v.z;
-          word[t][3] = v.w;
-        }
-        // the 2 << GS bytes of this block in the 16-byte piece of its row
-        const unsigned char *ps = w + Lc::W + row * 16 + (((here * (4 << GS)) & 15) + e * (2 << GS));
-        uint32_t s0, s1 = 0;
-        if constexpr (GS == 0) {
-          s0 = *reinterpret_cast<const unsigned short *>(ps);
-        } else {
-          s0 = *reinterpret_cast<const uint32_t *>(ps);
-          if constexpr (GS == 2) s1 = *reinterpret_cast<const uint32_t *>(ps + 4);
-        }
-        if (i & 1) {
-          sc[1][0] = s0;
-          sc[1][1] = s1;
-        } else {
-          sc[0][0] = s0;
-          sc[0][1] = s1;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {              // weights 64 h .. 64 h + 63: words j = 2h, 2h + 1
-          uint32_t r[32];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int h = 0; h < 2; ++h) {            // weights 64 h .. 64 h + 63: words j = 2h, 2h + 1
+            uint32_t r[32];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
+              const uint2 v = *reinterpret_cast<const uint2 *>(w + row * 128 + (((4 * e + t) ^ (row & 7)) << 4) + 8 * h);
               uint32_t p[4];
-              unpack8<false>(word[t][2 * h + j], p);
+              unpack8<false>(v.x, p);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) r[16 * j + 4 * t + q] = p[q];
+              for (int q = 0; q < 4; ++q) r[4 * t + q] = p[q];
+              unpack8<false>(v.y, p);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) r[16 + 4 * t + q] = p[q];
             }
-          __syncwarp();
-          tmem_st32(tl + (2 * e + (i & 1)) * 64 + 32 * h, r);
+            __syncwarp();
+            tmem_st32(tl + op * 64 + 32 * h, r);
+          }
+          tmem_wait_st();
         }
-        tmem_wait_st();
-      }
-      if (DB == 1 && i >= 1) take(i - 1);          // its accumulator is the next one's too
-      if (ok) {
-        tc_fence_before();
-        mbar_arrive(&a_full[2 * e + (i & 1)]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[sl]);
+        if (SETS == 2)
+          while (settled < i) settle(settled++);   // its accumulator is the next one's too
+        sc[0] = next[0];
+        sc[1] = next[1];
+        if (ok) {
+          tc_fence_before();
+          mbar_arrive(&a_full[op]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[sl]);
+        }
       }
       if (++here == A.nst) here = 0;
     }
-    if (DB == 2 && n >= 2) take(n - 2);
-    if (n >= 1) take(n - 1);
+    while (settled < n) settle(settled++);
     if (!ok && lane == 0) flag_error(err, kErrTimeout);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMma) {
     tc_fence_after();
     tmem_dealloc(tbase, Lc::COLS);
   }
@@ -1276,10 +1272,11 @@ bool x_map(CUtensorMap *tm, const void *x, int k, int B, int box_rows) {
 template <int N>
 cudaError_t run_matmul_tc_n(const asf_w4_matrix *m, const CUtensorMap &w, const CUtensorMap &s, const CUtensorMap &x,
                             const MatTcArgs &a, cudaStream_t st) {
-  const dim3 grid(dot_ctas()), block(kMatTcThreads);
-  return m->group == 128  ? launch(k_w4_matmul_tc<N, 0>, grid, block, MatTc<N, 0>::SMEM, st, w, s, x, a)
-         : m->group == 64 ? launch(k_w4_matmul_tc<N, 1>, grid, block, MatTc<N, 1>::SMEM, st, w, s, x, a)
-                          : launch(k_w4_matmul_tc<N, 2>, grid, block, MatTc<N, 2>::SMEM, st, w, s, x, a);
+  const dim3 grid(dot_ctas());
+  return m->group == 128 ? launch(k_w4_matmul_tc<N, 0>, grid, dim3(MatTc<N, 0>::THREADS), MatTc<N, 0>::SMEM, st, w, s, x, a)
+         : m->group == 64
+             ? launch(k_w4_matmul_tc<N, 1>, grid, dim3(MatTc<N, 1>::THREADS), MatTc<N, 1>::SMEM, st, w, s, x, a)
+             : launch(k_w4_matmul_tc<N, 2>, grid, dim3(MatTc<N, 2>::THREADS), MatTc<N, 2>::SMEM, st, w, s, x, a);
 }
 // false: no maps for these operands
 bool run_matmul_tc(const asf_w4_matrix *m, const void *x, MatTcArgs a, cudaStream_t st, cudaError_t &e) {
