@@ -947,7 +947,11 @@ __global__ void __launch_bounds__(MatTc<N, GS>::THREADS, 1)
 // ---------------------------------------------------- down projection --
 // y[b][c] = sum_j a[j][b] s[j][c / group] (q[j][c] - 8): the neurons are the
 // contracted dimension, so the scale, which changes with the neuron, joins the
-// activation: v = a s in fp32, split exactly into three bf16 parts as x above.
+// activation: v = a s in fp32, times a power of two, split into two fp16 parts,
+// hi = fp16(v) and lo = fp16(v - hi): v to 2^-22, as the products' fp32 sums.
+// The power of two keeps the parts in fp16's range: a warp's largest v so far
+// lies below 2^15, and what is 2^20 below it still has 16 bits.  When a larger
+// one comes, the warp's sums are rescaled (exactly) to the new power.
 // D is 16 columns x 8 tokens.  Two neurons' words give one operand register by
 // a byte permutation of the packed codes, before they are unpacked: a word's
 // low half holds its even weights, its high half the odd ones.
@@ -963,11 +967,14 @@ struct DownArgs {
   Header *hdr;
 };
 
-// A warp's stage: 16 neurons' codes of one block of 128 columns, their scales
+// A warp's stage: 32 neurons' codes of one block of 128 columns, their scales
 // and their activations.
-__host__ __device__ constexpr int down_stages(int NT) { return NT == 2 ? 5 : 6; }
+constexpr int kDownTile = 32;
+__host__ __device__ constexpr int down_stages(int NT) { return NT == 2 ? 3 : 4; }
 __host__ __device__ constexpr int down_scale_bytes(int GS) { return GS == 2 ? 8 : 4; }
-__host__ __device__ constexpr int down_stage_bytes(int NT, int GS) { return 1024 + 16 * down_scale_bytes(GS) + 512 * NT; }
+__host__ __device__ constexpr int down_stage_bytes(int NT, int GS) {
+  return kDownTile * (64 + down_scale_bytes(GS) + 32 * NT);
+}
 __host__ __device__ constexpr size_t down_smem(int NT, int GS) {
   const size_t ring = (size_t)kDownWarps * down_stages(NT) * down_stage_bytes(NT, GS);
   const size_t red = (size_t)(kDownWarps / 2) * kDownCols * (8 * NT + 1) * 4;
@@ -981,20 +988,21 @@ __host__ __device__ constexpr size_t down_smem(int NT, int GS) {
 // 16-byte read touch every bank once.  Codes and scales do not depend on the
 // gate/up kernel: the first stages are on their way while it still runs (it
 // passed its own wait before this grid could start, so the list and the rows
-// are complete).  With PC (one or two tokens) the three parts of an activation
-// are three columns of one product instead of three products.
+// are complete).  With PC (up to four tokens) the two parts of an activation
+// are two columns of one product instead of two products.
 template <int NT, int GS, bool PC>
 __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(DownArgs A) {
   extern __shared__ __align__(128) unsigned char sm[];
   constexpr int NS = down_stages(NT), SB = down_stage_bytes(NT, GS), SCB = down_scale_bytes(GS);
+  constexpr int kScales = kDownTile * 64, kActs = kScales + kDownTile * SCB;
   constexpr int RS = 8 * NT + 1;
-  constexpr int P = PC ? 1 : 3;
+  constexpr int P = PC ? 1 : 2;
   __shared__ uint32_t s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   int total = A.n;
   if (A.count) total = max(0, min(A.n, ld_cg_i32(A.count)));   // out of range: flagged by the gate/up kernel
-  const int ntile = ceil_div(total, 16);
+  const int ntile = ceil_div(total, kDownTile);
   const int R = max(1, min(A.R, ceil_div(ntile, kDownWarps / 2)));
   const int cu = blockIdx.x / A.R, r = blockIdx.x % A.R;
   if (r >= R) return;
@@ -1006,39 +1014,37 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
   unsigned char *ring = sm + (size_t)warp * NS * SB;
   const int first = r * (kDownWarps / 2) + (warp >> 1), step = R * (kDownWarps / 2);
   const int tiles = col0 < kp && first < ntile ? (ntile - first + step - 1) / step : 0;
-  auto id_of = [&](int i) {
-    const int pos = (first + i * step) * 16 + (lane & 15);
+  auto id_of = [&](int i) {                                    // this lane's neuron of stage i
+    const int pos = (first + i * step) * kDownTile + lane;
     int id = -1;
     if (pos < total) id = A.idx ? ld_cg_i32(A.idx + pos) : pos;
     return (unsigned)id < (unsigned)A.n ? id : -1;
   };
   int id = tiles > 0 ? id_of(0) : -1;
-  auto copy_rows = [&](int i) {                                // stage i's codes and scales
+  const unsigned char *codes = A.data + col0 / 2 + (lane & 3) * 16;
+  // one block's scales; a single one comes with its neighbour (4 bytes at least)
+  const unsigned char *scales = A.data + kp / 2 + (GS == 0 ? (col0 / kBlk) & ~1 : (col0 / kBlk) << GS) * 2;
+  auto copy_rows = [&](int i, int slot) {                      // stage i's codes and scales
     if (i >= tiles) return;
     const int now = id;
     if (i + 1 < tiles) id = id_of(i + 1);
-    unsigned char *to = ring + (i % NS) * SB;
-    const int part = lane & 3;
+    unsigned char *to = ring + slot * SB;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 4; ++h) {
       const int row = h * 8 + (lane >> 2);
       const int nrn = __shfl_sync(0xffffffffu, now, row);
-      const int x = ((row >> 1) & 1) | ((row & 4));
-      cp_async16(to + (row >> 1) * 128 + (((part * 2 + (row & 1)) ^ x) * 16),
-                 A.data + (int64_t)max(nrn, 0) * A.stride + col0 / 2 + part * 16, nrn >= 0 ? 16u : 0u);
+      const int x = ((row >> 1) & 1) | (row & 4);
+      cp_async16(to + (row >> 1) * 128 + ((((lane & 3) * 2 + (row & 1)) ^ x) * 16), codes + (int64_t)max(nrn, 0) * A.stride,
+                 nrn >= 0 ? 16u : 0u);
     }
-    if (lane < 16) {
-      // one block's scales; a single one comes with its neighbour (4 bytes at least)
-      const int at = GS == 0 ? (col0 / kBlk) & ~1 : (col0 / kBlk) << GS;
-      cp_async_small<SCB>(to + 1024 + lane * SCB, A.data + (int64_t)max(now, 0) * A.stride + kp / 2 + at * 2, now >= 0);
-    }
+    cp_async_small<SCB>(to + kScales + lane * SCB, scales + (int64_t)max(now, 0) * A.stride, now >= 0);
   };
-  auto copy_act = [&](int i) {
+  auto copy_act = [&](int i, int slot) {
     if (i < tiles) {
-      unsigned char *to = ring + (i % NS) * SB + 1024 + 16 * SCB;
-      const int64_t pos0 = (int64_t)(first + i * step) * 16;
+      unsigned char *to = ring + slot * SB + kActs;
+      const int64_t pos0 = (int64_t)(first + i * step) * kDownTile;
 #pragma unroll
-      for (int q = 0; q < NT; ++q) {
+      for (int q = 0; q < 2 * NT; ++q) {
         const int c = q * 32 + lane;
         const bool in = pos0 + c / (2 * NT) < total;
         cp_async16(to + c * 16, in ? A.a + pos0 * 8 * NT + c * 4 : A.a, in ? 16u : 0u);
@@ -1047,92 +1053,119 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < NS - 1; ++i) copy_rows(i);
+  for (int i = 0; i < NS - 1; ++i) copy_rows(i, i);
   pdl_wait();
   pdl_trigger();
 #pragma unroll
-  for (int i = 0; i < NS - 1; ++i) copy_act(i);
+  for (int i = 0; i < NS - 1; ++i) copy_act(i, i);
 
   float acc[8][NT][4];                             // [group of 32][half] x tokens
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
-  // PC: column g is part g % 3 of token g / 3
-  const uint32_t cut1 = PC && g % 3 >= 1 ? 0xffff0000u : 0u, cut2 = PC && g % 3 == 2 ? 0xffff0000u : 0u;
-  const int act0 = PC ? g / 3 : g;
+  float up = 0.f;                                  // the power of two of the sums; 0: none yet
+  // PC: column g is part g & 1 of token g / 2
+  const int act0 = PC ? g >> 1 : g;
   const int hi0 = GS == 0 ? (col0 / kBlk) & 1 : 0;
 
+  int slot = 0;
   for (int i = 0; i < tiles; ++i) {
     cp_async_wait<NS - 2>();
     __syncwarp();
-    copy_rows(i + NS - 1);                         // into the slot that the last step has read
-    copy_act(i + NS - 1);
-    const unsigned char *st = ring + (i % NS) * SB;
-    uint4 c[4];
-    uint32_t sc[4][GS == 2 ? 2 : 1];
-    float av[4][NT];
+    copy_rows(i + NS - 1, slot == 0 ? NS - 1 : slot - 1);      // into the slot that the last step has read
+    copy_act(i + NS - 1, slot == 0 ? NS - 1 : slot - 1);
+    const unsigned char *st = ring + slot * SB;
+    slot = slot + 1 == NS ? 0 : slot + 1;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {                  // this lane's neurons: 2t, 2t+1, 2t+8, 2t+9
-      const int row = 2 * t + (q & 1) + 8 * (q >> 1);
-      const int x = (t & 1) | ((t & 2) << 1);
-      c[q] = *reinterpret_cast<const uint4 *>(st + (row >> 1) * 128 + (((sub * 2 + (q & 1)) ^ x) * 16));
+    for (int kk = 0; kk < 2; ++kk) {               // 16 neurons
+      uint4 c[4];
+      uint32_t sc[4][GS == 2 ? 2 : 1];
+      float av[4][NT];
 #pragma unroll
-      for (int w = 0; w < (GS == 2 ? 2 : 1); ++w) sc[q][w] = *reinterpret_cast<const uint32_t *>(st + 1024 + row * SCB + 4 * w);
+      for (int q = 0; q < 4; ++q) {                // this lane's: 2t, 2t+1, 2t+8, 2t+9
+        const int row = 16 * kk + 2 * t + (q & 1) + 8 * (q >> 1);
+        const int x = (t & 1) | ((t & 2) << 1);
+        c[q] = *reinterpret_cast<const uint4 *>(st + (row >> 1) * 128 + (((sub * 2 + (q & 1)) ^ x) * 16));
 #pragma unroll
-      for (int n = 0; n < NT; ++n) av[q][n] = *reinterpret_cast<const float *>(st + 1024 + 16 * SCB + ((row * NT + n) * 8 + act0) * 4);
-    }
-    uint32_t bp[NT][P][2];
+        for (int w = 0; w < (GS == 2 ? 2 : 1); ++w)
+          sc[q][w] = *reinterpret_cast<const uint32_t *>(st + kScales + row * SCB + 4 * w);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j % (4 >> GS) == 0) {                    // a new group of columns: a * s
-        float s[4];
+        for (int n = 0; n < NT; ++n) av[q][n] = *reinterpret_cast<const float *>(st + kActs + ((row * NT + n) * 8 + act0) * 4);
+      }
+      uint32_t bp[NT][P][2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s[q] = half_of(sc[q][GS == 2 ? j >> 1 : 0], GS == 2 ? j & 1 : GS == 1 ? j >> 1 : hi0);
+      for (int j = 0; j < 4; ++j) {
+        if (j % (4 >> GS) == 0) {                  // a new group of columns: a * s
+          float s[4], v[NT][4];
+          uint32_t top = 0;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float v[4];
+          for (int q = 0; q < 4; ++q) s[q] = half_of(sc[q][GS == 2 ? j >> 1 : 0], GS == 2 ? j & 1 : GS == 1 ? j >> 1 : hi0);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = av[q][n] * s[q];
-          if constexpr (PC) {
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              v[q] -= __uint_as_float(__float_as_uint(v[q]) & cut1);
-              v[q] -= __uint_as_float(__float_as_uint(v[q]) & cut2);
+              v[n][q] = av[q][n] * s[q];
+              // (a token's infinity or NaN is its own affair)
+              const uint32_t u = __float_as_uint(v[n][q]) & 0x7fffffffu;
+              top = max(top, u < 0x7f800000u ? u : 0u);
             }
-            bp[n][0][0] = upper2(v[0], v[1]);
-            bp[n][0][1] = upper2(v[2], v[3]);
-          } else {
+          top = __reduce_max_sync(0xffffffffu, top);
+          // past the parts' range (or the first value at all): 2^11 <= the largest < 2^12 from here on
+          if ((up == 0.f || __uint_as_float(top) * up >= 32768.f) && top != 0) {
+            const int ex = min(max(127 + 11 - (int)(top >> 23) + 127, 1), 254);
+            const float now = __uint_as_float((uint32_t)ex << 23), f = up == 0.f ? 0.f : now / up;
+            up = now;
 #pragma unroll
-            for (int q = 0; q < 3; ++q) {
-              bp[n][q][0] = upper2(v[0], v[1]);
-              bp[n][q][1] = upper2(v[2], v[3]);
+            for (int e = 0; e < 8; ++e)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] -= trunc_bf16(v[e]);
-            }
+              for (int n = 0; n < NT; ++n) {
+                acc[e][n][0] *= f;
+                acc[e][n][1] *= f;
+                acc[e][n][2] *= f;
+                acc[e][n][3] *= f;
+              }
           }
+          const float m = up == 0.f ? 1.f : up;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float v0 = v[n][2 * q] * m, v1 = v[n][2 * q + 1] * m;
+              const __half2 hi = __floats2half2_rn(v0, v1);
+              const float2 back = __half22float2(hi);
+              const __half2 lo = __floats2half2_rn(v0 - back.x, v1 - back.y);
+              const uint32_t hw = *reinterpret_cast<const uint32_t *>(&hi), lw = *reinterpret_cast<const uint32_t *>(&lo);
+              if constexpr (PC) {
+                bp[n][0][q] = g & 1 ? lw : hw;
+              } else {
+                bp[n][0][q] = hw;
+                bp[n][1][q] = lw;
+              }
+            }
         }
+        const uint32_t w[4] = {j == 0 ? c[0].x : j == 1 ? c[0].y : j == 2 ? c[0].z : c[0].w,
+                               j == 0 ? c[1].x : j == 1 ? c[1].y : j == 2 ? c[1].z : c[1].w,
+                               j == 0 ? c[2].x : j == 1 ? c[2].y : j == 2 ? c[2].z : c[2].w,
+                               j == 0 ? c[3].x : j == 1 ? c[3].y : j == 2 ? c[3].z : c[3].w};
+        uint32_t lo[4], hi[4];
+        unpack8<false>(__byte_perm(w[0], w[1], sel), lo);      // [p] = weight 2p + (g >> 2) of neurons 2t, 2t+1
+        unpack8<false>(__byte_perm(w[2], w[3], sel), hi);      // of neurons 2t+8, 2t+9
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            mma16816<false>(acc[2 * j][n], lo[0], lo[1], hi[0], hi[1], bp[n][q][0], bp[n][q][1]);
+            mma16816<false>(acc[2 * j + 1][n], lo[2], lo[3], hi[2], hi[3], bp[n][q][0], bp[n][q][1]);
+          }
       }
-      const uint32_t w[4] = {j == 0 ? c[0].x : j == 1 ? c[0].y : j == 2 ? c[0].z : c[0].w,
-                             j == 0 ? c[1].x : j == 1 ? c[1].y : j == 2 ? c[1].z : c[1].w,
-                             j == 0 ? c[2].x : j == 1 ? c[2].y : j == 2 ? c[2].z : c[2].w,
-                             j == 0 ? c[3].x : j == 1 ? c[3].y : j == 2 ? c[3].z : c[3].w};
-      uint32_t lo[4], hi[4];
-      unpack8<true>(__byte_perm(w[0], w[1], sel), lo);         // [p] = weight 2p + (g >> 2) of neurons 2t, 2t+1
-      unpack8<true>(__byte_perm(w[2], w[3], sel), hi);         // of neurons 2t+8, 2t+9
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < P; ++q) {
-          mma16816<true>(acc[2 * j][n], lo[0], lo[1], hi[0], hi[1], bp[n][q][0], bp[n][q][1]);
-          mma16816<true>(acc[2 * j + 1][n], lo[2], lo[3], hi[2], hi[3], bp[n][q][0], bp[n][q][1]);
-        }
     }
   }
   // the four shares of a column, added in order
   cp_async_wait<0>();
   __syncthreads();
   float *red = reinterpret_cast<float *>(sm);                  // [share][256 columns][8 * NT + 1]
+  const float down = up == 0.f ? 1.f : 1.f / up;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -1142,7 +1175,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
         // row g of half h is weight 2p + (g >> 2) of word 4j + (g & 3), p = 2h (+1 for row g + 8)
         const int p = 2 * (i & 1) + (e >> 1);
         const int col = (warp & 1) * kBlk + (i >> 1) * 32 + sub * 8 + 2 * p + (g >> 2);
-        red[((warp >> 1) * kDownCols + col) * RS + 8 * n + 2 * t + (e & 1)] = acc[i][n][e];
+        red[((warp >> 1) * kDownCols + col) * RS + 8 * n + 2 * t + (e & 1)] = acc[i][n][e] * down;
       }
   __syncthreads();
   for (int i = threadIdx.x; i < A.B * kDownCols; i += blockDim.x) {
@@ -1152,7 +1185,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
 #pragma unroll
     for (int q = 0; q < kDownWarps / 2; ++q) {
       const float *from = red + (q * kDownCols + i % kDownCols) * RS;
-      v += PC ? (from[3 * b + 2] + from[3 * b + 1]) + from[3 * b] : from[b];
+      v += PC ? from[2 * b + 1] + from[2 * b] : from[b];
     }
     if (R == 1) A.y[(int64_t)b * A.d + c] = v;
     else __stcg(A.part + ((int64_t)r * A.B + b) * A.d + c, v);
@@ -1294,7 +1327,7 @@ bool run_matmul_tc(const asf_w4_matrix *m, const void *x, MatTcArgs a, cudaStrea
 template <int GS>
 cudaError_t run_down(const DownArgs &a, cudaStream_t st) {
   const dim3 grid(down_units(a.d) * a.R), block(kDownWarps * 32);
-  if (a.B <= 2) return launch(k_w4_down<1, GS, true>, grid, block, down_smem(1, GS), st, a);
+  if (a.B <= 4) return launch(k_w4_down<1, GS, true>, grid, block, down_smem(1, GS), st, a);
   switch (nt_of(a.B)) {
     case 1: return launch(k_w4_down<1, GS, false>, grid, block, down_smem(1, GS), st, a);
     case 2: return launch(k_w4_down<2, GS, false>, grid, block, down_smem(2, GS), st, a);
@@ -1365,7 +1398,13 @@ asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dtype xdty
   if (!al16(x) || !al4(y) || !al4(bias)) return ASF_ERR_MISALIGNED;
   s = check_ws(ws, ws_bytes, kHeaderBytes + dot_part_bytes(ceil_div(mat->rows, 16), mat->k, mat->group, B));
   if (s != ASF_OK) return s;
-  if (xdtype == ASF_F16) {
+  // From 16 stages (of 128 rows x 256 weights) a CTA on, or 8 for more than 8
+  // tokens: k_w4_matmul_tc costs 4 us more to start and end, and less per stage.
+  // us, one token: 4096 x 4096 (3.5 stages) 11.8 against 7.4, 8192 x 8192 (14)
+  // 17.0 against 15.0, 28672 x 8192 (48) 37.5 against 43; 16 tokens: 8192 x 4096
+  // (7) 14.1 against 13.9, 11008 x 4096 (9) 15.4 against 19.1.
+  const int64_t stages = (int64_t)ceil_div(mat->rows, 128) * ceil_div(w4_kp(mat->k), kTcStageK);
+  if (xdtype == ASF_F16 && stages >= (int64_t)(B <= 8 ? 16 : 8) * dot_ctas()) {
     MatTcArgs t{};
     t.rows = mat->rows;
     t.k = mat->k;

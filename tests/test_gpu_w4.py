@@ -179,6 +179,30 @@ def test_errors_of_the_list_are_flagged_and_skipped():
         _check_ffn(y, "reglu", data, bias, d, group, x.double().numpy(), ref)
 
 
+@pytest.mark.parametrize("B", [2, 3, 7, 12, 20])
+def test_activations_of_very_different_sizes(B):
+    """Activations that grow by 2^40 along the list, tokens 2^12 apart, one token with NaN: the others stay right."""
+    n, d, group = 640, 256, 64
+    data, bias = _layer("relu", n, d, group, 8)
+    rng = np.random.default_rng(B)
+    x = (rng.standard_normal((B, d)) * 2.0 ** -(6 * (np.arange(B) % 3))[:, None]).astype(np.float32)
+    # rows' scales grow with the neuron
+    grow = 2.0 ** np.linspace(-10, 10, n)
+    W = [_weights(n, d, 8 + i) * grow[:, None] for i in range(2)]
+    data = np.stack([O.w4_pack(w.astype(np.float32), group) for w in W], 1)
+    bias = np.zeros(n, np.float32)
+    bad = B - 1
+    xs = torch.from_numpy(x).cuda()
+    xs[bad, 5] = float("nan")
+    ffn = A.W4FFN("relu", torch.from_numpy(data).cuda(), torch.from_numpy(bias).cuda(), d, group)
+    ws = A.Workspace.for_w4(ffn, B)
+    y = torch.empty(B, d, device="cuda")
+    A.asf_w4_sparse_ffn(ffn, xs, None, None, y, ws)
+    assert torch.isnan(y[bad]).all()
+    keep = [b for b in range(B) if b != bad]
+    _check_ffn(y[keep], "relu", data, bias, d, group, x[keep].astype(np.float64), np.arange(n))
+
+
 def test_a_nan_group_reaches_only_its_rows():
     W = _weights(40, 512, 1)
     W[7, 300] = np.inf
