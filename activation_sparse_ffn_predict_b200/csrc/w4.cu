@@ -293,6 +293,7 @@ struct DotArgs {
   int relu;
   const int32_t *idx, *count;  // list form; null: all rows
   float *y;                    // dense: [B][rows]; list form: a [positions][8 * NT]
+  float *amax;                 // list form: a position's largest finite |a|
   int y16;                     // dense: y is fp16
   float *part;                 // partial tiles of a split k
   int most;                    // superblocks of k whose x fits a CTA
@@ -565,6 +566,7 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
       const int nrn = A.idx ? ld_cg_i32(A.idx + pos) : pos;
       const bool ok = (unsigned)nrn < (unsigned)A.rows;
       const float bias = ok ? __ldg(A.bias + nrn) : 0.f;
+      uint32_t top = 0;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float v[2];
@@ -574,9 +576,16 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
           a = a > 0.f ? a : (a != a ? a : 0.f);
           if (mode == kListGated) a *= tot[n][2 + c];
           v[c] = ok && 8 * n + 2 * t + c < A.B ? a : 0.f;
+          const uint32_t u = __float_as_uint(v[c]) & 0x7fffffffu;
+          if (u < 0x7f800000u) top = max(top, u);  // an infinity or NaN is its token's own affair
         }
         *reinterpret_cast<float2 *>(A.y + ((int64_t)pos * NT + n) * 8 + 2 * t) = make_float2(v[0], v[1]);
       }
+      // the four lanes of a row (all here, or none: pos is theirs)
+      const uint32_t quad = 0xfu << (lane & 28);
+      top = max(top, __shfl_xor_sync(quad, top, 1));
+      top = max(top, __shfl_xor_sync(quad, top, 2));
+      if (t == 0) A.amax[pos] = __uint_as_float(top);
     }
   };
   // the tile's partial sums, and with the unit's last ticket its whole sums
@@ -961,19 +970,20 @@ struct DownArgs {
   int n, d;
   const int32_t *idx, *count;
   const float *a;              // [positions][8 * NT]
+  const float *amax;           // [positions]: largest finite magnitude of a row of a
   int B, R;                    // tokens, list splits
   float *part;                 // [R][B][d]
   float *y;
   Header *hdr;
 };
 
-// A warp's stage: 32 neurons' codes of one block of 128 columns, their scales
-// and their activations.
+// A warp's stage: 32 neurons' codes of one block of 128 columns, their scales,
+// and their activations with the largest of each neuron's.
 constexpr int kDownTile = 32;
 __host__ __device__ constexpr int down_stages(int NT) { return NT == 2 ? 3 : 4; }
 __host__ __device__ constexpr int down_scale_bytes(int GS) { return GS == 2 ? 8 : 4; }
 __host__ __device__ constexpr int down_stage_bytes(int NT, int GS) {
-  return kDownTile * (64 + down_scale_bytes(GS) + 32 * NT);
+  return kDownTile * (64 + down_scale_bytes(GS) + 4 + 32 * NT);
 }
 __host__ __device__ constexpr size_t down_smem(int NT, int GS) {
   const size_t ring = (size_t)kDownWarps * down_stages(NT) * down_stage_bytes(NT, GS);
@@ -994,7 +1004,7 @@ template <int NT, int GS, bool PC>
 __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(DownArgs A) {
   extern __shared__ __align__(128) unsigned char sm[];
   constexpr int NS = down_stages(NT), SB = down_stage_bytes(NT, GS), SCB = down_scale_bytes(GS);
-  constexpr int kScales = kDownTile * 64, kActs = kScales + kDownTile * SCB;
+  constexpr int kScales = kDownTile * 64, kTops = kScales + kDownTile * SCB, kActs = kTops + kDownTile * 4;
   constexpr int RS = 8 * NT + 1;
   constexpr int P = PC ? 1 : 2;
   __shared__ uint32_t s_last;
@@ -1049,6 +1059,8 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
         const bool in = pos0 + c / (2 * NT) < total;
         cp_async16(to + c * 16, in ? A.a + pos0 * 8 * NT + c * 4 : A.a, in ? 16u : 0u);
       }
+      const bool in = pos0 + lane < total;
+      cp_async_small<4>(ring + slot * SB + kTops + lane * 4, in ? A.amax + pos0 + lane : A.amax, in);
     }
     cp_async_commit();
   };
@@ -1081,7 +1093,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
     for (int kk = 0; kk < 2; ++kk) {               // 16 neurons
       uint4 c[4];
       uint32_t sc[4][GS == 2 ? 2 : 1];
-      float av[4][NT];
+      float av[4][NT], most[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {                // this lane's: 2t, 2t+1, 2t+8, 2t+9
         const int row = 16 * kk + 2 * t + (q & 1) + 8 * (q >> 1);
@@ -1090,6 +1102,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
 #pragma unroll
         for (int w = 0; w < (GS == 2 ? 2 : 1); ++w)
           sc[q][w] = *reinterpret_cast<const uint32_t *>(st + kScales + row * SCB + 4 * w);
+        most[q] = *reinterpret_cast<const float *>(st + kTops + row * 4);
 #pragma unroll
         for (int n = 0; n < NT; ++n) av[q][n] = *reinterpret_cast<const float *>(st + kActs + ((row * NT + n) * 8 + act0) * 4);
       }
@@ -1097,19 +1110,14 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j % (4 >> GS) == 0) {                  // a new group of columns: a * s
-          float s[4], v[NT][4];
+          float s[4];
           uint32_t top = 0;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) s[q] = half_of(sc[q][GS == 2 ? j >> 1 : 0], GS == 2 ? j & 1 : GS == 1 ? j >> 1 : hi0);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              v[n][q] = av[q][n] * s[q];
-              // (a token's infinity or NaN is its own affair)
-              const uint32_t u = __float_as_uint(v[n][q]) & 0x7fffffffu;
-              top = max(top, u < 0x7f800000u ? u : 0u);
-            }
+          for (int q = 0; q < 4; ++q) {
+            s[q] = half_of(sc[q][GS == 2 ? j >> 1 : 0], GS == 2 ? j & 1 : GS == 1 ? j >> 1 : hi0);
+            const uint32_t u = __float_as_uint(most[q] * s[q]);
+            top = max(top, u < 0x7f800000u ? u : 0u);          // scales are not negative; a NaN one is its rows' affair
+          }
           top = __reduce_max_sync(0xffffffffu, top);
           // past the parts' range (or the first value at all): 2^11 <= the largest < 2^12 from here on
           if ((up == 0.f || __uint_as_float(top) * up >= 32768.f) && top != 0) {
@@ -1126,12 +1134,13 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
                 acc[e][n][3] *= f;
               }
           }
-          const float m = up == 0.f ? 1.f : up;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) s[q] *= up == 0.f ? 1.f : up;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const float v0 = v[n][2 * q] * m, v1 = v[n][2 * q + 1] * m;
+              const float v0 = av[2 * q][n] * s[2 * q], v1 = av[2 * q + 1][n] * s[2 * q + 1];
               const __half2 hi = __floats2half2_rn(v0, v1);
               const float2 back = __half22float2(hi);
               const __half2 lo = __floats2half2_rn(v0 - back.x, v1 - back.y);
@@ -1259,7 +1268,7 @@ int down_w4_splits(int d, int B) {
 }
 size_t ffn_w4_scratch(const asf_w4_ffn *f, int B) {
   const int tiles = ceil_div(f->n, f->act == ASF_ACT_REGLU ? 8 : 16);
-  return r256((size_t)f->n * nt_of(B) * 32) + dot_part_bytes(tiles, f->d, f->group, B) +
+  return r256((size_t)f->n * nt_of(B) * 32) + r256((size_t)f->n * 4) + dot_part_bytes(tiles, f->d, f->group, B) +
          r256((size_t)down_w4_splits(f->d, B) * B * f->d * 4);
 }
 
@@ -1459,6 +1468,8 @@ asf_status asf_w4_sparse_ffn(const asf_w4_ffn *f, const void *x, asf_dtype xdtyp
   a.count = count;
   a.y = reinterpret_cast<float *>(base);
   base += r256((size_t)f->n * nt_of(B) * 32);
+  a.amax = reinterpret_cast<float *>(base);
+  base += r256((size_t)f->n * 4);
   a.part = reinterpret_cast<float *>(base);
   base += dot_part_bytes(ceil_div(f->n, gated ? 8 : 16), f->d, f->group, B);
   a.hdr = static_cast<Header *>(ws);
@@ -1473,6 +1484,7 @@ asf_status asf_w4_sparse_ffn(const asf_w4_ffn *f, const void *x, asf_dtype xdtyp
   w.idx = idx;
   w.count = count;
   w.a = a.y;
+  w.amax = a.amax;
   w.B = B;
   w.R = down_w4_splits(f->d, B);
   w.part = reinterpret_cast<float *>(base);
