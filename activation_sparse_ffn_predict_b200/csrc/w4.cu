@@ -323,7 +323,8 @@ __device__ __forceinline__ int dot_per(int tiles, int nsb, int most, int ctas, i
     if (per <= most) {
       const int S = ceil_div(nsb, per);
       if (per == most || (int64_t)tiles * S <= room) {
-        const int u = max(8, ceil_div(ceil_div(tiles, ctas / S), 4) * 4);
+        const int c = ceil_div(tiles, ctas / S), w = c <= kDotWarps ? 4 : kDotWarps;
+        const int u = max(8, ceil_div(c, w) * w);
         const int64_t cost = 8 * (int64_t)u * per + (S > 1 ? 8 * (12 + S) + (int64_t)u * NT : 0);
         key = (uint32_t)min(cost, (int64_t)(1 << 23)) * 256u + (uint32_t)(255 - per);
       }
