@@ -49,25 +49,28 @@ def _arg(t: torch.Tensor, name: str, device, dtype=None) -> int:
     return t.data_ptr()
 
 
-class _on:
-    """The raw stream of a call whose tensors are on ``device``: the given one,
-    or that device's current stream; the device is current inside."""
-    __slots__ = ("device", "stream", "guard")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, device, stream):
-        self.device, self.stream, self.guard = device, stream, None
 
-    def __enter__(self) -> int:
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        if self.stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        return self.stream.cuda_stream if isinstance(self.stream, torch.cuda.Stream) else int(self.stream)
+def _invoke(name: str, device, stream, *args) -> None:
+    """Call a C entry point whose last argument is the stream: the given one, or
+    ``device``'s current stream; with ``device`` current.  Raises on an error status."""
+    fn = _FN.get(name) or _FN.setdefault(name, getattr(L.load(), name))
+    if stream is None:
+        st = _raw_stream(device.index)
+    else:
+        st = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, st)
+    if status != L.ASF_OK:
+        raise AsfError(status, name)
 
-    def __exit__(self, *exc) -> None:
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+
+_FN: dict = {}
 
 
 class Predictor:
@@ -178,8 +181,7 @@ class Workspace:
         self = cls.__new__(cls)
         self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.nbytes = nbytes
-        with _on(self.buf.device, stream) as st:
-            asf_workspace_init(self, st)
+        _invoke("asf_workspace_init", self.buf.device, stream, self.buf.data_ptr(), nbytes)
         return self
 
     @classmethod

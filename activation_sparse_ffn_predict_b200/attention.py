@@ -8,8 +8,7 @@ from typing import Optional
 import torch
 
 from . import _lib as L
-from ._lib import check
-from .api import Workspace, _arg, _on
+from .api import Workspace, _arg, _invoke
 
 
 class KVCache:
@@ -53,8 +52,7 @@ def asf_kv_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin
     dev = cache.device
     req = _requests(cache, table, lens, begin)
     kp, vp = _arg(k, "k", dev, torch.float16), _arg(v, "v", dev, torch.float16)
-    with _on(dev, stream) as st:
-        check(L.load().asf_kv_append(cache._ref, *req, k.shape[0], kp, vp, ws.on(dev), ws.nbytes, st), "asf_kv_append")
+    _invoke("asf_kv_append", dev, stream, cache._ref, *req, k.shape[0], kp, vp, ws.on(dev), ws.nbytes)
 
 
 def asf_tree_attention(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin: torch.Tensor, q: torch.Tensor,
@@ -74,6 +72,5 @@ def asf_tree_attention(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, 
     ap = _arg(anc, "anc", dev, torch.int32)
     if scale is None:
         scale = cache.head_dim ** -0.5
-    with _on(dev, stream) as st:
-        check(L.load().asf_tree_attention(cache._ref, *req, q.shape[0], q.shape[1], qp, ap, scale, op, ws.on(dev),
-                                          ws.nbytes, st), "asf_tree_attention")
+    _invoke("asf_tree_attention", dev, stream, cache._ref, *req, q.shape[0], q.shape[1], qp, ap, scale, op, ws.on(dev),
+            ws.nbytes)

@@ -8,8 +8,7 @@ from typing import Optional
 import torch
 
 from . import _lib as L
-from ._lib import check
-from .api import _ACT, _DT, Workspace, _arg, _on
+from .api import _ACT, _DT, Workspace, _arg, _invoke
 
 
 def asf_w4_row_bytes(k: int, group: int) -> int:
@@ -99,8 +98,7 @@ def _quantize(src: torch.Tensor, desc, device, stream) -> None:
     if src.dtype not in _DT:
         raise ValueError("weights must be float16 or float32")
     sp = _arg(src, "src", device)
-    with _on(device, stream) as st:
-        check(L.load().asf_w4_quantize(sp, _DT[src.dtype], ctypes.byref(desc), st), "asf_w4_quantize")
+    _invoke("asf_w4_quantize", device, stream, sp, _DT[src.dtype], ctypes.byref(desc))
 
 
 def asf_w4_quantize(src: torch.Tensor, mat: W4Matrix, stream=None) -> None:
@@ -115,8 +113,7 @@ def asf_w4_dequantize(mat: W4Matrix, dst: torch.Tensor, stream=None) -> None:
     if dst.shape != (mat.rows, mat.k) or dst.dtype not in _DT:
         raise ValueError("dst must be [rows, k], float16 or float32")
     dp = _arg(dst, "dst", mat.device)
-    with _on(mat.device, stream) as st:
-        check(L.load().asf_w4_dequantize(mat._ref, dp, _DT[dst.dtype], st), "asf_w4_dequantize")
+    _invoke("asf_w4_dequantize", mat.device, stream, mat._ref, dp, _DT[dst.dtype])
 
 
 def asf_w4_matmul(mat: W4Matrix, x: torch.Tensor, y: torch.Tensor, ws: Workspace,
@@ -134,9 +131,8 @@ def asf_w4_matmul(mat: W4Matrix, x: torch.Tensor, y: torch.Tensor, ws: Workspace
             raise ValueError("bias must be [rows]")
         bp = _arg(bias, "bias", dev, torch.float32)
     xp, yp = _arg(x, "x", dev), _arg(y, "y", dev)
-    with _on(dev, stream) as st:
-        check(L.load().asf_w4_matmul(mat._ref, xp, _DT[x.dtype], B, bp, int(bool(relu)), yp, _DT[y.dtype], ws.on(dev),
-                                     ws.nbytes, st), "asf_w4_matmul")
+    _invoke("asf_w4_matmul", dev, stream, mat._ref, xp, _DT[x.dtype], B, bp, int(bool(relu)), yp, _DT[y.dtype], ws.on(dev),
+            ws.nbytes)
 
 
 def asf_w4_sparse_ffn(ffn: W4FFN, x: torch.Tensor, idx: Optional[torch.Tensor], count: Optional[torch.Tensor],
@@ -156,6 +152,4 @@ def asf_w4_sparse_ffn(ffn: W4FFN, x: torch.Tensor, idx: Optional[torch.Tensor], 
             raise ValueError("idx must hold n entries and count one")
         ip, cp = _arg(idx, "idx", dev, torch.int32), _arg(count, "count", dev, torch.int32)
     xp, yp = _arg(x, "x", dev), _arg(y, "y", dev, torch.float32)
-    with _on(dev, stream) as st:
-        check(L.load().asf_w4_sparse_ffn(ffn._ref, xp, _DT[x.dtype], B, ip, cp, yp, ws.on(dev), ws.nbytes, st),
-              "asf_w4_sparse_ffn")
+    _invoke("asf_w4_sparse_ffn", dev, stream, ffn._ref, xp, _DT[x.dtype], B, ip, cp, yp, ws.on(dev), ws.nbytes)
