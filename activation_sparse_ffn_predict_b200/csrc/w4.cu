@@ -51,7 +51,7 @@ inline int64_t w4_row_bytes(int k, int group) { return (int64_t)w4_kp(k) / 2 + w
 // A CTA takes 1, 2, 4 or 8 rows, so that its eight warps have a superblock of
 // 512 weights each; a lane has 8 weights of each half of it, the group maximum
 // comes from group / 8 neighbouring lanes.  A code is the rounding of the IEEE
-// quotient v / s.  v (1/s) is within 2^-22 of it, relatively, and |v / s| < 16,
+// quotient v / s.  v (1/s) is within 2^-23 of it, relatively, and |v / s| < 8,
 // so wherever that product is 1e-5 or more off a half its rounding is the same;
 // the few others divide.  (Dividing always: 72 us for 11008 x 4096 in fp16.)
 __device__ __forceinline__ void rows_of_cta(int nsb, int warp, int &lsh, int &sb, int64_t &row) {
@@ -106,26 +106,34 @@ k_w4_quantize(const T *__restrict__ src, int rows, int k, int group, unsigned ch
         }
       }
 #pragma unroll
-      for (int o = 0; o < 4; ++o)
-        if (o < gsh) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1 << o));
+      for (int o = 0; o < 4; ++o) {
+        if (o >= gsh) break;
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1 << o));
+      }
       float top;
       if constexpr (sizeof(T) == 2) top = __half2float(__ushort_as_half((unsigned short)m));
       else top = __uint_as_float(m);
       const __half sh = __float2half_rn(__fdiv_rn(top, 7.f));
       const float s = __half2float(sh);
       const bool good = s <= kFp16Max;             // a group that fp16 scales cannot hold reads back as NaN
-      const float r = good && s > 0.f ? __frcp_rn(s) : 0.f;
+      // From fp16's normal range on |v / s| <= 7 (1 + 2^-11): no code is clamped.
+      const bool plain = good && s >= 6.103515625e-05f;
+      const float r = plain ? __frcp_rn(s) : 0.f;
+      constexpr float kMagic = 12582912.f;         // 1.5 * 2^23: adding it rounds to whole numbers, half to even
       uint32_t word = 0;
       float off = 0.f;
-      constexpr float kMagic = 12582912.f;         // 1.5 * 2^23: adding it rounds to whole numbers, half to even
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float q = good ? v[i] * r : 0.f;
-        const float t = fminf(fmaxf(q, -8.f), 7.f) + (kMagic + 8.f);
-        off = fmaxf(off, fabsf(q - (t - (kMagic + 8.f))));     // a clamped one is far off: it divides
-        word |= (__float_as_uint(t) & 15u) << (16 * (i & 1) + 4 * (i >> 1));
+        const float t = fmaf(v[i], r, kMagic);
+        off = fmaxf(off, fabsf(fmaf(v[i], r, kMagic - t)));
+        // t's bits are kMagic's plus the whole number: shifted sums of them are
+        // the codes' plus a constant, modulo 2^32
+        word += __float_as_uint(t) << (16 * (i & 1) + 4 * (i >> 1));
       }
-      if (off > 0.5f - 1e-5f && r > 0.f) {
+      word += 0x88888888u - 0x4b400000u * 0x1111u - ((0x4b400000u * 0x1111u) << 16);
+      if (!good || s == 0.f) {
+        word = 0x88888888u;
+      } else if (off > 0.5f - 1e-5f || !plain) {
         word = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
