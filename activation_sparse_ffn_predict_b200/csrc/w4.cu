@@ -1022,7 +1022,8 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
   int total = A.n;
   if (A.count) total = max(0, min(A.n, ld_cg_i32(A.count)));   // out of range: flagged by the gate/up kernel
   const int ntile = ceil_div(total, kDownTile);
-  const int R = max(1, min(A.R, ceil_div(ntile, kDownWarps / 2)));
+  // a warp takes two stages before the list is split further: a split costs its ticket
+  const int R = max(1, min(A.R, ceil_div(ntile, kDownWarps)));
   const int cu = blockIdx.x / A.R, r = blockIdx.x % A.R;
   if (r >= R) return;
   const int kp = w4_kp(A.d);
@@ -1213,13 +1214,29 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
   if (threadIdx.x == 0) s_last = ticket_acq_rel(&A.hdr->tile_done[cu]);
   __syncthreads();
   if (s_last != (uint32_t)(R - 1)) return;
-  for (int i = threadIdx.x; i < A.B * kDownCols; i += blockDim.x) {
-    const int b = i / kDownCols, c = cu * kDownCols + i % kDownCols;
-    if (c >= A.d) continue;
-    float v = 0.f;
-#pragma unroll 8
-    for (int q = 0; q < R; ++q) v += __ldcg(A.part + ((int64_t)q * A.B + b) * A.d + c);
-    A.y[(int64_t)b * A.d + c] = v;
+  // the list's parts in order; a thread has four columns of four tokens at a
+  // time, 16 loads in flight (one value at a time: 36 us for 32 tokens x 18 parts)
+  const int c4 = cu * kDownCols + 4 * (threadIdx.x & 63);
+  if (c4 < A.d) {
+    for (int k0 = threadIdx.x >> 6; k0 < A.B; k0 += 16) {
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int q = 0; q < R; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k0 + 4 * k < A.B) {
+            const float4 u = __ldcg(reinterpret_cast<const float4 *>(A.part + ((int64_t)q * A.B + k0 + 4 * k) * A.d + c4));
+            v[k].x += u.x; v[k].y += u.y; v[k].z += u.z; v[k].w += u.w;
+          }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k0 + 4 * k < A.B) {
+          float *to = A.y + (int64_t)(k0 + 4 * k) * A.d + c4;
+          to[0] = v[k].x; to[1] = v[k].y; to[2] = v[k].z; to[3] = v[k].w;
+        }
+    }
   }
   if (threadIdx.x == 0) A.hdr->tile_done[cu] = 0;
 }

@@ -108,7 +108,9 @@ def _layer(act, n, d, group, seed):
 @pytest.mark.parametrize("act,n,d,group,B,active", [
     ("reglu", 1376, 512, 32, 1, 140), ("relu", 1376, 512, 32, 2, 1), ("reglu", 300, 1096, 64, 8, 0),
     ("relu", 500, 136, 128, 9, 500), ("reglu", 700, 2048, 128, 17, 333), ("relu", 260, 4096, 64, 32, 100),
-    ("reglu", 64, 8, 32, 4, 17), ("reglu", 200, 8192, 128, 3, 77), ("relu", 120, 12288, 32, 16, 120)])
+    ("reglu", 64, 8, 32, 4, 17), ("reglu", 200, 8192, 128, 3, 77), ("relu", 120, 12288, 32, 16, 120),
+    ("reglu", 900, 1032, 64, 10, 700), ("relu", 3000, 264, 128, 12, 2900), ("reglu", 130, 4096, 32, 32, 65),
+    ("relu", 400, 2560, 64, 30, 129), ("reglu", 257, 264, 128, 25, 256), ("relu", 70, 8, 32, 9, 70)])
 def test_sparse_ffn(act, n, d, group, B, active, dt):
     rng = np.random.default_rng(n + d)
     data, bias = _layer(act, n, d, group, n)
@@ -154,8 +156,9 @@ def _check_ffn(y, act, data, bias, d, group, xn, ids):
     assert (np.abs(y - ref) - tol).max() <= 0, (np.abs(y - ref).max(), np.abs(ref).max())
 
 
-def test_errors_of_the_list_are_flagged_and_skipped():
-    n, d, group, B = 96, 256, 64, 3
+@pytest.mark.parametrize("B", [3, 11, 29])
+def test_errors_of_the_list_are_flagged_and_skipped(B):
+    n, d, group = 96, 256, 64
     data, bias = _layer("reglu", n, d, group, 5)
     x = torch.randn(B, d).half()
     ffn = A.W4FFN("reglu", torch.from_numpy(data).cuda(), torch.from_numpy(bias).cuda(), d, group)
