@@ -23,6 +23,7 @@ ASF_ACT_REGLU = 1
 ASF_MAX_BATCH = 32
 ASF_NOALLOC_SCRATCH_BYTES = 32 << 20
 ASF_W4_MAX_K = 65536
+ASF_W4_MAX_ROWS = 1 << 30
 ASF_MAX_KV_HEADS = 1024
 ASF_MAX_HEAD_GROUP = 128
 ASF_MAX_KEYS = 1 << 30

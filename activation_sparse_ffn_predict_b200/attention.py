@@ -12,8 +12,8 @@ from .api import Workspace, _arg, _invoke
 
 
 class KVCache:
-    """A layer's keys and values, fp16 [pages, page, heads, head_dim] each; any
-    strides (multiples of 8 elements) with a contiguous last dimension."""
+    """A layer's keys and values, fp16 [pages, page, heads, head_dim] each; strides are
+    multiples of 8 elements and at least head_dim, the last dimension is contiguous."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
         for name, x in (("k", k), ("v", v)):
@@ -26,7 +26,8 @@ class KVCache:
         self.k, self.v, self.device = k, v, k.device
         self.pages, self.page, self.heads, self.head_dim = (int(n) for n in k.shape)
         self.desc = L.asf_kv_cache(self.pages, self.page, self.heads, self.head_dim, k.data_ptr(), v.data_ptr(),
-                                   *(int(n) for n in k.stride()[:3]))
+                                   # the stride of a dimension of one is never used, and torch's can be anything
+                                   *(int(k.stride(i)) if k.shape[i] > 1 else self.head_dim for i in range(3)))
         self._ref = ctypes.byref(self.desc)
 
     def workspace_bytes(self, q_heads: int, requests: int, tokens: int) -> int:

@@ -44,7 +44,7 @@ struct AttnArgs {
   const int32_t *anc;
   float scale;                         // times log2(e)
   __half *o;
-  float *part;                         // [unit][MT][DP]
+  float *part;                         // [unit < target][MT][DP]
   float2 *ml;                          // [unit][MT]: maximum (log2) and sum
   int4 *plan;                          // per request, for the merge: first token, tokens, splits, first unit
   int target;                          // CTAs to aim at
@@ -147,17 +147,17 @@ __device__ __forceinline__ float exp2_fast(float v) {
   return r;
 }
 
-// CTAs of an SM: what their stages (48 or 96 KB), registers and, for tiles of
-// 8 x 16 rows, tensor memory leave.
+// CTAs of an SM: what their stages (48 or 96 KB), registers and, for k_tree_tc
+// (8 groups of 16 rows), tensor memory leave.
 __host__ __device__ constexpr int attn_resident(int DP, int WM) { return DP == 64 && WM < 8 ? 3 : 2; }
 
-// A CTA is one unit: WM groups of 16 query rows x KG groups of keys, a warp
-// each.  Keys and values of a tile go to shared memory by 16-byte cp.async, two
+// A CTA is one unit: WM (1 or 2) groups of 16 query rows x KG groups of keys, a
+// warp each.  Keys and values of a tile go to shared memory by 16-byte cp.async, two
 // tiles ahead; 16-byte chunk c of row i sits at c ^ (i & 7), so that the
 // 8 x 8 matrix loads touch every bank once.
 template <int DP, int WM>
-__global__ void __launch_bounds__((WM > 4 ? WM : 4) * 32, attn_resident(DP, WM)) k_tree_attn(AttnArgs A) {
-  constexpr int NW = WM > 4 ? WM : 4;
+__global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnArgs A) {
+  constexpr int NW = 4;
   constexpr int KG = NW / WM;          // key groups
   constexpr int KW = kTile / KG;       // keys of a warp
   constexpr int MT = WM * 16;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__((WM > 4 ? WM : 4) * 32, attn_resident(DP, WM))
     int64_t off = -1;
     if (kt0 + j < kt1 && pos < L) {
       const int pi = pos / A.page;
-      const int id = __ldg(A.table + (int64_t)req * A.max_pages + pi);
+      const int id = A.table[(int64_t)req * A.max_pages + pi];
       if ((unsigned)id < (unsigned)A.pages)
         off = (int64_t)id * A.page_stride + (int64_t)(pos - pi * A.page) * A.token_stride + (int64_t)head * A.head_stride;
       else
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__((WM > 4 ? WM : 4) * 32, attn_resident(DP, WM))
     const int m = row0 + wm * 16 + g + 8 * h;
     live[h] = m < rows;
     const int tok = t0 + (live[h] ? m / A.grp : 0), hq = head * A.grp + (live[h] ? m % A.grp : 0);
-    see[h] = live[h] ? (uint32_t)__ldg(A.anc + tok) : 0u;
+    see[h] = live[h] ? (uint32_t)A.anc[tok] : 0u;
     qp[h] = A.q + ((int64_t)tok * A.hkv * A.grp + hq) * A.D;
   }
 #pragma unroll
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__((WM > 4 ? WM : 4) * 32, attn_resident(DP, WM))
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = s * 16 + 2 * t + 8 * (i >> 1);
-      qf[s][i] = live[i & 1] && c < A.D ? __ldg(reinterpret_cast<const uint32_t *>(qp[i & 1] + c)) : 0u;
+      qf[s][i] = live[i & 1] && c < A.D ? *reinterpret_cast<const uint32_t *>(qp[i & 1] + c) : 0u;
     }
   __syncthreads();
   copy(0);
@@ -397,8 +397,8 @@ __global__ void __launch_bounds__((WM > 4 ? WM : 4) * 32, attn_resident(DP, WM))
 #pragma unroll
             for (int e = 0; e < DP / 8; ++e)
               if (e * 8 + 2 * t < A.D) {
-                acc[e][2 * h] = fmaf(p[h], __half2float(__ldg(vr + e * 8 + 2 * t)), acc[e][2 * h]);
-                acc[e][2 * h + 1] = fmaf(p[h], __half2float(__ldg(vr + e * 8 + 2 * t + 1)), acc[e][2 * h + 1]);
+                acc[e][2 * h] = fmaf(p[h], __half2float(vr[e * 8 + 2 * t]), acc[e][2 * h]);
+                acc[e][2 * h + 1] = fmaf(p[h], __half2float(vr[e * 8 + 2 * t + 1]), acc[e][2 * h + 1]);
               }
           }
         }
@@ -611,14 +611,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     uint64_t *full = is_k ? full_k : full_v, *empty = is_k ? empty_k : empty_v;
     int64_t(*off)[kTile] = s_off[warp - 4];
     auto offsets = [&](int j) {                    // two keys a lane
-      if (TMA || j >= tiles) return;
+      if (j >= tiles) return;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int pos = (kt0 + j) * kTile + 32 * h + lane;
         int64_t o = -1;
         if (pos < L) {
           const int pi = pos / A.page;
-          const int id = __ldg(A.table + (int64_t)req * A.max_pages + pi);
+          const int id = A.table[(int64_t)req * A.max_pages + pi];
           if ((unsigned)id < (unsigned)A.pages)
             o = (int64_t)id * A.page_stride + (int64_t)(pos - pi * A.page) * A.token_stride + (int64_t)head * A.head_stride;
           else
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     constexpr int RP = 32 / CH, ROWS = kTile / RP;
     const int r0 = lane / CH, c = lane % CH;
     const bool col = c * 8 < A.D;
-    offsets(0);
+    if (!TMA) offsets(0);
     // tile j has landed; drafted values are looked over first
     auto hand_on = [&](int j) {
       const int sl = j % NS, pos0 = (kt0 + j) * kTile;
@@ -667,27 +667,22 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     int marked = 0;                                // tiles that had to be looked over
     if (TMA) {
       const int nb = kTile / A.box;
-      // lane b: box b of tile j, as a page and a token of it
+      // lane b: box b of tile j, as the table's entry (looked at a tile later, when it
+      // has come) and a token of that page, -1: no such box
       auto page_of = [&](int j, int &tok) {
         const int pos = (kt0 + j) * kTile + lane * A.box;
-        int id = -1;
-        tok = 0;
-        if (j < tiles && lane < nb && pos < L) {
-          const int pi = pos / A.page;
-          tok = pos - pi * A.page;
-          id = __ldg(A.table + (int64_t)req * A.max_pages + pi);
-          if ((unsigned)id >= (unsigned)A.pages) {
-            flag_error(A.err, kErrIndex);
-            id = -1;
-          }
-        }
-        return id;
+        tok = -1;
+        if (j >= tiles || lane >= nb || pos >= L) return -1;
+        const int pi = pos / A.page;
+        tok = pos - pi * A.page;
+        return (int)A.table[(int64_t)req * A.max_pages + pi];
       };
       int tok, id = page_of(0, tok);
       const uint32_t bytes = kTile * DP * 2;
       for (int j = 0; j < tiles; ++j) {
         const int sl = j % NS, pos0 = (kt0 + j) * kTile;
-        const int now = id, at = tok;
+        const int at = tok, now = tok >= 0 && (unsigned)id < (unsigned)A.pages ? id : -1;
+        if (at >= 0 && now < 0) flag_error(A.err, kErrIndex);
         id = page_of(j + 1, tok);
         if (j >= NS) {
           ok = warp_wait(&empty[sl], (uint32_t)((j / NS) - 1) & 1u, kTcWaitNs);
@@ -824,7 +819,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const bool live = m < rows;
     const int tok = t0 + (live ? m / A.grp : 0);
     // drafted tokens that the row sees, by their place in the request
-    const uint32_t see = live ? ((uint32_t)__ldg(A.anc + tok) >> t0) & (n >= 32 ? 0xffffffffu : (1u << n) - 1u) : 0u;
+    const uint32_t see = live ? ((uint32_t)A.anc[tok] >> t0) & (n >= 32 ? 0xffffffffu : (1u << n) - 1u) : 0u;
     const uint32_t tl = tbase + ((uint32_t)(32 * warp) << 16);
     {
       // the row of Q; a row past the request's is zeros
@@ -845,7 +840,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       mbar_arrive(bq);
     }
     float ref = 0.f, sum = 0.f;
-    bool any = false, ok = true;                   // a key seen so far
+    bool ok = true;                                // sum: 0 until a key is seen (the reference's weighs 2^-8 at least; NaN stays)
     for (int j = 0; j < tiles; ++j) {
       const uint32_t sc = tl + 128 + 64 * (j & 1);
       const int pos0 = (kt0 + j) * kTile, sl = j % NS;
@@ -877,7 +872,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
       for (int i = 0; i < kTile; ++i) top = fmaxf(top, z[i]);
       // a new reference for the warp's rows where some row needs one
-      const bool grow = top != -INFINITY && (!any || top > ref + 8.f);
+      const bool grow = top != -INFINITY && (sum == 0.f || top > ref + 8.f);
       const bool redo = __any_sync(0xffffffffu, grow);
       const bool extra = d < kTile && s_any[sl];
       if ((redo || extra) && j > 0) {              // O must rest: the product of the last tile is done
@@ -888,29 +883,28 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       }
       if (redo) {
         const float now = grow ? top : ref;
-        const float f = any ? exp2_fast(ref - now) : 0.f;
+        const float f = sum != 0.f ? exp2_fast(ref - now) : 0.f;
         if (j > 0) {
 #pragma unroll
           for (int c = 0; c < DP; c += 16) {
             float o[16];
             tmem_ld16w(tl + c, o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = any ? o[i] * f : 0.f;
+            for (int i = 0; i < 16; ++i) o[i] = sum != 0.f ? o[i] * f : 0.f;
             tmem_st16(tl + c, o);
           }
           tmem_wait_st();
         }
-        sum = any ? sum * f : 0.f;
+        sum = sum != 0.f ? sum * f : 0.f;
         ref = now;
       }
-      any |= top != -INFINITY;
       if (extra) {
         // the chunks of v left out, for the rows that see their keys
 #pragma unroll 1
         for (int i = max(0, d); i < kTile && pos0 + i < L; ++i) {
           const uint32_t bad = s_nonfin[sl][i];
           if (!bad) continue;                      // the same for every lane
-          const int pos = pos0 + i, pi = pos / A.page, id = __ldg(A.table + (int64_t)req * A.max_pages + pi);
+          const int pos = pos0 + i, pi = pos / A.page, id = A.table[(int64_t)req * A.max_pages + pi];
           const __half *v = A.v + (int64_t)id * A.page_stride + (int64_t)(pos - pi * A.page) * A.token_stride +
                             (int64_t)head * A.head_stride;
           const bool on = (sees >> i) & 1;
@@ -923,7 +917,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             tmem_ld16w(tl + 8 * h, o);
 #pragma unroll
             for (int q = 0; q < 16; ++q)
-              if (on && ((bad >> (h + (q >> 3))) & 1u)) o[q] = fmaf(w, __half2float(__ldg(v + 8 * h + q)), o[q]);
+              if (on && ((bad >> (h + (q >> 3))) & 1u)) o[q] = fmaf(w, __half2float(v[8 * h + q]), o[q]);
             __syncwarp();
             tmem_st16(tl + 8 * h, o);
             tmem_wait_st();
@@ -954,7 +948,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     if (!ok && lane == 0) flag_error(A.err, kErrTimeout);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;                      // nothing seen: zeros
     const int64_t at = (int64_t)blockIdx.x * MT + tid;
-    if (splits > 1 && live) __stcg(A.ml + at, make_float2(any ? ref : -INFINITY, sum));
+    if (splits > 1 && live) __stcg(A.ml + at, make_float2(sum != 0.f ? ref : -INFINITY, sum));
     __half *op = A.o + ((int64_t)tok * A.hkv * A.grp + head * A.grp + (live ? m % A.grp : 0)) * A.D;
 #pragma unroll
     for (int c = 0; c < DP; c += 16) {
@@ -1055,9 +1049,16 @@ __global__ void __launch_bounds__(128) k_kv_append(AppendArgs A) {
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= A.T * per) return;
   const int tok = i / per, head = i % per / (A.D / 8), c = i % (A.D / 8);
-  int r = 0;                           // the request whose range holds the token
+  int r = 0, from_r = ld_cg_i32(A.begin);   // r: the request whose range holds the token
+  bool bad = from_r < 0;
 #pragma unroll 8
-  for (int q = 1; q <= A.R; ++q) r += tok >= ld_cg_i32(A.begin + q);
+  for (int q = 1; q <= A.R; ++q) {
+    const int b = ld_cg_i32(A.begin + q);
+    bad |= b < from_r || b > A.T;
+    from_r = b;
+    r += tok >= b;
+  }
+  if (bad && i == 0) flag_error(A.err, kErrIndex);
   if (r >= A.R) return;                // behind the last range: nothing is written
   const int t0 = ld_cg_i32(A.begin + r);
   if (tok < t0) return;
@@ -1065,7 +1066,7 @@ __global__ void __launch_bounds__(128) k_kv_append(AppendArgs A) {
   const int64_t pos = (int64_t)len + (tok - t0);
   const int64_t pi = pos / A.page;
   int id = -1;
-  if (t0 >= 0 && len >= 0 && pi < A.max_pages) id = __ldg(A.table + (int64_t)r * A.max_pages + pi);
+  if (t0 >= 0 && len >= 0 && pi < A.max_pages) id = A.table[(int64_t)r * A.max_pages + pi];
   if ((unsigned)id >= (unsigned)A.pages) {
     flag_error(A.err, kErrIndex);
     return;
@@ -1084,7 +1085,7 @@ asf_status check_cache(const asf_kv_cache *c) {
   if (c->head_dim % 8 || c->page_stride % 8 || c->token_stride % 8 || c->head_stride % 8) return ASF_ERR_MISALIGNED;
   if (!al16(c->k) || !al16(c->v)) return ASF_ERR_MISALIGNED;
   if (c->page_stride < 0 || c->token_stride < c->head_dim || c->head_stride < 0 ||
-      (c->heads > 1 && c->head_stride < c->head_dim))
+      (c->heads > 1 && c->head_stride < c->head_dim) || (c->pages > 1 && c->page_stride < c->head_dim))
     return ASF_ERR_INVALID_ARG;
   return ASF_OK;
 }
@@ -1113,15 +1114,14 @@ int attn_units_most(const asf_kv_cache *c, int grp, int R, int T, int wm) {
 }
 size_t attn_scratch(const asf_kv_cache *c, int grp, int R, int T) {
   const int wm = row_groups(grp, R, T);
-  const size_t rows = (size_t)attn_units_most(c, grp, R, T, wm) * 16 * wm;
+  const size_t rows = (size_t)attn_target(c, wm) * 16 * wm;   // more units than that: nothing is split
   return 512 + r256(rows * attn_dp(c) * 4) + r256(rows * 8);
 }
 
 template <int DP, int WM>
 cudaError_t run_attn(const AttnArgs &a, int units, cudaStream_t st) {
-  constexpr int NW = WM > 4 ? WM : 4;
   const size_t smem = (size_t)kStages * 2 * kTile * DP * 2;
-  return launch(k_tree_attn<DP, WM>, dim3(units), dim3(NW * 32), smem, st, a);
+  return launch(k_tree_attn<DP, WM>, dim3(units), dim3(128), smem, st, a);
 }
 // Map of a cache's keys or values: columns, tokens of a page, heads, pages; a
 // box is `box` tokens of one head and page by 64 columns, swizzled as the MMA
@@ -1205,6 +1205,8 @@ asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *table, i
   if (!al16(q) || !al16(o) || !al4(anc)) return ASF_ERR_MISALIGNED;
   s = check_ws(ws, ws_bytes, kHeaderBytes + attn_scratch(cache, grp, R, T));
   if (s != ASF_OK) return s;
+  const size_t bytes = (size_t)T * q_heads * cache->head_dim * 2;
+  if (overlap(q, bytes, o, bytes)) return ASF_ERR_INVALID_ARG;
   const int wm = row_groups(grp, R, T);
   const int units = attn_units_most(cache, grp, R, T, wm);
   unsigned char *base = static_cast<unsigned char *>(ws) + kHeaderBytes;
@@ -1228,11 +1230,12 @@ asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *table, i
   a.q = static_cast<const __half *>(q);
   a.anc = anc;
   a.scale = (float)((double)scale * 1.4426950408889634);
+  if (!std::isfinite(a.scale)) return ASF_ERR_INVALID_ARG;
   a.o = static_cast<__half *>(o);
   a.plan = reinterpret_cast<int4 *>(base);
   base += 512;
   a.part = reinterpret_cast<float *>(base);
-  a.ml = reinterpret_cast<float2 *>(base + r256((size_t)units * 16 * wm * attn_dp(cache) * 4));
+  a.ml = reinterpret_cast<float2 *>(base + r256((size_t)attn_target(cache, wm) * 16 * wm * attn_dp(cache) * 4));
   a.target = attn_target(cache, wm);
   a.err = &static_cast<Header *>(ws)->err;
   cudaStream_t st = (cudaStream_t)stream;

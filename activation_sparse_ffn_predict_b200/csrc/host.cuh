@@ -58,8 +58,11 @@ inline cudaError_t prepare_kernel(const void *kern, size_t smem, bool again) {
     if (e != cudaSuccess) return e;
   }
   cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared);
-  KernelAttrs &k = g_attrs[{kern, dev}];
-  k.smem = again ? smem : std::max(k.smem, smem);
+  try {
+    KernelAttrs &k = g_attrs[{kern, dev}];
+    k.smem = again ? smem : std::max(k.smem, smem);
+  } catch (...) {              // no memory to note it: set again by the next launch
+  }
   return cudaSuccess;
 }
 
@@ -91,6 +94,10 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, c
 
 inline bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool al4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
 inline size_t r256(size_t v) { return (v + 255) & ~size_t(255); }
 inline asf_status check_ws(void *ws, size_t ws_bytes, size_t need) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return ASF_ERR_WORKSPACE;

@@ -2,7 +2,7 @@
 // sparse FFN over 4-bit rows (include/asffn.h, "4-bit weights").
 //
 //   asf_w4_quantize / asf_w4_dequantize   k_w4_quantize, k_w4_dequantize
-//   asf_w4_matmul       y = act(W x + b)  k_w4_dot
+//   asf_w4_matmul       y = act(W x + b)  k_w4_dot, or k_w4_matmul_tc for fp16 x and many rows
 //   asf_w4_sparse_ffn   gate/up rows      k_w4_dot over the list
 //                       down projection   k_w4_down
 //
@@ -13,8 +13,8 @@
 // them as they are, straight from registers, and the group scale multiplies
 // the fp32 sum once per group: no weight is ever rounded.  x in fp16 is the
 // other operand as it is; x in fp32 is the exact sum of three bf16 parts
-// (8 + 8 + 8 mantissa bits, by truncation), multiplied in three instructions
-// into the same accumulators.
+// (8 + 8 + 8 mantissa bits, by truncation; below 2^-110 the last ones are lost),
+// multiplied in three instructions into the same accumulators.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -301,7 +301,6 @@ struct DotArgs {
   int relu;
   const int32_t *idx, *count;  // list form; null: all rows
   float *y;                    // dense: [B][rows]; list form: a [positions][8 * NT]
-  float *amax;                 // list form: a position's largest finite |a|
   int y16;                     // dense: y is fp16
   float *part;                 // partial tiles of a split k
   int most;                    // superblocks of k whose x fits a CTA
@@ -330,7 +329,7 @@ __device__ __forceinline__ int dot_per(int tiles, int nsb, int most, int ctas, i
     uint32_t key = 0xffffffffu;
     if (per <= most) {
       const int S = ceil_div(nsb, per);
-      if (per == most || (int64_t)tiles * S <= room) {
+      if (S <= ctas && (per == most || (int64_t)tiles * S <= room)) {
         const int c = ceil_div(tiles, ctas / S), w = c <= kDotWarps ? 4 : kDotWarps;
         const int u = max(8, ceil_div(c, w) * w);
         const int64_t cost = 8 * (int64_t)u * per + (S > 1 ? 8 * (12 + S) + (int64_t)u * NT : 0);
@@ -575,7 +574,6 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
       const int nrn = A.idx ? ld_cg_i32(A.idx + pos) : pos;
       const bool ok = (unsigned)nrn < (unsigned)A.rows;
       const float bias = ok ? __ldg(A.bias + nrn) : 0.f;
-      uint32_t top = 0;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float v[2];
@@ -585,16 +583,9 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
           a = a > 0.f ? a : (a != a ? a : 0.f);
           if (mode == kListGated) a *= tot[n][2 + c];
           v[c] = ok && 8 * n + 2 * t + c < A.B ? a : 0.f;
-          const uint32_t u = __float_as_uint(v[c]) & 0x7fffffffu;
-          if (u < 0x7f800000u) top = max(top, u);  // an infinity or NaN is its token's own affair
         }
         *reinterpret_cast<float2 *>(A.y + ((int64_t)pos * NT + n) * 8 + 2 * t) = make_float2(v[0], v[1]);
       }
-      // the four lanes of a row (all here, or none: pos is theirs)
-      const uint32_t quad = 0xfu << (lane & 28);
-      top = max(top, __shfl_xor_sync(quad, top, 1));
-      top = max(top, __shfl_xor_sync(quad, top, 2));
-      if (t == 0) A.amax[pos] = __uint_as_float(top);
     }
   };
   // the tile's partial sums, and with the unit's last ticket its whole sums
@@ -967,9 +958,10 @@ __global__ void __launch_bounds__(MatTc<N, GS>::THREADS, 1)
 // contracted dimension, so the scale, which changes with the neuron, joins the
 // activation: v = a s in fp32, times a power of two, split into two fp16 parts,
 // hi = fp16(v) and lo = fp16(v - hi): v to 2^-22, as the products' fp32 sums.
-// The power of two keeps the parts in fp16's range: a warp's largest v so far
-// lies below 2^15, and what is 2^20 below it still has 16 bits.  When a larger
-// one comes, the warp's sums are rescaled (exactly) to the new power.
+// The power of two keeps the parts in fp16's range.  Each warp has one for each
+// token, so that a token's sums do not depend on the others': its largest |v| so
+// far lies below 2^15, and what is 2^20 below it still has 16 bits.  When a
+// larger one comes, the token's sums are rescaled (exactly) to the new power.
 // D is 16 columns x 8 tokens.  Two neurons' words give one operand register by
 // a byte permutation of the packed codes, before they are unpacked: a word's
 // low half holds its even weights, its high half the odd ones.
@@ -979,20 +971,19 @@ struct DownArgs {
   int n, d;
   const int32_t *idx, *count;
   const float *a;              // [positions][8 * NT]
-  const float *amax;           // [positions]: largest finite magnitude of a row of a
   int B, R;                    // tokens, list splits
   float *part;                 // [R][B][d]
   float *y;
   Header *hdr;
 };
 
-// A warp's stage: 32 neurons' codes of one block of 128 columns, their scales,
-// and their activations with the largest of each neuron's.
+// A warp's stage: 32 neurons' codes of one block of 128 columns, their scales
+// and their activations.
 constexpr int kDownTile = 32;
 __host__ __device__ constexpr int down_stages(int NT) { return NT == 2 ? 3 : 4; }
 __host__ __device__ constexpr int down_scale_bytes(int GS) { return GS == 2 ? 8 : 4; }
 __host__ __device__ constexpr int down_stage_bytes(int NT, int GS) {
-  return kDownTile * (64 + down_scale_bytes(GS) + 4 + 32 * NT);
+  return kDownTile * (64 + down_scale_bytes(GS) + 32 * NT);
 }
 __host__ __device__ constexpr size_t down_smem(int NT, int GS) {
   const size_t ring = (size_t)kDownWarps * down_stages(NT) * down_stage_bytes(NT, GS);
@@ -1013,7 +1004,7 @@ template <int NT, int GS, bool PC>
 __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(DownArgs A) {
   extern __shared__ __align__(128) unsigned char sm[];
   constexpr int NS = down_stages(NT), SB = down_stage_bytes(NT, GS), SCB = down_scale_bytes(GS);
-  constexpr int kScales = kDownTile * 64, kTops = kScales + kDownTile * SCB, kActs = kTops + kDownTile * 4;
+  constexpr int kScales = kDownTile * 64, kActs = kScales + kDownTile * SCB;
   constexpr int RS = 8 * NT + 1;
   constexpr int P = PC ? 1 : 2;
   __shared__ uint32_t s_last;
@@ -1069,8 +1060,6 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
         const bool in = pos0 + c / (2 * NT) < total;
         cp_async16(to + c * 16, in ? A.a + pos0 * 8 * NT + c * 4 : A.a, in ? 16u : 0u);
       }
-      const bool in = pos0 + lane < total;
-      cp_async_small<4>(ring + slot * SB + kTops + lane * 4, in ? A.amax + pos0 + lane : A.amax, in);
     }
     cp_async_commit();
   };
@@ -1086,9 +1075,12 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
-  float up = 0.f;                                  // the power of two of the sums; 0: none yet
   // PC: column g is part g & 1 of token g / 2
   const int act0 = PC ? g >> 1 : g;
+  constexpr float kMostUp = 1.7014118e38f;         // 2^127
+  float up[NT];                                    // the power of two of column g of each token tile
+#pragma unroll
+  for (int n = 0; n < NT; ++n) up[n] = kMostUp;
   const int hi0 = GS == 0 ? (col0 / kBlk) & 1 : 0;
 
   int slot = 0;
@@ -1103,7 +1095,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
     for (int kk = 0; kk < 2; ++kk) {               // 16 neurons
       uint4 c[4];
       uint32_t sc[4][GS == 2 ? 2 : 1];
-      float av[4][NT], most[4];
+      float av[4][NT];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {                // this lane's: 2t, 2t+1, 2t+8, 2t+9
         const int row = 16 * kk + 2 * t + (q & 1) + 8 * (q >> 1);
@@ -1112,7 +1104,6 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
 #pragma unroll
         for (int w = 0; w < (GS == 2 ? 2 : 1); ++w)
           sc[q][w] = *reinterpret_cast<const uint32_t *>(st + kScales + row * SCB + 4 * w);
-        most[q] = *reinterpret_cast<const float *>(st + kTops + row * 4);
 #pragma unroll
         for (int n = 0; n < NT; ++n) av[q][n] = *reinterpret_cast<const float *>(st + kActs + ((row * NT + n) * 8 + act0) * 4);
       }
@@ -1120,37 +1111,54 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j % (4 >> GS) == 0) {                  // a new group of columns: a * s
-          float s[4];
-          uint32_t top = 0;
+          float v[NT][4], most = 0.f;
+          auto values = [&](int n) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            s[q] = half_of(sc[q][GS == 2 ? j >> 1 : 0], GS == 2 ? j & 1 : GS == 1 ? j >> 1 : hi0);
-            const uint32_t u = __float_as_uint(most[q] * s[q]);
-            top = max(top, u < 0x7f800000u ? u : 0u);          // scales are not negative; a NaN one is its rows' affair
+            for (int q = 0; q < 4; ++q) {
+              const float s = half_of(sc[q][GS == 2 ? j >> 1 : 0], GS == 2 ? j & 1 : GS == 1 ? j >> 1 : hi0);
+              v[n][q] = av[q][n] * s * up[n];      // (a s) first: s times the power alone can overflow
+            }
+          };
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            values(n);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) most = fmaxf(most, fabsf(v[n][q]));
           }
-          top = __reduce_max_sync(0xffffffffu, top);
-          // past the parts' range (or the first value at all): 2^11 <= the largest < 2^12 from here on
-          if ((up == 0.f || __uint_as_float(top) * up >= 32768.f) && top != 0) {
-            const int ex = min(max(127 + 11 - (int)(top >> 23) + 127, 1), 254);
-            const float now = __uint_as_float((uint32_t)ex << 23), f = up == 0.f ? 0.f : now / up;
-            up = now;
+          if (__any_sync(0xffffffffu, most >= 32768.f)) {      // past the parts' range: smaller powers
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int n = 0; n < NT; ++n) {
+              uint32_t top = 0;                    // the column's largest finite |a s|
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                acc[e][n][0] *= f;
-                acc[e][n][1] *= f;
-                acc[e][n][2] *= f;
-                acc[e][n][3] *= f;
+              for (int q = 0; q < 4; ++q) {
+                const float s = half_of(sc[q][GS == 2 ? j >> 1 : 0], GS == 2 ? j & 1 : GS == 1 ? j >> 1 : hi0);
+                const uint32_t u = __float_as_uint(av[q][n] * s) & 0x7fffffffu;
+                if (u < 0x7f800000u) top = max(top, u);        // an infinity or NaN is its token's own affair
               }
-          }
+              top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+              top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              float f = 1.f;
+              if (__uint_as_float(top) * up[n] >= 32768.f) {   // 2^11 <= the largest < 2^12 from here on
+                const float now = __uint_as_float((uint32_t)max(127 + 11 - (int)(top >> 23) + 127, 1) << 23);
+                f = now / up[n];
+                up[n] = now;
+              }
+              const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) s[q] *= up == 0.f ? 1.f : up;
+              for (int e = 0; e < 8; ++e) {        // columns 2t and 2t + 1
+                acc[e][n][0] *= f0;
+                acc[e][n][1] *= f1;
+                acc[e][n][2] *= f0;
+                acc[e][n][3] *= f1;
+              }
+              values(n);
+            }
+          }
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const float v0 = av[2 * q][n] * s[2 * q], v1 = av[2 * q + 1][n] * s[2 * q + 1];
+              const float v0 = v[n][2 * q], v1 = v[n][2 * q + 1];
               const __half2 hi = __floats2half2_rn(v0, v1);
               const float2 back = __half22float2(hi);
               const __half2 lo = __floats2half2_rn(v0 - back.x, v1 - back.y);
@@ -1184,7 +1192,12 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
   cp_async_wait<0>();
   __syncthreads();
   float *red = reinterpret_cast<float *>(sm);                  // [share][256 columns][8 * NT + 1]
-  const float down = up == 0.f ? 1.f : 1.f / up;
+  float down[NT][2];                               // of columns 2t and 2t + 1
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    down[n][0] = 1.f / __shfl_sync(0xffffffffu, up[n], 8 * t);
+    down[n][1] = 1.f / __shfl_sync(0xffffffffu, up[n], 8 * t + 4);
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -1194,7 +1207,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
         // row g of half h is weight 2p + (g >> 2) of word 4j + (g & 3), p = 2h (+1 for row g + 8)
         const int p = 2 * (i & 1) + (e >> 1);
         const int col = (warp & 1) * kBlk + (i >> 1) * 32 + sub * 8 + 2 * p + (g >> 2);
-        red[((warp >> 1) * kDownCols + col) * RS + 8 * n + 2 * t + (e & 1)] = acc[i][n][e] * down;
+        red[((warp >> 1) * kDownCols + col) * RS + 8 * n + 2 * t + (e & 1)] = acc[i][n][e] * down[n][e & 1];
       }
   __syncthreads();
   for (int i = threadIdx.x; i < A.B * kDownCols; i += blockDim.x) {
@@ -1247,7 +1260,7 @@ asf_status check_w4(const asf_w4_matrix *m) {
   if (m->group != 32 && m->group != 64 && m->group != 128) return ASF_ERR_UNSUPPORTED;
   if (m->rows <= 0 || m->k <= 0) return ASF_ERR_INVALID_ARG;
   if (m->k % 8 || m->row_stride % 16 || !al16(m->data)) return ASF_ERR_MISALIGNED;
-  if (m->k > ASF_W4_MAX_K) return ASF_ERR_UNSUPPORTED;
+  if (m->k > ASF_W4_MAX_K || m->rows > ASF_W4_MAX_ROWS) return ASF_ERR_UNSUPPORTED;
   if (m->row_stride < w4_row_bytes(m->k, m->group)) return ASF_ERR_INVALID_ARG;
   return ASF_OK;
 }
@@ -1263,7 +1276,7 @@ asf_status check_w4_ffn(const asf_w4_ffn *f) {
   if (f->group != 32 && f->group != 64 && f->group != 128) return ASF_ERR_UNSUPPORTED;
   if (f->d <= 0 || f->n <= 0) return ASF_ERR_INVALID_ARG;
   if (f->d % 8 || f->neuron_stride % 16 || !al16(f->data) || !al4(f->bias)) return ASF_ERR_MISALIGNED;
-  if (f->d > ASF_W4_MAX_K) return ASF_ERR_UNSUPPORTED;
+  if (f->d > ASF_W4_MAX_K || f->n > ASF_W4_MAX_ROWS) return ASF_ERR_UNSUPPORTED;
   if (f->neuron_stride < ffn_mats(f) * w4_row_bytes(f->d, f->group)) return ASF_ERR_INVALID_ARG;
   return ASF_OK;
 }
@@ -1294,7 +1307,7 @@ int down_w4_splits(int d, int B) {
 }
 size_t ffn_w4_scratch(const asf_w4_ffn *f, int B) {
   const int tiles = ceil_div(f->n, f->act == ASF_ACT_REGLU ? 8 : 16);
-  return r256((size_t)f->n * nt_of(B) * 32) + r256((size_t)f->n * 4) + dot_part_bytes(tiles, f->d, f->group, B) +
+  return r256((size_t)f->n * nt_of(B) * 32) + dot_part_bytes(tiles, f->d, f->group, B) +
          r256((size_t)down_w4_splits(f->d, B) * B * f->d * 4);
 }
 
@@ -1430,9 +1443,14 @@ asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dtype xdty
   if (!x || !y || B < 1 || B > ASF_MAX_BATCH || (relu != 0 && relu != 1)) return ASF_ERR_INVALID_ARG;
   if (xdtype != ASF_F16 && xdtype != ASF_F32) return ASF_ERR_UNSUPPORTED;
   if (ydtype != ASF_F16 && ydtype != ASF_F32) return ASF_ERR_UNSUPPORTED;
-  if (!al16(x) || !al4(y) || !al4(bias)) return ASF_ERR_MISALIGNED;
+  if (!al16(x) || (reinterpret_cast<uintptr_t>(y) & (ydtype == ASF_F16 ? 1u : 3u)) || !al4(bias)) return ASF_ERR_MISALIGNED;
   s = check_ws(ws, ws_bytes, kHeaderBytes + dot_part_bytes(ceil_div(mat->rows, 16), mat->k, mat->group, B));
   if (s != ASF_OK) return s;
+  if (overlap(x, (size_t)B * mat->k * (xdtype == ASF_F16 ? 2 : 4), y, (size_t)B * mat->rows * (ydtype == ASF_F16 ? 2 : 4)))
+    return ASF_ERR_INVALID_ARG;
+  // A part of k whose x fits a CTA is a CTA's at least: never so on a whole B200.
+  if (ceil_div(ceil_div(mat->k, kSuper), dot_most(mat->k, mat->group, B, xdtype == ASF_F32 ? 3 : 1)) > dot_ctas())
+    return ASF_ERR_UNSUPPORTED;
   // From 16 stages (of 128 rows x 256 weights) a CTA on, or 8 for more than 8
   // tokens: k_w4_matmul_tc costs 4 us more to start and end, and less per stage.
   // us, one token: 4096 x 4096 (3.5 stages) 11.8 against 7.4, 8192 x 8192 (14)
@@ -1478,6 +1496,8 @@ asf_status asf_w4_sparse_ffn(const asf_w4_ffn *f, const void *x, asf_dtype xdtyp
   if (!al16(x) || !al4(y) || !al4(idx) || !al4(count)) return ASF_ERR_MISALIGNED;
   s = check_ws(ws, ws_bytes, kHeaderBytes + ffn_w4_scratch(f, B));
   if (s != ASF_OK) return s;
+  if (ceil_div(ceil_div(f->d, kSuper), dot_most(f->d, f->group, B, xdtype == ASF_F32 ? 3 : 1)) > dot_ctas())
+    return ASF_ERR_UNSUPPORTED;
   const bool gated = f->act == ASF_ACT_REGLU;
   unsigned char *base = static_cast<unsigned char *>(ws) + kHeaderBytes;
   const int64_t rb = w4_row_bytes(f->d, f->group);
@@ -1494,8 +1514,6 @@ asf_status asf_w4_sparse_ffn(const asf_w4_ffn *f, const void *x, asf_dtype xdtyp
   a.count = count;
   a.y = reinterpret_cast<float *>(base);
   base += r256((size_t)f->n * nt_of(B) * 32);
-  a.amax = reinterpret_cast<float *>(base);
-  base += r256((size_t)f->n * 4);
   a.part = reinterpret_cast<float *>(base);
   base += dot_part_bytes(ceil_div(f->n, gated ? 8 : 16), f->d, f->group, B);
   a.hdr = static_cast<Header *>(ws);
@@ -1510,7 +1528,6 @@ asf_status asf_w4_sparse_ffn(const asf_w4_ffn *f, const void *x, asf_dtype xdtyp
   w.idx = idx;
   w.count = count;
   w.a = a.y;
-  w.amax = a.amax;
   w.B = B;
   w.R = down_w4_splits(f->d, B);
   w.part = reinterpret_cast<float *>(base);

@@ -33,8 +33,8 @@ class AttentionStage:
     def __init__(self, caches: Sequence[KVCache], q_heads: int, requests: int, max_pages: int, batch: int,
                  out: Optional[Sequence[W4Matrix]] = None):
         c0, n = caches[0], len(caches)
-        if any((c.heads, c.head_dim, c.device) != (c0.heads, c0.head_dim, c0.device) for c in caches):
-            raise ValueError("the layers' caches must have one head layout and device")
+        if any((c.heads, c.head_dim, c.page, c.device) != (c0.heads, c0.head_dim, c0.page, c0.device) for c in caches):
+            raise ValueError("the layers' caches must have one head layout, page size and device")
         if out is not None and (len(out) != n or any(m.k != q_heads * c0.head_dim for m in out)):
             raise ValueError("one projection of q_heads * head_dim columns per layer")
         self.caches, self.out, self.R, self.max_pages = list(caches), out, int(requests), int(max_pages)

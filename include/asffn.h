@@ -268,8 +268,11 @@ ASF_API asf_status asf_sparse_ffn_noalloc(const asf_ffn *ffn, const void *x, int
  * and asf_permute_rows move them.
  *
  * No weight is rounded on its way through a product: sums run in fp32, scales
- * multiply fp32 sums.  x is fp16 or fp32 (an fp32 x enters exactly). */
+ * multiply fp32 sums.  x is fp16 or fp32 (an fp32 x enters exactly; it must be
+ * finite and below 2^117, since a group's sum is formed before its scale).  A
+ * token's result does not depend on the call's other tokens' values. */
 #define ASF_W4_MAX_K 65536
+#define ASF_W4_MAX_ROWS (1 << 30)    /* rows of a matrix, neurons of a layer */
 
 typedef struct {
   int32_t rows, k;      /* weights are [rows][k]; k a multiple of 8, at most ASF_W4_MAX_K */
@@ -296,7 +299,7 @@ ASF_API int64_t asf_w4_row_bytes(int32_t k, int32_t group);
 /* Rows [rows][k] (fp16 or fp32, contiguous, 16-byte aligned) to 4 bits, into
  * mat->data: per group scale = fp16(max |w| / 7), code = clamp(round half to
  * even(w / scale), -8, 7) + 8, evaluated in fp32; a group of scale 0 gets code
- * 8.  A group with a NaN, an infinity or a maximum past fp16's range gets the
+ * 8.  A group with a NaN, an infinity or a scale past fp16's range gets the
  * scale NaN, so that no product over it looks sound. */
 ASF_API asf_status asf_w4_quantize(const void *src, asf_dtype dtype, const asf_w4_matrix *mat, asf_stream_t stream);
 
@@ -309,17 +312,19 @@ ASF_API asf_status asf_w4_dequantize(const asf_w4_matrix *mat, void *dst, asf_dt
 ASF_API size_t asf_w4_workspace_bytes(const asf_w4_matrix *mat, const asf_w4_ffn *ffn, int32_t max_batch);
 
 /* y[b][i] = act(sum_k w[i][k] x[b][k] + bias[i]) for 1 <= B <= ASF_MAX_BATCH tokens.
- *   x     device [B][k] in xdtype, 16-byte aligned (an fp32 x must be finite)
+ *   x     device [B][k] in xdtype, 16-byte aligned
  *   bias  device fp32 [rows], or NULL
  *   relu  0: none, 1: max(., 0)
- *   y     device [B][rows] in ydtype (fp16: the fp32 sum rounded once), overwritten */
+ *   y     device [B][rows] in ydtype (fp16: the fp32 sum rounded once), overwritten;
+ *         must not overlap x */
 ASF_API asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dtype xdtype, int32_t B,
                                  const float *bias, int32_t relu, void *y, asf_dtype ydtype, void *ws,
                                  size_t ws_bytes, asf_stream_t stream);
 
 /* asf_sparse_ffn over 4-bit rows: x [B][d] in xdtype, idx/count/y as there;
  * idx and count both NULL runs all n neurons (asf_dense_ffn).  The activations
- * between the two products stay fp32. */
+ * between the two products are fp32; with its scale, one enters the second
+ * product in 22 bits (16 where it is 2^20 below its token's largest). */
 ASF_API asf_status asf_w4_sparse_ffn(const asf_w4_ffn *ffn, const void *x, asf_dtype xdtype, int32_t B,
                                      const int32_t *idx, const int32_t *count, float *y, void *ws, size_t ws_bytes,
                                      asf_stream_t stream);
@@ -355,7 +360,9 @@ typedef struct {
   int32_t pages, page;               /* pages, and tokens in each */
   int32_t heads, head_dim;           /* kv heads; head_dim a multiple of 8, at most 128 */
   void *k, *v;                       /* device fp16, 16-byte aligned, one layout for both */
-  int64_t page_stride, token_stride, head_stride;   /* elements, multiples of 8 */
+  /* elements, multiples of 8; token_stride, and the others where there are
+   * several pages or heads, at least head_dim */
+  int64_t page_stride, token_stride, head_stride;
 } asf_kv_cache;
 
 /* Workspace bytes of asf_tree_attention for up to R requests and T tokens with
@@ -370,7 +377,7 @@ ASF_API asf_status asf_kv_append(const asf_kv_cache *cache, const int32_t *table
 
 /* o[t][h] = sum over the keys p that t sees of softmax_p(scale q[t][h] . k_p) v_p,
  * query head h reading kv head h / (q_heads / heads).
- *   q, o  device fp16 [T][q_heads][head_dim], 16-byte aligned
+ *   q, o  device fp16 [T][q_heads][head_dim], 16-byte aligned, without overlap
  *   anc   device 32-bit masks [T] */
 ASF_API asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
                                       const int32_t *lens, const int32_t *begin, int32_t T, int32_t q_heads,

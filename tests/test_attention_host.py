@@ -65,6 +65,16 @@ def test_arguments_refused(lib):
         assert lib.asf_attention_workspace_bytes(ctypes.byref(c), *bad) == 0
 
 
+def test_overlaps_are_refused(lib):
+    c = ctypes.byref(_cache())
+    ws = lib.asf_attention_workspace_bytes(c, 4, 1, 1)
+    for o in (FAKE, FAKE + 4 * 64 * 2 - 16):
+        assert lib.asf_tree_attention(c, FAKE, 4, 1, FAKE, FAKE, 1, 4, FAKE, FAKE, 1.0, o, FAKE, ws, None) == L.ASF_ERR_INVALID_ARG
+    assert lib.asf_attention_workspace_bytes(ctypes.byref(_cache(ps=56)), 4, 1, 1) == 0     # pages over one another
+    assert lib.asf_tree_attention(c, FAKE, 4, 1, FAKE, FAKE, 1, 4, FAKE, FAKE, 3e38, FAKE + 4096, FAKE, ws, None) \
+        == L.ASF_ERR_INVALID_ARG
+
+
 def test_workspace_covers_fewer_requests_and_tokens(lib):
     c = ctypes.byref(_cache(heads=8, hs=64, ts=512, ps=8192))
     got = lib.asf_attention_workspace_bytes(c, 64, 4, 32)

@@ -157,6 +157,28 @@ def test_what_a_row_does_not_see_does_not_reach_it(n, grp, D, page):
     assert np.isnan(got[4, :grp, 3]).all() and np.isfinite(got[4, grp:]).all()
 
 
+@pytest.mark.parametrize("grp,page", [(2, 16), (40, 16), (40, 20)])
+def test_a_key_of_nan_that_is_seen_is_not_lost(grp, page):
+    """Scores that are all NaN for a tile, finite ones after it: NaN, as the softmax has it; the other head is sound."""
+    c = Case([200], [2], grp=grp, page=page, seed=13)
+    pg, sl = O.positions(c.table[0], page, 64)
+    c.k[pg, sl, 0] = np.nan
+    got = c.run()["o"].cpu().numpy()
+    assert np.isnan(got[:, :grp]).all() and np.isfinite(got[:, grp:]).all()
+
+
+def test_strides_of_dimensions_of_one():
+    c = Case([40], [1], hkv=1, grp=3, page=64, D=64, seed=14)
+    d = c.device()
+    pages = c.k.shape[0]
+    odd = lambda a: torch.as_strided(torch.from_numpy(a).cuda(), (pages, 64, 1, 64), (64 * 64, 64, 1, 1))  # noqa: E731
+    d["cache"] = A.KVCache(odd(c.k), odd(c.v))
+    c.check(c.run(d))
+    one = torch.from_numpy(c.k[:, 0]).cuda()                 # pages of one token, page by page
+    kk = torch.as_strided(one, (pages, 1, 1, 64), (64, 1, 1, 1))
+    assert A.KVCache(kk, kk).workspace_bytes(1, 1, 1) > 0
+
+
 @pytest.mark.parametrize("grp,D", [(2, 64), (16, 64), (12, 104)])
 def test_strided_caches(grp, D):
     """Pages laid out head by head, and keys and values side by side in one tensor."""
@@ -271,7 +293,7 @@ def test_python_refusals():
                 lambda: A.asf_kv_append(d["cache"], d["table"], d["lens"], d["begin"], d["kn"][:, :1], d["vn"], d["ws"])):
         with pytest.raises(ValueError):
             bad()
-    for bad in (lambda: att(q=d["q"][:, :3].contiguous(), o=d["o"][:, :3].contiguous()),
+    for bad in (lambda: att(q=d["q"][:, :3].contiguous(), o=d["o"][:, :3].contiguous()), lambda: att(o=d["q"]),
                 lambda: att(ws=A.Workspace._sized(4096, d["q"].device, None, "test"))):
         with pytest.raises(A.AsfError):
             bad()

@@ -206,6 +206,43 @@ def test_activations_of_very_different_sizes(B):
     _check_ffn(y[keep], "relu", data, bias, d, group, x[keep].astype(np.float64), np.arange(n))
 
 
+@pytest.mark.parametrize("B", [2, 4, 8, 16, 32])
+@pytest.mark.parametrize("act", ["relu", "reglu"])
+def test_a_token_does_not_depend_on_the_others(act, B):
+    """Every other token of the batch huge (a padded row that holds anything): the rest give the same bits as beside zeros."""
+    n, d, group = 700, 512, 128
+    data, bias = _layer(act, n, d, group, 21)
+    ffn = A.W4FFN(act, torch.from_numpy(data).cuda(), torch.from_numpy(bias).cuda(), d, group)
+    ws = A.Workspace.for_w4(ffn, B)
+    rng = np.random.default_rng(B)
+    x = rng.standard_normal((B, d)).astype(np.float32)
+    ys = []
+    for size in (0.0, 6e4):
+        x[1::2] = rng.standard_normal(x[1::2].shape).clip(-1, 1) * size
+        y = torch.empty(B, d, device="cuda")
+        A.asf_w4_sparse_ffn(ffn, torch.from_numpy(x).cuda().half(), None, None, y, ws)
+        _check_ffn(y, act, data, bias, d, group, torch.from_numpy(x).half().double().numpy(), np.arange(n))
+        ys.append(y[::2].clone())
+    assert torch.equal(*ys)
+
+
+@pytest.mark.parametrize("B", [1, 6, 12])
+def test_tiny_activations_beside_large_scales(B):
+    """Activations of 2^-115 and down weights of 2^-5, then zero activations and down weights of 2^9."""
+    n, d, group = 64, 256, 32
+    W = [_weights(n, d, 31 + i) for i in range(2)]
+    W[0][32:] = 0
+    W[1] *= np.where(np.arange(n) < 32, 2.0 ** -5, 2.0 ** 9)[:, None]
+    data = np.stack([O.w4_pack(w.astype(np.float32), group) for w in W], 1)
+    bias = np.zeros(n, np.float32)
+    x = (np.random.default_rng(B).standard_normal((B, d)) * 2.0 ** -115).astype(np.float32)
+    ffn = A.W4FFN("relu", torch.from_numpy(data).cuda(), torch.from_numpy(bias).cuda(), d, group)
+    y = torch.empty(B, d, device="cuda")
+    A.asf_w4_sparse_ffn(ffn, torch.from_numpy(x).cuda(), None, None, y, A.Workspace.for_w4(ffn, B))
+    _check_ffn(y, "relu", data, bias, d, group, x.astype(np.float64), np.arange(n))
+    assert (y != 0).any()
+
+
 def test_a_nan_group_reaches_only_its_rows():
     W = _weights(40, 512, 1)
     W[7, 300] = np.inf

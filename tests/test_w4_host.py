@@ -116,3 +116,12 @@ def test_workspace_grows_with_the_batch(lib):
     assert got == sorted(got)
     assert lib.asf_w4_workspace_bytes(None, None, 1) == 0
     assert lib.asf_w4_workspace_bytes(ctypes.byref(m), None, 0) == lib.asf_w4_workspace_bytes(ctypes.byref(m), None, 33) == 0
+
+
+def test_overlap_and_too_many_rows_are_refused(lib):
+    m = ctypes.byref(_mat())
+    ws = lib.asf_w4_workspace_bytes(m, None, 1)
+    for y in (FAKE, FAKE + 2 * 256 - 4):
+        assert lib.asf_w4_matmul(m, FAKE, L.ASF_F16, 1, None, 0, y, L.ASF_F32, FAKE, ws, None) == L.ASF_ERR_INVALID_ARG
+    assert lib.asf_w4_workspace_bytes(ctypes.byref(_mat(rows=L.ASF_W4_MAX_ROWS + 1)), None, 1) == 0
+    assert lib.asf_w4_matmul(m, FAKE, L.ASF_F16, 1, None, 0, FAKE + 1, L.ASF_F16, FAKE, ws, None) == L.ASF_ERR_MISALIGNED
