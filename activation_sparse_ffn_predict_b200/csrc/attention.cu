@@ -981,17 +981,18 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   }
 }
 
-// The splits of a row, in order: one warp per (token, query head).
-template <int DP>
+// The splits of a row (token, query head): W warps take every W-th split each,
+// with up to AHEAD in flight, and their sums meet in a fixed order.  What bounds
+// it is latency: plan, then maxima and sums beside the first parts.
+template <int DP, int W, int AHEAD>
 __global__ void __launch_bounds__(128) k_tree_merge(AttnArgs A, int MT) {
   constexpr int V = DP / 32;
+  __shared__ float s_m[4], s_l[4], s_o[4][DP];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int4 q = __ldcg(A.plan + lane);
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int hq = A.hkv * A.grp, tok = row / hq, hd = row % hq;
-  if (tok >= A.T) return;
+  const int row = blockIdx.x * (4 / W) + warp / W, hq = A.hkv * A.grp, tok = row / hq, hd = row % hq;
   const uint32_t who = __ballot_sync(0xffffffffu, tok >= q.x && tok < q.x + q.y);   // ranges do not overlap
   if (!who) return;
   const int r = __ffs(who) - 1;
@@ -1000,38 +1001,86 @@ __global__ void __launch_bounds__(128) k_tree_merge(AttnArgs A, int MT) {
   if (splits == 1) return;
   const int m = (tok - t0) * A.grp + hd % A.grp, head = hd / A.grp;
   const int64_t first = ((int64_t)base + (int64_t)head * splits * rt + m / MT) * MT + m % MT, step = (int64_t)rt * MT;
-  float M = -INFINITY;
-  for (int s = lane; s < splits; s += 32) M = fmaxf(M, __ldcg(&A.ml[first + s * step].x));
+  float M = -INFINITY, l = 0.f, o[V] = {};
+  for (int s0 = warp % W; s0 < splits; s0 += 32 * W) {         // this warp's: s0, s0 + W, ..., 32 of them at most
+    const int n = min(32, (splits - s0 + W - 1) / W);
+    auto part = [&](int i, float (&v)[V]) {
+      const float *p = A.part + (first + (int64_t)(s0 + W * i) * step) * DP + lane * V;
+      if constexpr (V == 4) {
+        const float4 u = __ldcg(reinterpret_cast<const float4 *>(p));
+        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+      } else {
+        const float2 u = __ldcg(reinterpret_cast<const float2 *>(p));
+        v[0] = u.x; v[1] = u.y;
+      }
+    };
+    float v[AHEAD][V] = {};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -INFINITY ? 0.f : M;
-  float l = 0.f, o[V] = {};
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s) {
-    const int64_t at = first + s * step;
-    const float2 ml = __ldcg(A.ml + at);
-    const float f = exp2_fast(ml.x - ref);
-    const float *p = A.part + at * DP + lane * V;
-    float v[V];
-    if constexpr (V == 4) {
-      const float4 u = __ldcg(reinterpret_cast<const float4 *>(p));
-      v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-    } else {
-      const float2 u = __ldcg(reinterpret_cast<const float2 *>(p));
-      v[0] = u.x; v[1] = u.y;
+    for (int i = 0; i < AHEAD; ++i)
+      if (i < n) part(i, v[i]);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n) ml = __ldcg(A.ml + first + (int64_t)(s0 + W * lane) * step);
+    float top = ml.x;
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    top = fmaxf(top, M);
+    const float ref = top == -INFINITY ? 0.f : top, fix = exp2_fast(M - ref), f = exp2_fast(ml.x - ref);
+    M = top;
+    l = fmaf(l, fix, f * ml.y);                    // a lane's share
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] *= fix;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const float w = __shfl_sync(0xffffffffu, f, i);
+      if (i < n) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[k] = fmaf(w, v[i][k], o[k]);
+      }
     }
-    l = fmaf(f, ml.y, l);
+#pragma unroll 8
+    for (int i = AHEAD; i < n; ++i) {
+      const float w = __shfl_sync(0xffffffffu, f, i);
+      part(i, v[0]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = fmaf(f, v[i], o[i]);
+      for (int k = 0; k < V; ++k) o[k] = fmaf(w, v[0][k], o[k]);
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  __half *op = A.o + (int64_t)row * A.D + lane * V;
 #pragma unroll
-  for (int i = 0; i < V; i += 2)
-    if (lane * V + i < A.D) *reinterpret_cast<uint32_t *>(op + i) = pack_h2(o[i] * inv, o[i + 1] * inv);
+  for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+  if (lane == 0) {
+    s_m[warp] = M;
+    s_l[warp] = l;
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) s_o[warp][lane * V + k] = o[k];
+  if (W == 1) __syncwarp();
+  else named_sync(1 + warp / W, 32 * W);
+  const int w0 = warp / W * W;
+  float top = s_m[w0], sum = 0.f;
+#pragma unroll
+  for (int w = 1; w < W; ++w) top = fmaxf(top, s_m[w0 + w]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float f[W];
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    f[w] = exp2_fast(s_m[w0 + w] - ref);
+    sum = fmaf(f[w], s_l[w0 + w], sum);
+  }
+  for (int d = 2 * (threadIdx.x % (32 * W)); d < A.D; d += 64 * W) {
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      x = fmaf(f[w], s_o[w0 + w][d], x);
+      y = fmaf(f[w], s_o[w0 + w][d + 1], y);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint32_t *>(A.o + (int64_t)row * A.D + d) = pack_h2(x * inv, y * inv);
+  }
 }
 
-// One 16-byte chunk of a token's keys and values per thread.
+// One 16-byte chunk of a token's keys and values per thread.  A lane of every
+// warp reads one request's range and length, all at once: the chain to the first
+// store is two loads (these, then the table) instead of four.
 struct AppendArgs {
   __half *k, *v;
   int64_t page_stride, token_stride, head_stride;
@@ -1045,24 +1094,24 @@ struct AppendArgs {
 __global__ void __launch_bounds__(128) k_kv_append(AppendArgs A) {
   pdl_wait();
   pdl_trigger();
-  const int per = A.hkv * (A.D / 8);
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= A.T * per) return;
-  const int tok = i / per, head = i % per / (A.D / 8), c = i % (A.D / 8);
-  int r = 0, from_r = ld_cg_i32(A.begin);   // r: the request whose range holds the token
-  bool bad = from_r < 0;
-#pragma unroll 8
-  for (int q = 1; q <= A.R; ++q) {
-    const int b = ld_cg_i32(A.begin + q);
-    bad |= b < from_r || b > A.T;
-    from_r = b;
-    r += tok >= b;
+  const int lane = threadIdx.x & 31;
+  const int per = A.hkv * (A.D / 8), total = A.T * per;
+  const int i = blockIdx.x * blockDim.x + threadIdx.x, at = min(i, total - 1);
+  const int tok = at / per, head = at % per / (A.D / 8), c = at % (A.D / 8);
+  const int64_t from = ((int64_t)tok * A.hkv + head) * A.D + c * 8;
+  const uint4 key = *reinterpret_cast<const uint4 *>(A.kn + from), val = *reinterpret_cast<const uint4 *>(A.vn + from);
+  int b0 = 0, b1 = A.T, n = 0;
+  if (lane < A.R) {
+    b0 = ld_cg_i32(A.begin + lane);
+    b1 = ld_cg_i32(A.begin + lane + 1);
+    n = ld_cg_i32(A.lens + lane);
   }
+  const bool bad = __any_sync(0xffffffffu, b0 < 0 || b1 < b0 || b1 > A.T);
   if (bad && i == 0) flag_error(A.err, kErrIndex);
-  if (r >= A.R) return;                // behind the last range: nothing is written
-  const int t0 = ld_cg_i32(A.begin + r);
-  if (tok < t0) return;
-  const int len = ld_cg_i32(A.lens + r);
+  int r = 0;                           // the request whose range holds the token
+  for (int q = 0; q < A.R; ++q) r += tok >= __shfl_sync(0xffffffffu, b1, q);
+  const int t0 = __shfl_sync(0xffffffffu, b0, r & 31), len = __shfl_sync(0xffffffffu, n, r & 31);
+  if (i >= total || r >= A.R || tok < t0) return;   // behind the last range: nothing is written
   const int64_t pos = (int64_t)len + (tok - t0);
   const int64_t pi = pos / A.page;
   int id = -1;
@@ -1071,10 +1120,9 @@ __global__ void __launch_bounds__(128) k_kv_append(AppendArgs A) {
     flag_error(A.err, kErrIndex);
     return;
   }
-  const int64_t at = (int64_t)id * A.page_stride + (pos - pi * A.page) * A.token_stride + (int64_t)head * A.head_stride + c * 8;
-  const int64_t from = ((int64_t)tok * A.hkv + head) * A.D + c * 8;
-  *reinterpret_cast<uint4 *>(A.k + at) = *reinterpret_cast<const uint4 *>(A.kn + from);
-  *reinterpret_cast<uint4 *>(A.v + at) = *reinterpret_cast<const uint4 *>(A.vn + from);
+  const int64_t to = (int64_t)id * A.page_stride + (pos - pi * A.page) * A.token_stride + (int64_t)head * A.head_stride + c * 8;
+  *reinterpret_cast<uint4 *>(A.k + to) = key;
+  *reinterpret_cast<uint4 *>(A.v + to) = val;
 }
 
 // ------------------------------------------------------------------ host --
@@ -1158,7 +1206,11 @@ cudaError_t run_attn_any(const AttnArgs &a, int wm, int units, cudaStream_t st) 
   if (e != cudaSuccess) return e;
   if ((int64_t)a.max_pages * a.page <= kWhole * kTile) return e;
   const int rows = a.T * a.hkv * a.grp;
-  return launch(k_tree_merge<DP>, dim3((rows + 3) / 4), dim3(128), 0, st, a, 16 * wm);
+  // Four warps a row where that is a few CTAs an SM at most, else one.  us of the
+  // whole call, one and four warps: 64 rows x 55 splits 42.9 and 35.8, 1024 rows
+  // 69.9 and 64.2; 2048 rows x 6 splits 65.6 and 70.1, 4096 rows 32.8 and 36.5.
+  return rows <= 8 * sm_count() ? launch(k_tree_merge<DP, 4, 16>, dim3(rows), dim3(128), 0, st, a, 16 * wm)
+                                : launch(k_tree_merge<DP, 1, 8>, dim3((rows + 3) / 4), dim3(128), 0, st, a, 16 * wm);
 }
 
 }  // namespace
