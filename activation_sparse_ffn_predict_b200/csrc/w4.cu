@@ -386,6 +386,21 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
   const int stages = ceil_div(b1 - b0, 2);
   const int step = ctas * kDotWarps;
 
+  // x's part: [P][B][b1-b0 blocks], rows 64 bytes past a multiple of 128 apart
+  // (eight lanes of a 16-byte read then touch every bank once)
+  const int kw = stages * 2 * kBlk;                // a last stage of one block multiplies zeros
+  const int xrow = kw * 2 + 64;
+  for (int i = threadIdx.x; i < kw / 8; i += blockDim.x)
+    *reinterpret_cast<uint4 *>(sx + (size_t)P * A.B * xrow + i * 16) = make_uint4(0, 0, 0, 0);
+  if constexpr (!BF) {                             // all of it in flight ahead of the rings (waiting for it: OPT shape, 16 tokens, 2 us more)
+    for (int i = threadIdx.x; i < A.B * (kw / 8); i += blockDim.x) {
+      const int b = i / (kw / 8), c = (i % (kw / 8)) * 8, kk = b0 * kBlk + c;
+      const __half *src = static_cast<const __half *>(A.x) + (int64_t)b * A.k + kk;
+      cp_async16(sx + (size_t)b * xrow + c * 2, kk < A.k ? src : A.x, kk < A.k ? 16u : 0u);
+    }
+    cp_async_commit();
+  }
+
   // ---- the copying side, ahead of the computing side
   struct {
     int unit, tile, stage;
@@ -455,19 +470,9 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
 #pragma unroll
   for (int i = 0; i < NS - 1; ++i) copy(i);
 
-  // x's part: [P][B][b1-b0 blocks], rows 64 bytes past a multiple of 128 apart
-  // (eight lanes of a 16-byte read then touch every bank once)
-  const int kw = stages * 2 * kBlk;                // a last stage of one block multiplies zeros
-  const int xrow = kw * 2 + 64;
-  for (int i = threadIdx.x; i < kw / 8; i += blockDim.x)
-    *reinterpret_cast<uint4 *>(sx + (size_t)P * A.B * xrow + i * 16) = make_uint4(0, 0, 0, 0);
-  for (int i = threadIdx.x; i < A.B * (kw / 8); i += blockDim.x) {
-    const int b = i / (kw / 8), c = (i % (kw / 8)) * 8, kk = b0 * kBlk + c;
-    if constexpr (!BF) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (kk < A.k) v = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(A.x) + (int64_t)b * A.k + kk);
-      *reinterpret_cast<uint4 *>(sx + (size_t)b * xrow + c * 2) = v;
-    } else {
+  if constexpr (BF) {
+    for (int i = threadIdx.x; i < A.B * (kw / 8); i += blockDim.x) {
+      const int b = i / (kw / 8), c = (i % (kw / 8)) * 8, kk = b0 * kBlk + c;
       float f[8] = {};
       if (kk < A.k) {
         const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(A.x) + (int64_t)b * A.k + kk);
@@ -483,6 +488,8 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A, int mod
         for (int e = 0; e < 8; ++e) f[e] -= trunc_bf16(f[e]);
       }
     }
+  } else {
+    cp_async_wait<NS - 1>();                       // x, the oldest group
   }
   __syncthreads();
 
