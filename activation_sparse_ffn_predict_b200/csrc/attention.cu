@@ -29,7 +29,8 @@ using namespace asf;
 namespace {
 
 constexpr int kTile = 64;              // keys per tile
-constexpr int kStages = 3;             // tiles in shared memory
+constexpr int kStages = 3;             // tiles in shared memory (k_tree_attn)
+constexpr int kClusterTiles = 4;       // key tiles that each CTA of a cluster takes at most
 constexpr int kMinChunk = 4;           // key tiles per split, at least
 constexpr int kWhole = 8;              // key tiles up to which nothing is split (no merge to launch)
 
@@ -48,6 +49,8 @@ struct AttnArgs {
   float2 *ml;                          // [unit][MT]: maximum (log2) and sum
   int4 *plan;                          // per request, for the merge: first token, tokens, splits, first unit
   int target;                          // CTAs to aim at
+  int whole;                           // key tiles up to which nothing is split
+  int cluster;                         // CTAs that share a unit
   int box;                             // keys of a TMA load, or 0
   int32_t *err;
 };
@@ -102,7 +105,7 @@ __device__ __forceinline__ Req plan_lane(const AttnArgs &A, int MT, int lane, in
     W += __shfl_xor_sync(0xffffffffu, W, o);
     most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
   }
-  C = max(most <= kWhole ? kWhole : kMinChunk, (int)((W * A.hkv + A.target - 1) / A.target));
+  C = max(most <= A.whole ? A.whole : kMinChunk, (int)((W * A.hkv + A.target - 1) / A.target));
   while (true) {
     q.splits = (q.nkt + C - 1) / C;
     int u = q.rt * q.splits * A.hkv;
@@ -147,6 +150,29 @@ __device__ __forceinline__ float exp2_fast(float v) {
   return r;
 }
 
+// shared memory of CTA `rank` of the cluster, at the address of this CTA's p
+__device__ __forceinline__ uint32_t peer_smem(const void *p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 ld_peer2(const void *p, int rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(peer_smem(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_peer4(const void *p, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer_smem(p, rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // CTAs of an SM: what their stages (48 or 96 KB), registers and, for k_tree_tc
 // (8 groups of 16 rows), tensor memory leave.
 __host__ __device__ constexpr int attn_resident(int DP, int WM) { return DP == 64 && WM < 8 ? 3 : 2; }
@@ -154,8 +180,11 @@ __host__ __device__ constexpr int attn_resident(int DP, int WM) { return DP == 6
 // A CTA is one unit: WM (1 or 2) groups of 16 query rows x KG groups of keys, a
 // warp each.  Keys and values of a tile go to shared memory by 16-byte cp.async, two
 // tiles ahead; 16-byte chunk c of row i sits at c ^ (i & 7), so that the
-// 8 x 8 matrix loads touch every bank once.
-template <int DP, int WM>
+// 8 x 8 matrix loads touch every bank once.  With CL > 1 a cluster of CTAs shares
+// the unit's tiles, CTA c every CL-th from c on, and adds its parts over
+// distributed shared memory: the form for few units of few tiles, which
+// otherwise leave most SMs idle and yet are not worth a merge of their own.
+template <int DP, int WM, int CL>
 __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnArgs A) {
   constexpr int NW = 4;
   constexpr int KG = NW / WM;          // key groups
@@ -163,12 +192,14 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
   constexpr int MT = WM * 16;
   constexpr int CH = DP / 8;           // 16-byte chunks of a row
   extern __shared__ __align__(128) unsigned char sm[];
-  __shared__ int64_t s_off[4][kTile];  // element offset of a key's row, -1: no such key
-  __shared__ int s_special[4];         // a tile with a key that some row does not see
+  constexpr int NST = kStages, SLOTS = 4;   // NST + 1 at least
+  __shared__ int64_t s_off[SLOTS][kTile];   // element offset of a key's row, -1: no such key
+  __shared__ int s_special[SLOTS];     // a tile with a key that some row does not see
   __shared__ int s_unit[10];
   __shared__ uint32_t s_nonfin[2];     // drafted values of a tile that are not finite
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
+  if (tid >= 32 && tid < 32 + SLOTS) s_special[tid - 32] = 0;
   pdl_wait();
   pdl_trigger();
   if (warp == 0) {
@@ -177,7 +208,7 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
     const Req q = plan_lane(A, MT, lane, C, units, bad);
     if (bad && blockIdx.x == 0) flag_error(A.err, kErrIndex);
     if (blockIdx.x == 0) A.plan[lane] = make_int4(q.t0, q.n, q.splits, q.base);
-    const int mine = q.rt * q.splits * A.hkv, u = (int)blockIdx.x - q.base;
+    const int mine = q.rt * q.splits * A.hkv, u = (int)blockIdx.x / CL - q.base;
     if (lane == 0) s_unit[0] = -1;
     __syncwarp();
     if (u >= 0 && u < mine) {
@@ -197,36 +228,55 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
   __syncthreads();
   const int req = s_unit[0];
   if (req < 0) return;
-  const int head = s_unit[1], row0 = s_unit[2] * MT, kt0 = s_unit[3], kt1 = s_unit[4];
+  // this CTA's tiles: kt0, kt0 + CL, ...
+  const int head = s_unit[1], row0 = s_unit[2] * MT, kt0 = s_unit[3] + (int)blockIdx.x % CL, kt1 = s_unit[4];
   const int t0 = s_unit[5], n = s_unit[6], len = s_unit[7], L = s_unit[8], splits = s_unit[9];
   const int rows = n * A.grp;
   const int wm = warp % WM, kg = warp / WM;
 
+  // a key's page, as the table has it
+  auto page_of = [&](int pos) { return A.table[(int64_t)req * A.max_pages + pos / A.page]; };
+  auto offset_of = [&](int pos, int id) -> int64_t {
+    if ((unsigned)id >= (unsigned)A.pages) {
+      flag_error(A.err, kErrIndex);
+      return -1;
+    }
+    return (int64_t)id * A.page_stride + (int64_t)(pos % A.page) * A.token_stride + (int64_t)head * A.head_stride;
+  };
   // offsets of a tile's keys
   auto offsets = [&](int j) {
     if (tid >= kTile) return;
-    const int slot = j & 3, pos = (kt0 + j) * kTile + tid;
-    int64_t off = -1;
-    if (kt0 + j < kt1 && pos < L) {
-      const int pi = pos / A.page;
-      const int id = A.table[(int64_t)req * A.max_pages + pi];
-      if ((unsigned)id < (unsigned)A.pages)
-        off = (int64_t)id * A.page_stride + (int64_t)(pos - pi * A.page) * A.token_stride + (int64_t)head * A.head_stride;
-      else
-        flag_error(A.err, kErrIndex);
-    }
+    const int slot = j & (SLOTS - 1), pos = (kt0 + j * CL) * kTile + tid;
+    const int64_t off = kt0 + j * CL < kt1 && pos < L ? offset_of(pos, page_of(pos)) : -1;
     s_off[slot][tid] = off;
     const bool sp = off < 0 || pos >= len;
     if (tid == 0) s_special[slot] = 0;
     asm volatile("bar.sync 1, 64;" ::: "memory");
     if (sp) s_special[slot] = 1;
   };
+  {
+    // of the first NST tiles, their table entries all at once (tile by tile: 2 us more)
+    int id[(NST + 1) / 2];
+#pragma unroll
+    for (int i = 0; i < (NST + 1) / 2; ++i) {
+      const int j = 2 * i + (tid >> 6), pos = (kt0 + j * CL) * kTile + (tid & 63);
+      id[i] = j < NST && kt0 + j * CL < kt1 && pos < L ? page_of(pos) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < (NST + 1) / 2; ++i) {
+      const int j = 2 * i + (tid >> 6), pos = (kt0 + j * CL) * kTile + (tid & 63);
+      if (j >= NST) continue;
+      const int64_t off = kt0 + j * CL < kt1 && pos < L ? offset_of(pos, id[i]) : -1;
+      s_off[j][tid & 63] = off;
+      if (off < 0 || pos >= len) s_special[j] = 1;
+    }
+  }
   auto copy = [&](int j) {             // 8 lanes a row: whole 128-byte lines
-    if (kt0 + j < kt1) {
-      unsigned char *kb = sm + (size_t)(j % kStages) * (2 * kTile * DP * 2), *vb = kb + kTile * DP * 2;
+    if (kt0 + j * CL < kt1) {
+      unsigned char *kb = sm + (size_t)(j % NST) * (2 * kTile * DP * 2), *vb = kb + kTile * DP * 2;
 #pragma unroll
       for (int i = tid >> 3; i < kTile; i += NW * 4) {
-        const int64_t off = s_off[j & 3][i];
+        const int64_t off = s_off[j & (SLOTS - 1)][i];
 #pragma unroll
         for (int c = tid & 7; c < CH; c += 8) {
           const bool in = off >= 0 && c * 8 < A.D;
@@ -238,9 +288,6 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
     }
     cp_async_commit();
   };
-  offsets(0);
-  offsets(1);
-  offsets(2);
 
   // this lane's two rows, their masks and their queries
   uint32_t see[2];
@@ -263,29 +310,29 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
       qf[s][i] = live[i & 1] && c < A.D ? *reinterpret_cast<const uint32_t *>(qp[i & 1] + c) : 0u;
     }
   __syncthreads();
-  copy(0);
-  copy(1);
+#pragma unroll
+  for (int j = 0; j < NST - 1; ++j) copy(j);
 
   float acc[DP / 8][4], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < DP / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
   const uint32_t smb = smem_u32(sm);
-  const int tiles = kt1 - kt0;
+  const int tiles = (kt1 - kt0 + CL - 1) / CL;
   for (int j = 0; j < tiles; ++j) {
-    cp_async_wait<kStages - 2>();
+    cp_async_wait<NST - 2>();
     __syncthreads();
-    copy(j + 2);
-    const uint32_t kb = smb + (uint32_t)(j % kStages) * (2 * kTile * DP * 2), vb = kb + kTile * DP * 2;
-    const bool special = s_special[j & 3];
+    copy(j + NST - 1);
+    const uint32_t kb = smb + (uint32_t)(j % NST) * (2 * kTile * DP * 2), vb = kb + kTile * DP * 2;
+    const bool special = s_special[j & (SLOTS - 1)];
     const int key0 = kg * KW;
-    const int pos0 = (kt0 + j) * kTile;
+    const int pos0 = (kt0 + j * CL) * kTile;
     uint32_t nonfin[2] = {0u, 0u};
     if (special && pos0 + kTile > len) {
       // A drafted value that is not finite would reach rows that do not see it
       // as 0 * NaN: take such rows of v out of the product, add them below.
       if (tid < 2) s_nonfin[tid] = 0u;
       __syncthreads();
-      unsigned char *vp = sm + (size_t)(j % kStages) * (2 * kTile * DP * 2) + kTile * DP * 2;
+      unsigned char *vp = sm + (size_t)(j % NST) * (2 * kTile * DP * 2) + kTile * DP * 2;
       for (int i = tid; i < kTile * CH; i += NW * 32) {
         if (pos0 + i / CH < len) continue;
         const uint4 u = *reinterpret_cast<const uint4 *>(vp + i * 16);
@@ -329,7 +376,7 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = key0 + i * 8 + 2 * t + (e & 1), d = pos0 + key - len;
-          const bool ok = s_off[j & 3][key] >= 0 && (d < 0 || ((see[e >> 1] >> ((t0 + d) & 31)) & 1u));
+          const bool ok = s_off[j & (SLOTS - 1)][key] >= 0 && (d < 0 || ((see[e >> 1] >> ((t0 + d) & 31)) & 1u));
           if (!ok) z[i][e] = -INFINITY;
         }
     }
@@ -390,7 +437,7 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
           float p[2];
           p[0] = __shfl_sync(0xffffffffu, c & 1 ? z[i][1] : z[i][0], from);
           p[1] = __shfl_sync(0xffffffffu, c & 1 ? z[i][3] : z[i][2], from);
-          const __half *vr = A.v + s_off[j & 3][key];
+          const __half *vr = A.v + s_off[j & (SLOTS - 1)][key];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (!((see[h] >> ((t0 + d) & 31)) & 1u)) continue;
@@ -404,7 +451,7 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
         }
     }
     __syncwarp();
-    offsets(j + 3);                    // its slot was last read before this iteration's barrier
+    offsets(j + NST);                  // its slot was last read before this iteration's barrier
   }
   cp_async_wait<0>();
 #pragma unroll
@@ -412,7 +459,7 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
     sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
     sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
   }
-  if constexpr (KG > 1) {              // the key groups' parts meet in shared memory
+  if constexpr (KG > 1 || CL > 1) {    // the key groups' parts meet in shared memory
     __syncthreads();
     float *so = reinterpret_cast<float *>(sm);                           // [KG][MT][DP]
     float *sml = so + KG * MT * DP;                                      // [KG][MT][2]
@@ -426,6 +473,38 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
 #pragma unroll
       for (int i = 0; i < DP / 8; ++i)
         *reinterpret_cast<float2 *>(so + (kg * MT + m) * DP + i * 8 + 2 * t) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+    }
+    if constexpr (CL > 1) {
+      // all CL x KG parts of a row, MT / CL rows a CTA, four columns a thread
+      cluster_sync();
+      const int rank = (int)blockIdx.x % CL;
+      for (int i = tid; i < MT / CL * (DP / 4); i += 128) {
+        const int row = rank * (MT / CL) + i / (DP / 4), c = i % (DP / 4) * 4, m = row0 + row;
+        float M = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 ml[CL * KG];
+        float4 v[CL * KG];
+#pragma unroll
+        for (int p = 0; p < CL * KG; ++p) {
+          ml[p] = ld_peer2(sml + ((p % KG) * MT + row) * 2, p / KG);
+          v[p] = ld_peer4(so + ((p % KG) * MT + row) * DP + c, p / KG);
+          M = fmaxf(M, ml[p].x);
+        }
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int p = 0; p < CL * KG; ++p) {
+          const float f = exp2_fast(ml[p].x - ref);
+          l = fmaf(f, ml[p].y, l);
+          o[0] = fmaf(f, v[p].x, o[0]); o[1] = fmaf(f, v[p].y, o[1]); o[2] = fmaf(f, v[p].z, o[2]); o[3] = fmaf(f, v[p].w, o[3]);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;                      // nothing seen: zeros
+        if (m < rows && c < A.D) {
+          __half *op = A.o + ((int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp) * A.D + c;
+          *reinterpret_cast<uint2 *>(op) = make_uint2(pack_h2(o[0] * inv, o[1] * inv), pack_h2(o[2] * inv, o[3] * inv));
+        }
+      }
+      __syncwarp();
+      cluster_sync();                  // nobody leaves while its parts are read
+      return;
     }
     __syncthreads();
     if (kg != 0) return;
@@ -1157,19 +1236,29 @@ int row_groups(int grp, int R, int T) {
 int row_tiles_most(int grp, int R, int T, int wm) { return T * grp / (16 * wm) + R; }
 int attn_dp(const asf_kv_cache *c) { return c->head_dim <= 64 ? 64 : 128; }
 int attn_target(const asf_kv_cache *c, int wm) { return sm_count() * attn_resident(attn_dp(c), wm); }
-int attn_units_most(const asf_kv_cache *c, int grp, int R, int T, int wm) {
-  return attn_target(c, wm) + c->heads * row_tiles_most(grp, R, T, wm);
-}
 size_t attn_scratch(const asf_kv_cache *c, int grp, int R, int T) {
   const int wm = row_groups(grp, R, T);
   const size_t rows = (size_t)attn_target(c, wm) * 16 * wm;   // more units than that: nothing is split
   return 512 + r256(rows * attn_dp(c) * 4) + r256(rows * 8);
 }
 
+// CTAs that share a unit (k_tree_attn), 1: no cluster, and splits with a merge
+// from kWhole tiles on.  A cluster where its CTAs find room at once and have
+// few tiles each; eight CTAs where that leaves an SM to each.  us of the call
+// with 1, 4 and 8: 8 heads x 200 keys 11.4, 9.4, 10.1; 500 keys 15.0, 10.2, 9.9;
+// 1000 keys 13.8, 12.4, 10.9; 2000 keys 14.0, 16.8, 13.0; 32 heads x 333 keys
+// 13.2, 10.7, 12.6; 1000 keys 15.3, 12.4, 13.2; 2000 keys 17.4, 17.9, 16.9.
+int cluster_of(int64_t keys, int units, int target) {
+  if (keys <= kTile) return 1;
+  if (keys > 4 * kTile && keys <= 8 * kClusterTiles * kTile && units * 8 <= sm_count()) return 8;
+  return keys <= 4 * kClusterTiles * kTile && units * 4 <= target ? 4 : 1;
+}
 template <int DP, int WM>
 cudaError_t run_attn(const AttnArgs &a, int units, cudaStream_t st) {
   const size_t smem = (size_t)kStages * 2 * kTile * DP * 2;
-  return launch(k_tree_attn<DP, WM>, dim3(units), dim3(128), smem, st, a);
+  if (a.cluster == 8) return launch_clusters(k_tree_attn<DP, WM, 8>, dim3(units * 8), dim3(128), smem, st, 8, a);
+  if (a.cluster == 4) return launch_clusters(k_tree_attn<DP, WM, 4>, dim3(units * 4), dim3(128), smem, st, 4, a);
+  return launch(k_tree_attn<DP, WM, 1>, dim3(units), dim3(128), smem, st, a);
 }
 // Map of a cache's keys or values: columns, tokens of a page, heads, pages; a
 // box is `box` tokens of one head and page by 64 columns, swizzled as the MMA
@@ -1204,7 +1293,7 @@ cudaError_t run_attn_any(const AttnArgs &a, int wm, int units, cudaStream_t st) 
                         : wm == 2 ? run_attn<DP, 2>(a, units, st)
                                   : run_tc<DP>(a, units, st);
   if (e != cudaSuccess) return e;
-  if ((int64_t)a.max_pages * a.page <= kWhole * kTile) return e;
+  if ((int64_t)a.max_pages * a.page <= a.whole * kTile) return e;       // no request can have splits
   const int rows = a.T * a.hkv * a.grp;
   // Four warps a row where that is a few CTAs an SM at most, else one.  us of the
   // whole call, one and four warps: 64 rows x 55 splits 42.9 and 35.8, 1024 rows
@@ -1260,7 +1349,11 @@ asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *table, i
   const size_t bytes = (size_t)T * q_heads * cache->head_dim * 2;
   if (overlap(q, bytes, o, bytes)) return ASF_ERR_INVALID_ARG;
   const int wm = row_groups(grp, R, T);
-  const int units = attn_units_most(cache, grp, R, T, wm);
+  const int64_t keys = (int64_t)max_pages * cache->page;
+  int units = cache->heads * row_tiles_most(grp, R, T, wm);
+  const int cluster = wm <= 2 ? cluster_of(keys, units, attn_target(cache, wm)) : 1;
+  const int whole = cluster > 1 ? kClusterTiles * cluster : kWhole;
+  if (keys > whole * kTile) units += attn_target(cache, wm);
   unsigned char *base = static_cast<unsigned char *>(ws) + kHeaderBytes;
   AttnArgs a{};
   a.k = static_cast<const __half *>(cache->k);
@@ -1289,6 +1382,8 @@ asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *table, i
   a.part = reinterpret_cast<float *>(base);
   a.ml = reinterpret_cast<float2 *>(base + r256((size_t)attn_target(cache, wm) * 16 * wm * attn_dp(cache) * 4));
   a.target = attn_target(cache, wm);
+  a.whole = whole;
+  a.cluster = cluster;
   a.err = &static_cast<Header *>(ws)->err;
   cudaStream_t st = (cudaStream_t)stream;
   return cuda_status(attn_dp(cache) == 64 ? run_attn_any<64>(a, wm, units, st) : run_attn_any<128>(a, wm, units, st));

@@ -66,9 +66,10 @@ inline cudaError_t prepare_kernel(const void *kern, size_t smem, bool again) {
   return cudaSuccess;
 }
 
+// cluster: CTAs of a thread-block cluster along x (1: none)
 template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                   Args... args) {
+cudaError_t launch_clusters(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, int cluster,
+                            Args... args) {
   cudaError_t e = prepare_kernel((const void *)kern, smem, false);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
@@ -77,11 +78,14 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, c
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
   if (e == cudaErrorInvalidValue || e == cudaErrorLaunchOutOfResources) {
     // a device that was reset has forgotten the attributes: once more with them
@@ -90,6 +94,11 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, c
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
   }
   return e;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
+  return launch_clusters(kern, grid, block, smem, st, 1, args...);
 }
 
 inline bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -51,7 +51,10 @@ class AttentionStage:
     def launches(self) -> int:
         """Kernels per layer: append, attention, the merge of split keys unless the table is too
         short for a split, and the projection."""
-        split = self.max_pages * self.caches[0].page > 512
+        c = self.caches[0]
+        sms = torch.cuda.get_device_properties(c.device).multi_processor_count
+        split = _attention_splits(self.max_pages * c.page, c.heads, c.head_dim, self.q.shape[2] // c.heads, self.R,
+                                  self.q.shape[1], sms)
         return 2 + int(split) + int(self.out is not None)
 
     def enqueue(self, l: int, x: torch.Tensor, stream=None) -> None:
@@ -213,6 +216,20 @@ class LayerStack:
 
     def release(self) -> None:
         self.graph = None
+
+
+def _attention_splits(keys: int, heads: int, head_dim: int, grp: int, R: int, T: int, sms: int) -> bool:
+    """Whether asf_tree_attention may split a request's keys (and then launches the merge) for a table
+    of that many keys: from 512 keys on, or 1024 or 2048 where few units have a cluster of 4 or 8 CTAs each."""
+    rows = -(-T // R) * grp
+    wm = 1 if rows <= 16 else 2 if rows <= 32 else 8
+    units = heads * (T * grp // (16 * wm) + R)
+    room = sms * (3 if head_dim <= 64 else 2)
+    if wm <= 2 and 256 < keys <= 2048 and units * 8 <= sms:
+        return False
+    if wm <= 2 and 64 < keys <= 1024 and units * 4 <= room:
+        return False
+    return keys > 512
 
 
 def _fused_sparse_ffn(d: int, dtype, B: int) -> bool:

@@ -103,6 +103,23 @@ def test_against_the_definition(lens, toks, kw):
     assert torch.equal(d["o"], first)                       # no order depends on timing
 
 
+@pytest.mark.parametrize("lens,toks,kw", [
+    ([64], [1], dict(hkv=1, grp=3, page=66)), ([2045], [3], dict(hkv=2, grp=4, D=128, page=2048)),
+    ([2046], [3], dict(hkv=2, grp=4, D=128, page=2049)), ([1000], [2], dict(hkv=32, grp=1, D=128, page=1024)),
+    ([0], [2], dict(hkv=8, grp=9, page=512)), ([255], [1], dict(hkv=8, grp=32, D=96, page=256)),
+    ([3, 300, 0, 129], [2, 1, 0, 4], dict(hkv=2, grp=2, D=40, page=128)), ([70, 1], [1, 1], dict(hkv=40, grp=2, page=64)),
+    ([100], [1], dict(hkv=100, grp=2, D=64, page=101)), ([900], [1], dict(hkv=74, grp=1, D=128, page=1024))])
+def test_short_requests(lens, toks, kw):
+    """Around the sizes at which a cluster takes a request's keys, of 4 or 8 CTAs, some of them without a tile."""
+    c = Case(lens, toks, seed=sum(lens) + len(toks), **kw)
+    d = c.run()
+    c.check(d)
+    first = d["o"].clone()
+    d["o"].fill_(0)
+    c.run(d)
+    assert torch.equal(d["o"], first)
+
+
 @pytest.mark.parametrize("grp,D", [(2, 64), (8, 64), (16, 64), (40, 128)])
 def test_large_scores_and_scale(grp, D):
     c = Case([700], [4], grp=grp, D=D, spread=40.0, seed=3)  # one key takes nearly all of the weight
