@@ -293,7 +293,6 @@ struct DotArgs {
   const unsigned char *data;   // first row (gate rows of the list form)
   int64_t stride;              // bytes from row to row (neuron to neuron)
   int64_t up;                  // bytes from a neuron's gate row to its up row
-  bool gated;                  // list form: REGLU (tiles of 8 gate rows over their 8 up rows)
   int rows;                    // rows, or neurons the list may name
   int k;
   const void *x;
@@ -348,9 +347,12 @@ __device__ __forceinline__ int dot_per(int tiles, int nsb, int most, int ctas, i
 // x's part sits in shared memory for the CTA's life.  With k split, a tile's
 // partial sums meet in the workspace and the warp that takes the tile's last
 // ticket adds them in the order of the splits.
-template <bool BF, int NT, int GS, bool LIST>
+enum { kDense = 0, kListUp = 1, kListGated = 2 };   // gated: tiles of 8 gate rows over their 8 up rows
+
+template <bool BF, int NT, int GS, int MODE>
 __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A) {
   extern __shared__ __align__(128) unsigned char sm[];
+  constexpr bool LIST = MODE != kDense, gated = MODE == kListGated;
   constexpr int P = BF ? 3 : 1;                    // parts of x
   constexpr int AC = NT == 1 ? 2 : 1;              // accumulators of a group: a shorter chain where one token tile is all
   constexpr int NS = dot_stages(NT), SB = dot_stage_bytes(GS), SCB = 4 << GS;
@@ -358,7 +360,6 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A) {
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const bool gated = LIST && A.gated;
   int total = A.rows;
   if (LIST && A.count) {
     total = ld_cg_i32(A.count);
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A) {
       total = total < 0 ? 0 : A.rows;
     }
   }
-  const int per = gated ? 8 : 16;
+  constexpr int per = gated ? 8 : 16;
   const int tiles = ceil_div(total, per);
   const int nblk = w4_kp(A.k) / kBlk, nsb = ceil_div(nblk, 4);
   const int sb_per = dot_per(tiles, nsb, A.most, gridDim.x, NT, lane);
@@ -591,25 +592,25 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A) {
             else A.y[(int64_t)b * A.rows + r] = v;
           }
       }
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 1 && gated) continue;
-      const int pos = tile * per + g + 8 * h;
-      if (pos >= total) continue;
-      const bool ok = (unsigned)nrn[h] < (unsigned)A.rows;
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && gated) continue;
+        const int pos = tile * per + g + 8 * h;
+        if (pos >= total) continue;
+        const bool ok = (unsigned)nrn[h] < (unsigned)A.rows;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float v[2];
+        for (int n = 0; n < NT; ++n) {
+          float v[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float a = tot[n][2 * h + c] + bias[h];
-          a = a > 0.f ? a : (a != a ? a : 0.f);
-          if (gated) a *= tot[n][2 + c];
-          v[c] = ok && 8 * n + 2 * t + c < A.B ? a : 0.f;
+          for (int c = 0; c < 2; ++c) {
+            float a = tot[n][2 * h + c] + bias[h];
+            a = a > 0.f ? a : (a != a ? a : 0.f);
+            if (gated) a *= tot[n][2 + c];
+            v[c] = ok && 8 * n + 2 * t + c < A.B ? a : 0.f;
+          }
+          *reinterpret_cast<float2 *>(A.y + ((int64_t)pos * NT + n) * 8 + 2 * t) = make_float2(v[0], v[1]);
         }
-        *reinterpret_cast<float2 *>(A.y + ((int64_t)pos * NT + n) * 8 + 2 * t) = make_float2(v[0], v[1]);
       }
     }
   };
@@ -1344,22 +1345,22 @@ size_t ffn_w4_scratch(const asf_w4_ffn *f, int B) {
          r256((size_t)down_w4_splits(f->d, B) * B * f->d * 4);
 }
 
-template <bool BF, int NT, bool LIST>
+template <bool BF, int NT, int MODE>
 cudaError_t run_dot_nt(const DotArgs &a, int group, cudaStream_t st) {
   const size_t smem = dot_ring_bytes(NT, gs_of(group)) + x_bytes(a.B, BF ? 3 : 1, a.most);
   const dim3 grid(dot_ctas()), block(kDotWarps * 32);
-  return group == 128  ? launch(k_w4_dot<BF, NT, 0, LIST>, grid, block, smem, st, a)
-         : group == 64 ? launch(k_w4_dot<BF, NT, 1, LIST>, grid, block, smem, st, a)
-                       : launch(k_w4_dot<BF, NT, 2, LIST>, grid, block, smem, st, a);
+  return group == 128  ? launch(k_w4_dot<BF, NT, 0, MODE>, grid, block, smem, st, a)
+         : group == 64 ? launch(k_w4_dot<BF, NT, 1, MODE>, grid, block, smem, st, a)
+                       : launch(k_w4_dot<BF, NT, 2, MODE>, grid, block, smem, st, a);
 }
-template <bool LIST>
+template <int MODE>
 cudaError_t run_dot(DotArgs a, int group, asf_dtype xdtype, cudaStream_t st) {
   const bool bf = xdtype == ASF_F32;
   a.most = dot_most(a.k, group, a.B, bf ? 3 : 1);
   switch (nt_of(a.B)) {
-    case 1: return bf ? run_dot_nt<true, 1, LIST>(a, group, st) : run_dot_nt<false, 1, LIST>(a, group, st);
-    case 2: return bf ? run_dot_nt<true, 2, LIST>(a, group, st) : run_dot_nt<false, 2, LIST>(a, group, st);
-    default: return bf ? run_dot_nt<true, 4, LIST>(a, group, st) : run_dot_nt<false, 4, LIST>(a, group, st);
+    case 1: return bf ? run_dot_nt<true, 1, MODE>(a, group, st) : run_dot_nt<false, 1, MODE>(a, group, st);
+    case 2: return bf ? run_dot_nt<true, 2, MODE>(a, group, st) : run_dot_nt<false, 2, MODE>(a, group, st);
+    default: return bf ? run_dot_nt<true, 4, MODE>(a, group, st) : run_dot_nt<false, 4, MODE>(a, group, st);
   }
 }
 
@@ -1518,7 +1519,7 @@ asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dtype xdty
   a.y16 = ydtype == ASF_F16;
   a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(ws) + kHeaderBytes);
   a.hdr = static_cast<Header *>(ws);
-  return cuda_status(run_dot<false>(a, mat->group, xdtype, (cudaStream_t)stream));
+  return cuda_status(run_dot<kDense>(a, mat->group, xdtype, (cudaStream_t)stream));
 }
 
 asf_status asf_w4_sparse_ffn(const asf_w4_ffn *f, const void *x, asf_dtype xdtype, int32_t B, const int32_t *idx,
@@ -1539,7 +1540,6 @@ asf_status asf_w4_sparse_ffn(const asf_w4_ffn *f, const void *x, asf_dtype xdtyp
   a.data = static_cast<const unsigned char *>(f->data);
   a.stride = f->neuron_stride;
   a.up = rb;
-  a.gated = gated;
   a.rows = f->n;
   a.k = f->d;
   a.x = x;
@@ -1553,7 +1553,7 @@ asf_status asf_w4_sparse_ffn(const asf_w4_ffn *f, const void *x, asf_dtype xdtyp
   base += dot_part_bytes(ceil_div(f->n, gated ? 8 : 16), f->d, f->group, B);
   a.hdr = static_cast<Header *>(ws);
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = run_dot<true>(a, f->group, xdtype, st);
+  const cudaError_t e = gated ? run_dot<kListGated>(a, f->group, xdtype, st) : run_dot<kListUp>(a, f->group, xdtype, st);
   if (e != cudaSuccess) return ASF_ERR_CUDA;
   DownArgs w{};
   w.data = a.data + (ffn_mats(f) - 1) * rb;
