@@ -1486,13 +1486,15 @@ asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dtype xdty
   // A part of k whose x fits a CTA is a CTA's at least: never so on a whole B200.
   if (ceil_div(ceil_div(mat->k, kSuper), dot_most(mat->k, mat->group, B, xdtype == ASF_F32 ? 3 : 1)) > dot_ctas())
     return ASF_ERR_UNSUPPORTED;
-  // From 16 stages (of 128 rows x 256 weights) a CTA on, or 8 for more than 8
-  // tokens: k_w4_matmul_tc costs 4 us more to start and end, and less per stage.
-  // us, one token: 4096 x 4096 (3.5 stages) 11.8 against 7.4, 8192 x 8192 (14)
-  // 17.0 against 15.0, 28672 x 8192 (48) 37.5 against 43; 16 tokens: 8192 x 4096
-  // (7) 14.1 against 13.9, 11008 x 4096 (9) 15.4 against 19.1.
+  // k_w4_matmul_tc from so many stages (of 128 rows x 256 weights) a CTA on: it
+  // costs 4 us more to start and end, and less per stage, the more so the more
+  // tokens share the unpacked weights.  us of k_w4_dot and of it, one token:
+  // 8192 x 8192 (14 stages) 13.7 and 16.9, 28672 x 8192 (48) 41.5 and 37.6;
+  // 16 tokens: 11008 x 4096 (9) 13.9 and 15.2, 8192 x 8192 18.3 and 19.3, 28672 x
+  // 8192 56 and 39; 32 tokens: 8192 x 4096 (7) 16.5 and 19.4, 11008 x 4096 21.8
+  // and 19.9, 28672 x 8192 93 and 47.
   const int64_t stages = (int64_t)ceil_div(mat->rows, 128) * ceil_div(w4_kp(mat->k), kTcStageK);
-  if (xdtype == ASF_F16 && stages >= (int64_t)(B <= 8 ? 16 : 8) * dot_ctas()) {
+  if (xdtype == ASF_F16 && stages >= (int64_t)(B <= 8 ? 28 : B <= 16 ? 16 : 10) * dot_ctas()) {
     MatTcArgs t{};
     t.rows = mat->rows;
     t.k = mat->k;

@@ -97,6 +97,66 @@ def test_matmul(m, k, group, B, dt):
     assert A.asf_read_error(ws) == 0
 
 
+@pytest.mark.parametrize("m,k,group,B,pad", [
+    (34000, 4096, 128, 1, 0), (20011, 6920, 32, 3, 48), (12345, 12296, 64, 8, 0), (9001, 8712, 32, 13, 16),
+    (19000, 4096, 128, 16, 0), (1270, 65536, 64, 16, 0), (5000, 9608, 32, 32, 0), (12000, 4104, 64, 17, 32),
+    (100000, 264, 128, 29, 0), (200000, 8, 128, 20, 0), (25000, 2048, 64, 31, 0)])
+def test_matmul_of_many_rows(m, k, group, B, pad):
+    """fp16 x and enough rows for the product in tensor memory, against float64 products of the dequantised weights."""
+    torch.manual_seed(m)
+    W = torch.randn(m, k, device="cuda") * torch.exp2(torch.randint(-3, 3, (m, 1), device="cuda").float())
+    rb = A.asf_w4_row_bytes(k, group)
+    mat = A.W4Matrix(torch.full((m, rb + pad), 0xff, dtype=torch.uint8, device="cuda"), k, group)
+    A.asf_w4_quantize(W, mat)
+    assert (mat.data[:, rb:] == 0xff).all()
+    A.asf_w4_dequantize(mat, W)                             # exact in fp32
+    x = torch.randn(B, k, device="cuda").half()
+    bias = torch.randn(m, device="cuda")
+    ws = A.Workspace.for_w4(mat, B)
+    ref, mass = torch.empty(B, m, device="cuda", dtype=torch.float64), torch.empty(B, m, device="cuda", dtype=torch.float64)
+    for i in range(0, m, 8192):
+        w = W[i:i + 8192].double().t()
+        ref[:, i:i + 8192], mass[:, i:i + 8192] = x.double() @ w, x.double().abs() @ w.abs()
+    for use_bias, relu in ((False, False), (True, True)):
+        kw = dict(bias=bias if use_bias else None, relu=relu)
+        want = ref + (bias.double() if use_bias else 0)
+        want = want.clamp(min=0) if relu else want
+        y, again = (torch.full((B, m), float("nan"), device="cuda") for _ in range(2))
+        A.asf_w4_matmul(mat, x, y, ws, **kw)
+        _check(y, want.cpu().numpy(), (mass + bias.double().abs()).cpu().numpy(), k // group + 1)
+        A.asf_w4_matmul(mat, x, again, ws, **kw)
+        assert torch.equal(y, again)
+        half = torch.empty(B, m, device="cuda", dtype=torch.float16)
+        A.asf_w4_matmul(mat, x, half, ws, **kw)
+        assert torch.equal(half, y.half())
+    if B > 1:                                               # a token of NaN and infinities is its own affair
+        x[B - 1, 0], x[B - 1, k - 1] = float("nan"), float("inf")
+        A.asf_w4_matmul(mat, x, again, ws, bias=bias, relu=True)
+        assert torch.equal(y[:B - 1], again[:B - 1]) and torch.isnan(again[B - 1]).all()
+    assert A.asf_read_error(ws) == 0
+
+
+def test_matmul_of_many_rows_in_a_graph_on_another_stream():
+    m, k, B = 12000, 4104, 24
+    mat = A.W4Matrix.quantize(torch.randn(m, k, device="cuda"), 64)
+    ws = A.Workspace.for_w4(mat, B)
+    x, y = torch.randn(B, k, device="cuda").half(), torch.empty(B, m, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        A.asf_w4_matmul(mat, x, y, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        A.asf_w4_matmul(mat, x, y, ws)
+    for seed in range(3):
+        x.copy_(torch.randn(B, k))
+        graph.replay()
+        got = y.clone()
+        A.asf_w4_matmul(mat, x, y, ws)
+        assert torch.equal(got, y)
+
+
 def _layer(act, n, d, group, seed):
     mats = 3 if act == "reglu" else 2
     data = np.stack([O.w4_pack(_weights(n, d, seed + i), group) for i in range(mats)], 1)

@@ -101,3 +101,38 @@ def test_stack_refuses_what_does_not_fit():
     got = st.idx[0, :int(st.count[0])].cpu().numpy()
     ref = OW.w4_ffn("reglu", w4.data.cpu().numpy(), w.bias.cpu().numpy(), cfg.d, 32, st.x[0].double().cpu().numpy(), got)
     assert np.abs(st.y[0].cpu().numpy() - ref).max() <= 1e-5 * np.abs(ref).max() and st.read_error() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Products and attention side by side, each with its own workspace: the same bits as one after the other."""
+    ensure_built()
+    torch.manual_seed(3)
+    mat = A.W4Matrix.quantize(torch.randn(12000, 4096, device="cuda"), 64)
+    x, out = torch.randn(24, 4096, device="cuda").half(), torch.empty(24, 12000, device="cuda")
+    ffn = A.W4FFN.quantize("relu", None, torch.randn(900, 2048, device="cuda"), torch.randn(900, 2048, device="cuda"),
+                           torch.zeros(900, device="cuda"), 128)
+    xf, y = torch.randn(16, 2048, device="cuda").half(), torch.empty(16, 2048, device="cuda")
+    c = Case([3000, 17], [20, 2], hkv=4, grp=8, D=128, page=64, seed=5)
+    d = c.run()
+    wm, wf = A.Workspace.for_w4(mat, 24), A.Workspace.for_w4(ffn, 16)
+
+    def one():
+        A.asf_w4_matmul(mat, x, out, wm)
+        A.asf_w4_sparse_ffn(ffn, xf, None, None, y, wf)
+
+    one()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (out, y, d["o"])]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for t in (out, y, d["o"]):
+            t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            with torch.cuda.stream(streams[0]):
+                one()
+            with torch.cuda.stream(streams[1]):
+                c.run(d)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (out, y, d["o"])))
+    assert A.asf_read_error(wm) == A.asf_read_error(wf) == A.asf_read_error(d["ws"]) == 0
