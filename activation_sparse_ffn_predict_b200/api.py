@@ -40,9 +40,9 @@ def _stream(stream) -> ctypes.c_void_p:
 
 def _arg(t: torch.Tensor, name: str, device, dtype=None) -> int:
     """Address of a contiguous tensor on ``device``."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.get_device() != device.index:    # -1: not on a GPU
         raise ValueError(f"{name} must be a tensor on {device}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -53,15 +53,19 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _invoke(name: str, device, stream, *args) -> None:
     """Call a C entry point whose last argument is the stream: the given one, or
     ``device``'s current stream; with ``device`` current.  Raises on an error status."""
     fn = _FN.get(name) or _FN.setdefault(name, getattr(L.load(), name))
+    index = device.index
     if stream is None:
-        st = _raw_stream(device.index)
+        st = _raw_stream(index)
     else:
         st = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if device.index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, st)
     else:
         with torch.cuda.device(device):
@@ -197,7 +201,7 @@ class Workspace:
 
     def on(self, device) -> int:
         """Its address, for a call on ``device``."""
-        if self.buf.device != device:
+        if self.buf.get_device() != device.index:
             raise ValueError(f"the workspace must be on {device}")
         return self.buf.data_ptr()
 

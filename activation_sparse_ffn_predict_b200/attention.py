@@ -35,25 +35,26 @@ class KVCache:
 
 
 def _requests(cache: KVCache, table, lens, begin):
-    dev = cache.device
-    if table.dim() != 2 or lens.dim() != 1 or lens.shape[0] != table.shape[0]:
+    dev, of = cache.device, table.shape
+    if len(of) != 2 or lens.shape != of[:1]:
         raise ValueError("table must be [R, max_pages] and lens [R]")
-    R = lens.shape[0]
-    if begin.dim() != 1 or begin.shape[0] != R + 1:
+    R, max_pages = of
+    if begin.shape != (R + 1,):
         raise ValueError("begin must be [R + 1]")
-    return (_arg(table, "table", dev, torch.int32), int(table.shape[1]), R, _arg(lens, "lens", dev, torch.int32),
+    return (_arg(table, "table", dev, torch.int32), max_pages, R, _arg(lens, "lens", dev, torch.int32),
             _arg(begin, "begin", dev, torch.int32))
 
 
 def asf_kv_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin: torch.Tensor, k: torch.Tensor,
                   v: torch.Tensor, ws: Workspace, stream=None) -> None:
     """Write the tokens' k and v [T, heads, head_dim] at positions lens[r] + i of their requests."""
-    if k.dim() != 3 or k.shape[1] != cache.heads or k.shape[2] != cache.head_dim or v.shape != k.shape:
+    of = k.shape
+    if len(of) != 3 or of[1] != cache.heads or of[2] != cache.head_dim or v.shape != of:
         raise ValueError("k and v must be [T, heads, head_dim]")
     dev = cache.device
     req = _requests(cache, table, lens, begin)
     kp, vp = _arg(k, "k", dev, torch.float16), _arg(v, "v", dev, torch.float16)
-    _invoke("asf_kv_append", dev, stream, cache._ref, *req, k.shape[0], kp, vp, ws.on(dev), ws.nbytes)
+    _invoke("asf_kv_append", dev, stream, cache._ref, *req, of[0], kp, vp, ws.on(dev), ws.nbytes)
 
 
 def asf_tree_attention(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin: torch.Tensor, q: torch.Tensor,
@@ -63,9 +64,10 @@ def asf_tree_attention(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, 
 
     table int32 [R, max_pages], lens int32 [R], begin int32 [R + 1]; anc int32 [T]: which of the call's
     tokens each token sees, beside every key before lens.  scale: head_dim ** -0.5 unless given."""
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or o.shape != q.shape:
+    of = q.shape
+    if len(of) != 3 or of[2] != cache.head_dim or o.shape != of:
         raise ValueError("q and o must be [T, q_heads, head_dim]")
-    if anc.dim() != 1 or anc.shape[0] != q.shape[0]:
+    if anc.shape != of[:1]:
         raise ValueError("anc must be [T]")
     dev = cache.device
     req = _requests(cache, table, lens, begin)
@@ -73,5 +75,5 @@ def asf_tree_attention(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, 
     ap = _arg(anc, "anc", dev, torch.int32)
     if scale is None:
         scale = cache.head_dim ** -0.5
-    _invoke("asf_tree_attention", dev, stream, cache._ref, *req, q.shape[0], q.shape[1], qp, ap, scale, op, ws.on(dev),
+    _invoke("asf_tree_attention", dev, stream, cache._ref, *req, of[0], of[1], qp, ap, scale, op, ws.on(dev),
             ws.nbytes)

@@ -54,6 +54,8 @@ inline int64_t w4_row_bytes(int k, int group) { return (int64_t)w4_kp(k) / 2 + w
 // quotient v / s.  v (1/s) is within 2^-23 of it, relatively, and |v / s| < 8,
 // so wherever that product is 1e-5 or more off a half its rounding is the same;
 // the few others divide.  (Dividing always: 72 us for 11008 x 4096 in fp16.)
+// 11008 x 4096 in fp16 with the way back: 55 us, 4.1 TB/s of the four passes;
+// issue slots bound it (3.5 instructions a clock of 4).
 __device__ __forceinline__ void rows_of_cta(int nsb, int warp, int &lsh, int &sb, int64_t &row) {
   lsh = nsb > 4 ? 3 : nsb > 2 ? 2 : nsb > 1 ? 1 : 0;           // log2 of the warps of a row
   sb = warp & ((1 << lsh) - 1);
@@ -239,6 +241,7 @@ __device__ __forceinline__ uint32_t upper2(float lo, float hi) {
 
 // ----------------------------------------------------------- dequantize --
 // fp16: (c - 8) is exact in fp16, and its product with the scale rounds once.
+// HBM bounds it: 11008 x 4096 alone 22.6 us, 5.0 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_w4_dequantize(const unsigned char *__restrict__ src, int64_t stride, int rows, int k, int group, T *__restrict__ dst) {
@@ -347,6 +350,11 @@ __device__ __forceinline__ int dot_per(int tiles, int nsb, int most, int ctas, i
 // x's part sits in shared memory for the CTA's life.  With k split, a tile's
 // partial sums meet in the workspace and the warp that takes the tile's last
 // ticket adds them in the order of the splits.
+// What bounds it: start, first rows and ticket (4 us of the 6.8 us of 4096 x 4096
+// for one token; L2 holds its 9 MB); on long streams the unpacking and waits for
+// rows, 28672 x 8192 for one token 41.5 us, 2.9 TB/s.  The three forms are compiled
+// apart: one body for all took 7.25 us for 4096 x 4096, and 96 us instead of 88 for
+// the OPT-shaped layer of 16 tokens.
 enum { kDense = 0, kListUp = 1, kListGated = 2 };   // gated: tiles of 8 gate rows over their 8 up rows
 
 template <bool BF, int NT, int GS, int MODE>
@@ -684,6 +692,9 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A) {
 // The (row tile, stage) pairs are dealt out in one run of equal lengths per
 // CTA; tiles that fall to several CTAs meet in the workspace, where the one that
 // takes a tile's last ticket adds the parts in the order of the CTAs.
+// 28672 x 8192 (121 MB): 37.5 us for one token, 3.2 TB/s, 47 us for 32 tokens.
+// The unpacking warps bound it (issue slots 58% used, tensor pipe 9%), and with
+// many tokens the passes over the accumulators (32 tokens, groups of 64: 50.6 us).
 constexpr int kTcStageK = 256;
 template <int N, int GS>
 struct MatTc {
@@ -1034,6 +1045,11 @@ __host__ __device__ constexpr size_t down_smem(int NT, int GS) {
 // passed its own wait before this grid could start, so the list and the rows
 // are complete).  With PC (up to four tokens) the two parts of an activation
 // are two columns of one product instead of two products.
+// What bounds it: for one token its chain of loads and the ticket (3440 neurons of
+// d 8192, 14.5 MB: 17.9 us alone with cold rows, 26.3 us together with gate/up);
+// for 16 tokens the splitting, unpacking and products share the issue slots with
+// 16 warps an SM, all that the accumulators leave (13000 neurons of d 12288, 84 MB:
+// 60 us alone, tensor pipe 37%).
 template <int NT, int GS, bool PC>
 __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(DownArgs A) {
   extern __shared__ __align__(128) unsigned char sm[];

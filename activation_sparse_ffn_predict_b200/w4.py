@@ -119,10 +119,11 @@ def asf_w4_dequantize(mat: W4Matrix, dst: torch.Tensor, stream=None) -> None:
 def asf_w4_matmul(mat: W4Matrix, x: torch.Tensor, y: torch.Tensor, ws: Workspace,
                   bias: Optional[torch.Tensor] = None, relu: bool = False, stream=None) -> None:
     """y [B, m] = x [B, k] times the 4-bit rows (+ bias [m], then ReLU); x and y fp16 or fp32."""
-    if x.dtype not in _DT or x.dim() != 2 or x.shape[1] != mat.k:
+    xt, yt, of = _DT.get(x.dtype), _DT.get(y.dtype), x.shape
+    if xt is None or len(of) != 2 or of[1] != mat.k:
         raise ValueError("x must be [B, k], float16 or float32")
-    B = x.shape[0]
-    if y.dtype not in _DT or y.dim() != 2 or y.shape[0] != B or y.shape[1] != mat.rows:
+    B = of[0]
+    if yt is None or y.shape != (B, mat.rows):
         raise ValueError("y must be [B, rows], float16 or float32")
     dev = mat.device
     bp = None
@@ -131,17 +132,16 @@ def asf_w4_matmul(mat: W4Matrix, x: torch.Tensor, y: torch.Tensor, ws: Workspace
             raise ValueError("bias must be [rows]")
         bp = _arg(bias, "bias", dev, torch.float32)
     xp, yp = _arg(x, "x", dev), _arg(y, "y", dev)
-    _invoke("asf_w4_matmul", dev, stream, mat._ref, xp, _DT[x.dtype], B, bp, int(bool(relu)), yp, _DT[y.dtype], ws.on(dev),
-            ws.nbytes)
+    _invoke("asf_w4_matmul", dev, stream, mat._ref, xp, xt, B, bp, int(bool(relu)), yp, yt, ws.on(dev), ws.nbytes)
 
 
 def asf_w4_sparse_ffn(ffn: W4FFN, x: torch.Tensor, idx: Optional[torch.Tensor], count: Optional[torch.Tensor],
                       y: torch.Tensor, ws: Workspace, stream=None) -> None:
     """asf_sparse_ffn over 4-bit rows (x fp16 or fp32, y fp32); idx and count both None: all neurons."""
-    if x.dtype not in _DT or x.dim() != 2 or x.shape[1] != ffn.d:
+    xt, of = _DT.get(x.dtype), x.shape
+    if xt is None or len(of) != 2 or of[1] != ffn.d:
         raise ValueError("x must be [B, d], float16 or float32")
-    B = x.shape[0]
-    if y.dim() != 2 or y.shape[0] != B or y.shape[1] != ffn.d:
+    if y.shape != of:
         raise ValueError("y must be [B, d]")
     dev = ffn.device
     ip = cp = None
@@ -152,4 +152,4 @@ def asf_w4_sparse_ffn(ffn: W4FFN, x: torch.Tensor, idx: Optional[torch.Tensor], 
             raise ValueError("idx must hold n entries and count one")
         ip, cp = _arg(idx, "idx", dev, torch.int32), _arg(count, "count", dev, torch.int32)
     xp, yp = _arg(x, "x", dev), _arg(y, "y", dev, torch.float32)
-    _invoke("asf_w4_sparse_ffn", dev, stream, ffn._ref, xp, _DT[x.dtype], B, ip, cp, yp, ws.on(dev), ws.nbytes)
+    _invoke("asf_w4_sparse_ffn", dev, stream, ffn._ref, xp, xt, of[0], ip, cp, yp, ws.on(dev), ws.nbytes)
