@@ -10,9 +10,15 @@
 // m = max z_p and l = sum_p e^(z_p - m).  One pass over the keys keeps the
 // running m, l and the unnormalised sum; parts over disjoint keys merge by
 // rescaling to the larger m, which is how warps and splits of the keys meet.
-// All of it in fp32 in units of log2 (scale log2(e) joins the score); the
-// weights e^(z - m) are rounded to fp16 for the product with v, half a step of
-// 2^-11 each, as much as the output's own rounding and averaged over the keys.
+// All of it in fp32 in units of log2 (scale log2(e) joins the score).
+//
+// The weights are rounded to fp16 for the product with v, as much as the output's
+// own rounding.  Any reference in the place of m is right, since it cancels in
+// o, so m is lowered by kLift (k_tree_attn; kLiftTc in k_tree_tc) to put the
+// largest weights near the top of fp16's range.  A weight then has an error of
+// 2^-12 of itself (half a step of 2^-11) down to 2^-29 (2^-25) of the row's
+// largest, and of 2^-40 (2^-36) of the largest below that.  (Without kLift what
+// lay 2^-25 below the largest was lost to o, yet counted in l.)
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,6 +40,12 @@ constexpr int kStages = 3;             // tiles in shared memory (k_tree_attn)
 constexpr int kClusterTiles = 4;       // key tiles that each CTA of a cluster takes at most
 constexpr int kMinChunk = 4;           // key tiles per split, at least
 constexpr int kWhole = 8;              // key tiles up to which nothing is split (no merge to launch)
+constexpr float kTopLog2 = 15.99f;     // of a weight at most: below fp16's largest, 65504
+constexpr float kLift = 15.f;
+// k_tree_tc lets a row outgrow its reference by the rest, 2^5.  8 ragged requests, and 16
+// tokens over 65500 keys, us of the call with a lift of 0 to 9: 33.9, 71.0; 11: 34.1,
+// 71.2; 12: 34.9, 72.2, since rows outgrow their references more often.
+constexpr float kLiftTc = 11.f;
 
 struct AttnArgs {
   const __half *k, *v;
@@ -47,7 +59,7 @@ struct AttnArgs {
   float scale;                         // times log2(e)
   __half *o;
   float *part;                         // [unit < target][MT][DP]
-  float2 *ml;                          // [unit][MT]: maximum (log2) and sum
+  float2 *ml;                          // [unit][MT]: reference (log2) and sum
   int4 *plan;                          // per request, for the merge: first token, tokens, splits, first unit
   int target;                          // CTAs to aim at
   int whole;                           // key tiles up to which nothing is split
@@ -317,7 +329,7 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
 #pragma unroll
   for (int j = 0; j < NST - 1; ++j) copy(j);
 
-  float acc[DP / 8][4], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+  float acc[DP / 8][4], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};   // mx: the rows' references
 #pragma unroll
   for (int i = 0; i < DP / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
   const uint32_t smb = smem_u32(sm);
@@ -393,10 +405,12 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
     for (int h = 0; h < 2; ++h) {
       top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
       top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-      top[h] = fmaxf(top[h], mx[h]);
-      const float ref = top[h] == -INFINITY ? 0.f : top[h];   // nothing seen yet: every weight is 2^-inf = 0
+      float low = top[h] - kLift;
+      if (!(top[h] - low <= kTopLog2)) low = top[h];             // scores so large that this rounds, and infinities
+      low = fmaxf(low, mx[h]);
+      const float ref = low == -INFINITY ? 0.f : low;         // nothing seen yet: every weight is 2^-inf = 0
       fix[h] = exp2_fast(mx[h] - ref);
-      mx[h] = top[h];
+      mx[h] = low;
       top[h] = ref;
       sum[h] *= fix[h];
     }
@@ -572,9 +586,9 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
 // values have slots of their own: the keys' are free as soon as S is there, so
 // only their copy has to be ahead, and a tile's values arrive under its
 // exponentials.  O is rescaled
-// only when some row of a warp has outgrown its reference by 2^8: any reference
-// is right as long as the weights (up to 2^8 here) and their sums stay finite,
-// and it spares a pass over O in tensor memory per tile.  Two CTAs share an SM,
+// only when the weights of some row of a warp would pass fp16's range, 2^5 above where
+// its last reference put the largest: that spares a pass over O in tensor memory per
+// tile.  Two CTAs share an SM,
 // one's products under the other's exponentials.
 //
 // 16 tokens x 64 heads over 65500 keys (8 kv heads, 268 MB): 55.7 us alone, 4.8
@@ -928,7 +942,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       mbar_arrive(bq);
     }
     float ref = 0.f, sum = 0.f;
-    bool ok = true;                                // sum: 0 until a key is seen (the reference's weighs 2^-8 at least; NaN stays)
+    bool ok = true;                                // sum: 0 until a key is seen (2^11 at least from then on; NaN stays)
     for (int j = 0; j < tiles; ++j) {
       const uint32_t sc = tl + 128 + 64 * (j & 1);
       const int pos0 = (kt0 + j) * kTile, sl = j % NS;
@@ -960,7 +974,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
       for (int i = 0; i < kTile; ++i) top = fmaxf(top, z[i]);
       // a new reference for the warp's rows where some row needs one
-      const bool grow = top != -INFINITY && (sum == 0.f || top > ref + 8.f);
+      const bool grow = top != -INFINITY && (sum == 0.f || top - ref > kTopLog2);
       const bool redo = __any_sync(0xffffffffu, grow);
       const bool extra = d < kTile && s_any[sl];
       if ((redo || extra) && j > 0) {              // O must rest: the product of the last tile is done
@@ -970,7 +984,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         __syncwarp();
       }
       if (redo) {
-        const float now = grow ? top : ref;
+        float now = grow ? top - kLiftTc : ref;
+        if (grow && !(top - now <= kTopLog2)) now = top;       // scores so large that this rounds, and infinities
         const float f = sum != 0.f ? exp2_fast(ref - now) : 0.f;
         if (j > 0) {
 #pragma unroll

@@ -314,3 +314,38 @@ def test_python_refusals():
                 lambda: att(ws=A.Workspace._sized(4096, d["q"].device, None, "test"))):
         with pytest.raises(A.AsfError):
             bad()
+
+
+@pytest.mark.parametrize("low", [3.5, 4.0])
+@pytest.mark.parametrize("grp,hkv,page", [(2, 300, 16), (20, 300, 64), (40, 150, 64), (40, 150, 20), (2, 4, 16), (40, 4, 64)])
+def test_many_small_weights_beside_a_large_one(grp, hkv, page, low):
+    """The first key takes the weight and has v = 0; 8000 keys 18 or 16 nats below it make the output.
+
+    Many kv heads: one unit has all of a head's keys, four: they are split.  An error of 2^-36 of the
+    largest weight per key, v <= 1: 8000 x 2^-36 = 1.2e-7 in all at most, and check() allows
+    (2^-11 + 2^-20) mass + 2^-24 = 1.2e-7 beside the output's own rounding (18 nats: mass >= 6e-5)."""
+    n = 8000
+    c = Case([n], [1], hkv=hkv, grp=grp, D=8, page=page, seed=17)
+    c.k[:], c.kn[:], c.q[:] = 0, 0, 0
+    c.k[..., 0], c.kn[..., 0], c.q[..., 0] = low, low, 4.0
+    c.v[:], c.vn[:] = 0.5 + 0.5 * c.rng.random(c.v.shape), 0.75
+    pg, sl = O.positions(c.table[0], page, 1)
+    c.k[pg, sl, :, 0], c.v[pg, sl] = 8.0, 0
+    c.check(c.run(scale=1.0), scale=1.0)
+
+
+@pytest.mark.parametrize("grp", [2, 20, 40])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_beyond_24_bits(grp, sign):
+    """Equal scores of up to 2^33, where a float's step is wider than the range of the weights: the plain mean of v.
+
+    Equal weights are equal in fp16 too, so that their rounding cancels up to a step of 2^-11 of v."""
+    for e in range(12):
+        c = Case([500], [1], hkv=2, grp=grp, D=8, seed=e)
+        c.k[:], c.kn[:], c.q[:] = 0, 0, 0
+        c.k[..., 0], c.kn[..., 0], c.q[..., 0] = 6e4, 6e4, sign * 6e4
+        got = c.run(scale=2.0 ** -e)["o"].cpu().numpy().astype(np.float64)
+        pg, sl = O.positions(c.table[0], c.page, 500)
+        v = np.concatenate([c.v[pg, sl], c.vn]).astype(np.float64)
+        ref, mass = (np.repeat(f(v).mean(0)[None], grp, 1).reshape(1, 2 * grp, 8) for f in (np.asarray, np.abs))
+        assert (np.abs(got - ref) <= 2.0 ** -11 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -20) * mass + 2.0 ** -24).all()
