@@ -998,11 +998,20 @@ __global__ void __launch_bounds__(MatTc<N, GS>::THREADS, 1)
   }
 }
 
+// two floats as an fp16 pair (lo first), an infinity as the largest finite value
+__device__ __forceinline__ uint32_t half2_finite(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // ---------------------------------------------------- down projection --
 // y[b][c] = sum_j a[j][b] s[j][c / group] (q[j][c] - 8): the neurons are the
 // contracted dimension, so the scale, which changes with the neuron, joins the
 // activation: v = a s in fp32, times a power of two, split into two fp16 parts,
-// hi = fp16(v) and lo = fp16(v - hi): v to 2^-22, as the products' fp32 sums.
+// hi = fp16(v) and lo = fp16(v - hi): v to 2^-22, as the products' fp32 sums.  An
+// infinite v has the largest fp16 as hi and itself as lo, so that it gives infinities
+// of the weights' signs, and NaN where a weight is 0.
 // The power of two keeps the parts in fp16's range.  Each warp has one for each
 // token, so that a token's sums do not depend on the others': its largest |v| so
 // far lies below 2^15, and what is 2^20 below it still has 16 bits.  When a
@@ -1190,7 +1199,7 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
               float f = 1.f;
               if (__uint_as_float(top) * up[n] >= 32768.f) {   // 2^11 <= the largest < 2^12 from here on
                 const float now = __uint_as_float((uint32_t)max(127 + 11 - (int)(top >> 23) + 127, 1) << 23);
-                f = now / up[n];
+                f = fmaxf(now / up[n], 1.17549435e-38f);       // never 0, which an infinite sum would turn into NaN
                 up[n] = now;
               }
               const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
@@ -1209,10 +1218,10 @@ __global__ void __launch_bounds__(kDownWarps * 32, NT <= 2 ? 2 : 1) k_w4_down(Do
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               const float v0 = v[n][2 * q], v1 = v[n][2 * q + 1];
-              const __half2 hi = __floats2half2_rn(v0, v1);
-              const float2 back = __half22float2(hi);
+              const uint32_t hw = half2_finite(v0, v1);
+              const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hw));
               const __half2 lo = __floats2half2_rn(v0 - back.x, v1 - back.y);
-              const uint32_t hw = *reinterpret_cast<const uint32_t *>(&hi), lw = *reinterpret_cast<const uint32_t *>(&lo);
+              const uint32_t lw = *reinterpret_cast<const uint32_t *>(&lo);
               if constexpr (PC) {
                 bp[n][0][q] = g & 1 ? lw : hw;
               } else {

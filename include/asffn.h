@@ -324,7 +324,10 @@ ASF_API asf_status asf_w4_matmul(const asf_w4_matrix *mat, const void *x, asf_dt
 /* asf_sparse_ffn over 4-bit rows: x [B][d] in xdtype, idx/count/y as there;
  * idx and count both NULL runs all n neurons (asf_dense_ffn).  The activations
  * between the two products are fp32; with its scale, one enters the second
- * product in 22 bits (16 where it is 2^20 below its token's largest). */
+ * product in 22 bits (16 where it is 2^20 below its token's largest).  An
+ * activation that passes fp32's range, by itself or times a group's scale, is an
+ * infinity: its token's y is infinite, with the signs of the down weights, and NaN
+ * where such a weight is 0. */
 ASF_API asf_status asf_w4_sparse_ffn(const asf_w4_ffn *ffn, const void *x, asf_dtype xdtype, int32_t B,
                                      const int32_t *idx, const int32_t *count, float *y, void *ws, size_t ws_bytes,
                                      asf_stream_t stream);

@@ -374,3 +374,44 @@ def test_python_refusals():
             bad()
     with pytest.raises(A.AsfError):
         A.asf_w4_matmul(mat, torch.randn(33, 256, device="cuda"), torch.empty(33, 32, device="cuda"), ws)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+@pytest.mark.parametrize("act,group", [("relu", 32), ("reglu", 64), ("reglu", 128)])
+@pytest.mark.parametrize("B", [1, 3, 7, 12, 20])
+def test_an_infinite_activation(B, act, group, dt):
+    """One neuron's activation overflows (fp32: for token 0 by its x, fp16: for all by the bias): infinities of the down
+    weights' signs, NaN where a weight is 0, and the other tokens unharmed.  fp32: a later neuron of the same warp, eight
+    tiles of 32 on, is token 0's only other active one, 2^40."""
+    n, d, j, later = 300, 264, 10, 261
+    rng = np.random.default_rng(B)
+    W = [_weights(n, d, 50 + i) for i in range(3 if act == "reglu" else 2)]
+    for w in W[:-1]:
+        w[:, 8:16] = 0
+        w[j, 8], w[later, 9] = 2.0 ** 18, 2.0 ** 10
+    data = np.stack([O.w4_pack(w, group) for w in W], 1)
+    bias = np.zeros(n, np.float32)
+    x = rng.standard_normal((B, d)).astype(np.float32)
+    x[:, 8:16] = 0
+    if dt == "f32":
+        x[0] = 0
+        x[0, 8], x[0, 9] = 2.0 ** 115, 2.0 ** 30
+    else:
+        bias[j] = np.inf
+        x[:, 8] = 1
+    xt = torch.from_numpy(x).to(DT[dt])
+    ffn = A.W4FFN(act, torch.from_numpy(data).cuda(), torch.from_numpy(bias).cuda(), d, group)
+    ws = A.Workspace.for_w4(ffn, B)
+    y = torch.empty(B, d, device="cuda")
+    A.asf_w4_sparse_ffn(ffn, xt.cuda(), None, None, y, ws)
+    hit = [0] if dt == "f32" else list(range(B))
+    down = O.w4_unpack(data[j, -1], d, group)
+    with np.errstate(invalid="ignore"):
+        want = np.inf * down
+    assert np.isnan(want).any() and (want == np.inf).any() and (want == -np.inf).any()
+    got = y.cpu().numpy()
+    assert all(np.array_equal(got[b], want.astype(np.float32), equal_nan=True) for b in hit)
+    rest = [b for b in range(B) if b not in hit]
+    if rest:
+        _check_ffn(y[rest], act, data, bias, d, group, xt.double().numpy()[rest], np.arange(n))
+    assert A.asf_read_error(ws) == 0
