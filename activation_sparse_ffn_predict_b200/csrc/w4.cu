@@ -635,6 +635,7 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A) {
     if (lane == 0) old = (ticket_acq_rel(word, 1u << sh) >> sh) & 255u;
     old = __shfl_sync(0xffffffffu, old, 0);
     if (old != (uint32_t)(S - 1)) return;
+    __syncwarp();                                  // lane 0's acquire, then every lane's reads of the parts
     for (int tl = unit * tpu; tl <= tile; ++tl) {
       clear();
       if (LIST && unit * tpu != tile) {  // a unit of several tiles: the registers hold the last one's

@@ -415,3 +415,56 @@ def test_an_infinite_activation(B, act, group, dt):
     if rest:
         _check_ffn(y[rest], act, data, bias, d, group, xt.double().numpy()[rest], np.arange(n))
     assert A.asf_read_error(ws) == 0
+
+
+@pytest.mark.parametrize("m,k,group,B", [(62017, 1032, 128, 32), (61449, 2568, 32, 9), (125001, 1032, 64, 25)])
+def test_matmul_with_several_tiles_under_a_ticket(m, k, group, B):
+    """fp32 x too wide for a CTA, so that k is split, and more row tiles than tickets: units of two and three tiles."""
+    torch.manual_seed(m)
+    W = torch.randn(m, k, device="cuda")
+    mat = A.W4Matrix.quantize(W, group)
+    A.asf_w4_dequantize(mat, W)
+    x, bias = torch.randn(B, k, device="cuda"), torch.randn(m, device="cuda")
+    ws = A.Workspace.for_w4(mat, B)
+    ref, mass = torch.empty(B, m, device="cuda", dtype=torch.float64), torch.empty(B, m, device="cuda", dtype=torch.float64)
+    for i in range(0, m, 8192):
+        w = W[i:i + 8192].double().t()
+        ref[:, i:i + 8192], mass[:, i:i + 8192] = x.double() @ w, x.double().abs() @ w.abs()
+    want = (ref + bias.double()).clamp(min=0).cpu().numpy()
+    ys = [torch.full((B, m), float("nan"), device="cuda") for _ in range(3)]
+    for y in ys:
+        A.asf_w4_matmul(mat, x, y, ws, bias=bias, relu=True)
+        _check(y, want, (mass + bias.double().abs()).cpu().numpy(), k // group + 1)
+        assert torch.equal(y, ys[0]) and not ws.buf[64:4096].any()           # the tickets are zero again
+    assert A.asf_read_error(ws) == 0
+
+
+@pytest.mark.parametrize("act,n,active,d,B", [("reglu", 31001, 30999, 1032, 32), ("relu", 62100, 61990, 1032, 25)])
+def test_sparse_ffn_with_several_tiles_under_a_ticket(act, n, active, d, B):
+    """The same over a list, in no order; its names and biases are read again for a unit's earlier tiles."""
+    torch.manual_seed(n)
+    group, mats = 128, 3 if act == "reglu" else 2
+    W = [torch.randn(n, d, device="cuda") / d ** 0.5 for _ in range(mats)]
+    bias = torch.randn(n, device="cuda") * 0.3
+    ffn = A.W4FFN.quantize(act, W[0] if mats == 3 else None, W[-2], W[-1], bias, group)
+    back = torch.empty(n * mats, d, device="cuda")
+    A.asf_w4_dequantize(A.W4Matrix(ffn.data.view(n * mats, -1), d, group), back)
+    idx = torch.randperm(n, device="cuda").int()
+    cnt = torch.tensor([active], dtype=torch.int32, device="cuda")
+    x = torch.randn(B, d, device="cuda")
+    rows = [w.double() for w in back.view(n, mats, d)[idx[:active].long()].unbind(1)]
+    b, xd, u = bias[idx[:active].long()].double(), x.double(), (24 + d // group + 1 + 256) * 2.0 ** -23
+    a = (xd @ rows[0].t() + b).clamp(min=0)
+    da = u * (xd.abs() @ rows[0].abs().t() + b.abs())
+    if act == "reglu":
+        up, dup = xd @ rows[1].t(), u * (xd.abs() @ rows[1].abs().t())
+        a, da = a * up, da * up.abs() + a * dup + da * dup
+    v = (3 * active / 16 + 3 + 300) * 2.0 ** -23
+    ref, tol = a @ rows[-1], (da + v * (a.abs() + da)) @ rows[-1].abs()
+    ws = A.Workspace.for_w4(ffn, B)
+    ys = [torch.full((B, d), float("nan"), device="cuda") for _ in range(3)]
+    for y in ys:
+        A.asf_w4_sparse_ffn(ffn, x, idx, cnt, y, ws)
+        assert ((y.double() - ref).abs() <= tol).all()
+        assert torch.equal(y, ys[0]) and not ws.buf[64:4096].any()
+    assert A.asf_read_error(ws) == 0
