@@ -14,7 +14,7 @@ from typing import List, Optional, Sequence, Union
 import torch
 
 from .api import (FFN, Predictor, Workspace, asf_dense_ffn, asf_predict, asf_predict_sparse_ffn, asf_read_error,
-                  asf_sparse_ffn)
+                  asf_sparse_ffn, asf_workspace_bytes)
 from .attention import KVCache, asf_kv_append, asf_tree_attention
 from .w4 import W4FFN, W4Matrix, asf_w4_matmul, asf_w4_sparse_ffn
 
@@ -35,8 +35,9 @@ class AttentionStage:
         c0, n = caches[0], len(caches)
         if any((c.heads, c.head_dim, c.page, c.device) != (c0.heads, c0.head_dim, c0.page, c0.device) for c in caches):
             raise ValueError("the layers' caches must have one head layout, page size and device")
-        if out is not None and (len(out) != n or any(m.k != q_heads * c0.head_dim for m in out)):
-            raise ValueError("one projection of q_heads * head_dim columns per layer")
+        if out is not None and (len(out) != n
+                                or any((m.k, m.rows) != (q_heads * c0.head_dim, out[0].rows) for m in out)):
+            raise ValueError("one projection of q_heads * head_dim columns per layer, all of one hidden size")
         self.caches, self.out, self.R, self.max_pages = list(caches), out, int(requests), int(max_pages)
         half = lambda *s: torch.zeros(*s, dtype=torch.float16, device=c0.device)  # noqa: E731
         ints = lambda *s: torch.zeros(*s, dtype=torch.int32, device=c0.device)  # noqa: E731
@@ -45,7 +46,7 @@ class AttentionStage:
         self.o = half(batch, q_heads, c0.head_dim)
         self.table, self.lens, self.begin, self.anc = ints(requests, max_pages), ints(requests), ints(requests + 1), ints(batch)
         self.ws = Workspace.for_attention(c0, q_heads, requests, batch)
-        self.ws_out = Workspace.for_w4(out[0], batch) if out is not None else None
+        self.ws_out = _widest_w4(out, batch) if out is not None else None
         self.width = out[0].rows if out is not None else q_heads * c0.head_dim
 
     def launches(self) -> int:
@@ -76,7 +77,8 @@ class LayerStack:
         asf_predict followed by asf_sparse_ffn (same results).  FFNs of 4-bit
         rows (all layers or none) take the predicted list from asf_predict.
         attention: what computes x[l] before each layer; without it the caller
-        fills x."""
+        fills x.  Layers share the hidden size; neurons, predictor widths, groups
+        and activations may differ (idx is as wide as the widest layer)."""
         if mode not in ("predict", "sparse", "dense"):
             raise ValueError("mode must be predict, sparse or dense")
         self.preds = list(preds)
@@ -93,8 +95,14 @@ class LayerStack:
             raise ValueError("4-bit FFNs: all layers or none")
         if self.w4:
             self.combined = False
-        p0 = self.preds[0] if (self.preds and mode == "predict") else None
-        self.d, self.n = f0.d, f0.n
+        predict = mode == "predict"
+        p0 = self.preds[0] if (self.preds and predict) else None
+        self.d, self.n = f0.d, max(f.n for f in self.ffns)
+        if any(f.d != self.d for f in self.ffns):
+            raise ValueError("the layers must have one hidden size")
+        if predict and (len(self.preds) < self.L or any(
+                p is None or p.d != self.d or p.n > f.n or p.dtype != p0.dtype for p, f in zip(self.preds, self.ffns))):
+            raise ValueError("a predictor per layer, of its hidden size, no more neurons and one dtype")
         self.dtype = (p0.dtype if p0 is not None else torch.float16) if self.w4 else f0.dtype
         self.attention = attention
         if attention is not None and (attention.width != self.d or attention.q.shape[:2] != (self.L, self.B)
@@ -104,9 +112,12 @@ class LayerStack:
         self.y = torch.zeros(self.L, self.B, self.d, dtype=torch.float32, device=dev)
         self.idx = torch.zeros(self.L, self.n, dtype=torch.int32, device=dev)
         self.count = torch.zeros(self.L, dtype=torch.int32, device=dev)
-        self.ws = Workspace(p0, f0, self.B, device=dev) if not self.w4 else (
-            Workspace(p0, None, self.B, device=dev) if p0 is not None else None)
-        self.ws_w4 = Workspace.for_w4(f0, self.B) if self.w4 else None
+        # one workspace for all layers, as large as the layer that needs most asks for
+        pairs = [(p if predict else None, None if self.w4 else f)
+                 for p, f in zip(self.preds if predict else self.ffns, self.ffns)]
+        self.ws = Workspace(*max(pairs, key=lambda pf: asf_workspace_bytes(*pf, self.B)), self.B, device=dev) \
+            if predict or not self.w4 else None
+        self.ws_w4 = _widest_w4(self.ffns, self.B) if self.w4 else None
         self.graph: Optional[torch.cuda.CUDAGraph] = None
 
     def launches_per_step(self) -> int:
@@ -216,6 +227,11 @@ class LayerStack:
 
     def release(self) -> None:
         self.graph = None
+
+
+def _widest_w4(ops: Sequence[Union[W4FFN, W4Matrix]], batch: int) -> Workspace:
+    """A workspace that is enough for each of the operators in turn."""
+    return Workspace.for_w4(max(ops, key=lambda op: op.workspace_bytes(batch)), batch)
 
 
 def _attention_splits(keys: int, heads: int, head_dim: int, grp: int, R: int, T: int, sms: int) -> bool:

@@ -136,3 +136,48 @@ def test_calls_on_two_streams_at_once():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, (out, y, d["o"])))
     assert A.asf_read_error(wm) == A.asf_read_error(wf) == A.asf_read_error(d["ws"]) == 0
+
+
+@pytest.mark.parametrize("mode", ["predict", "dense"])
+def test_layers_of_different_groups_and_widths(mode):
+    """Every later layer needs more workspace than the one before: the same bits as single calls with workspaces of their own."""
+    ensure_built()
+    torch.manual_seed(12)
+    d, B, D, hq, T = 512, 9, 64, 8, 9
+    half = lambda *s: torch.randn(*s, device="cuda").half()  # noqa: E731
+    preds, ffns, outs, caches = [], [], [], []
+    for n, r, group, act in ((600, 64, 128, "relu"), (20000, 96, 64, "relu"), (30000, 160, 32, "reglu")):
+        preds.append(A.Predictor(half(r, d) * d ** -0.5, torch.zeros(r, device="cuda"), half(n, r) * r ** -0.5,
+                                 torch.full((n,), -0.1, device="cuda")))
+        ffns.append(A.W4FFN.quantize(act, half(n, d) * d ** -0.5, half(n, d) * d ** -0.5, half(n, d) * d ** -0.5,
+                                     torch.zeros(n, device="cuda"), group))
+        outs.append(A.W4Matrix.quantize(half(d, hq * D) * (hq * D) ** -0.5, group))
+        caches.append(A.KVCache(half(4, 64, 2, D), half(4, 64, 2, D)))
+    assert sorted(f.workspace_bytes(B) for f in ffns) == [f.workspace_bytes(B) for f in ffns]
+    stage = A.AttentionStage(caches, hq, 1, 4, B, outs)
+    stage.q.normal_(), stage.k.normal_(), stage.v.normal_()
+    stage.table.copy_(torch.arange(4)[None])
+    stage.lens.fill_(100)
+    stage.begin[1] = T
+    stage.anc.copy_((2 ** (torch.arange(T) + 1) - 1).int())
+    st = A.LayerStack(preds, ffns, B, 0.5, mode=mode, attention=stage)
+    assert st.idx.shape == (3, 30000)
+    st.capture()
+    st.step()
+    for l in range(3):
+        x, y = torch.empty(B, d, device="cuda").half(), torch.empty(B, d, device="cuda")
+        o = torch.empty(B, hq, D, device="cuda").half()
+        A.asf_tree_attention(caches[l], stage.table, stage.lens, stage.begin, stage.q[l], stage.anc, o,
+                             A.Workspace.for_attention(caches[l], hq, 1, B))
+        A.asf_w4_matmul(outs[l], o.view(B, -1), x, A.Workspace.for_w4(outs[l], B))
+        assert torch.equal(x, st.x[l]) and x.abs().max() > 0
+        idx, cnt = torch.zeros(ffns[l].n, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        if mode == "predict":
+            A.asf_predict(preds[l], x, 0.5, idx, cnt, A.Workspace(preds[l], None, B))
+            c = int(cnt)
+            assert c == int(st.count[l]) > 0 and torch.equal(idx[:c], st.idx[l, :c])
+        A.asf_w4_sparse_ffn(ffns[l], x, *((idx, cnt) if mode == "predict" else (None, None)), y,
+                            A.Workspace.for_w4(ffns[l], B))
+        assert torch.equal(y, st.y[l])
+    assert st.read_error() == 0
+    st.release()

@@ -53,3 +53,35 @@ def test_launches_per_step(B, dtype, mode, combined, per_layer):
 def test_launches_per_step_wide_layers(d, B, per_layer):
     st = _Stub(d, torch.float16, B, 80, "predict", True)
     assert ST.LayerStack.launches_per_step(st) == 80 * per_layer
+
+
+def _w4(d, n):
+    f = ST.W4FFN.__new__(ST.W4FFN)
+    f.d, f.n, f.tensors = d, n, (None, torch.zeros(1))
+    return f
+
+
+def _pred(d, n, dtype=torch.float16):
+    p = ST.Predictor.__new__(ST.Predictor)
+    p.d, p.n, p.dtype = d, n, dtype
+    return p
+
+
+@pytest.mark.parametrize("preds,ffns", [
+    ([_pred(64, 100)] * 2, [_w4(64, 100), _w4(72, 100)]),               # another hidden size
+    ([_pred(64, 100), _pred(64, 101)], [_w4(64, 100), _w4(64, 100)]),   # would name neurons that the layer has not
+    ([_pred(64, 100), _pred(72, 100)], [_w4(64, 100)] * 2), ([_pred(64, 100)], [_w4(64, 100)] * 2), ([], [_w4(64, 100)]),
+    ([_pred(64, 100), None], [_w4(64, 100)] * 2),
+    ([_pred(64, 100), _pred(64, 100, torch.float32)], [_w4(64, 100)] * 2)])
+def test_layers_that_do_not_fit_are_refused(preds, ffns):
+    with pytest.raises(ValueError):
+        ST.LayerStack(preds, ffns, 1)
+
+
+def test_projections_that_do_not_fit_are_refused():
+    of = lambda cls, **kw: (lambda x: x.__dict__.update(kw) or x)(cls.__new__(cls))  # noqa: E731
+    cache = of(ST.KVCache, heads=2, head_dim=64, page=16, device=torch.device("cpu"))
+    ok, wide, long = (of(ST.W4Matrix, k=k, rows=m) for k, m in ((256, 96), (320, 96), (256, 104)))
+    for out in ([ok], [ok, wide], [ok, long]):
+        with pytest.raises(ValueError):
+            ST.AttentionStage([cache, cache], 4, 1, 2, 1, out)
