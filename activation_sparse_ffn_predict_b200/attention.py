@@ -47,7 +47,9 @@ def _requests(cache: KVCache, table, lens, begin):
 
 def asf_kv_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin: torch.Tensor, k: torch.Tensor,
                   v: torch.Tensor, ws: Workspace, stream=None) -> None:
-    """Write the tokens' k and v [T, heads, head_dim] at positions lens[r] + i of their requests."""
+    """Write the tokens' k and v [T, heads, head_dim] at positions lens[r] + i of their requests.
+
+    k and v may be rows of the cache only where the call does not write: copy them where it may."""
     of = k.shape
     if len(of) != 3 or of[1] != cache.heads or of[2] != cache.head_dim or v.shape != of:
         raise ValueError("k and v must be [T, heads, head_dim]")

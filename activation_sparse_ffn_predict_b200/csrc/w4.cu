@@ -1324,6 +1324,11 @@ asf_status check_w4(const asf_w4_matrix *m) {
   if (m->row_stride < w4_row_bytes(m->k, m->group)) return ASF_ERR_INVALID_ARG;
   return ASF_OK;
 }
+// whether contiguous [rows][k] values share memory with the matrix: warps of a row read and write at their own pace
+bool rows_overlap(const asf_w4_matrix *m, const void *dense, asf_dtype dtype) {
+  return overlap(dense, (size_t)m->rows * m->k * (dtype == ASF_F16 ? 2 : 4), m->data,
+                 (size_t)(m->rows - 1) * m->row_stride + w4_row_bytes(m->k, m->group));
+}
 // CTAs of the row-wise kernels (rows_of_cta)
 unsigned row_ctas(const asf_w4_matrix *m) {
   const int nsb = ceil_div(m->k, kSuper), per = nsb > 4 ? 1 : nsb > 2 ? 2 : nsb > 1 ? 4 : 8;
@@ -1472,6 +1477,7 @@ asf_status asf_w4_quantize(const void *src, asf_dtype dtype, const asf_w4_matrix
   if (!src) return ASF_ERR_INVALID_ARG;
   if (dtype != ASF_F16 && dtype != ASF_F32) return ASF_ERR_UNSUPPORTED;
   if (!al16(src)) return ASF_ERR_MISALIGNED;
+  if (rows_overlap(mat, src, dtype)) return ASF_ERR_INVALID_ARG;
   const dim3 grid(row_ctas(mat)), block(256);
   unsigned char *dst = static_cast<unsigned char *>(const_cast<void *>(mat->data));
   cudaStream_t st = (cudaStream_t)stream;
@@ -1488,6 +1494,7 @@ asf_status asf_w4_dequantize(const asf_w4_matrix *mat, void *dst, asf_dtype dtyp
   if (!dst) return ASF_ERR_INVALID_ARG;
   if (dtype != ASF_F16 && dtype != ASF_F32) return ASF_ERR_UNSUPPORTED;
   if (!al16(dst)) return ASF_ERR_MISALIGNED;
+  if (rows_overlap(mat, dst, dtype)) return ASF_ERR_INVALID_ARG;
   const dim3 grid(row_ctas(mat)), block(256);
   const unsigned char *src = static_cast<const unsigned char *>(mat->data);
   cudaStream_t st = (cudaStream_t)stream;

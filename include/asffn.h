@@ -296,14 +296,15 @@ typedef struct {
 /* Bytes of one row, or 0 for a k or group that the format does not have. */
 ASF_API int64_t asf_w4_row_bytes(int32_t k, int32_t group);
 
-/* Rows [rows][k] (fp16 or fp32, contiguous, 16-byte aligned) to 4 bits, into
- * mat->data: per group scale = fp16(max |w| / 7), code = clamp(round half to
+/* Rows [rows][k] (fp16 or fp32, contiguous, 16-byte aligned, apart from the
+ * matrix) to 4 bits, into mat->data: per group scale = fp16(max |w| / 7), code = clamp(round half to
  * even(w / scale), -8, 7) + 8, evaluated in fp32; a group of scale 0 gets code
  * 8.  A group with a NaN, an infinity or a scale past fp16's range gets the
  * scale NaN, so that no product over it looks sound. */
 ASF_API asf_status asf_w4_quantize(const void *src, asf_dtype dtype, const asf_w4_matrix *mat, asf_stream_t stream);
 
-/* The weights back as contiguous [rows][k] fp16 (rounded once) or fp32 (exact). */
+/* The weights back as contiguous [rows][k] fp16 (rounded once) or fp32 (exact),
+ * apart from the matrix. */
 ASF_API asf_status asf_w4_dequantize(const asf_w4_matrix *mat, void *dst, asf_dtype dtype, asf_stream_t stream);
 
 /* Workspace bytes of asf_w4_matmul / asf_w4_sparse_ffn for batches up to
@@ -373,7 +374,7 @@ typedef struct {
 ASF_API size_t asf_attention_workspace_bytes(const asf_kv_cache *cache, int32_t q_heads, int32_t R, int32_t T);
 
 /* Writes the tokens' keys and values (device fp16 [T][heads][head_dim], 16-byte
- * aligned) at their positions.  ws: at least 4096 bytes, for the error word. */
+ * aligned; rows of the cache only where the call does not write) at their positions.  ws: at least 4096 bytes, for the error word. */
 ASF_API asf_status asf_kv_append(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
                                  const int32_t *lens, const int32_t *begin, int32_t T, const void *k, const void *v,
                                  void *ws, size_t ws_bytes, asf_stream_t stream);

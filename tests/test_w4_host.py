@@ -125,3 +125,14 @@ def test_overlap_and_too_many_rows_are_refused(lib):
         assert lib.asf_w4_matmul(m, FAKE, L.ASF_F16, 1, None, 0, y, L.ASF_F32, FAKE, ws, None) == L.ASF_ERR_INVALID_ARG
     assert lib.asf_w4_workspace_bytes(ctypes.byref(_mat(rows=L.ASF_W4_MAX_ROWS + 1)), None, 1) == 0
     assert lib.asf_w4_matmul(m, FAKE, L.ASF_F16, 1, None, 0, FAKE + 1, L.ASF_F16, FAKE, ws, None) == L.ASF_ERR_MISALIGNED
+
+
+def test_quantize_and_dequantize_refuse_shared_memory(lib):
+    m = _mat()                                              # 64 rows of 256, at FAKE
+    end = 64 * O.row_bytes(256, 128)
+    for dt, size in ((L.ASF_F16, 2), (L.ASF_F32, 4)):
+        for at in (FAKE, FAKE + end - 16, FAKE - 64 * 256 * size + 16):
+            assert lib.asf_w4_quantize(at, dt, ctypes.byref(m), None) == L.ASF_ERR_INVALID_ARG
+            assert lib.asf_w4_dequantize(ctypes.byref(m), at, dt, None) == L.ASF_ERR_INVALID_ARG
+    rows = _mat(stride=512)                                 # 4-bit rows inside the rows that they come from
+    assert lib.asf_w4_quantize(FAKE, L.ASF_F16, ctypes.byref(rows), None) == L.ASF_ERR_INVALID_ARG
