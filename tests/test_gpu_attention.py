@@ -349,3 +349,16 @@ def test_scores_beyond_24_bits(grp, sign):
         v = np.concatenate([c.v[pg, sl], c.vn]).astype(np.float64)
         ref, mass = (np.repeat(f(v).mean(0)[None], grp, 1).reshape(1, 2 * grp, 8) for f in (np.asarray, np.abs))
         assert (np.abs(got - ref) <= 2.0 ** -11 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -20) * mass + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("lens,toks,kw", [
+    ([333], [1], dict(hkv=32, grp=1, D=128)), ([40, 0, 7], [2, 1, 3], dict(hkv=2, grp=4)),
+    ([100, 30], [4, 4], dict(hkv=2, grp=16, page=64)), ([700], [5], dict(hkv=1, grp=9, D=80, page=20))])
+def test_tables_wider_than_the_requests(lens, toks, kw):
+    """Room for 4096 keys and more: the table's width chooses the form, and entries past a request's keys are not read."""
+    c = Case(lens, toks, seed=sum(lens), **kw)
+    for keys in (512, 1024, 2048, 4096, 70000):
+        more = -(-keys // c.page) - c.table.shape[1]
+        if more > 0:
+            c.table = np.concatenate([c.table, np.full((len(lens), more), 2 ** 31 - 1)], 1)
+        c.check(c.run())
