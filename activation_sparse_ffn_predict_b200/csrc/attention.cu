@@ -198,8 +198,9 @@ __host__ __device__ constexpr int attn_resident(int DP, int WM) { return DP == 6
 // distributed shared memory: the form for few units of few tiles, which
 // otherwise leave most SMs idle and yet are not worth a merge of their own.
 // Latency bounds it below some MB of keys (32 heads of 333 keys, 5.5 MB: 10.8 us
-// with the append), the loads in flight above: 32 requests of 4096 keys (8 kv
-// heads, 537 MB) 98.7 us, 5.4 TB/s.
+// with the append, and 15.9 where the table has room for 4096 keys, which takes the
+// form without clusters and the merge's launch), the loads in flight above: 32
+// requests of 4096 keys (8 kv heads, 537 MB) 98.8 us, 5.4 TB/s.
 template <int DP, int WM, int CL>
 __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnArgs A) {
   constexpr int NW = 4;
@@ -591,9 +592,9 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
 // tile.  Two CTAs share an SM,
 // one's products under the other's exponentials.
 //
-// 16 tokens x 64 heads over 65500 keys (8 kv heads, 268 MB): 55.7 us alone, 4.8
+// 16 tokens x 64 heads over 65500 keys (8 kv heads, 268 MB): 54.9 us alone, 4.9
 // TB/s; what is left is the exponentials and the passes between registers and
-// tensor memory (issue slots 39% used, tensor pipe 35%).  The kernel above with
+// tensor memory (issue slots 39% used, tensor pipe 34%).  The kernel above with
 // eight row groups took 150 us for the call, this one 64.
 template <int DP>
 struct TreeTc {
@@ -1267,7 +1268,8 @@ size_t attn_scratch(const asf_kv_cache *c, int grp, int R, int T) {
 }
 
 // CTAs that share a unit (k_tree_attn), 1: no cluster, and splits with a merge
-// from kWhole tiles on.  A cluster where its CTAs find room at once and have
+// from kWhole tiles on.  `keys` is what a request's table has room for, all that the
+// host knows: a short request in a wide table takes no cluster.  A cluster where its CTAs find room at once and have
 // few tiles each; eight CTAs where that leaves an SM to each.  us of the call
 // with 1, 4 and 8: 8 heads x 200 keys 11.4, 9.4, 10.1; 500 keys 15.0, 10.2, 9.9;
 // 1000 keys 13.8, 12.4, 10.9; 2000 keys 14.0, 16.8, 13.0; 32 heads x 333 keys

@@ -55,7 +55,7 @@ inline int64_t w4_row_bytes(int k, int group) { return (int64_t)w4_kp(k) / 2 + w
 // so wherever that product is 1e-5 or more off a half its rounding is the same;
 // the few others divide.  (Dividing always: 72 us for 11008 x 4096 in fp16.)
 // 11008 x 4096 in fp16 with the way back: 55 us, 4.1 TB/s of the four passes;
-// issue slots bound it (3.5 instructions a clock of 4).
+// issue slots bound the quantizer (0.85 instructions a scheduler and cycle).
 __device__ __forceinline__ void rows_of_cta(int nsb, int warp, int &lsh, int &sb, int64_t &row) {
   lsh = nsb > 4 ? 3 : nsb > 2 ? 2 : nsb > 1 ? 1 : 0;           // log2 of the warps of a row
   sb = warp & ((1 << lsh) - 1);
@@ -159,7 +159,10 @@ k_w4_quantize(const T *__restrict__ src, int rows, int k, int group, unsigned ch
 // ---------------------------------------------------- codes to operands --
 // The four pairs (weights 2p, 2p+1 of a word) as fp16 or bf16 whole numbers
 // -8..7.  Or-ing a nibble into the mantissa of 1024 (fp16: pair 0, and pair 1
-// as 1024 + 16 q) or of 128 (bf16) is exact, and so is what follows.
+// as 1024 + 16 q) or of 128 (bf16) is exact, and so is what follows: the method
+// of Kim, Henry, Fahim and Awadalla, "Who Says Elephants Can't Run: Bringing Large
+// Scale MoE Models into Cloud Scale Production" (2022), with this format's zero
+// point and order of weights.
 __device__ __forceinline__ uint32_t lop_or(uint32_t w, uint32_t mask, uint32_t magic) {
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));   // (w & mask) | magic
@@ -694,8 +697,10 @@ __global__ void __launch_bounds__(kDotWarps * 32, 1) k_w4_dot(DotArgs A) {
 // CTA; tiles that fall to several CTAs meet in the workspace, where the one that
 // takes a tile's last ticket adds the parts in the order of the CTAs.
 // 28672 x 8192 (121 MB): 37.5 us for one token, 3.2 TB/s, 47 us for 32 tokens.
-// The unpacking warps bound it (issue slots 58% used, tensor pipe 9%), and with
-// many tokens the passes over the accumulators (32 tokens, groups of 64: 50.6 us).
+// No unit is full (issue slots 58% used, DRAM 37%, tensor pipe 9%): the unpacking
+// warps wait for their stages and for their own chain of unpacking and stores, and
+// with many tokens for the passes over the accumulators (32 tokens, groups of 64:
+// 50.8 us).
 constexpr int kTcStageK = 256;
 template <int N, int GS>
 struct MatTc {

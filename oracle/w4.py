@@ -57,13 +57,6 @@ def w4_unpack(rows, k: int, group: int) -> np.ndarray:
     return (c.astype(np.float64) - 8) * s[..., i // group]
 
 
-def w4_matmul(rows, k: int, group: int, x, bias=None, relu: bool = False) -> np.ndarray:
-    y = np.asarray(x, np.float64) @ w4_unpack(rows, k, group).T
-    if bias is not None:
-        y = y + np.asarray(bias, np.float64)
-    return np.maximum(y, 0) if relu else y
-
-
 def w4_ffn(act: str, data, bias, d: int, group: int, x, idx) -> np.ndarray:
     """Sparse FFN over the listed neurons; data uint8 [n, mats, row_bytes]."""
     idx = np.asarray(idx, dtype=np.int64)
