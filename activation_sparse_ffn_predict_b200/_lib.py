@@ -3,7 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libasffn.so")
 
@@ -27,6 +27,14 @@ ASF_W4_MAX_ROWS = 1 << 30
 ASF_MAX_KV_HEADS = 1024
 ASF_MAX_HEAD_GROUP = 128
 ASF_MAX_KEYS = 1 << 30
+ASF_MAX_ROTARY_DIM = 512
+ASF_MAX_ROTARY_HEADS = 65535
+ASF_ROTARY_HALF = 0
+ASF_ROTARY_PAIRS = 1
+ASF_ROTARY_PLAIN = 0
+ASF_ROTARY_LINEAR = 1
+ASF_ROTARY_NTK = 2
+ASF_ROTARY_YARN = 3
 ASF_INJECT_NONE = 0
 ASF_INJECT_WITHHOLD_FFN_COPIES = 1
 
@@ -63,6 +71,10 @@ class asf_w4_ffn(ctypes.Structure):
 class asf_kv_cache(ctypes.Structure):
     _fields_ = [("pages", c_int32), ("page", c_int32), ("heads", c_int32), ("head_dim", c_int32), ("k", c_void_p),
                 ("v", c_void_p), ("page_stride", c_int64), ("token_stride", c_int64), ("head_stride", c_int64)]
+
+
+class asf_rotary(ctypes.Structure):
+    _fields_ = [("head_dim", c_int32), ("rot_dim", c_int32), ("layout", c_int32), ("scale", c_float), ("turns", c_void_p)]
 
 
 # name -> (restype, argtypes), exactly the declarations of include/asffn.h
@@ -110,6 +122,14 @@ PROTOTYPES = {
                               c_void_p, c_void_p, c_size_t, c_void_p]),
     "asf_tree_attention": (c_int, [POINTER(asf_kv_cache), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32,
                                    c_int32, c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "asf_rotary_frequencies": (c_int, [c_int32, c_double, c_int32, c_double, c_double, POINTER(c_double),
+                                       POINTER(c_float)]),
+    "asf_rotary_turns": (c_int, [POINTER(c_double), c_int32, POINTER(c_uint64)]),
+    "asf_rotary_apply": (c_int, [POINTER(asf_rotary), c_void_p, c_int, c_int32, c_int32, c_int64, c_int64, c_void_p,
+                                 c_void_p, c_int64, c_int64, c_void_p]),
+    "asf_rotary_append": (c_int, [POINTER(asf_rotary), POINTER(asf_kv_cache), c_void_p, c_int32, c_int32, c_void_p,
+                                  c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_int64, c_void_p, c_void_p, c_int64,
+                                  c_void_p, c_int64, c_void_p, c_size_t, c_void_p]),
     "asf_read_error": (c_int, [c_void_p, POINTER(c_int32), c_void_p]),
     "asf_status_string": (c_char_p, [c_int]),
     "asf_version": (c_int32, []),

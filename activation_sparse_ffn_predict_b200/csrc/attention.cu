@@ -30,6 +30,7 @@
 #include "asffn.h"
 #include "common.cuh"
 #include "host.cuh"
+#include "paged.cuh"
 
 using namespace asf;
 
@@ -1182,9 +1183,7 @@ __global__ void __launch_bounds__(128) k_tree_merge(AttnArgs A, int MT) {
   }
 }
 
-// One 16-byte chunk of a token's keys and values per thread.  A lane of every
-// warp reads one request's range and length, all at once: the chain to the first
-// store is two loads (these, then the table) instead of four.
+// One 16-byte chunk of a token's keys and values per thread.
 struct AppendArgs {
   __half *k, *v;
   int64_t page_stride, token_stride, head_stride;
@@ -1198,60 +1197,26 @@ struct AppendArgs {
 __global__ void __launch_bounds__(128) k_kv_append(AppendArgs A) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
   const int per = A.hkv * (A.D / 8), total = A.T * per;
   const int i = blockIdx.x * blockDim.x + threadIdx.x, at = min(i, total - 1);
   const int tok = at / per, head = at % per / (A.D / 8), c = at % (A.D / 8);
   const int64_t from = ((int64_t)tok * A.hkv + head) * A.D + c * 8;
   const uint4 key = *reinterpret_cast<const uint4 *>(A.kn + from), val = *reinterpret_cast<const uint4 *>(A.vn + from);
-  int b0 = 0, b1 = A.T, n = 0;
-  if (lane < A.R) {
-    b0 = ld_cg_i32(A.begin + lane);
-    b1 = ld_cg_i32(A.begin + lane + 1);
-    n = ld_cg_i32(A.lens + lane);
-  }
-  const bool bad = __any_sync(0xffffffffu, b0 < 0 || b1 < b0 || b1 > A.T);
-  if (bad && i == 0) flag_error(A.err, kErrIndex);
-  int r = 0;                           // the request whose range holds the token
-  for (int q = 0; q < A.R; ++q) r += tok >= __shfl_sync(0xffffffffu, b1, q);
-  const int t0 = __shfl_sync(0xffffffffu, b0, r & 31), len = __shfl_sync(0xffffffffu, n, r & 31);
-  if (i >= total || r >= A.R || tok < t0) return;   // behind the last range: nothing is written
-  const int64_t pos = (int64_t)len + (tok - t0);
-  const int64_t pi = pos / A.page;
+  const Place w = place_of(A.lens, A.begin, A.R, A.T, tok, A.err, i == 0);
+  if (i >= total || w.r < 0) return;   // behind the last range: nothing is written
+  const int64_t pi = w.pos / A.page;
   int id = -1;
-  if (t0 >= 0 && len >= 0 && pi < A.max_pages) id = A.table[(int64_t)r * A.max_pages + pi];
+  if (w.pos >= 0 && pi < A.max_pages) id = A.table[(int64_t)w.r * A.max_pages + pi];
   if ((unsigned)id >= (unsigned)A.pages) {
     flag_error(A.err, kErrIndex);
     return;
   }
-  const int64_t to = (int64_t)id * A.page_stride + (pos - pi * A.page) * A.token_stride + (int64_t)head * A.head_stride + c * 8;
+  const int64_t to = (int64_t)id * A.page_stride + (w.pos - pi * A.page) * A.token_stride + (int64_t)head * A.head_stride + c * 8;
   *reinterpret_cast<uint4 *>(A.k + to) = key;
   *reinterpret_cast<uint4 *>(A.v + to) = val;
 }
 
 // ------------------------------------------------------------------ host --
-asf_status check_cache(const asf_kv_cache *c) {
-  if (!c || !c->k || !c->v) return ASF_ERR_INVALID_ARG;
-  if (c->pages <= 0 || c->page <= 0 || c->heads <= 0 || c->head_dim <= 0) return ASF_ERR_INVALID_ARG;
-  if (c->head_dim > 128 || c->heads > ASF_MAX_KV_HEADS) return ASF_ERR_UNSUPPORTED;
-  if (c->head_dim % 8 || c->page_stride % 8 || c->token_stride % 8 || c->head_stride % 8) return ASF_ERR_MISALIGNED;
-  if (!al16(c->k) || !al16(c->v)) return ASF_ERR_MISALIGNED;
-  if (c->page_stride < 0 || c->token_stride < c->head_dim || c->head_stride < 0 ||
-      (c->heads > 1 && c->head_stride < c->head_dim) || (c->pages > 1 && c->page_stride < c->head_dim))
-    return ASF_ERR_INVALID_ARG;
-  return ASF_OK;
-}
-asf_status check_requests(const int32_t *table, int max_pages, int R, const int32_t *lens, const int32_t *begin, int T) {
-  if (!table || !lens || !begin) return ASF_ERR_INVALID_ARG;
-  if (max_pages < 1 || R < 1 || R > ASF_MAX_BATCH || T < 1 || T > ASF_MAX_BATCH) return ASF_ERR_INVALID_ARG;
-  return ASF_OK;
-}
-asf_status check_tables(const int32_t *table, int max_pages, int page, const int32_t *lens, const int32_t *begin) {
-  if ((int64_t)max_pages * page > ASF_MAX_KEYS) return ASF_ERR_UNSUPPORTED;
-  if (!al4(table) || !al4(lens) || !al4(begin)) return ASF_ERR_MISALIGNED;
-  return ASF_OK;
-}
-
 // Groups of 16 rows a CTA takes: enough for a request's rows where the tokens
 // are shared out evenly (any number is right, the rest become row tiles).
 int row_groups(int grp, int R, int T) {

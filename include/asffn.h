@@ -389,6 +389,74 @@ ASF_API asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *
                                       size_t ws_bytes, asf_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Rotary positions: queries and keys are turned before they meet in tree
+ * attention.  Of a head's head_dim columns the first rot_dim are turned in pairs,
+ * the others pass bit for bit: pair j of a token at position p, (u, w), becomes
+ * scale (u cos a - w sin a, w cos a + u sin a) with a = p f_j, where pair j is
+ * columns j and j + rot_dim / 2 (ASF_ROTARY_HALF) or 2j and 2j + 1
+ * (ASF_ROTARY_PAIRS).  Computed in fp32 and rounded once; the angle, modulo a
+ * turn, in whole numbers, so that it is as exact at position 2^31 as at 1.
+ * Positions are any int32 values; -p turns back what p has turned. */
+#define ASF_MAX_ROTARY_DIM 512
+#define ASF_MAX_ROTARY_HEADS 65535
+#define ASF_ROTARY_HALF 0
+#define ASF_ROTARY_PAIRS 1
+
+typedef struct {
+  int32_t head_dim, rot_dim;   /* rot_dim even, at most head_dim */
+  int32_t layout;              /* ASF_ROTARY_HALF or ASF_ROTARY_PAIRS */
+  float scale;                 /* of cos and sin: 1, or what asf_rotary_frequencies says */
+  const uint64_t *turns;       /* device [rot_dim / 2], 8-byte aligned: f_j in 2^-64 turns, see asf_rotary_turns */
+} asf_rotary;
+
+/* Host: the usual frequencies, radians per position, and the scale that goes with
+ * them.  f_j = base^(-2j / rot_dim), and for contexts `factor` (>= 1) times as long
+ *   ASF_ROTARY_LINEAR  f_j / factor
+ *   ASF_ROTARY_NTK     of the base base * factor^(rot_dim / (rot_dim - 2)), as
+ *                      which the slowest pair is LINEAR's and the fastest PLAIN's
+ *   ASF_ROTARY_YARN    "YaRN: Efficient Context Window Extension of Large Language
+ *                      Models": f_j (1 - m_j) + m_j f_j / factor, m_j rising from 0
+ *                      to 1 between the (rounded) pairs that make 32 turns and one
+ *                      turn in the `original` context; scale 1 + 0.1 ln(factor)
+ * freq_out: host double [rot_dim / 2].  factor and original are read by the
+ * scalings that name them. */
+#define ASF_ROTARY_PLAIN 0
+#define ASF_ROTARY_LINEAR 1
+#define ASF_ROTARY_NTK 2
+#define ASF_ROTARY_YARN 3
+ASF_API asf_status asf_rotary_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor, double original,
+                                          double *freq_out, float *scale_out);
+
+/* Host: freq [n] (any finite values, radians per position) as turns modulo 1, in
+ * units of 2^-64, rounded to the nearest. */
+ASF_API asf_status asf_rotary_turns(const double *freq, int32_t n, uint64_t *turns_out);
+
+/* y = x turned, [T][heads][head_dim] each in dtype, T any positive number: token t's
+ * head h starts t * token_stride + h * head_stride elements from x or y.
+ *   x, y    16-byte aligned, strides not negative and multiples of 16 bytes, head_dim
+ *           too; y's heads do not meet.  y is x (same strides), or apart from it
+ *           from first to last byte
+ *   pos     device int32 [T] */
+ASF_API asf_status asf_rotary_apply(const asf_rotary *rot, const void *x, asf_dtype dtype, int32_t T, int32_t heads,
+                                    int64_t x_token_stride, int64_t x_head_stride, const int32_t *pos, void *y,
+                                    int64_t y_token_stride, int64_t y_head_stride, asf_stream_t stream);
+
+/* asf_kv_append with the turn in front of it, in one launch: the tokens' keys go to
+ * the cache turned, their values as they are, and q_out [T][q_heads][head_dim]
+ * (contiguous) becomes q turned.  q, k and v are fp16, their heads contiguous, their
+ * tokens q_stride, k_stride and v_stride elements apart (multiples of 8, at least a
+ * token's width): slices of one joint projection.  Tokens outside every range take no
+ * part.  q_out may be q where q is contiguous, else it is apart from q, k, v and the cache.
+ *   pos    device int32 [T], the tokens' positions: not lens[r] + i where tokens of a
+ *          tree are alternatives, or where keys have been evicted
+ * Everything else, and errors, as for asf_kv_append. */
+ASF_API asf_status asf_rotary_append(const asf_rotary *rot, const asf_kv_cache *cache, const int32_t *table,
+                                     int32_t max_pages, int32_t R, const int32_t *lens, const int32_t *begin, int32_t T,
+                                     const int32_t *pos, int32_t q_heads, const void *q, int64_t q_stride, void *q_out,
+                                     const void *k, int64_t k_stride, const void *v, int64_t v_stride, void *ws,
+                                     size_t ws_bytes, asf_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Neuron-sharded layer across GPUs (the layer + neuron partitioning of the
  * "PowerInfer_x64" page's multi-GPU coordination): rank r holds the predictor
  * rows and FFN rows of its own neurons, and the ranks' partial outputs are
