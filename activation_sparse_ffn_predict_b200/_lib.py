@@ -122,6 +122,10 @@ PROTOTYPES = {
                               c_void_p, c_void_p, c_size_t, c_void_p]),
     "asf_tree_attention": (c_int, [POINTER(asf_kv_cache), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32,
                                    c_int32, c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "asf_attention_scored_workspace_bytes": (c_size_t, [POINTER(asf_kv_cache), c_int32, c_int32, c_int32, c_int32]),
+    "asf_tree_attention_scored": (c_int, [POINTER(asf_kv_cache), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32,
+                                          c_int32, c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_int32, c_void_p,
+                                          c_size_t, c_void_p]),
     "asf_rotary_frequencies": (c_int, [c_int32, c_double, c_int32, c_double, c_double, POINTER(c_double),
                                        POINTER(c_float)]),
     "asf_rotary_turns": (c_int, [POINTER(c_double), c_int32, POINTER(c_uint64)]),

@@ -194,9 +194,11 @@ class Workspace:
         return cls._sized(op.workspace_bytes(max_batch), op.device, stream, "asf_w4_workspace_bytes")
 
     @classmethod
-    def for_attention(cls, cache, q_heads: int, requests: int, tokens: int, stream=None) -> "Workspace":
-        """Scratch of asf_kv_append and asf_tree_attention over a KVCache, up to that many requests and tokens."""
-        return cls._sized(cache.workspace_bytes(q_heads, requests, tokens), cache.device, stream,
+    def for_attention(cls, cache, q_heads: int, requests: int, tokens: int, stream=None,
+                      scored_pages: Optional[int] = None) -> "Workspace":
+        """Scratch of the appends and asf_tree_attention over a KVCache, up to that many requests and tokens;
+        with scored_pages of asf_tree_attention_scored too, for tables up to that wide."""
+        return cls._sized(cache.workspace_bytes(q_heads, requests, tokens, scored_pages), cache.device, stream,
                           "asf_attention_workspace_bytes")
 
     def on(self, device) -> int:

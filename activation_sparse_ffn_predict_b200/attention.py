@@ -30,7 +30,10 @@ class KVCache:
                                    *(int(k.stride(i)) if k.shape[i] > 1 else self.head_dim for i in range(3)))
         self._ref = ctypes.byref(self.desc)
 
-    def workspace_bytes(self, q_heads: int, requests: int, tokens: int) -> int:
+    def workspace_bytes(self, q_heads: int, requests: int, tokens: int, scored_pages: Optional[int] = None) -> int:
+        if scored_pages is not None:
+            return int(L.load().asf_attention_scored_workspace_bytes(self._ref, int(q_heads), int(requests), int(tokens),
+                                                                     int(scored_pages)))
         return int(L.load().asf_attention_workspace_bytes(self._ref, int(q_heads), int(requests), int(tokens)))
 
 
@@ -59,13 +62,7 @@ def asf_kv_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin
     _invoke("asf_kv_append", dev, stream, cache._ref, *req, of[0], kp, vp, ws.on(dev), ws.nbytes)
 
 
-def asf_tree_attention(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin: torch.Tensor, q: torch.Tensor,
-                       anc: torch.Tensor, o: torch.Tensor, ws: Workspace, scale: Optional[float] = None,
-                       stream=None) -> None:
-    """o [T, q_heads, head_dim] = attention of the call's tokens over their requests' keys.
-
-    table int32 [R, max_pages], lens int32 [R], begin int32 [R + 1]; anc int32 [T]: which of the call's
-    tokens each token sees, beside every key before lens.  scale: head_dim ** -0.5 unless given."""
+def _attend(cache: KVCache, table, lens, begin, q, anc, o, ws, scale):
     of = q.shape
     if len(of) != 3 or of[2] != cache.head_dim or o.shape != of:
         raise ValueError("q and o must be [T, q_heads, head_dim]")
@@ -75,7 +72,30 @@ def asf_tree_attention(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, 
     req = _requests(cache, table, lens, begin)
     qp, op = _arg(q, "q", dev, torch.float16), _arg(o, "o", dev, torch.float16)
     ap = _arg(anc, "anc", dev, torch.int32)
-    if scale is None:
-        scale = cache.head_dim ** -0.5
-    _invoke("asf_tree_attention", dev, stream, cache._ref, *req, of[0], of[1], qp, ap, scale, op, ws.on(dev),
-            ws.nbytes)
+    return (cache._ref, *req, of[0], of[1], qp, ap, cache.head_dim ** -0.5 if scale is None else scale, op)
+
+
+def asf_tree_attention(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin: torch.Tensor, q: torch.Tensor,
+                       anc: torch.Tensor, o: torch.Tensor, ws: Workspace, scale: Optional[float] = None,
+                       stream=None) -> None:
+    """o [T, q_heads, head_dim] = attention of the call's tokens over their requests' keys.
+
+    table int32 [R, max_pages], lens int32 [R], begin int32 [R + 1]; anc int32 [T]: which of the call's
+    tokens each token sees, beside every key before lens.  scale: head_dim ** -0.5 unless given."""
+    args = _attend(cache, table, lens, begin, q, anc, o, ws, scale)
+    _invoke("asf_tree_attention", cache.device, stream, *args, ws.on(cache.device), ws.nbytes)
+
+
+def asf_tree_attention_scored(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin: torch.Tensor,
+                              q: torch.Tensor, anc: torch.Tensor, o: torch.Tensor, scores: torch.Tensor, ws: Workspace,
+                              scale: Optional[float] = None, stream=None) -> None:
+    """asf_tree_attention that adds to scores fp32 [R, heads, S] the weight that each cached key received.
+
+    S covers the positions seen; the call's own tokens' positions are set instead.  ws:
+    Workspace.for_attention(..., scored_pages=the table's width)."""
+    args = _attend(cache, table, lens, begin, q, anc, o, ws, scale)
+    of = scores.shape
+    if len(of) != 3 or of[0] != lens.shape[0] or of[1] != cache.heads:
+        raise ValueError("scores must be [R, heads, S]")
+    sp = _arg(scores, "scores", cache.device, torch.float32)
+    _invoke("asf_tree_attention_scored", cache.device, stream, *args, sp, of[2], ws.on(cache.device), ws.nbytes)

@@ -2,6 +2,7 @@
 // append that fills it (include/asffn.h, "Tree attention").
 //
 //   asf_kv_append        k_kv_append
+//   asf_tree_attention_scored   the same, then k_tree_score
 //   asf_tree_attention   k_tree_attn, or k_tree_tc for more than 32 query rows of
 //                        a request and kv head; then k_tree_merge over split requests
 //
@@ -67,6 +68,9 @@ struct AttnArgs {
   int cluster;                         // CTAs that share a unit
   int box;                             // keys of a TMA load, or 0
   int32_t *err;
+  float2 *stats;                       // scored: per row (token, query head) its reference (log2) and sum
+  float *scores;                       // [R][hkv][S]
+  int S;
 };
 
 // One request, as every kernel here sees it.
@@ -517,6 +521,8 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
           o[0] = fmaf(f, v[p].x, o[0]); o[1] = fmaf(f, v[p].y, o[1]); o[2] = fmaf(f, v[p].z, o[2]); o[3] = fmaf(f, v[p].w, o[3]);
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;                      // nothing seen: zeros
+        if (A.stats && m < rows && c == 0)
+          __stcg(A.stats + (int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp, make_float2(M, l));
         if (m < rows && c < A.D) {
           __half *op = A.o + ((int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp) * A.D + c;
           *reinterpret_cast<uint2 *>(op) = make_uint2(pack_h2(o[0] * inv, o[1] * inv), pack_h2(o[2] * inv, o[3] * inv));
@@ -559,7 +565,9 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
     const int m = row0 + wm * 16 + g + 8 * h;
     if (splits == 1) {
       const float inv = sum[h] == 0.f ? 0.f : 1.f / sum[h];              // nothing seen: zeros
-      __half *op = A.o + ((int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp) * A.D;
+      const int64_t row = (int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp;
+      if (A.stats && t == 0) __stcg(A.stats + row, make_float2(mx[h], sum[h]));
+      __half *op = A.o + row * A.D;
 #pragma unroll
       for (int i = 0; i < DP / 8; ++i)
         if (i * 8 + 2 * t < A.D)
@@ -1054,7 +1062,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const float inv = sum == 0.f ? 0.f : 1.f / sum;                      // nothing seen: zeros
     const int64_t at = (int64_t)blockIdx.x * MT + tid;
     if (splits > 1 && live) __stcg(A.ml + at, make_float2(sum != 0.f ? ref : -INFINITY, sum));
-    __half *op = A.o + ((int64_t)tok * A.hkv * A.grp + head * A.grp + (live ? m % A.grp : 0)) * A.D;
+    const int64_t row = (int64_t)tok * A.hkv * A.grp + head * A.grp + (live ? m % A.grp : 0);
+    if (A.stats && splits == 1 && live) __stcg(A.stats + row, make_float2(ref, sum));
+    __half *op = A.o + row * A.D;
 #pragma unroll
     for (int c = 0; c < DP; c += 16) {
       float o[16];
@@ -1171,6 +1181,7 @@ __global__ void __launch_bounds__(128) k_tree_merge(AttnArgs A, int MT) {
     f[w] = exp2_fast(s_m[w0 + w] - ref);
     sum = fmaf(f[w], s_l[w0 + w], sum);
   }
+  if (A.stats && threadIdx.x % (32 * W) == 0) __stcg(A.stats + row, make_float2(ref, sum));
   for (int d = 2 * (threadIdx.x % (32 * W)); d < A.D; d += 64 * W) {
     float x = 0.f, y = 0.f;
 #pragma unroll
@@ -1180,6 +1191,136 @@ __global__ void __launch_bounds__(128) k_tree_merge(AttnArgs A, int MT) {
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint32_t *>(A.o + (int64_t)row * A.D + d) = pack_h2(x * inv, y * inv);
+  }
+}
+
+// --------------------------------------------- weights that keys received --
+// scores[r][head][p] += (= for the call's own tokens) the sum over the request's
+// rows of softmax_p: with every row's reference M and sum l known, the weight of a
+// score z is 2^(z - M) / l, and a key's rows are added in a fixed order.  A tile of
+// 64 keys is read again and multiplied with all of the request's rows, 16 at a time,
+// a warp every fourth group of them.  Rows that saw nothing have l = 0 and add nothing.
+template <int DP>
+__global__ void __launch_bounds__(128) k_tree_score(AttnArgs A) {
+  constexpr int CH = DP / 8;
+  __shared__ __align__(128) unsigned char sk[kTile * DP * 2];
+  __shared__ float s_sum[4][kTile];
+  __shared__ int64_t s_off[kTile];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  int C, units;
+  bool bad;
+  const Req q = plan_lane(A, 16, lane, C, units, bad);                   // bad requests have been flagged
+  int end = q.n ? q.nkt * A.hkv : 0;                                     // this request's tiles, all heads
+  const int own = end;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, end, o);
+    if (lane >= o) end += v;
+  }
+  const int total = __shfl_sync(0xffffffffu, end, 31);
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    const int req = __popc(__ballot_sync(0xffffffffu, end <= u));
+    const int in = u - __shfl_sync(0xffffffffu, end - own, req), nkt = __shfl_sync(0xffffffffu, q.nkt, req);
+    const int t0 = __shfl_sync(0xffffffffu, q.t0, req), n = __shfl_sync(0xffffffffu, q.n, req);
+    const int len = __shfl_sync(0xffffffffu, q.len, req), L = __shfl_sync(0xffffffffu, q.L, req);
+    const int head = in / nkt, pos0 = (in - head * nkt) * kTile, rows = n * A.grp;
+    if (tid < kTile) {
+      const int pos = pos0 + tid;
+      int64_t off = -1;
+      if (pos < L) {
+        const int id = A.table[(int64_t)req * A.max_pages + pos / A.page];
+        if ((unsigned)id < (unsigned)A.pages)
+          off = (int64_t)id * A.page_stride + (int64_t)(pos % A.page) * A.token_stride + (int64_t)head * A.head_stride;
+      }
+      s_off[tid] = off;
+    }
+    __syncthreads();
+    for (int i = tid >> 3; i < kTile; i += 16) {
+      const int64_t off = s_off[i];
+#pragma unroll
+      for (int c = tid & 7; c < CH; c += 8) {
+        const bool in_row = off >= 0 && c * 8 < A.D;
+        cp_async16(sk + i * DP * 2 + ((c ^ (i & 7)) * 16), A.k + (in_row ? off + c * 8 : 0), in_row ? 16u : 0u);
+      }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    const bool special = pos0 + kTile > len;
+    float acc[kTile / 8][2];
+#pragma unroll
+    for (int i = 0; i < kTile / 8; ++i) acc[i][0] = acc[i][1] = 0.f;
+    const uint32_t kb = smem_u32(sk);
+    for (int m0 = warp * 16; m0 < rows; m0 += 64) {
+      uint32_t qf[DP / 16][4], see[2];
+      float M[2], inv[2];
+      const __half *qp[2];
+      bool live[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int m = m0 + g + 8 * h;
+        live[h] = m < rows;
+        const int tok = t0 + (live[h] ? m / A.grp : 0);
+        const int64_t row = (int64_t)tok * A.hkv * A.grp + head * A.grp + (live[h] ? m % A.grp : 0);
+        see[h] = live[h] ? (uint32_t)A.anc[tok] : 0u;
+        qp[h] = A.q + row * A.D;
+        const float2 st = __ldcg(A.stats + row);
+        const bool none = !live[h] || st.y == 0.f;
+        M[h] = none ? INFINITY : st.x;
+        inv[h] = none ? 0.f : 1.f / st.y;
+      }
+#pragma unroll
+      for (int s = 0; s < DP / 16; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = s * 16 + 2 * t + 8 * (i >> 1);
+          qf[s][i] = live[i & 1] && c < A.D ? *reinterpret_cast<const uint32_t *>(qp[i & 1] + c) : 0u;
+        }
+      float z[kTile / 8][4];
+#pragma unroll
+      for (int i = 0; i < kTile / 8; ++i) z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.f;
+#pragma unroll
+      for (int s = 0; s < DP / 16; ++s)
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i) {
+          uint32_t b[4];
+          const int row = i * 16 + (lane >> 4) * 8 + (lane & 7), c = s * 2 + ((lane >> 3) & 1);
+          ldsm4(b, kb + row * DP * 2 + ((c ^ (row & 7)) * 16));
+          mma_f16(z[2 * i], qf[s], b[0], b[1]);
+          mma_f16(z[2 * i + 1], qf[s], b[2], b[3]);
+        }
+#pragma unroll
+      for (int i = 0; i < kTile / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = i * 8 + 2 * t + (e & 1), d = pos0 + key - len, h = e >> 1;
+          const bool ok = live[h] && (!special || (s_off[key] >= 0 && (d < 0 || ((see[h] >> ((t0 + d) & 31)) & 1u))));
+          const float w = exp2_fast(fmaf(z[i][e], A.scale, -M[h]));
+          acc[i][e & 1] = ok ? fmaf(w, inv[h], acc[i][e & 1]) : acc[i][e & 1];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kTile / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) acc[i][e] += __shfl_xor_sync(0xffffffffu, acc[i][e], o);
+        if (g == 0) s_sum[warp][i * 8 + 2 * t + e] = acc[i][e];
+      }
+    __syncthreads();
+    if (tid < kTile && pos0 + tid < L) {
+      const int pos = pos0 + tid;
+      if (pos >= A.S) {
+        flag_error(A.err, kErrIndex);
+      } else {
+        float *to = A.scores + ((int64_t)req * A.hkv + head) * A.S + pos;
+        const float w = s_sum[0][tid] + s_sum[1][tid] + s_sum[2][tid] + s_sum[3][tid];
+        if (pos >= len) *to = w;
+        else if (s_off[tid] >= 0) *to += w;
+      }
+    }
   }
 }
 
@@ -1293,40 +1434,13 @@ cudaError_t run_attn_any(const AttnArgs &a, int wm, int units, cudaStream_t st) 
                                 : launch(k_tree_merge<DP, 1, 8>, dim3((rows + 3) / 4), dim3(128), 0, st, a, 16 * wm);
 }
 
-}  // namespace
+// rows' references and sums
+size_t scored_scratch(int q_heads, int T) { return r256((size_t)T * q_heads * 8); }
 
-extern "C" {
-
-size_t asf_attention_workspace_bytes(const asf_kv_cache *cache, int32_t q_heads, int32_t R, int32_t T) {
-  if (check_cache(cache) != ASF_OK || q_heads < 1 || q_heads % cache->heads) return 0;
-  if (R < 1 || R > ASF_MAX_BATCH || T < 1 || T > ASF_MAX_BATCH || q_heads / cache->heads > ASF_MAX_HEAD_GROUP) return 0;
-  size_t need = 0;
-  for (int r = 1; r <= R; ++r)
-    for (int t = 1; t <= T; ++t) need = std::max(need, attn_scratch(cache, q_heads / cache->heads, r, t));
-  return kHeaderBytes + need;
-}
-
-asf_status asf_kv_append(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
-                         const int32_t *lens, const int32_t *begin, int32_t T, const void *k, const void *v, void *ws,
-                         size_t ws_bytes, asf_stream_t stream) {
-  asf_status s = check_cache(cache);
-  if (s == ASF_OK) s = check_requests(table, max_pages, R, lens, begin, T);
-  if (s == ASF_OK) s = check_tables(table, max_pages, cache->page, lens, begin);
-  if (s != ASF_OK) return s;
-  if (!k || !v) return ASF_ERR_INVALID_ARG;
-  if (!al16(k) || !al16(v)) return ASF_ERR_MISALIGNED;
-  s = check_ws(ws, ws_bytes, kHeaderBytes);
-  if (s != ASF_OK) return s;
-  AppendArgs a{static_cast<__half *>(cache->k), static_cast<__half *>(cache->v), cache->page_stride, cache->token_stride,
-               cache->head_stride, cache->pages, cache->page, cache->heads, cache->head_dim, table, max_pages, R, T, lens,
-               begin, static_cast<const __half *>(k), static_cast<const __half *>(v), &static_cast<Header *>(ws)->err};
-  const int chunks = T * cache->heads * (cache->head_dim / 8);
-  return cuda_status(launch(k_kv_append, dim3((chunks + 127) / 128), dim3(128), 0, (cudaStream_t)stream, a));
-}
-
-asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
-                              const int32_t *lens, const int32_t *begin, int32_t T, int32_t q_heads, const void *q,
-                              const int32_t *anc, float scale, void *o, void *ws, size_t ws_bytes, asf_stream_t stream) {
+// both forms of the call: scores null, or [R][heads][S]
+asf_status tree_attention(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R, const int32_t *lens,
+                          const int32_t *begin, int32_t T, int32_t q_heads, const void *q, const int32_t *anc, float scale,
+                          void *o, float *scores, int32_t S, void *ws, size_t ws_bytes, cudaStream_t st) {
   asf_status s = check_cache(cache);
   if (s == ASF_OK) s = check_requests(table, max_pages, R, lens, begin, T);
   if (s == ASF_OK) s = check_tables(table, max_pages, cache->page, lens, begin);
@@ -1335,10 +1449,15 @@ asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *table, i
   const int grp = q_heads / cache->heads;
   if (grp > ASF_MAX_HEAD_GROUP) return ASF_ERR_UNSUPPORTED;
   if (!al16(q) || !al16(o) || !al4(anc)) return ASF_ERR_MISALIGNED;
-  s = check_ws(ws, ws_bytes, kHeaderBytes + attn_scratch(cache, grp, R, T));
+  const size_t scratch = attn_scratch(cache, grp, R, T);
+  s = check_ws(ws, ws_bytes, kHeaderBytes + scratch + (scores ? scored_scratch(q_heads, T) : 0));
   if (s != ASF_OK) return s;
   const size_t bytes = (size_t)T * q_heads * cache->head_dim * 2;
   if (overlap(q, bytes, o, bytes)) return ASF_ERR_INVALID_ARG;
+  if (scores) {
+    const size_t all = (size_t)R * cache->heads * S * 4;
+    if (overlap(q, bytes, scores, all) || overlap(o, bytes, scores, all)) return ASF_ERR_INVALID_ARG;
+  }
   const int wm = row_groups(grp, R, T);
   const int64_t keys = (int64_t)max_pages * cache->page;
   int units = cache->heads * row_tiles_most(grp, R, T, wm);
@@ -1376,8 +1495,74 @@ asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *table, i
   a.whole = whole;
   a.cluster = cluster;
   a.err = &static_cast<Header *>(ws)->err;
-  cudaStream_t st = (cudaStream_t)stream;
-  return cuda_status(attn_dp(cache) == 64 ? run_attn_any<64>(a, wm, units, st) : run_attn_any<128>(a, wm, units, st));
+  if (scores) {
+    a.stats = reinterpret_cast<float2 *>(static_cast<unsigned char *>(ws) + kHeaderBytes + scratch);
+    a.scores = scores;
+    a.S = S;
+  }
+  cudaError_t e = attn_dp(cache) == 64 ? run_attn_any<64>(a, wm, units, st) : run_attn_any<128>(a, wm, units, st);
+  if (e == cudaSuccess && scores) {
+    const int64_t tiles = R * cache->heads * ((keys + kTile - 1) / kTile);
+    const dim3 grid((unsigned)std::min<int64_t>(tiles, 8 * sm_count()));
+    e = attn_dp(cache) == 64 ? launch(k_tree_score<64>, grid, dim3(128), 0, st, a)
+                             : launch(k_tree_score<128>, grid, dim3(128), 0, st, a);
+  }
+  return cuda_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t asf_attention_workspace_bytes(const asf_kv_cache *cache, int32_t q_heads, int32_t R, int32_t T) {
+  if (check_cache(cache) != ASF_OK || q_heads < 1 || q_heads % cache->heads) return 0;
+  if (R < 1 || R > ASF_MAX_BATCH || T < 1 || T > ASF_MAX_BATCH || q_heads / cache->heads > ASF_MAX_HEAD_GROUP) return 0;
+  size_t need = 0;
+  for (int r = 1; r <= R; ++r)
+    for (int t = 1; t <= T; ++t) need = std::max(need, attn_scratch(cache, q_heads / cache->heads, r, t));
+  return kHeaderBytes + need;
+}
+
+asf_status asf_kv_append(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
+                         const int32_t *lens, const int32_t *begin, int32_t T, const void *k, const void *v, void *ws,
+                         size_t ws_bytes, asf_stream_t stream) {
+  asf_status s = check_cache(cache);
+  if (s == ASF_OK) s = check_requests(table, max_pages, R, lens, begin, T);
+  if (s == ASF_OK) s = check_tables(table, max_pages, cache->page, lens, begin);
+  if (s != ASF_OK) return s;
+  if (!k || !v) return ASF_ERR_INVALID_ARG;
+  if (!al16(k) || !al16(v)) return ASF_ERR_MISALIGNED;
+  s = check_ws(ws, ws_bytes, kHeaderBytes);
+  if (s != ASF_OK) return s;
+  AppendArgs a{static_cast<__half *>(cache->k), static_cast<__half *>(cache->v), cache->page_stride, cache->token_stride,
+               cache->head_stride, cache->pages, cache->page, cache->heads, cache->head_dim, table, max_pages, R, T, lens,
+               begin, static_cast<const __half *>(k), static_cast<const __half *>(v), &static_cast<Header *>(ws)->err};
+  const int chunks = T * cache->heads * (cache->head_dim / 8);
+  return cuda_status(launch(k_kv_append, dim3((chunks + 127) / 128), dim3(128), 0, (cudaStream_t)stream, a));
+}
+
+asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
+                              const int32_t *lens, const int32_t *begin, int32_t T, int32_t q_heads, const void *q,
+                              const int32_t *anc, float scale, void *o, void *ws, size_t ws_bytes, asf_stream_t stream) {
+  return tree_attention(cache, table, max_pages, R, lens, begin, T, q_heads, q, anc, scale, o, nullptr, 0, ws, ws_bytes,
+                        (cudaStream_t)stream);
+}
+
+size_t asf_attention_scored_workspace_bytes(const asf_kv_cache *cache, int32_t q_heads, int32_t R, int32_t T,
+                                            int32_t max_pages) {
+  const size_t need = asf_attention_workspace_bytes(cache, q_heads, R, T);
+  if (need == 0 || max_pages < 1 || (int64_t)max_pages * cache->page > ASF_MAX_KEYS) return 0;
+  return need + scored_scratch(q_heads, T);
+}
+
+asf_status asf_tree_attention_scored(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
+                                     const int32_t *lens, const int32_t *begin, int32_t T, int32_t q_heads, const void *q,
+                                     const int32_t *anc, float scale, void *o, float *scores, int32_t S, void *ws,
+                                     size_t ws_bytes, asf_stream_t stream) {
+  if (!scores || S < 1) return ASF_ERR_INVALID_ARG;
+  if (!al4(scores)) return ASF_ERR_MISALIGNED;
+  return tree_attention(cache, table, max_pages, R, lens, begin, T, q_heads, q, anc, scale, o, scores, S, ws, ws_bytes,
+                        (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -388,6 +388,21 @@ ASF_API asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *
                                       const void *q, const int32_t *anc, float scale, void *o, void *ws,
                                       size_t ws_bytes, asf_stream_t stream);
 
+/* asf_tree_attention, and for each key the attention weight that it received:
+ * scores (device fp32 [R][heads][S], request by request, by position) gains, for every
+ * key before lens[r], the sum over request r's tokens and the kv head's query heads of
+ * softmax_p; the positions of the call's own tokens are set to their sums, whatever
+ * was there (drafted tokens that were not accepted leave nothing behind).  Positions
+ * from lens[r] + the request's tokens on, and requests without tokens, stay as they
+ * are.  S has to cover the positions seen: those from S on are skipped and flagged.
+ * scores is apart from q and o.  o is asf_tree_attention's, bit for bit. */
+ASF_API size_t asf_attention_scored_workspace_bytes(const asf_kv_cache *cache, int32_t q_heads, int32_t R, int32_t T,
+                                                    int32_t max_pages);
+ASF_API asf_status asf_tree_attention_scored(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
+                                             const int32_t *lens, const int32_t *begin, int32_t T, int32_t q_heads,
+                                             const void *q, const int32_t *anc, float scale, void *o, float *scores,
+                                             int32_t S, void *ws, size_t ws_bytes, asf_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * Rotary positions: queries and keys are turned before they meet in tree
  * attention.  Of a head's head_dim columns the first rot_dim are turned in pairs,

@@ -41,3 +41,30 @@ def tree_attention(k, v, table, lens, begin, q, anc, scale: float):
                 mass[t, h] = p @ np.abs(vr[see, h // grp])
                 big[t, h] = abs(scale) * (np.abs(kr[see, h // grp]) @ np.abs(qq)).max()
     return o, mass, big
+
+
+def received(k, table, lens, begin, q, anc, scale: float, scores):
+    """(scores after the call, bound of sum_rows w x the row's score error in units of 2^-23): what each key has received."""
+    out, err = np.array(scores, np.float64), np.zeros(np.shape(scores))
+    D, grp = q.shape[2], q.shape[1] // k.shape[2]
+    for r, n in enumerate(lens):
+        m = begin[r + 1] - begin[r]
+        if m == 0:
+            continue
+        pg, sl = positions(table[r], k.shape[1], n + m)
+        kr = k[pg, sl].astype(np.float64)
+        out[r, :, n:n + m] = 0
+        for t in range(begin[r], begin[r + 1]):
+            see = np.concatenate([np.ones(n, bool), [(int(anc[t]) >> j) & 1 for j in range(begin[r], begin[r + 1])]]).astype(bool)
+            if not see.any():
+                continue
+            for h in range(q.shape[1]):
+                qq = q[t, h].astype(np.float64)
+                z = scale * (kr[see, h // grp] @ qq)
+                w = np.exp(z - z.max())
+                w /= w.sum()
+                big = abs(scale) * (np.abs(kr[see, h // grp]) @ np.abs(qq)).max()
+                at = np.flatnonzero(see)
+                out[r, h // grp, at] += w
+                err[r, h // grp, at] += w * big
+    return out, err * (D + 16)
