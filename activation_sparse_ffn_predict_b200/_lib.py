@@ -27,6 +27,7 @@ ASF_W4_MAX_ROWS = 1 << 30
 ASF_MAX_KV_HEADS = 1024
 ASF_MAX_HEAD_GROUP = 128
 ASF_MAX_KEYS = 1 << 30
+ASF_HEADER_BYTES = 4096          # a workspace that holds the error word alone
 ASF_MAX_ROTARY_DIM = 512
 ASF_MAX_ROTARY_HEADS = 65535
 ASF_ROTARY_HALF = 0
@@ -126,6 +127,9 @@ PROTOTYPES = {
     "asf_tree_attention_scored": (c_int, [POINTER(asf_kv_cache), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32,
                                           c_int32, c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_int32, c_void_p,
                                           c_size_t, c_void_p]),
+    "asf_kv_evict": (c_int, [POINTER(asf_kv_cache), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32, c_int32,
+                             c_int32, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_size_t,
+                             c_void_p]),
     "asf_rotary_frequencies": (c_int, [c_int32, c_double, c_int32, c_double, c_double, POINTER(c_double),
                                        POINTER(c_float)]),
     "asf_rotary_turns": (c_int, [POINTER(c_double), c_int32, POINTER(c_uint64)]),

@@ -201,6 +201,11 @@ class Workspace:
         return cls._sized(cache.workspace_bytes(q_heads, requests, tokens, scored_pages), cache.device, stream,
                           "asf_attention_workspace_bytes")
 
+    @classmethod
+    def for_eviction(cls, cache, stream=None) -> "Workspace":
+        """What asf_kv_evict needs (any workspace of the cache's other calls will do as well)."""
+        return cls._sized(L.ASF_HEADER_BYTES, cache.device, stream, "asf_kv_evict")
+
     def on(self, device) -> int:
         """Its address, for a call on ``device``."""
         if self.buf.get_device() != device.index:

@@ -1,5 +1,6 @@
-"""Tree attention over a paged key/value cache: tensor-level binding of
-asf_kv_append and asf_tree_attention (include/asffn.h, "Tree attention")."""
+"""Tree attention over a paged key/value cache, and eviction from it: tensor-level
+binding of asf_kv_append, asf_tree_attention, asf_tree_attention_scored and
+asf_kv_evict (include/asffn.h, "Tree attention" and "Eviction")."""
 from __future__ import annotations
 
 import ctypes
@@ -99,3 +100,28 @@ def asf_tree_attention_scored(cache: KVCache, table: torch.Tensor, lens: torch.T
         raise ValueError("scores must be [R, heads, S]")
     sp = _arg(scores, "scores", cache.device, torch.float32)
     _invoke("asf_tree_attention_scored", cache.device, stream, *args, sp, of[2], ws.on(cache.device), ws.nbytes)
+
+
+def asf_kv_evict(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, scores: torch.Tensor, keep: int,
+                 table_out: torch.Tensor, lens_out: torch.Tensor, scores_out: torch.Tensor, kept: torch.Tensor,
+                 ws: Workspace, first: int = 0, recent: int = 0, stream=None) -> None:
+    """Each request's kv heads keep `keep` keys each, on the pages of table_out [R, max_pages]: the first `first`,
+    the last `recent` and those with the largest scores fp32 [R, heads, S], in their order.
+
+    lens_out int32 [R], kept int32 [R, heads, keep] (the old positions) and scores_out fp32 [R, heads,
+    >= keep] are written as far as keys are kept."""
+    dev, of, R = cache.device, scores.shape, lens.shape[0]
+    if table.dim() != 2 or table_out.dim() != 2 or table.shape[0] != R or table_out.shape[0] != R or lens.dim() != 1:
+        raise ValueError("table and table_out must be [R, max_pages], lens [R]")
+    if len(of) != 3 or of[0] != R or of[1] != cache.heads:
+        raise ValueError("scores must be [R, heads, S]")
+    if lens_out.shape != (R,) or kept.shape != (R, cache.heads, keep):
+        raise ValueError("lens_out must be [R] and kept [R, heads, keep]")
+    to = scores_out.shape
+    if len(to) != 3 or to[0] != R or to[1] != cache.heads:
+        raise ValueError("scores_out must be [R, heads, S_out]")
+    i32, f32 = torch.int32, torch.float32
+    _invoke("asf_kv_evict", dev, stream, cache._ref, _arg(table, "table", dev, i32), table.shape[1], R,
+            _arg(lens, "lens", dev, i32), _arg(scores, "scores", dev, f32), of[2], int(keep), int(first), int(recent),
+            _arg(table_out, "table_out", dev, i32), table_out.shape[1], _arg(lens_out, "lens_out", dev, i32),
+            _arg(scores_out, "scores_out", dev, f32), to[2], _arg(kept, "kept", dev, i32), ws.on(dev), ws.nbytes)

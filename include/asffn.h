@@ -404,6 +404,32 @@ ASF_API asf_status asf_tree_attention_scored(const asf_kv_cache *cache, const in
                                              int32_t S, void *ws, size_t ws_bytes, asf_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Eviction: requests whose caches have grown too long keep `keep` of their keys, the
+ * same number for each kv head, but each head its own: the first `first` and the last
+ * `recent` positions, and of those between the ones with the largest scores (as
+ * asf_tree_attention_scored adds them up; equal scores: the lower position; NaN is
+ * below everything).  A request of at most `keep` keys keeps all.  What stays keeps its
+ * order, and moves to the pages of table_out, from its position 0 on:
+ *   lens_out    device int32 [R]: min(lens[r], keep)
+ *   kept        device int32 [R][heads][keep]: the old positions, ascending
+ *   scores_out  device fp32 [R][heads][S_out], S_out >= keep: their scores
+ * and of the cache the rows of table_out's pages; past lens_out[r] everything stays
+ * as it is, and so do table's pages, which may be shared with other requests and are
+ * the caller's to reuse once the call has run.  Pages of table_out are pages of no
+ * table, and listed once.  first + recent <= keep.  scores as there ([R][heads][S]).
+ * Rows are moved with their bits: turned keys stay turned by their first positions, so
+ * new tokens' positions (asf_rotary_append's pos) go on from the old length.
+ *
+ * Bad pages, lengths below 0 or past S or the table, and kept keys past table_out
+ * are skipped, clamped and flagged as for asf_tree_attention.  ws: at least 4096
+ * bytes, for the error word.  Outputs are apart from inputs and from one another. */
+ASF_API asf_status asf_kv_evict(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
+                                const int32_t *lens, const float *scores, int32_t S, int32_t keep, int32_t first,
+                                int32_t recent, const int32_t *table_out, int32_t max_pages_out, int32_t *lens_out,
+                                float *scores_out, int32_t S_out, int32_t *kept, void *ws, size_t ws_bytes,
+                                asf_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Rotary positions: queries and keys are turned before they meet in tree
  * attention.  Of a head's head_dim columns the first rot_dim are turned in pairs,
  * the others pass bit for bit: pair j of a token at position p, (u, w), becomes

@@ -68,3 +68,24 @@ def received(k, table, lens, begin, q, anc, scale: float, scores):
                 out[r, h // grp, at] += w
                 err[r, h // grp, at] += w * big
     return out, err * (D + 16)
+
+
+def evict(k, v, table, lens, scores, keep: int, first: int, recent: int, table_out):
+    """In place on k and v: the kept rows on table_out's pages.  (positions, scores) kept, by request and head."""
+    page, kept, best = k.shape[1], [], []
+    for r, n in enumerate(lens):
+        kept.append([])
+        best.append([])
+        for h in range(k.shape[2]):
+            p = list(range(n))
+            if n > keep:
+                value = lambda i: -np.inf if np.isnan(scores[r, h, i]) else float(scores[r, h, i])  # noqa: E731
+                # NaN is below the lowest number, too
+                middle = sorted(range(first, n - recent), key=lambda i: (bool(np.isnan(scores[r, h, i])), -value(i), i))
+                p = p[:first] + sorted(middle[:keep - first - recent]) + p[n - recent:]
+            kept[-1].append(np.array(p, int))
+            best[-1].append(scores[r, h, p])
+            for j, i in enumerate(p):
+                to, at = (table_out[r][j // page], j % page, h), (table[r][i // page], i % page, h)
+                k[to], v[to] = k[at], v[at]
+    return kept, best
