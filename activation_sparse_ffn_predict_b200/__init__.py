@@ -18,5 +18,5 @@ from .stack import AttentionStage, LayerStack  # noqa: F401
 from .rotary import Rotary, asf_rotary_append, asf_rotary_apply  # noqa: F401
 from .attention import (KVCache, asf_kv_append, asf_kv_evict, asf_tree_attention,  # noqa: F401
                         asf_tree_attention_scored)
-from .w4 import (W4FFN, W4Matrix, asf_w4_dequantize, asf_w4_matmul, asf_w4_quantize, asf_w4_row_bytes,  # noqa: F401
-                 asf_w4_sparse_ffn)
+from .w4 import (LoraSet, W4FFN, W4Matrix, asf_w4_dequantize, asf_w4_matmul, asf_w4_matmul_lora,  # noqa: F401
+                 asf_w4_quantize, asf_w4_row_bytes, asf_w4_sparse_ffn)

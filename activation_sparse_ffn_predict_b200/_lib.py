@@ -24,6 +24,7 @@ ASF_MAX_BATCH = 32
 ASF_NOALLOC_SCRATCH_BYTES = 32 << 20
 ASF_W4_MAX_K = 65536
 ASF_W4_MAX_ROWS = 1 << 30
+ASF_MAX_LORA_RANK = 256
 ASF_MAX_KV_HEADS = 1024
 ASF_MAX_HEAD_GROUP = 128
 ASF_MAX_KEYS = 1 << 30
@@ -74,6 +75,11 @@ class asf_kv_cache(ctypes.Structure):
                 ("v", c_void_p), ("page_stride", c_int64), ("token_stride", c_int64), ("head_stride", c_int64)]
 
 
+class asf_lora(ctypes.Structure):
+    _fields_ = [("adapters", c_int32), ("rank", c_int32), ("k", c_int32), ("rows", c_int32), ("dtype", c_int),
+                ("A", c_void_p), ("B", c_void_p), ("scale", c_void_p)]
+
+
 class asf_rotary(ctypes.Structure):
     _fields_ = [("head_dim", c_int32), ("rot_dim", c_int32), ("layout", c_int32), ("scale", c_float), ("turns", c_void_p)]
 
@@ -118,6 +124,9 @@ PROTOTYPES = {
                               c_void_p, c_size_t, c_void_p]),
     "asf_w4_sparse_ffn": (c_int, [POINTER(asf_w4_ffn), c_void_p, c_int, c_int32, c_void_p, c_void_p, c_void_p,
                                   c_void_p, c_size_t, c_void_p]),
+    "asf_w4_lora_workspace_bytes": (c_size_t, [POINTER(asf_w4_matrix), POINTER(asf_lora), c_int32]),
+    "asf_w4_matmul_lora": (c_int, [POINTER(asf_w4_matrix), POINTER(asf_lora), c_void_p, c_void_p, c_int, c_int32, c_void_p,
+                                   c_int32, c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
     "asf_attention_workspace_bytes": (c_size_t, [POINTER(asf_kv_cache), c_int32, c_int32, c_int32]),
     "asf_kv_append": (c_int, [POINTER(asf_kv_cache), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32, c_void_p,
                               c_void_p, c_void_p, c_size_t, c_void_p]),

@@ -189,9 +189,11 @@ class Workspace:
         return self
 
     @classmethod
-    def for_w4(cls, op, max_batch: int, stream=None) -> "Workspace":
-        """Scratch of asf_w4_matmul (op a W4Matrix) or asf_w4_sparse_ffn (a W4FFN)."""
-        return cls._sized(op.workspace_bytes(max_batch), op.device, stream, "asf_w4_workspace_bytes")
+    def for_w4(cls, op, max_batch: int, stream=None, lora=None) -> "Workspace":
+        """Scratch of asf_w4_matmul (op a W4Matrix) or asf_w4_sparse_ffn (a W4FFN), and with lora (a LoraSet)
+        of asf_w4_matmul_lora."""
+        need = op.workspace_bytes(max_batch) if lora is None else op.workspace_bytes(max_batch, lora)
+        return cls._sized(need, op.device, stream, "asf_w4_workspace_bytes")
 
     @classmethod
     def for_attention(cls, cache, q_heads: int, requests: int, tokens: int, stream=None,

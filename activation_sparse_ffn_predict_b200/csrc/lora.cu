@@ -1,0 +1,331 @@
+// Low-rank adapters of many tokens beside a 4-bit product that they share
+// (include/asffn.h, "Adapters").
+//
+//   asf_w4_matmul_lora    k_lora_down, the product of asf_w4_matmul, k_lora_up
+//
+// Mathematics.  y = act(W x + bias + s_a B_a (A_a x)) with a token's own adapter a:
+// h = s_a A_a x has `rank` values, kept in fp32, and so is W x, so that y is rounded
+// once.  Both steps read each adapter in use once: the first token of the call that
+// has it (its leader) takes all of its tokens along, eight at a time.  A token's sums
+// are added in the same order whoever comes along.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "asffn.h"
+#include "common.cuh"
+#include "host.cuh"
+
+using namespace asf;
+
+namespace {
+
+constexpr int kDownThreads = 256;
+constexpr int kUpThreads = 128;
+constexpr int kUpRows = 128;           // rows of y that a CTA takes
+constexpr int kAlong = 8;              // tokens at a time
+
+struct LoraArgs {
+  int adapters, rank, k, rows, B;
+  const void *A, *Bm;                  // [adapters][rank][k], [adapters][rows][rank]
+  const float *scale;                  // [adapters], or null: 1
+  const int32_t *which;                // [B]
+  const void *x;
+  float *h;                            // [B][rank]
+  const float *base;                   // [B][rows]: W x + bias
+  void *y;
+  int y16, relu;
+  int32_t *err;
+};
+
+// The tokens that use token b's adapter, if b is the first of them; 0 else.  a: the
+// adapter, -1 without one.  Whole warps call it.
+__device__ __forceinline__ uint32_t led_by(const LoraArgs &A, int b, int &a) {
+  const int lane = threadIdx.x & 31;
+  int w = -1;
+  if (lane < A.B) {
+    w = ld_cg_i32(A.which + lane);
+    if (w >= A.adapters) {
+      flag_error(A.err, kErrIndex);
+      w = -1;
+    }
+    w = max(w, -1);
+  }
+  a = __shfl_sync(0xffffffffu, w, b);
+  const uint32_t all = __ballot_sync(0xffffffffu, lane < A.B && w == a);
+  return __ffs(all) - 1 == b ? all : 0u;
+}
+// the next (up to) NB tokens of a set, the last one again where there are fewer
+template <int NB>
+__device__ __forceinline__ int take(uint32_t &set, int (&tok)[NB]) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    if (set) {
+      tok[i] = __ffs(set) - 1;
+      set &= set - 1;
+      ++n;
+    } else {
+      tok[i] = i ? tok[i - 1] : 0;
+    }
+  }
+  return n;
+}
+
+// v[i] summed over the warp; lane l is left with the sum of v[i] for i = l / (32 / N)
+// in the order 16, 8, 4, 2, 1 of lanes, which is every N's.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = N / 2, o = 16; n > 0; n /= 2, o /= 2) {
+    const bool hi = lane & o;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      if (i < n) {
+        const float keep = hi ? v[i + n] : v[i], give = hi ? v[i] : v[i + n];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+  }
+#pragma unroll
+  for (int o = 16 / N; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
+}
+
+template <typename T, int RW, int NB>
+__device__ __forceinline__ void down_rows(const LoraArgs &A, int a, int row0, uint32_t &set, float *s_red) {
+  constexpr int E = Vec<T>::N;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int tok[NB];
+  const int n = take<NB>(set, tok);
+  const T *w = static_cast<const T *>(A.A) + ((int64_t)a * A.rank + row0) * A.k;
+  const T *x = static_cast<const T *>(A.x);
+  float acc[RW * NB];
+#pragma unroll
+  for (int i = 0; i < RW * NB; ++i) acc[i] = 0.f;
+#pragma unroll 2
+  for (int i = tid * E; i < A.k; i += kDownThreads * E) {
+    uint4 wv[RW], xv[NB];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) wv[r] = __ldg(reinterpret_cast<const uint4 *>(w + (int64_t)r * A.k + i));
+#pragma unroll
+    for (int b = 0; b < NB; ++b) xv[b] = __ldcg(reinterpret_cast<const uint4 *>(x + (int64_t)tok[b] * A.k + i));
+#pragma unroll
+    for (int r = 0; r < RW; ++r)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[r * NB + b] = Vec<T>::dot(wv[r], xv[b], acc[r * NB + b]);
+  }
+  constexpr int N = RW * NB, SPAN = 32 / N;
+  const float v = warp_sums<N>(acc);
+  __syncthreads();                     // the last sums have been read
+  if (lane % SPAN == 0) s_red[warp * N + lane / SPAN] = v;
+  __syncthreads();
+  if (tid < N && tid % NB < n) {
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < kDownThreads / 32; ++q) sum += s_red[q * N + tid];
+    const float s = A.scale ? __ldg(A.scale + a) : 1.f;
+    int t = tok[0];
+#pragma unroll
+    for (int b = 1; b < NB; ++b) t = tid % NB == b ? tok[b] : t;
+    __stcg(A.h + (int64_t)t * A.rank + row0 + tid / NB, s * sum);
+  }
+}
+
+// h = s A x: a CTA is RW rows of the adapter that its token leads, over all of k.
+template <typename T, int RW>
+__global__ void __launch_bounds__(kDownThreads) k_lora_down(LoraArgs A) {
+  __shared__ float s_red[kDownThreads / 32 * 32];
+  pdl_wait();
+  pdl_trigger();
+  int a;
+  uint32_t set = led_by(A, blockIdx.y, a);
+  if (!set || a < 0) return;
+  const int row0 = blockIdx.x * RW;    // rank is a multiple of 8
+  while (set) {
+    const int left = __popc(set);
+    if (left > 4) down_rows<T, RW, 8>(A, a, row0, set, s_red);
+    else if (left > 2) down_rows<T, RW, 4>(A, a, row0, set, s_red);
+    else if (left > 1) down_rows<T, RW, 2>(A, a, row0, set, s_red);
+    else down_rows<T, RW, 1>(A, a, row0, set, s_red);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<__half>(const __half *p, float (&v)[8]) {
+  Vec<__half>::to_float(__ldg(reinterpret_cast<const uint4 *>(p)), v);
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float *p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+template <typename T, int NB>
+__device__ __forceinline__ void up_rows(const LoraArgs &A, int a, int row0, int lpr, uint32_t &set, float *s_out) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int tok[NB];
+  const int n = take<NB>(set, tok);
+  const int part = lane & (lpr - 1), per = 32 / lpr;                   // rows a warp has at a time
+  const bool in = part * 8 < A.rank;
+  float h[NB][8];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      const float4 u = in ? __ldcg(reinterpret_cast<const float4 *>(A.h + (int64_t)tok[b] * A.rank + part * 8 + e))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+      h[b][e] = u.x; h[b][e + 1] = u.y; h[b][e + 2] = u.z; h[b][e + 3] = u.w;
+    }
+  const T *w = static_cast<const T *>(A.Bm) + (int64_t)a * A.rows * A.rank + part * 8;
+  __syncthreads();                     // s_out has been read
+#pragma unroll 4
+  for (int i = warp * 32 + lane / lpr; i < warp * 32 + 32; i += per) {
+    const int row = row0 + i;
+    float v[8], acc[NB];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    if (in && row < A.rows) load8<T>(w + (int64_t)row * A.rank, v);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      acc[b] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[b] = fmaf(v[e], h[b][e], acc[b]);
+    }
+    for (int o = lpr / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[b] += __shfl_xor_sync(0xffffffffu, acc[b], o);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (part == (b & (lpr - 1))) s_out[b * kUpRows + i] = acc[b];
+  }
+  __syncthreads();
+  const int row = row0 + tid;
+  if (row < A.rows)
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (b < n) {
+        const int64_t at = (int64_t)tok[b] * A.rows + row;
+        float v = __ldcg(A.base + at) + s_out[b * kUpRows + tid];
+        if (A.relu) v = v > 0.f ? v : (v != v ? v : 0.f);
+        if (A.y16) static_cast<__half *>(A.y)[at] = __float2half_rn(v);
+        else static_cast<float *>(A.y)[at] = v;
+      }
+}
+
+// y = act(base + B h): a CTA is 128 rows of the adapter that its token leads; lanes
+// lie side by side along a row of B, eight ranks each, so that a warp reads whole
+// rows one after the other, and the tokens' sums go through shared memory to come
+// out row by row.
+template <typename T>
+__global__ void __launch_bounds__(kUpThreads) k_lora_up(LoraArgs A, int lpr) {
+  __shared__ float s_out[kAlong * kUpRows];
+  pdl_wait();
+  pdl_trigger();
+  int a;
+  uint32_t set = led_by(A, blockIdx.y, a);
+  if (!set) return;
+  const int row0 = blockIdx.x * kUpRows;
+  if (a < 0) {                         // no adapter: the activation and the rounding are left to do
+    const int row = row0 + threadIdx.x;
+    if (row >= A.rows || (static_cast<const void *>(A.base) == A.y && !A.relu)) return;
+    for (; set; set &= set - 1) {
+      const int64_t at = (int64_t)(__ffs(set) - 1) * A.rows + row;
+      float v = __ldcg(A.base + at);
+      if (A.relu) v = v > 0.f ? v : (v != v ? v : 0.f);
+      if (A.y16) static_cast<__half *>(A.y)[at] = __float2half_rn(v);
+      else static_cast<float *>(A.y)[at] = v;
+    }
+    return;
+  }
+  while (set) {
+    const int left = __popc(set);
+    if (left > 4) up_rows<T, 8>(A, a, row0, lpr, set, s_out);
+    else if (left > 2) up_rows<T, 4>(A, a, row0, lpr, set, s_out);
+    else if (left > 1) up_rows<T, 2>(A, a, row0, lpr, set, s_out);
+    else up_rows<T, 1>(A, a, row0, lpr, set, s_out);
+  }
+}
+
+// ------------------------------------------------------------------ host --
+asf_status check_lora(const asf_lora *l) {
+  if (!l || !l->A || !l->B || l->adapters < 1 || l->rank < 1 || l->k < 1 || l->rows < 1) return ASF_ERR_INVALID_ARG;
+  if (l->dtype != ASF_F16 && l->dtype != ASF_F32) return ASF_ERR_UNSUPPORTED;
+  if (l->rank % 8 || l->k % 8 || !al16(l->A) || !al16(l->B) || !al4(l->scale)) return ASF_ERR_MISALIGNED;
+  if (l->rank > ASF_MAX_LORA_RANK || l->k > ASF_W4_MAX_K || l->rows > ASF_W4_MAX_ROWS) return ASF_ERR_UNSUPPORTED;
+  return ASF_OK;
+}
+size_t lora_scratch(const asf_lora *l, int B) { return r256((size_t)B * l->rank * 4) + r256((size_t)B * l->rows * 4); }
+
+template <typename T>
+cudaError_t run_down(const LoraArgs &a, cudaStream_t st) {
+  // four rows a CTA where that still is a CTA an SM, for adapters as many as may be
+  return a.rank / 4 * std::min(a.B, a.adapters) >= sm_count()
+             ? launch(k_lora_down<T, 4>, dim3(a.rank / 4, a.B), dim3(kDownThreads), 0, st, a)
+             : launch(k_lora_down<T, 1>, dim3(a.rank, a.B), dim3(kDownThreads), 0, st, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t asf_w4_lora_workspace_bytes(const asf_w4_matrix *mat, const asf_lora *lora, int32_t max_batch) {
+  const size_t need = asf_w4_workspace_bytes(mat, nullptr, max_batch);
+  if (need == 0 || check_lora(lora) != ASF_OK || lora->k != mat->k || lora->rows != mat->rows) return 0;
+  return r256(need) + lora_scratch(lora, max_batch);
+}
+
+asf_status asf_w4_matmul_lora(const asf_w4_matrix *mat, const asf_lora *lora, const int32_t *which, const void *x,
+                              asf_dtype xdtype, int32_t B, const float *bias, int32_t relu, void *y, asf_dtype ydtype,
+                              void *ws, size_t ws_bytes, asf_stream_t stream) {
+  asf_status s = check_lora(lora);
+  if (s != ASF_OK) return s;
+  if (!mat || !which || !x || !y || lora->k != mat->k || lora->rows != mat->rows || B < 1 || B > ASF_MAX_BATCH ||
+      (relu != 0 && relu != 1))
+    return ASF_ERR_INVALID_ARG;
+  if ((ydtype != ASF_F16 && ydtype != ASF_F32) || xdtype != lora->dtype) return ASF_ERR_UNSUPPORTED;
+  if (!al4(which) || !al16(x) || (reinterpret_cast<uintptr_t>(y) & (ydtype == ASF_F16 ? 1u : 3u))) return ASF_ERR_MISALIGNED;
+  const size_t plain = r256(asf_w4_workspace_bytes(mat, nullptr, B));
+  if (plain) {
+    s = check_ws(ws, ws_bytes, plain + lora_scratch(lora, B));
+    if (s != ASF_OK) return s;
+  }
+  if (overlap(x, (size_t)B * mat->k * (xdtype == ASF_F16 ? 2 : 4), y, (size_t)B * mat->rows * (ydtype == ASF_F16 ? 2 : 4)))
+    return ASF_ERR_INVALID_ARG;
+  unsigned char *at = static_cast<unsigned char *>(ws) + plain;
+  LoraArgs a{};
+  a.adapters = lora->adapters;
+  a.rank = lora->rank;
+  a.k = lora->k;
+  a.rows = lora->rows;
+  a.B = B;
+  a.A = lora->A;
+  a.Bm = lora->B;
+  a.scale = lora->scale;
+  a.which = which;
+  a.x = x;
+  a.h = reinterpret_cast<float *>(at);
+  a.y = y;
+  a.y16 = ydtype == ASF_F16;
+  float *base = a.y16 ? reinterpret_cast<float *>(at + r256((size_t)B * lora->rank * 4)) : static_cast<float *>(y);
+  a.base = base;
+  a.relu = relu;
+  a.err = plain ? &static_cast<Header *>(ws)->err : nullptr;
+  // the product first: it refuses what is wrong with the matrix before anything is enqueued
+  s = asf_w4_matmul(mat, x, xdtype, B, bias, 0, base, ASF_F32, ws, plain, stream);
+  if (s != ASF_OK) return s;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = xdtype == ASF_F16 ? run_down<__half>(a, st) : run_down<float>(a, st);
+  if (e != cudaSuccess) return ASF_ERR_CUDA;
+  int lpr = 1;
+  while (lpr * 8 < a.rank) lpr *= 2;
+  const dim3 grid((a.rows + kUpRows - 1) / kUpRows, B);
+  e = xdtype == ASF_F16 ? launch(k_lora_up<__half>, grid, dim3(kUpThreads), 0, st, a, lpr)
+                        : launch(k_lora_up<float>, grid, dim3(kUpThreads), 0, st, a, lpr);
+  return cuda_status(e);
+}
+
+}  // extern "C"

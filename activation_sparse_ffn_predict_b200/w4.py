@@ -49,8 +49,30 @@ class W4Matrix:
         asf_w4_quantize(W, mat, stream)
         return mat
 
-    def workspace_bytes(self, max_batch: int) -> int:
+    def workspace_bytes(self, max_batch: int, lora: Optional["LoraSet"] = None) -> int:
+        if lora is not None:
+            return int(L.load().asf_w4_lora_workspace_bytes(self._ref, lora._ref, int(max_batch)))
         return int(L.load().asf_w4_workspace_bytes(self._ref, None, int(max_batch)))
+
+
+class LoraSet:
+    """Low-rank adapters of one projection: A [n, rank, k] and B [n, m, rank], fp16 or fp32, scale fp32 [n] (1 without);
+    rank a multiple of 8 up to 256: adapters of smaller ranks are padded with zeros."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: Optional[torch.Tensor] = None):
+        if not isinstance(A, torch.Tensor) or not A.is_cuda or A.dtype not in _DT or A.dim() != 3:
+            raise ValueError("A must be a float16 or float32 CUDA tensor [n, rank, k]")
+        n, rank, k = A.shape
+        if B.dim() != 3 or B.shape[0] != n or B.shape[2] != rank or A.numel() == 0 or B.numel() == 0:
+            raise ValueError("B must be [n, m, rank]")
+        if scale is not None and scale.shape != (n,):
+            raise ValueError("scale must be [n]")
+        self.A, self.B, self.scale, self.device = A, B, scale, A.device
+        self.adapters, self.rank, self.k, self.rows, self.dtype = int(n), int(rank), int(k), int(B.shape[1]), A.dtype
+        self.desc = L.asf_lora(self.adapters, self.rank, self.k, self.rows, _DT[A.dtype], _arg(A, "A", A.device),
+                               _arg(B, "B", A.device, A.dtype),
+                               _arg(scale, "scale", A.device, torch.float32) if scale is not None else None)
+        self._ref = ctypes.byref(self.desc)
 
 
 class W4FFN:
@@ -116,9 +138,7 @@ def asf_w4_dequantize(mat: W4Matrix, dst: torch.Tensor, stream=None) -> None:
     _invoke("asf_w4_dequantize", mat.device, stream, mat._ref, dp, _DT[dst.dtype])
 
 
-def asf_w4_matmul(mat: W4Matrix, x: torch.Tensor, y: torch.Tensor, ws: Workspace,
-                  bias: Optional[torch.Tensor] = None, relu: bool = False, stream=None) -> None:
-    """y [B, m] = x [B, k] times the 4-bit rows (+ bias [m], then ReLU); x and y fp16 or fp32."""
+def _product(mat: W4Matrix, x, y, bias, relu):
     xt, yt, of = _DT.get(x.dtype), _DT.get(y.dtype), x.shape
     if xt is None or len(of) != 2 or of[1] != mat.k:
         raise ValueError("x must be [B, k], float16 or float32")
@@ -131,8 +151,26 @@ def asf_w4_matmul(mat: W4Matrix, x: torch.Tensor, y: torch.Tensor, ws: Workspace
         if bias.shape != (mat.rows,):
             raise ValueError("bias must be [rows]")
         bp = _arg(bias, "bias", dev, torch.float32)
-    xp, yp = _arg(x, "x", dev), _arg(y, "y", dev)
-    _invoke("asf_w4_matmul", dev, stream, mat._ref, xp, xt, B, bp, int(bool(relu)), yp, yt, ws.on(dev), ws.nbytes)
+    return _arg(x, "x", dev), xt, B, bp, int(bool(relu)), _arg(y, "y", dev), yt
+
+
+def asf_w4_matmul(mat: W4Matrix, x: torch.Tensor, y: torch.Tensor, ws: Workspace,
+                  bias: Optional[torch.Tensor] = None, relu: bool = False, stream=None) -> None:
+    """y [B, m] = x [B, k] times the 4-bit rows (+ bias [m], then ReLU); x and y fp16 or fp32."""
+    _invoke("asf_w4_matmul", mat.device, stream, mat._ref, *_product(mat, x, y, bias, relu), ws.on(mat.device), ws.nbytes)
+
+
+def asf_w4_matmul_lora(mat: W4Matrix, lora: LoraSet, which: torch.Tensor, x: torch.Tensor, y: torch.Tensor, ws: Workspace,
+                       bias: Optional[torch.Tensor] = None, relu: bool = False, stream=None) -> None:
+    """asf_w4_matmul with each token's own adapter beside it: which int32 [B], negative for none; x in the
+    adapters' dtype.  ws: Workspace.for_w4(mat, B, lora=lora)."""
+    args = _product(mat, x, y, bias, relu)
+    if which.shape != x.shape[:1]:
+        raise ValueError("which must be [B]")
+    if lora.device != mat.device or x.dtype is not lora.dtype:
+        raise ValueError(f"the adapters must be on {mat.device} and in x's dtype")
+    _invoke("asf_w4_matmul_lora", mat.device, stream, mat._ref, lora._ref, _arg(which, "which", mat.device, torch.int32),
+            *args, ws.on(mat.device), ws.nbytes)
 
 
 def asf_w4_sparse_ffn(ffn: W4FFN, x: torch.Tensor, idx: Optional[torch.Tensor], count: Optional[torch.Tensor],

@@ -334,6 +334,34 @@ ASF_API asf_status asf_w4_sparse_ffn(const asf_w4_ffn *ffn, const void *x, asf_d
                                      asf_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Adapters: low-rank corrections of a 4-bit matrix, of which each token of a call
+ * uses its own, or none, beside the product that all of them share. */
+#define ASF_MAX_LORA_RANK 256
+
+typedef struct {
+  int32_t adapters, rank;  /* rank a multiple of 8, at most ASF_MAX_LORA_RANK (pad with zeros) */
+  int32_t k, rows;         /* of the matrix */
+  asf_dtype dtype;         /* of A and B, and of x */
+  const void *A;           /* device [adapters][rank][k], 16-byte aligned */
+  const void *B;           /* device [adapters][rows][rank], 16-byte aligned */
+  const float *scale;      /* device fp32 [adapters], or NULL: 1 */
+} asf_lora;
+
+/* Workspace bytes of asf_w4_matmul_lora for batches up to max_batch (enough for
+ * asf_w4_matmul on the same matrix, too).  0 on invalid arguments. */
+ASF_API size_t asf_w4_lora_workspace_bytes(const asf_w4_matrix *mat, const asf_lora *lora, int32_t max_batch);
+
+/* y[b] = act(W x[b] + bias + scale[a] B[a] (A[a] x[b])), a = which[b]
+ *   which  device int32 [batch]: a token's adapter, negative for none; one from
+ *          `adapters` on counts as none and is flagged
+ * All else as for asf_w4_matmul, with x in the adapters' dtype.  Everything between x
+ * and y is fp32, y is rounded once, and a token's result does not depend on the call's
+ * other tokens, nor on their adapters. */
+ASF_API asf_status asf_w4_matmul_lora(const asf_w4_matrix *mat, const asf_lora *lora, const int32_t *which, const void *x,
+                                      asf_dtype xdtype, int32_t batch, const float *bias, int32_t relu, void *y,
+                                      asf_dtype ydtype, void *ws, size_t ws_bytes, asf_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Tree attention: the attention step in front of the predictor (PowerInfer_x64
  * page: attention, then predictor, then the sparse operators) for the tokens
  * of one call, over a paged key/value cache in fp16.
