@@ -15,8 +15,9 @@ import torch
 
 from .api import (FFN, Predictor, Workspace, asf_dense_ffn, asf_predict, asf_predict_sparse_ffn, asf_read_error,
                   asf_sparse_ffn, asf_workspace_bytes)
-from .attention import KVCache, asf_kv_append, asf_tree_attention
-from .w4 import W4FFN, W4Matrix, asf_w4_matmul, asf_w4_sparse_ffn
+from .attention import KVCache, asf_kv_append, asf_kv_evict, asf_tree_attention, asf_tree_attention_scored
+from .rotary import Rotary, asf_rotary_append
+from .w4 import LoraSet, W4FFN, W4Matrix, asf_w4_matmul, asf_w4_matmul_lora, asf_w4_sparse_ffn
 
 
 class AttentionStage:
@@ -28,16 +29,28 @@ class AttentionStage:
     q_heads * head_dim is the hidden size), or its product with the 4-bit
     projection out[l] [hidden, q_heads * head_dim].  The caller fills q, k, v
     and, for all layers alike, table [R, max_pages], lens [R], begin [R + 1]
-    and anc [B]."""
+    and anc [B].
+
+    rotary: q and k are turned by the tokens' positions, which the caller fills
+    in pos [B].  scored: scores[l] [R, heads, max_pages * page] adds up the weight
+    that each cached key receives, for evict().  adapters: adapters[l] beside
+    out[l]; the caller fills which [B] (-1, none, at first)."""
 
     def __init__(self, caches: Sequence[KVCache], q_heads: int, requests: int, max_pages: int, batch: int,
-                 out: Optional[Sequence[W4Matrix]] = None):
+                 out: Optional[Sequence[W4Matrix]] = None, rotary: Optional[Rotary] = None, scored: bool = False,
+                 adapters: Optional[Sequence[LoraSet]] = None):
         c0, n = caches[0], len(caches)
         if any((c.heads, c.head_dim, c.page, c.device) != (c0.heads, c0.head_dim, c0.page, c0.device) for c in caches):
             raise ValueError("the layers' caches must have one head layout, page size and device")
         if out is not None and (len(out) != n
                                 or any((m.k, m.rows) != (q_heads * c0.head_dim, out[0].rows) for m in out)):
             raise ValueError("one projection of q_heads * head_dim columns per layer, all of one hidden size")
+        if rotary is not None and (rotary.head_dim != c0.head_dim or rotary.device != c0.device):
+            raise ValueError("the rotary table must be of the caches' head_dim and device")
+        if adapters is not None and (out is None or len(adapters) != n or any(
+                (a.k, a.rows, a.dtype) != (m.k, m.rows, torch.float16) for a, m in zip(adapters, out))):
+            raise ValueError("one set of float16 adapters per projection, of its shape")
+        self.rotary, self.adapters = rotary, adapters
         self.caches, self.out, self.R, self.max_pages = list(caches), out, int(requests), int(max_pages)
         half = lambda *s: torch.zeros(*s, dtype=torch.float16, device=c0.device)  # noqa: E731
         ints = lambda *s: torch.zeros(*s, dtype=torch.int32, device=c0.device)  # noqa: E731
@@ -45,26 +58,58 @@ class AttentionStage:
         self.k, self.v = half(n, batch, c0.heads, c0.head_dim), half(n, batch, c0.heads, c0.head_dim)
         self.o = half(batch, q_heads, c0.head_dim)
         self.table, self.lens, self.begin, self.anc = ints(requests, max_pages), ints(requests), ints(requests + 1), ints(batch)
-        self.ws = Workspace.for_attention(c0, q_heads, requests, batch)
-        self.ws_out = _widest_w4(out, batch) if out is not None else None
+        self.ws = Workspace.for_attention(c0, q_heads, requests, batch, scored_pages=max_pages if scored else None)
+        self.ws_out = _widest_w4(out, batch, adapters) if out is not None else None
+        self.pos, self.q_turned = (ints(batch), torch.zeros_like(self.q[0])) if rotary is not None else (None, None)
+        self.scores = torch.zeros(n, requests, c0.heads, max_pages * c0.page, device=c0.device) if scored else None
+        self.which = ints(batch) - 1 if adapters is not None else None
         self.width = out[0].rows if out is not None else q_heads * c0.head_dim
 
     def launches(self) -> int:
         """Kernels per layer: append, attention, the merge of split keys unless the table is too
-        short for a split, and the projection."""
+        short for a split, the scores, the projection and the two steps of its adapters."""
         c = self.caches[0]
         sms = torch.cuda.get_device_properties(c.device).multi_processor_count
         split = _attention_splits(self.max_pages * c.page, c.heads, c.head_dim, self.q.shape[2] // c.heads, self.R,
                                   self.q.shape[1], sms)
-        return 2 + int(split) + int(self.out is not None)
+        return 2 + int(split) + int(self.scores is not None) + int(self.out is not None) + 2 * int(self.adapters is not None)
 
     def enqueue(self, l: int, x: torch.Tensor, stream=None) -> None:
         o = self.o if self.out is not None else x.view(self.o.shape)
-        asf_kv_append(self.caches[l], self.table, self.lens, self.begin, self.k[l], self.v[l], self.ws, stream)
-        asf_tree_attention(self.caches[l], self.table, self.lens, self.begin, self.q[l], self.anc, o, self.ws,
-                           stream=stream)
-        if self.out is not None:
+        cache, q, req = self.caches[l], self.q[l], (self.table, self.lens, self.begin)
+        if self.rotary is not None:
+            asf_rotary_append(self.rotary, cache, *req, self.pos, q, self.q_turned, self.k[l], self.v[l], self.ws, stream)
+            q = self.q_turned
+        else:
+            asf_kv_append(cache, *req, self.k[l], self.v[l], self.ws, stream)
+        if self.scores is not None:
+            asf_tree_attention_scored(cache, *req, q, self.anc, o, self.scores[l], self.ws, stream=stream)
+        else:
+            asf_tree_attention(cache, *req, q, self.anc, o, self.ws, stream=stream)
+        if self.adapters is not None:
+            asf_w4_matmul_lora(self.out[l], self.adapters[l], self.which, o.view(x.shape[0], -1), x, self.ws_out, stream=stream)
+        elif self.out is not None:
             asf_w4_matmul(self.out[l], o.view(x.shape[0], -1), x, self.ws_out, stream=stream)
+
+    def evict(self, keep: int, table: torch.Tensor, first: int = 0, recent: int = 0) -> torch.Tensor:
+        """Between steps, with scored: every request's layers and kv heads keep `keep` keys (asf_kv_evict) on the pages
+        of `table` int32 [R, pages], which are then the stage's.  Returns the kept positions int32 [layers, R, heads, keep].
+
+        The stage's table, lens and scores go over to what is left, in place, so that a captured stack runs on."""
+        if self.scores is None:
+            raise ValueError("eviction goes by the scores of a scored stage")
+        n, R, heads, S = self.scores.shape
+        if table.dim() != 2 or table.shape[0] != R or table.shape[1] > self.max_pages or keep > S:
+            raise ValueError("table must be [R, pages] with at most the stage's pages, and keep fit its scores")
+        kept = torch.zeros(n, R, heads, keep, dtype=torch.int32, device=self.scores.device)
+        lens, scores = torch.empty_like(self.lens), torch.zeros_like(self.scores[0])
+        for l, cache in enumerate(self.caches):
+            asf_kv_evict(cache, self.table, self.lens, self.scores[l], keep, table, lens, scores, kept[l], self.ws, first=first,
+                         recent=recent)
+            self.scores[l].copy_(scores)
+        self.table[:, :table.shape[1]].copy_(table)
+        self.lens.copy_(lens)
+        return kept
 
 
 class LayerStack:
@@ -229,8 +274,12 @@ class LayerStack:
         self.graph = None
 
 
-def _widest_w4(ops: Sequence[Union[W4FFN, W4Matrix]], batch: int) -> Workspace:
+def _widest_w4(ops: Sequence[Union[W4FFN, W4Matrix]], batch: int,
+               adapters: Optional[Sequence[LoraSet]] = None) -> Workspace:
     """A workspace that is enough for each of the operators in turn."""
+    if adapters is not None:
+        op, lora = max(zip(ops, adapters), key=lambda pair: pair[0].workspace_bytes(batch, pair[1]))
+        return Workspace.for_w4(op, batch, lora=lora)
     return Workspace.for_w4(max(ops, key=lambda op: op.workspace_bytes(batch)), batch)
 
 

@@ -1,0 +1,97 @@
+"""The attention stage with rotary positions, scores and adapters, captured with its layers: every stage has the
+bits of the single calls, before an eviction and after it."""
+import pytest
+import torch
+
+from tests.gpu_util import ensure_built
+
+import activation_sparse_ffn_predict_b200 as A
+
+pytestmark = pytest.mark.gpu
+
+
+def _model(layers, B, hkv, grp, D, page, pages, d=512, adapters=True):
+    torch.manual_seed(21)
+    half = lambda *s: torch.randn(*s, device="cuda").half()  # noqa: E731
+    hq = hkv * grp
+    caches = [A.KVCache(half(pages, page, hkv, D), half(pages, page, hkv, D)) for _ in range(layers)]
+    outs = [A.W4Matrix.quantize(half(d, hq * D) * (hq * D) ** -0.5, 64) for _ in range(layers)]
+    loras = [A.LoraSet(half(3, 8 * (l + 1), hq * D) * (hq * D) ** -0.5, half(3, d, 8 * (l + 1)), torch.rand(3, device="cuda"))
+             for l in range(layers)] if adapters else None
+    ffns = [A.W4FFN.quantize("relu", None, half(700, d) * d ** -0.5, half(700, d) * d ** -0.5, torch.zeros(700, device="cuda"), 64)
+            for _ in range(layers)]
+    return caches, outs, loras, ffns
+
+
+@pytest.mark.parametrize("hkv,grp,D,page,R,T", [(2, 4, 64, 16, 2, 5), (1, 16, 80, 20, 1, 6)])
+def test_steps_and_an_eviction(hkv, grp, D, page, R, T):
+    ensure_built()
+    layers, width, d, hq = 2, 12, 512, hkv * grp
+    caches, outs, loras, ffns = _model(layers, T, hkv, grp, D, page, 2 * R * width)
+    twins = [A.KVCache(c.k.clone(), c.v.clone()) for c in caches]
+    rot = A.Rotary(D, D // 2, scaling="yarn", factor=4.0)
+    stage = A.AttentionStage(caches, hq, R, width, T, outs, rotary=rot, scored=True, adapters=loras)
+    st = A.LayerStack([], ffns, T, mode="dense", attention=stage)
+    order = torch.randperm(2 * R * width).int().cuda()
+    stage.table.copy_(order[:R * width].view(R, width))
+    stage.lens.copy_(torch.tensor([150, 40][:R]))
+    stage.begin.copy_(torch.tensor([0, T - 2, T] if R == 2 else [0, T]))
+    stage.anc.copy_((2 ** (torch.arange(T) + 1) - 1).int())
+    stage.which.copy_((torch.arange(T) % 4 - 1).int())
+    stage.pos.copy_(torch.arange(T).int() + 1000)
+    stage.q.normal_(), stage.k.normal_(), stage.v.normal_()
+    st.capture()                                             # its warm-up runs add to the scores
+    assert st.kernel_nodes() == st.launches_per_step()
+    stage.scores.zero_()
+    scores = stage.scores.clone()
+
+    def by_hand():
+        for l in range(layers):
+            ws = A.Workspace.for_attention(twins[l], hq, R, T, scored_pages=width)
+            q, o = torch.zeros_like(stage.q[l]), torch.zeros_like(stage.q[l])
+            x, y = torch.empty(T, d, device="cuda").half(), torch.empty(T, d, device="cuda")
+            req = (stage.table, stage.lens, stage.begin)
+            A.asf_rotary_append(rot, twins[l], *req, stage.pos, stage.q[l], q, stage.k[l], stage.v[l], ws)
+            A.asf_tree_attention_scored(twins[l], *req, q, stage.anc, o, scores[l], ws)
+            A.asf_w4_matmul_lora(outs[l], loras[l], stage.which, o.view(T, -1), x, A.Workspace.for_w4(outs[l], T, lora=loras[l]))
+            A.asf_w4_sparse_ffn(ffns[l], x, None, None, y, A.Workspace.for_w4(ffns[l], T))
+            torch.cuda.synchronize()
+            assert torch.equal(x, st.x[l]) and torch.equal(y, st.y[l]) and x.abs().max() > 0
+            assert torch.equal(scores[l], stage.scores[l])
+            assert torch.equal(twins[l].k, caches[l].k) and torch.equal(twins[l].v, caches[l].v)
+
+    for _ in range(2):
+        st.step()
+        by_hand()
+        stage.lens.add_(stage.begin[1:] - stage.begin[:-1])
+        stage.pos.add_(T)
+        stage.q.normal_(), stage.k.normal_(), stage.v.normal_()
+    fresh = order[R * width:].view(R, width)[:, :8].contiguous()
+    keep = 64
+    want = torch.zeros(layers, R, hkv, keep, dtype=torch.int32, device="cuda")
+    lens, out = torch.empty_like(stage.lens), torch.zeros_like(scores[0])
+    for l in range(layers):
+        A.asf_kv_evict(twins[l], stage.table, stage.lens, scores[l], keep, fresh, lens, out, want[l], A.Workspace.for_eviction(twins[l]),
+                       first=2, recent=20)
+        scores[l].copy_(out)
+    kept = stage.evict(keep, fresh, first=2, recent=20)
+    assert torch.equal(kept, want) and torch.equal(stage.lens, lens) and lens.max() == keep
+    assert torch.equal(stage.table[:, :8], fresh) and torch.equal(stage.scores, scores)
+    st.step()                                                # the captured step goes on over what is left
+    by_hand()
+    assert st.read_error() == 0
+    st.release()
+
+
+def test_stage_refuses_what_does_not_fit():
+    ensure_built()
+    caches, outs, loras, ffns = _model(2, 1, 2, 2, 64, 16, 8)
+    args = (caches, 4, 1, 4, 1)
+    for bad in (lambda: A.AttentionStage(*args, outs, rotary=A.Rotary(128)), lambda: A.AttentionStage(*args, adapters=loras),
+                lambda: A.AttentionStage(*args, outs, adapters=loras[:1]),
+                lambda: A.AttentionStage(*args, outs, adapters=[A.LoraSet(a.A.float(), a.B.float()) for a in loras]),
+                lambda: A.AttentionStage(*args, outs).evict(4, torch.zeros(1, 2, dtype=torch.int32, device="cuda")),
+                lambda: A.AttentionStage(*args, outs, scored=True).evict(4, torch.zeros(1, 5, dtype=torch.int32, device="cuda")),
+                lambda: A.AttentionStage(*args, outs, scored=True).evict(65, torch.zeros(1, 4, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
