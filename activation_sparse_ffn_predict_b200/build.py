@@ -14,9 +14,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libasffn.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("asffn.cu", "w4.cu", "attention.cu", "rotary.cu", "evict.cu",
+SOURCES = [os.path.join(CSRC, f) for f in ("asffn.cu", "w4.cu", "attention.cu", "score.cu", "rotary.cu", "evict.cu",
                                               "lora.cu")]
-HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "host.cuh"), os.path.join(CSRC, "paged.cuh"),
+HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "host.cuh"), os.path.join(CSRC, "paged.cuh"), os.path.join(CSRC, "attn.cuh"),
            os.path.join(INCLUDE, "asffn.h")]
 DEPS = SOURCES + HEADERS
 

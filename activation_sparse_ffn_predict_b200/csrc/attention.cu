@@ -2,7 +2,7 @@
 // append that fills it (include/asffn.h, "Tree attention").
 //
 //   asf_kv_append        k_kv_append
-//   asf_tree_attention_scored   the same, then k_tree_score
+//   asf_tree_attention_scored   the same, then score.cu's kernels
 //   asf_tree_attention   k_tree_attn, or k_tree_tc for more than 32 query rows of
 //                        a request and kv head; then k_tree_merge over split requests
 //
@@ -29,18 +29,14 @@
 #include <cstring>
 
 #include "asffn.h"
-#include "common.cuh"
-#include "host.cuh"
-#include "paged.cuh"
+#include "attn.cuh"
 
 using namespace asf;
 
 namespace {
 
-constexpr int kTile = 64;              // keys per tile
 constexpr int kStages = 3;             // tiles in shared memory (k_tree_attn)
 constexpr int kClusterTiles = 4;       // key tiles that each CTA of a cluster takes at most
-constexpr int kMinChunk = 4;           // key tiles per split, at least
 constexpr int kWhole = 8;              // key tiles up to which nothing is split (no merge to launch)
 constexpr float kTopLog2 = 15.99f;     // of a weight at most: below fp16's largest, 65504
 constexpr float kLift = 15.f;
@@ -48,125 +44,6 @@ constexpr float kLift = 15.f;
 // tokens over 65500 keys, us of the call with a lift of 0 to 9: 33.9, 71.0; 11: 34.1,
 // 71.2; 12: 34.9, 72.2, since rows outgrow their references more often.
 constexpr float kLiftTc = 11.f;
-
-struct AttnArgs {
-  const __half *k, *v;
-  int64_t page_stride, token_stride, head_stride;
-  int pages, page, hkv, D;
-  const int32_t *table;
-  int max_pages, R, T, grp;
-  const int32_t *lens, *begin;
-  const __half *q;
-  const int32_t *anc;
-  float scale;                         // times log2(e)
-  __half *o;
-  float *part;                         // [unit < target][MT][DP]
-  float2 *ml;                          // [unit][MT]: reference (log2) and sum
-  int4 *plan;                          // per request, for the merge: first token, tokens, splits, first unit
-  int target;                          // CTAs to aim at
-  int whole;                           // key tiles up to which nothing is split
-  int cluster;                         // CTAs that share a unit
-  int box;                             // keys of a TMA load, or 0
-  int32_t *err;
-  float2 *stats;                       // scored: per row (token, query head) its reference (log2) and sum
-  float *scores;                       // [R][hkv][S]
-  int S;
-};
-
-// One request, as every kernel here sees it.
-struct Req {
-  int t0, n;                           // its tokens
-  int len, L;                          // keys before them, and with them
-  int nkt, rt;                         // key tiles, row tiles
-  int splits, base;                    // splits of the keys, first unit
-};
-
-// The plan: lane r holds request r.  C key tiles per unit, the fewest for
-// which the units (request, kv head, row tile, split) fit `target` CTAs (one
-// split each where even that is more).  Bad inputs are clamped; the flag says so.
-__device__ __forceinline__ Req plan_lane(const AttnArgs &A, int MT, int lane, int &C, int &units, bool &bad) {
-  Req q{};
-  bad = false;
-  if (lane < A.R) {
-    int t0 = ld_cg_i32(A.begin + lane), t1 = ld_cg_i32(A.begin + lane + 1);
-    bad = t0 < 0 || t1 < t0 || t1 > A.T;
-    t0 = min(max(t0, 0), A.T);
-    t1 = min(max(t1, t0), A.T);
-    q.t0 = t0;
-    q.n = t1 - t0;
-  }
-  int end = q.t0 + q.n;                // ranges stay apart whatever `begin` holds: the units then fit the grid
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, end, o);
-    if (lane >= o) end = max(end, v);
-  }
-  int before = __shfl_up_sync(0xffffffffu, end, 1);
-  if (lane == 0) before = 0;
-  if (lane < A.R) {
-    const int t1 = q.t0 + q.n, t0 = max(q.t0, min(before, t1));
-    int len = ld_cg_i32(A.lens + lane);
-    const int64_t cap = (int64_t)A.max_pages * A.page;
-    bad |= len < 0 || (int64_t)len + (t1 - t0) > cap;
-    len = (int)min((int64_t)max(len, 0), cap);
-    q.t0 = t0;
-    q.n = t1 - t0;
-    q.len = len;
-    q.L = (int)min((int64_t)len + q.n, cap);
-    q.nkt = max(1, (q.L + kTile - 1) / kTile);
-    q.rt = (q.n * A.grp + MT - 1) / MT;
-  }
-  int64_t W = (int64_t)q.rt * q.nkt;
-  int most = q.rt ? q.nkt : 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    W += __shfl_xor_sync(0xffffffffu, W, o);
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-  }
-  C = max(most <= A.whole ? A.whole : kMinChunk, (int)((W * A.hkv + A.target - 1) / A.target));
-  while (true) {
-    q.splits = (q.nkt + C - 1) / C;
-    int u = q.rt * q.splits * A.hkv;
-    const int own = u;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, u, o);
-      if (lane >= o) u += v;
-    }
-    q.base = u - own;
-    units = __shfl_sync(0xffffffffu, u, 31);
-    if (units <= A.target || C >= most) break;
-    C += max(1, C / 16);
-  }
-  return q;
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float exp2_fast(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 
 // shared memory of CTA `rank` of the cluster, at the address of this CTA's p
 __device__ __forceinline__ uint32_t peer_smem(const void *p, int rank) {
@@ -206,7 +83,10 @@ __host__ __device__ constexpr int attn_resident(int DP, int WM) { return DP == 6
 // with the append, and 15.9 where the table has room for 4096 keys, which takes the
 // form without clusters and the merge's launch), the loads in flight above: 32
 // requests of 4096 keys (8 kv heads, 537 MB) 98.8 us, 5.4 TB/s.
-template <int DP, int WM, int CL>
+// SC: the call is scored.  Rows' references and sums are left for score.cu, and the
+// scores themselves where there is room: 4 bytes a row and key, written and read
+// through L2, where reading the keys again takes 2 head_dim.
+template <int DP, int WM, int CL, bool SC>
 __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnArgs A) {
   constexpr int NW = 4;
   constexpr int KG = NW / WM;          // key groups
@@ -402,6 +282,18 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
           if (!ok) z[i][e] = -INFINITY;
         }
     }
+    if constexpr (SC) {
+      if (A.z) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int m = row0 + wm * 16 + g + 8 * h;
+          if (!live[h]) continue;
+          float *to = A.z + ((int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp) * A.zs + pos0 + key0 + 2 * t;
+#pragma unroll
+          for (int i = 0; i < KW / 8; ++i) __stcg(reinterpret_cast<float2 *>(to + i * 8), make_float2(z[i][2 * h], z[i][2 * h + 1]));
+        }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < KW / 8; ++i)
 #pragma unroll
@@ -521,7 +413,7 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
           o[0] = fmaf(f, v[p].x, o[0]); o[1] = fmaf(f, v[p].y, o[1]); o[2] = fmaf(f, v[p].z, o[2]); o[3] = fmaf(f, v[p].w, o[3]);
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;                      // nothing seen: zeros
-        if (A.stats && m < rows && c == 0)
+        if (SC && m < rows && c == 0)
           __stcg(A.stats + (int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp, make_float2(M, l));
         if (m < rows && c < A.D) {
           __half *op = A.o + ((int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp) * A.D + c;
@@ -566,7 +458,7 @@ __global__ void __launch_bounds__(128, attn_resident(DP, WM)) k_tree_attn(AttnAr
     if (splits == 1) {
       const float inv = sum[h] == 0.f ? 0.f : 1.f / sum[h];              // nothing seen: zeros
       const int64_t row = (int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp;
-      if (A.stats && t == 0) __stcg(A.stats + row, make_float2(mx[h], sum[h]));
+      if (SC && t == 0) __stcg(A.stats + row, make_float2(mx[h], sum[h]));
       __half *op = A.o + row * A.D;
 #pragma unroll
       for (int i = 0; i < DP / 8; ++i)
@@ -615,7 +507,6 @@ struct TreeTc {
   static constexpr uint32_t COLS = 256;            // O: DP columns at 0; S and P: 64 each at 128 and 192
 };
 constexpr int kTcThreads = 7 * 32;
-constexpr uint64_t kTcWaitNs = 200ull * 1000 * 1000;   // bound on any mbarrier wait
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
@@ -1194,136 +1085,6 @@ __global__ void __launch_bounds__(128) k_tree_merge(AttnArgs A, int MT) {
   }
 }
 
-// --------------------------------------------- weights that keys received --
-// scores[r][head][p] += (= for the call's own tokens) the sum over the request's
-// rows of softmax_p: with every row's reference M and sum l known, the weight of a
-// score z is 2^(z - M) / l, and a key's rows are added in a fixed order.  A tile of
-// 64 keys is read again and multiplied with all of the request's rows, 16 at a time,
-// a warp every fourth group of them.  Rows that saw nothing have l = 0 and add nothing.
-template <int DP>
-__global__ void __launch_bounds__(128) k_tree_score(AttnArgs A) {
-  constexpr int CH = DP / 8;
-  __shared__ __align__(128) unsigned char sk[kTile * DP * 2];
-  __shared__ float s_sum[4][kTile];
-  __shared__ int64_t s_off[kTile];
-  pdl_wait();
-  pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  int C, units;
-  bool bad;
-  const Req q = plan_lane(A, 16, lane, C, units, bad);                   // bad requests have been flagged
-  int end = q.n ? q.nkt * A.hkv : 0;                                     // this request's tiles, all heads
-  const int own = end;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, end, o);
-    if (lane >= o) end += v;
-  }
-  const int total = __shfl_sync(0xffffffffu, end, 31);
-  for (int u = blockIdx.x; u < total; u += gridDim.x) {
-    const int req = __popc(__ballot_sync(0xffffffffu, end <= u));
-    const int in = u - __shfl_sync(0xffffffffu, end - own, req), nkt = __shfl_sync(0xffffffffu, q.nkt, req);
-    const int t0 = __shfl_sync(0xffffffffu, q.t0, req), n = __shfl_sync(0xffffffffu, q.n, req);
-    const int len = __shfl_sync(0xffffffffu, q.len, req), L = __shfl_sync(0xffffffffu, q.L, req);
-    const int head = in / nkt, pos0 = (in - head * nkt) * kTile, rows = n * A.grp;
-    if (tid < kTile) {
-      const int pos = pos0 + tid;
-      int64_t off = -1;
-      if (pos < L) {
-        const int id = A.table[(int64_t)req * A.max_pages + pos / A.page];
-        if ((unsigned)id < (unsigned)A.pages)
-          off = (int64_t)id * A.page_stride + (int64_t)(pos % A.page) * A.token_stride + (int64_t)head * A.head_stride;
-      }
-      s_off[tid] = off;
-    }
-    __syncthreads();
-    for (int i = tid >> 3; i < kTile; i += 16) {
-      const int64_t off = s_off[i];
-#pragma unroll
-      for (int c = tid & 7; c < CH; c += 8) {
-        const bool in_row = off >= 0 && c * 8 < A.D;
-        cp_async16(sk + i * DP * 2 + ((c ^ (i & 7)) * 16), A.k + (in_row ? off + c * 8 : 0), in_row ? 16u : 0u);
-      }
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncthreads();
-    const bool special = pos0 + kTile > len;
-    float acc[kTile / 8][2];
-#pragma unroll
-    for (int i = 0; i < kTile / 8; ++i) acc[i][0] = acc[i][1] = 0.f;
-    const uint32_t kb = smem_u32(sk);
-    for (int m0 = warp * 16; m0 < rows; m0 += 64) {
-      uint32_t qf[DP / 16][4], see[2];
-      float M[2], inv[2];
-      const __half *qp[2];
-      bool live[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int m = m0 + g + 8 * h;
-        live[h] = m < rows;
-        const int tok = t0 + (live[h] ? m / A.grp : 0);
-        const int64_t row = (int64_t)tok * A.hkv * A.grp + head * A.grp + (live[h] ? m % A.grp : 0);
-        see[h] = live[h] ? (uint32_t)A.anc[tok] : 0u;
-        qp[h] = A.q + row * A.D;
-        const float2 st = __ldcg(A.stats + row);
-        const bool none = !live[h] || st.y == 0.f;
-        M[h] = none ? INFINITY : st.x;
-        inv[h] = none ? 0.f : 1.f / st.y;
-      }
-#pragma unroll
-      for (int s = 0; s < DP / 16; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = s * 16 + 2 * t + 8 * (i >> 1);
-          qf[s][i] = live[i & 1] && c < A.D ? *reinterpret_cast<const uint32_t *>(qp[i & 1] + c) : 0u;
-        }
-      float z[kTile / 8][4];
-#pragma unroll
-      for (int i = 0; i < kTile / 8; ++i) z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.f;
-#pragma unroll
-      for (int s = 0; s < DP / 16; ++s)
-#pragma unroll
-        for (int i = 0; i < kTile / 16; ++i) {
-          uint32_t b[4];
-          const int row = i * 16 + (lane >> 4) * 8 + (lane & 7), c = s * 2 + ((lane >> 3) & 1);
-          ldsm4(b, kb + row * DP * 2 + ((c ^ (row & 7)) * 16));
-          mma_f16(z[2 * i], qf[s], b[0], b[1]);
-          mma_f16(z[2 * i + 1], qf[s], b[2], b[3]);
-        }
-#pragma unroll
-      for (int i = 0; i < kTile / 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = i * 8 + 2 * t + (e & 1), d = pos0 + key - len, h = e >> 1;
-          const bool ok = live[h] && (!special || (s_off[key] >= 0 && (d < 0 || ((see[h] >> ((t0 + d) & 31)) & 1u))));
-          const float w = exp2_fast(fmaf(z[i][e], A.scale, -M[h]));
-          acc[i][e & 1] = ok ? fmaf(w, inv[h], acc[i][e & 1]) : acc[i][e & 1];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kTile / 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) acc[i][e] += __shfl_xor_sync(0xffffffffu, acc[i][e], o);
-        if (g == 0) s_sum[warp][i * 8 + 2 * t + e] = acc[i][e];
-      }
-    __syncthreads();
-    if (tid < kTile && pos0 + tid < L) {
-      const int pos = pos0 + tid;
-      if (pos >= A.S) {
-        flag_error(A.err, kErrIndex);
-      } else {
-        float *to = A.scores + ((int64_t)req * A.hkv + head) * A.S + pos;
-        const float w = s_sum[0][tid] + s_sum[1][tid] + s_sum[2][tid] + s_sum[3][tid];
-        if (pos >= len) *to = w;
-        else if (s_off[tid] >= 0) *to += w;
-      }
-    }
-  }
-}
-
 // One 16-byte chunk of a token's keys and values per thread.
 struct AppendArgs {
   __half *k, *v;
@@ -1385,27 +1146,12 @@ int cluster_of(int64_t keys, int units, int target) {
   if (keys > 4 * kTile && keys <= 8 * kClusterTiles * kTile && units * 8 <= sm_count()) return 8;
   return keys <= 4 * kClusterTiles * kTile && units * 4 <= target ? 4 : 1;
 }
-template <int DP, int WM>
+template <int DP, int WM, bool SC>
 cudaError_t run_attn(const AttnArgs &a, int units, cudaStream_t st) {
   const size_t smem = (size_t)kStages * 2 * kTile * DP * 2;
-  if (a.cluster == 8) return launch_clusters(k_tree_attn<DP, WM, 8>, dim3(units * 8), dim3(128), smem, st, 8, a);
-  if (a.cluster == 4) return launch_clusters(k_tree_attn<DP, WM, 4>, dim3(units * 4), dim3(128), smem, st, 4, a);
-  return launch(k_tree_attn<DP, WM, 1>, dim3(units), dim3(128), smem, st, a);
-}
-// Map of a cache's keys or values: columns, tokens of a page, heads, pages; a
-// box is `box` tokens of one head and page by 64 columns, swizzled as the MMA
-// reads it.  Columns past head_dim and pages past the last read as zeros.
-bool cache_map(CUtensorMap *tm, const void *base, const AttnArgs &a) {
-  TmapEncodeFn enc = tmap_encoder();
-  if (!enc) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.page, (cuuint64_t)a.hkv, (cuuint64_t)a.pages};
-  // the stride of a dimension of one is never used, but has to be legal
-  const cuuint64_t strides[3] = {(cuuint64_t)a.token_stride * 2, (cuuint64_t)std::max<int64_t>(a.head_stride, 8) * 2,
-                                 (cuuint64_t)std::max<int64_t>(a.page_stride, 8) * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)a.box, 1, 1}, one[4] = {1, 1, 1, 1};
-  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(base), dims, strides, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  if (a.cluster == 8) return launch_clusters(k_tree_attn<DP, WM, 8, SC>, dim3(units * 8), dim3(128), smem, st, 8, a);
+  if (a.cluster == 4) return launch_clusters(k_tree_attn<DP, WM, 4, SC>, dim3(units * 4), dim3(128), smem, st, 4, a);
+  return launch(k_tree_attn<DP, WM, 1, SC>, dim3(units), dim3(128), smem, st, a);
 }
 
 template <int DP>
@@ -1413,7 +1159,7 @@ cudaError_t run_tc(AttnArgs a, int units, cudaStream_t st) {
   CUtensorMap mk, mv;
   std::memset(&mk, 0, sizeof(mk));
   std::memset(&mv, 0, sizeof(mv));
-  a.box = a.page >= kTile ? (a.page % kTile ? 0 : kTile) : a.page >= 8 && kTile % a.page == 0 ? a.page : 0;
+  a.box = tma_box(a.page);
   if (a.box && cache_map(&mk, a.k, a) && cache_map(&mv, a.v, a))
     return launch(k_tree_tc<DP, true>, dim3(units), dim3(kTcThreads), TreeTc<DP>::SMEM, st, mk, mv, a);
   return launch(k_tree_tc<DP, false>, dim3(units), dim3(kTcThreads), TreeTc<DP>::SMEM, st, mk, mv, a);
@@ -1421,9 +1167,10 @@ cudaError_t run_tc(AttnArgs a, int units, cudaStream_t st) {
 
 template <int DP>
 cudaError_t run_attn_any(const AttnArgs &a, int wm, int units, cudaStream_t st) {
-  const cudaError_t e = wm == 1   ? run_attn<DP, 1>(a, units, st)
-                        : wm == 2 ? run_attn<DP, 2>(a, units, st)
-                                  : run_tc<DP>(a, units, st);
+  const cudaError_t e = wm == 8     ? run_tc<DP>(a, units, st)
+                        : a.scores ? (wm == 1 ? run_attn<DP, 1, true>(a, units, st) : run_attn<DP, 2, true>(a, units, st))
+                        : wm == 1  ? run_attn<DP, 1, false>(a, units, st)
+                                   : run_attn<DP, 2, false>(a, units, st);
   if (e != cudaSuccess) return e;
   if ((int64_t)a.max_pages * a.page <= a.whole * kTile) return e;       // no request can have splits
   const int rows = a.T * a.hkv * a.grp;
@@ -1434,8 +1181,16 @@ cudaError_t run_attn_any(const AttnArgs &a, int wm, int units, cudaStream_t st) 
                                 : launch(k_tree_merge<DP, 1, 8>, dim3((rows + 3) / 4), dim3(128), 0, st, a, 16 * wm);
 }
 
-// rows' references and sums
-size_t scored_scratch(int q_heads, int T) { return r256((size_t)T * q_heads * 8); }
+// Rows' references and sums, and their scores: of k_tree_attn's calls, and up to
+// kKeptScores bytes (a table may be far wider than its requests are long).
+constexpr int64_t kKeptScores = 512 << 20;
+int64_t kept_scores(const asf_kv_cache *c, int q_heads, int R, int T, int max_pages) {
+  const int64_t zs = ((int64_t)max_pages * c->page + kTile - 1) / kTile * kTile, all = zs * T * q_heads * 4;
+  return row_groups(q_heads / c->heads, R, T) <= 2 && all <= kKeptScores ? all : 0;
+}
+size_t scored_scratch(const asf_kv_cache *c, int q_heads, int R, int T, int max_pages) {
+  return r256((size_t)T * q_heads * 8) + (size_t)kept_scores(c, q_heads, R, T, max_pages);
+}
 
 // both forms of the call: scores null, or [R][heads][S]
 asf_status tree_attention(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R, const int32_t *lens,
@@ -1450,7 +1205,7 @@ asf_status tree_attention(const asf_kv_cache *cache, const int32_t *table, int32
   if (grp > ASF_MAX_HEAD_GROUP) return ASF_ERR_UNSUPPORTED;
   if (!al16(q) || !al16(o) || !al4(anc)) return ASF_ERR_MISALIGNED;
   const size_t scratch = attn_scratch(cache, grp, R, T);
-  s = check_ws(ws, ws_bytes, kHeaderBytes + scratch + (scores ? scored_scratch(q_heads, T) : 0));
+  s = check_ws(ws, ws_bytes, kHeaderBytes + scratch + (scores ? scored_scratch(cache, q_heads, R, T, max_pages) : 0));
   if (s != ASF_OK) return s;
   const size_t bytes = (size_t)T * q_heads * cache->head_dim * 2;
   if (overlap(q, bytes, o, bytes)) return ASF_ERR_INVALID_ARG;
@@ -1496,17 +1251,17 @@ asf_status tree_attention(const asf_kv_cache *cache, const int32_t *table, int32
   a.cluster = cluster;
   a.err = &static_cast<Header *>(ws)->err;
   if (scores) {
-    a.stats = reinterpret_cast<float2 *>(static_cast<unsigned char *>(ws) + kHeaderBytes + scratch);
+    unsigned char *more = static_cast<unsigned char *>(ws) + kHeaderBytes + scratch;
+    a.stats = reinterpret_cast<float2 *>(more);
+    if (kept_scores(cache, q_heads, R, T, max_pages)) {
+      a.z = reinterpret_cast<float *>(more + r256((size_t)T * q_heads * 8));
+      a.zs = (keys + kTile - 1) / kTile * kTile;
+    }
     a.scores = scores;
     a.S = S;
   }
   cudaError_t e = attn_dp(cache) == 64 ? run_attn_any<64>(a, wm, units, st) : run_attn_any<128>(a, wm, units, st);
-  if (e == cudaSuccess && scores) {
-    const int64_t tiles = R * cache->heads * ((keys + kTile - 1) / kTile);
-    const dim3 grid((unsigned)std::min<int64_t>(tiles, 8 * sm_count()));
-    e = attn_dp(cache) == 64 ? launch(k_tree_score<64>, grid, dim3(128), 0, st, a)
-                             : launch(k_tree_score<128>, grid, dim3(128), 0, st, a);
-  }
+  if (e == cudaSuccess && scores) e = run_scores(a, st);
   return cuda_status(e);
 }
 
@@ -1552,7 +1307,16 @@ size_t asf_attention_scored_workspace_bytes(const asf_kv_cache *cache, int32_t q
                                             int32_t max_pages) {
   const size_t need = asf_attention_workspace_bytes(cache, q_heads, R, T);
   if (need == 0 || max_pages < 1 || (int64_t)max_pages * cache->page > ASF_MAX_KEYS) return 0;
-  return need + scored_scratch(q_heads, T);
+  size_t more = 0;                                 // fewer requests, tokens and pages may keep scores where these do not
+  for (int r = 1; r <= R; ++r)
+    for (int t = 1; t <= T; ++t) {
+      more = std::max(more, scored_scratch(cache, q_heads, r, t, max_pages));
+      // the widest table whose scores are kept
+      int64_t wide = std::min<int64_t>(max_pages, kKeptScores / ((int64_t)t * q_heads * 4) / cache->page);
+      while (wide > 1 && row_groups(q_heads / cache->heads, r, t) <= 2 && !kept_scores(cache, q_heads, r, t, (int)wide)) --wide;
+      if (wide >= 1) more = std::max(more, scored_scratch(cache, q_heads, r, t, (int)wide));
+    }
+  return need + more;
 }
 
 asf_status asf_tree_attention_scored(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,

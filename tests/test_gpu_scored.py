@@ -73,7 +73,9 @@ def _check(c, d, scale=None, error=0):
     ([640], [8], dict(hkv=1, grp=9, D=128, page=640)), ([300, 400, 500], [0, 5, 0], dict(D=40)),
     ([2045], [3], dict(hkv=2, grp=4, D=128, page=2048)), ([900], [1], dict(hkv=74, grp=1, D=128, page=1024)),
     ([9000], [1], dict(hkv=1, grp=16, D=128, page=16)), ([9000, 50], [4, 4], dict(hkv=1, grp=8, D=64, page=32)),
-    ([200], [12], dict(hkv=2, grp=11, D=64, page=32)), ([100, 100], [16, 16], dict(hkv=1, grp=128, D=128, page=64))])
+    ([200], [12], dict(hkv=2, grp=11, D=64, page=32)), ([5000, 90], [31, 1], dict(hkv=2, grp=128, D=128, page=64)),
+    ([3000], [32], dict(hkv=3, grp=7, D=80, page=8)), ([127, 128, 129], [8, 8, 8], dict(hkv=1, grp=16, D=64, page=128)),
+    ([260], [9], dict(hkv=1, grp=15, D=72, page=64)), ([100, 100], [16, 16], dict(hkv=1, grp=128, D=128, page=64))])
 def test_against_the_definition(lens, toks, kw):
     c = Case(lens, toks, seed=sum(lens) + len(toks), **kw)
     d = _run(_device(c))
@@ -89,6 +91,24 @@ def test_against_the_definition(lens, toks, kw):
         once = first[0, :, :n].cpu().double().numpy() - c.old[0, :, :n]
         assert np.abs(twice - 2 * once).max() <= 2.0 ** -22 * np.abs(first[0, :, :n].cpu().numpy()).max() * 2
     assert torch.equal(d["scores"][0, :, n:], first[0, :, n:])
+
+
+@pytest.mark.parametrize("page", [64, 16, 20])
+@pytest.mark.parametrize("lens,toks,grp", [([700, 33], [6, 2], 8), ([2000], [8], 2)])
+def test_tables_too_wide_to_keep_scores(lens, toks, grp, page):
+    """More than 512 MB of scores if they were kept: the keys are read again instead."""
+    c = Case(lens, toks, hkv=4, grp=grp, D=128, page=page, seed=17)
+    wide = (512 << 20) // (4 * c.T * 4 * grp) // page + 2
+    c.table = np.pad(c.table, ((0, 0), (0, wide - c.table.shape[1])))
+    d = _run(_device(c))
+    _check(c, d)
+    assert d["ws"].nbytes > 512 << 20                       # narrower tables on the same workspace do keep theirs
+    first = d["scores"].clone()
+    d["scores"].copy_(torch.from_numpy(c.old))
+    d["table"] = d["table"][:, :wide // 2].contiguous()
+    _run(d)
+    _check(c, d)
+    assert (first - d["scores"]).abs().max() <= 2.0 ** -18 * first.abs().max()
 
 
 @pytest.mark.parametrize("grp", [2, 16, 40])
