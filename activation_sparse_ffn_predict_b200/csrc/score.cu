@@ -21,13 +21,12 @@ using namespace asf;
 namespace {
 
 // ---------------------------------------- the attention's own scores ----
-// k_tree_attn has kept its scores: each is read once, a thread a key, every row in turn.
+// k_tree_attn has kept its scores: each is read once, a thread four keys, every row in turn.
 constexpr int kSumKeys = 512;          // of a unit
 constexpr int kSumThreads = 128;
 constexpr int kSumRows = 64;           // whose references are in shared memory
 
 __global__ void __launch_bounds__(kSumThreads) k_score_sum(AttnArgs A) {
-  constexpr int U = kSumKeys / kSumThreads;
   __shared__ float2 s_stat[kSumRows];  // reference, 1 / sum
   pdl_wait();
   pdl_trigger();
@@ -48,15 +47,13 @@ __global__ void __launch_bounds__(kSumThreads) k_score_sum(AttnArgs A) {
     const int in = u - __shfl_sync(0xffffffffu, end - own, req), np = __shfl_sync(0xffffffffu, parts, req);
     const int t0 = __shfl_sync(0xffffffffu, q.t0, req), rows = __shfl_sync(0xffffffffu, q.n, req) * A.grp;
     const int len = __shfl_sync(0xffffffffu, q.len, req), L = __shfl_sync(0xffffffffu, q.L, req);
-    const int head = in / np, p0 = (in - head * np) * kSumKeys + tid;
+    const int head = in / np, p0 = (in - head * np) * kSumKeys + 4 * tid;
+    const bool there = p0 < L;                     // then its tile of 64 keys has scores, to the end
     float *scores = A.scores + ((int64_t)req * A.hkv + head) * A.S;
-    float old[U], acc[U];
+    float old[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int p = p0 + k * kSumThreads;
-      old[k] = p < len && p < A.S ? scores[p] : 0.f;
-      acc[k] = 0.f;
-    }
+    for (int k = 0; k < 4; ++k) old[k] = p0 + k < len && p0 + k < A.S ? scores[p0 + k] : 0.f;
+    const int64_t hop = (int64_t)(A.hkv - 1) * A.grp * A.zs;             // from a token's last row to the next token's first
     for (int m0 = 0; m0 < rows; m0 += kSumRows) {
       const int n = min(kSumRows, rows - m0);
       __syncthreads();
@@ -65,26 +62,37 @@ __global__ void __launch_bounds__(kSumThreads) k_score_sum(AttnArgs A) {
         const float2 st = __ldcg(A.stats + (int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp);
         s_stat[tid] = st.y == 0.f ? make_float2(0.f, 0.f) : make_float2(st.x, 1.f / st.y);
       }
-      __syncthreads();
       int tok = m0 / A.grp, g = m0 - tok * A.grp;
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float *z = A.z + ((int64_t)(t0 + tok) * A.hkv * A.grp + head * A.grp + g) * A.zs + p0;
-        const float2 st = s_stat[i];
+      const float *z = A.z + ((int64_t)(t0 + tok) * A.hkv * A.grp + head * A.grp + g) * A.zs + p0;
+      constexpr int U = 8;                         // rows in flight
+      for (int i = 0; i < n; i += U) {
+        float4 v[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-          const float v = p0 + k * kSumThreads < L ? __ldcs(z + k * kSumThreads) : -INFINITY;
-          if (v != -INFINITY) acc[k] = fmaf(exp2_fast(v - st.x), st.y, acc[k]);
+          v[k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          if (i + k < n && there) v[k] = __ldcg(reinterpret_cast<const float4 *>(z));
+          z += A.zs;
+          if (++g == A.grp) {
+            g = 0;
+            z += hop;
+          }
         }
-        if (++g == A.grp) {
-          g = 0;
-          ++tok;
+        if (i == 0) __syncthreads();               // the references are there
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const float2 st = s_stat[min(i + k, n - 1)];
+          const float w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = exp2_fast(w[e] - st.x);
+            acc[e] = w[e] != -INFINITY ? fmaf(x, st.y, acc[e]) : acc[e];
+          }
         }
       }
     }
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int p = p0 + k * kSumThreads;
+    for (int k = 0; k < 4; ++k) {
+      const int p = p0 + k;
       if (p >= L) continue;
       if (p >= A.S) flag_error(A.err, kErrIndex);
       else scores[p] = old[k] + acc[k];
@@ -222,12 +230,28 @@ __global__ void __launch_bounds__(128) k_tree_score(AttnArgs A) {
 // For many rows.  S^T = K Q^T: a tile of 128 keys is the M of the product and the
 // request's rows are its N, 64 at a time, so that a thread of the softmax warps has a key
 // and adds its rows up without meeting another thread.
-//   warp 4     copies tiles of 128 keys by TMA, a load per page and 64 columns
-//   warps 6, 7 a thread a row: its query, reference, 1 / sum and mask, into one of two
-//              slots; up to 128 rows stay there, more go round for every tile
-//   warp 5     one thread issues the products into one of four accumulators
-//   warps 0-3  read an accumulator, hand it back, and add up 2^(z - M) / l
+//   warp 8        copies tiles of 128 keys by TMA, a load per page and 64 columns
+//   warps 10, 11  a thread a row: its query, reference, 1 / sum and mask, into one of two
+//                 slots; up to 128 rows stay there, more go round for every tile
+//   warp 9        one thread issues the products into one of four accumulators
+//   warps 0-7     read an accumulator, hand it back, and add up 2^(z - M) / l: four warps
+//                 take the even tiles, four the odd ones
 // A CTA takes a run of tiles of one kv head; two CTAs share an SM.
+// 32 columns of this thread's tensor-memory lane, and the wait that makes them usable
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+      "[%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+
 template <int DP>
 struct ScoreTc {
   static constexpr int KEYS = 128, ROWS = 64;
@@ -238,7 +262,7 @@ struct ScoreTc {
   static constexpr int NB = 4;                     // accumulators, ROWS columns each
   static constexpr uint32_t COLS = NB * ROWS;
 };
-constexpr int kScoreThreads = 8 * 32;
+constexpr int kScoreThreads = 12 * 32;
 
 template <int DP>
 __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_constant__ CUtensorMap map_k, AttnArgs A) {
@@ -270,7 +294,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
     fence_mbar_init();
     prefetch_map(&map_k);
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(tslot, Lc::COLS);
     tmem_relinquish();
   }
@@ -324,7 +348,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
   const uint32_t tbase = *tslot;
   const int req = s_unit[0];
   if (req < 0) {
-    if (warp == 5) tmem_dealloc(tbase, Lc::COLS);
+    if (warp == 9) tmem_dealloc(tbase, Lc::COLS);
     return;
   }
   const int head = s_unit[1], kt0 = s_unit[2], tiles = s_unit[3] - kt0;
@@ -335,7 +359,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
   auto slot_of = [&](int i, int g) { return stay ? g : i & 1; };
   auto fill_of = [&](int i) { return stay ? 0u : (uint32_t)(i >> 1) & 1u; };
 
-  if (warp == 4) {
+  if (warp == 8) {
     // ------------------------------------------------------------------ keys --
     const int nb = KEYS / A.box;
     auto page_of = [&](int j, int &tok) {          // lane b: box b of tile j
@@ -370,9 +394,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
       __syncwarp();
     }
     if (!ok) flag_error(A.err, kErrTimeout);
-  } else if (warp >= 6) {
+  } else if (warp >= 10) {
     // ------------------------------------------------------------------ rows --
-    const int r = tid - 6 * 32;
+    const int r = tid - 10 * 32;
     bool ok = true;
     const int fills = stay ? rt : tiles * rt;
     for (int i = 0, g = 0; i < fills; ++i) {
@@ -402,7 +426,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
       if (++g == rt) g = 0;
     }
     if (!ok) flag_error(A.err, kErrTimeout);
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ------------------------------------------------------------------- MMA --
     constexpr uint32_t idesc = umma_idesc_f16(KEYS, ROWS, 0, 0);
     const uint64_t dk = umma_desc(sk, 16, 1024, kSwz128), dq = umma_desc(sq, 16, 1024, kSwz128);
@@ -432,11 +456,11 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
     if (!ok && lane == 0) flag_error(A.err, kErrTimeout);
   } else {
     // --------------------------------------------------------------- weights --
-    const uint32_t tl = tbase + ((uint32_t)(32 * warp) << 16);
+    const uint32_t tl = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
     float *scores = A.scores + ((int64_t)req * A.hkv + head) * A.S;
     bool ok = true;
-    for (int j = 0, i = 0; j < tiles && ok; ++j) {
-      const int pos = (kt0 + j) * KEYS + tid, d = pos - len;
+    for (int j = warp >> 2; j < tiles && ok; j += 2) {
+      const int pos = (kt0 + j) * KEYS + (tid & 127), d = pos - len;
       float old = 0.f;
       int id = -1;
       if (pos < L) {
@@ -445,34 +469,40 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
       }
       const bool special = (kt0 + j + 1) * KEYS > len;
       float a0 = 0.f, a1 = 0.f;
-      for (int g = 0; g < rt; ++g, ++i) {
+      for (int g = 0, i = j * rt; g < rt; ++g, ++i) {
         const int b = i % NB, sl = slot_of(i, g), live = rows - g * ROWS;
         ok = warp_wait(&full_q[sl], fill_of(i), kTcWaitNs);
         if (ok) ok = warp_wait(&bs[b], (uint32_t)(i / NB) & 1u, kTcWaitNs);
         if (!ok) break;
         tc_fence_after();
         __syncwarp();
-        float z[ROWS];
-        tmem_ld64(tl + b * ROWS, z);
-        tc_fence_before();
-        mbar_arrive(&be[b]);
-        const float4 *st = s_stat + sl * (ROWS / 2);
-        if (!special && live >= ROWS) {
 #pragma unroll
-          for (int m = 0; m < ROWS; m += 2) {
-            const float4 u = st[m / 2];
-            a0 = fmaf(exp2_fast(fmaf(z[m], A.scale, -u.x)), u.y, a0);
-            a1 = fmaf(exp2_fast(fmaf(z[m + 1], A.scale, -u.z)), u.w, a1);
+        for (int c = 0; c < ROWS; c += 32) {
+          float z[32];
+          tmem_ld32(tl + b * ROWS + c, z);
+          if (c + 32 == ROWS) {
+            tc_fence_before();
+            mbar_arrive(&be[b]);
           }
-        } else {
-          const uint32_t *see = s_see + sl * ROWS;
+          const float4 *st = s_stat + sl * (ROWS / 2) + c / 2;
+          if (!special && live >= c + 32) {
 #pragma unroll
-          for (int m = 0; m < ROWS; m += 2) {
-            const float4 u = st[m / 2];
-            const float w0 = exp2_fast(fmaf(z[m], A.scale, -u.x)), w1 = exp2_fast(fmaf(z[m + 1], A.scale, -u.z));
-            if (m < live && (d < 0 || (d < 32 && (see[m] >> d) & 1u))) a0 = fmaf(w0, u.y, a0);
-            if (m + 1 < live && (d < 0 || (d < 32 && (see[m + 1] >> d) & 1u))) a1 = fmaf(w1, u.w, a1);
+            for (int m = 0; m < 32; m += 2) {
+              const float4 u = st[m / 2];
+              a0 = fmaf(exp2_fast(fmaf(z[m], A.scale, -u.x)), u.y, a0);
+              a1 = fmaf(exp2_fast(fmaf(z[m + 1], A.scale, -u.z)), u.w, a1);
+            }
+          } else {
+            const uint32_t *see = s_see + sl * ROWS + c;
+#pragma unroll
+            for (int m = 0; m < 32; m += 2) {
+              const float4 u = st[m / 2];
+              const float w0 = exp2_fast(fmaf(z[m], A.scale, -u.x)), w1 = exp2_fast(fmaf(z[m + 1], A.scale, -u.z));
+              if (c + m < live && (d < 0 || (d < 32 && (see[m] >> d) & 1u))) a0 = fmaf(w0, u.y, a0);
+              if (c + m + 1 < live && (d < 0 || (d < 32 && (see[m + 1] >> d) & 1u))) a1 = fmaf(w1, u.w, a1);
+            }
           }
+          __syncwarp();
         }
         if (!stay) mbar_arrive(&empty_q[sl]);
       }
@@ -485,7 +515,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tbase, Lc::COLS);
   }
