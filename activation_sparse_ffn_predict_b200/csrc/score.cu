@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
     if (warp == 9) tmem_dealloc(tbase, Lc::COLS);
     return;
   }
-  const int head = s_unit[1], kt0 = s_unit[2], tiles = s_unit[3] - kt0;
+  const int head = s_unit[1], kt1 = s_unit[3], tiles = kt1 - s_unit[2];   // from the last tile on: the attention read it last
   const int t0 = s_unit[4], n = s_unit[5], len = s_unit[6], L = s_unit[7], rt = s_unit[8];
   const int rows = n * A.grp;
   const bool stay = rt <= 2;                       // the rows stay in their slots
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
     // ------------------------------------------------------------------ keys --
     const int nb = KEYS / A.box;
     auto page_of = [&](int j, int &tok) {          // lane b: box b of tile j
-      const int pos = (kt0 + j) * KEYS + lane * A.box;
+      const int pos = (kt1 - 1 - j) * KEYS + lane * A.box;
       tok = -1;
       if (j >= tiles || lane >= nb || pos >= L) return -1;
       const int pi = pos / A.page;
@@ -460,14 +460,14 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
     float *scores = A.scores + ((int64_t)req * A.hkv + head) * A.S;
     bool ok = true;
     for (int j = warp >> 2; j < tiles && ok; j += 2) {
-      const int pos = (kt0 + j) * KEYS + (tid & 127), d = pos - len;
+      const int pos = (kt1 - 1 - j) * KEYS + (tid & 127), d = pos - len;
       float old = 0.f;
       int id = -1;
       if (pos < L) {
         id = A.table[(int64_t)req * A.max_pages + pos / A.page];
         if (d < 0 && pos < A.S) old = scores[pos];
       }
-      const bool special = (kt0 + j + 1) * KEYS > len;
+      const bool special = (kt1 - j) * KEYS > len;
       float a0 = 0.f, a1 = 0.f;
       for (int g = 0, i = j * rt; g < rt; ++g, ++i) {
         const int b = i % NB, sl = slot_of(i, g), live = rows - g * ROWS;
