@@ -38,6 +38,8 @@ struct AttnArgs {
   int box;                             // keys of a TMA load, or 0
   int32_t *err;
   float2 *stats;                       // scored: per row (token, query head) its reference (log2) and sum
+  int mt;                              // rows of the attention's row tiles
+  bool beside;                         // the scores are summed beside the merge, from the splits' references and sums
   float *z;                            // [row][zs]: every row's scores (log2, -inf where it sees nothing), or null
   int64_t zs;
   float *scores;                       // [R][hkv][S]

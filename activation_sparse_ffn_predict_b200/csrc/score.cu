@@ -6,6 +6,13 @@
 // (in units of log2, over scores that carry log2(e)); the weight of a score z is then
 // 2^(z - M) / l, in fp32, and a key's rows are added in a fixed order.  Rows that saw
 // nothing have l = 0 and add nothing.
+//
+// The kernels start while the attention's last kernel runs.  That one has passed its own
+// dependency wait before it let them start, so what the call was given (requests, table,
+// queries, keys, scores) is complete, and is read from L2; what it writes is read after
+// the wait.  With `beside` the last kernel is the merge, and the sum reads only what is
+// in front of that.  The wait comes before the end in any case: a grid's end is
+// its predecessors' end, too.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -20,6 +27,23 @@ using namespace asf;
 
 namespace {
 
+// What the attention has left for a row: for each split, or in stats where there is one.
+struct Left {
+  const float2 *first;
+  int64_t step;
+  int splits;
+};
+__device__ __forceinline__ Left left_of(const AttnArgs &A, int4 plan, int head, int m, int64_t row) {
+  if (plan.z == 1) return {A.stats + row, 0, 1};
+  const int rt = (plan.y * A.grp + A.mt - 1) / A.mt;
+  return {A.ml + ((int64_t)plan.w + (int64_t)head * plan.z * rt + m / A.mt) * A.mt + m % A.mt, (int64_t)rt * A.mt, plan.z};
+}
+// (reference, 1 / sum) of parts (reference, sum)
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float M = fmaxf(a.x, b.x), ref = M == -INFINITY ? 0.f : M;
+  return make_float2(M, fmaf(exp2_fast(a.x - ref), a.y, exp2_fast(b.x - ref) * b.y));
+}
+
 // ---------------------------------------- the attention's own scores ----
 // k_tree_attn has kept its scores: each is read once, a thread four keys, every row in turn.
 constexpr int kSumKeys = 512;          // of a unit
@@ -28,7 +52,6 @@ constexpr int kSumRows = 64;           // whose references are in shared memory
 
 __global__ void __launch_bounds__(kSumThreads) k_score_sum(AttnArgs A) {
   __shared__ float2 s_stat[kSumRows];  // reference, 1 / sum
-  pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31;
   bool bad;
@@ -42,25 +65,40 @@ __global__ void __launch_bounds__(kSumThreads) k_score_sum(AttnArgs A) {
     if (lane >= o) end += v;
   }
   const int total = __shfl_sync(0xffffffffu, end, 31);
+  if (!A.beside) pdl_wait();
+  const int4 plans = __ldcg(A.plan + lane);
   for (int u = blockIdx.x; u < total; u += gridDim.x) {
     const int req = __popc(__ballot_sync(0xffffffffu, end <= u));
     const int in = u - __shfl_sync(0xffffffffu, end - own, req), np = __shfl_sync(0xffffffffu, parts, req);
     const int t0 = __shfl_sync(0xffffffffu, q.t0, req), rows = __shfl_sync(0xffffffffu, q.n, req) * A.grp;
     const int len = __shfl_sync(0xffffffffu, q.len, req), L = __shfl_sync(0xffffffffu, q.L, req);
+    const int4 plan = make_int4(0, __shfl_sync(0xffffffffu, plans.y, req), __shfl_sync(0xffffffffu, plans.z, req),
+                                __shfl_sync(0xffffffffu, plans.w, req));
     const int head = in / np, p0 = (in - head * np) * kSumKeys + 4 * tid;
     const bool there = p0 < L;                     // then its tile of 64 keys has scores, to the end
     float *scores = A.scores + ((int64_t)req * A.hkv + head) * A.S;
     float old[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) old[k] = p0 + k < len && p0 + k < A.S ? scores[p0 + k] : 0.f;
+    for (int k = 0; k < 4; ++k) old[k] = p0 + k < len && p0 + k < A.S ? __ldcg(scores + p0 + k) : 0.f;
     const int64_t hop = (int64_t)(A.hkv - 1) * A.grp * A.zs;             // from a token's last row to the next token's first
     for (int m0 = 0; m0 < rows; m0 += kSumRows) {
       const int n = min(kSumRows, rows - m0);
       __syncthreads();
-      if (tid < n) {
-        const int m = m0 + tid;
-        const float2 st = __ldcg(A.stats + (int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp);
-        s_stat[tid] = st.y == 0.f ? make_float2(0.f, 0.f) : make_float2(st.x, 1.f / st.y);
+      auto put = [&](int i, float2 st) { s_stat[i] = st.y == 0.f ? make_float2(0.f, 0.f) : make_float2(st.x, 1.f / st.y); };
+      auto row_of = [&](int m) { return (int64_t)(t0 + m / A.grp) * A.hkv * A.grp + head * A.grp + m % A.grp; };
+      if (!A.beside) {
+        if (tid < n) put(tid, __ldcg(A.stats + row_of(m0 + tid)));
+      } else {
+        // a warp a row, a lane a split (or every 32nd)
+        for (int i = tid >> 5; i < n; i += kSumThreads / 32) {
+          const Left left = left_of(A, plan, head, m0 + i, row_of(m0 + i));
+          float2 st = make_float2(-INFINITY, 0.f);
+          for (int p = lane; p < left.splits; p += 32) st = join(st, __ldcg(left.first + p * left.step));
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+            st = join(st, make_float2(__shfl_xor_sync(0xffffffffu, st.x, o), __shfl_xor_sync(0xffffffffu, st.y, o)));
+          if (lane == 0) put(i, st);
+        }
       }
       int tok = m0 / A.grp, g = m0 - tok * A.grp;
       const float *z = A.z + ((int64_t)(t0 + tok) * A.hkv * A.grp + head * A.grp + g) * A.zs + p0;
@@ -98,6 +136,7 @@ __global__ void __launch_bounds__(kSumThreads) k_score_sum(AttnArgs A) {
       else scores[p] = old[k] + acc[k];
     }
   }
+  if (A.beside) pdl_wait();
 }
 
 // ------------------------------------- keys again, any page size: mma.sync --
@@ -230,12 +269,12 @@ __global__ void __launch_bounds__(128) k_tree_score(AttnArgs A) {
 // For many rows.  S^T = K Q^T: a tile of 128 keys is the M of the product and the
 // request's rows are its N, 64 at a time, so that a thread of the softmax warps has a key
 // and adds its rows up without meeting another thread.
-//   warp 8        copies tiles of 128 keys by TMA, a load per page and 64 columns
-//   warps 10, 11  a thread a row: its query, reference, 1 / sum and mask, into one of two
-//                 slots; up to 128 rows stay there, more go round for every tile
-//   warp 9        one thread issues the products into one of four accumulators
-//   warps 0-7     read an accumulator, hand it back, and add up 2^(z - M) / l: four warps
-//                 take the even tiles, four the odd ones
+//   warp 4     copies tiles of 128 keys by TMA, a load per page and 64 columns
+//   warps 6, 7 a thread a row: its query, reference, 1 / sum and mask, into one of two
+//              slots; up to 128 rows stay there, more go round for every two tiles
+//   warp 5     one thread issues the products into one of four accumulators
+//   warps 0-3  read the accumulators of two tiles, hand them back, and add up 2^(z - M) / l:
+//              with two keys a thread, a reference read from shared memory serves both
 // A CTA takes a run of tiles of one kv head; two CTAs share an SM.
 // 32 columns of this thread's tensor-memory lane, and the wait that makes them usable
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
@@ -262,7 +301,7 @@ struct ScoreTc {
   static constexpr int NB = 4;                     // accumulators, ROWS columns each
   static constexpr uint32_t COLS = NB * ROWS;
 };
-constexpr int kScoreThreads = 12 * 32;
+constexpr int kScoreThreads = 8 * 32;
 
 template <int DP>
 __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_constant__ CUtensorMap map_k, AttnArgs A) {
@@ -294,11 +333,10 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
     fence_mbar_init();
     prefetch_map(&map_k);
   }
-  if (warp == 9) {
+  if (warp == 5) {
     tmem_alloc(tslot, Lc::COLS);
     tmem_relinquish();
   }
-  pdl_wait();
   pdl_trigger();
   if (warp == 0) {
     // C tiles a unit, the fewest for which the units fit `target` CTAs (one unit a kv head where even that is more)
@@ -348,18 +386,20 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
   const uint32_t tbase = *tslot;
   const int req = s_unit[0];
   if (req < 0) {
-    if (warp == 9) tmem_dealloc(tbase, Lc::COLS);
+    if (warp == 5) tmem_dealloc(tbase, Lc::COLS);
+    pdl_wait();
     return;
   }
   const int head = s_unit[1], kt1 = s_unit[3], tiles = kt1 - s_unit[2];   // from the last tile on: the attention read it last
   const int t0 = s_unit[4], n = s_unit[5], len = s_unit[6], L = s_unit[7], rt = s_unit[8];
   const int rows = n * A.grp;
   const bool stay = rt <= 2;                       // the rows stay in their slots
-  // pair i: tile i / rt, rows of group i % rt; its slot and the parity of its filling
+  // step i: the i / rt-th two tiles with the rows of group i % rt; the rows' slot and the parity of its filling
   auto slot_of = [&](int i, int g) { return stay ? g : i & 1; };
   auto fill_of = [&](int i) { return stay ? 0u : (uint32_t)(i >> 1) & 1u; };
+  const int twos = (tiles + 1) / 2;
 
-  if (warp == 8) {
+  if (warp == 4) {
     // ------------------------------------------------------------------ keys --
     const int nb = KEYS / A.box;
     auto page_of = [&](int j, int &tok) {          // lane b: box b of tile j
@@ -368,7 +408,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
       if (j >= tiles || lane >= nb || pos >= L) return -1;
       const int pi = pos / A.page;
       tok = pos - pi * A.page;
-      return (int)A.table[(int64_t)req * A.max_pages + pi];
+      return __ldcg(A.table + (int64_t)req * A.max_pages + pi);
     };
     bool ok = true;
     int tok, id = page_of(0, tok);
@@ -394,11 +434,11 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
       __syncwarp();
     }
     if (!ok) flag_error(A.err, kErrTimeout);
-  } else if (warp >= 10) {
+  } else if (warp >= 6) {
     // ------------------------------------------------------------------ rows --
-    const int r = tid - 10 * 32;
+    const int r = tid - 6 * 32;
     bool ok = true;
-    const int fills = stay ? rt : tiles * rt;
+    const int fills = stay ? rt : twos * rt;
     for (int i = 0, g = 0; i < fills; ++i) {
       const int sl = slot_of(i, g), m = g * ROWS + r;
       if (!stay && i >= 2) {
@@ -416,106 +456,132 @@ __global__ void __launch_bounds__(kScoreThreads, 2) k_score_tc(const __grid_cons
                    in ? 16u : 0u);
       }
       cp_async_commit();
+      const uint32_t see = live ? (uint32_t)__ldcg(A.anc + tok) >> t0 : 0u;
+      if (i == 0) pdl_wait();
       const float2 st = __ldcg(A.stats + row);
       const bool none = !live || st.y == 0.f;
       reinterpret_cast<float2 *>(s_stat + sl * (ROWS / 2))[r] = make_float2(none ? INFINITY : st.x, none ? 0.f : 1.f / st.y);
-      s_see[sl * ROWS + r] = live ? (uint32_t)A.anc[tok] >> t0 : 0u;
+      s_see[sl * ROWS + r] = see;
       cp_async_wait<0>();
       fence_proxy_async_smem();
       mbar_arrive(&full_q[sl]);
       if (++g == rt) g = 0;
     }
     if (!ok) flag_error(A.err, kErrTimeout);
-  } else if (warp == 9) {
+  } else if (warp == 5) {
     // ------------------------------------------------------------------- MMA --
     constexpr uint32_t idesc = umma_idesc_f16(KEYS, ROWS, 0, 0);
     const uint64_t dk = umma_desc(sk, 16, 1024, kSwz128), dq = umma_desc(sq, 16, 1024, kSwz128);
     bool ok = true;
-    for (int j = 0, i = 0; j < tiles && ok; ++j) {
-      const int ks = j % NS;
-      ok = warp_wait(&full_k[ks], (uint32_t)(j / NS) & 1u, kTcWaitNs);
+    for (int two = 0, i = 0; two < twos && ok; ++two) {
+      const int there = min(2, tiles - 2 * two);
       for (int g = 0; g < rt && ok; ++g, ++i) {
-        const int qs = slot_of(i, g), b = i % NB;
+        const int qs = slot_of(i, g);
         ok = warp_wait(&full_q[qs], fill_of(i), kTcWaitNs);
-        if (ok && i >= NB) ok = warp_wait(&be[b], (uint32_t)((i / NB) - 1) & 1u, kTcWaitNs);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t ak = dk + (uint64_t)(ks * (Lc::K >> 4)), bq = dq + (uint64_t)(qs * (Lc::Q >> 4));
-        if (elect_one()) {
+        for (int h = 0; h < there && ok; ++h) {
+          const int j = 2 * two + h, ks = j % NS, use = 2 * i + h, b = use % NB;
+          if (g == 0) ok = warp_wait(&full_k[ks], (uint32_t)(j / NS) & 1u, kTcWaitNs);
+          if (ok && use >= NB) ok = warp_wait(&be[b], (uint32_t)((use / NB) - 1) & 1u, kTcWaitNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t ak = dk + (uint64_t)(ks * (Lc::K >> 4)), bq = dq + (uint64_t)(qs * (Lc::Q >> 4));
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < DP / 16; ++k)
-            umma_f16(tbase + b * ROWS, ak + ((k >> 2) * (KEYS * 128) + (k & 3) * 32) / 16, bq + ((k >> 2) * (ROWS * 128) + (k & 3) * 32) / 16,
-                     idesc, k != 0);
-          umma_commit(&bs[b]);
-          if (!stay) umma_commit(&empty_q[qs]);
-          if (g == rt - 1) umma_commit(&empty_k[ks]);
+            for (int k = 0; k < DP / 16; ++k)
+              umma_f16(tbase + b * ROWS, ak + ((k >> 2) * (KEYS * 128) + (k & 3) * 32) / 16,
+                       bq + ((k >> 2) * (ROWS * 128) + (k & 3) * 32) / 16, idesc, k != 0);
+            umma_commit(&bs[b]);
+            if (!stay && h == there - 1) umma_commit(&empty_q[qs]);
+            if (g == rt - 1) umma_commit(&empty_k[ks]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
     if (!ok && lane == 0) flag_error(A.err, kErrTimeout);
   } else {
     // --------------------------------------------------------------- weights --
-    const uint32_t tl = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t tl = tbase + ((uint32_t)(32 * warp) << 16);
     float *scores = A.scores + ((int64_t)req * A.hkv + head) * A.S;
     bool ok = true;
-    for (int j = warp >> 2; j < tiles && ok; j += 2) {
-      const int pos = (kt1 - 1 - j) * KEYS + (tid & 127), d = pos - len;
-      float old = 0.f;
-      int id = -1;
-      if (pos < L) {
-        id = A.table[(int64_t)req * A.max_pages + pos / A.page];
-        if (d < 0 && pos < A.S) old = scores[pos];
+    for (int two = 0, i = 0; two < twos && ok; ++two) {
+      const int there = min(2, tiles - 2 * two);
+      int pos[2], d[2], id[2] = {-1, -1};
+      float old[2] = {0.f, 0.f}, acc[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        pos[h] = (kt1 - 1 - 2 * two - h) * KEYS + tid;
+        d[h] = pos[h] - len;
+        if (h >= there) pos[h] = L;                // the other accumulator holds what it held
+        if (pos[h] < L) {
+          id[h] = __ldcg(A.table + (int64_t)req * A.max_pages + pos[h] / A.page);
+          if (d[h] < 0 && pos[h] < A.S) old[h] = __ldcg(scores + pos[h]);
+        }
       }
-      const bool special = (kt1 - j) * KEYS > len;
-      float a0 = 0.f, a1 = 0.f;
-      for (int g = 0, i = j * rt; g < rt; ++g, ++i) {
-        const int b = i % NB, sl = slot_of(i, g), live = rows - g * ROWS;
+      const bool special = (kt1 - 2 * two) * KEYS > len;
+      for (int g = 0; g < rt; ++g, ++i) {
+        const int b = 2 * i % NB, sl = slot_of(i, g), live = rows - g * ROWS;
+        const uint32_t done = (uint32_t)(2 * i / NB) & 1u;
         ok = warp_wait(&full_q[sl], fill_of(i), kTcWaitNs);
-        if (ok) ok = warp_wait(&bs[b], (uint32_t)(i / NB) & 1u, kTcWaitNs);
+        if (ok) ok = warp_wait(&bs[b], done, kTcWaitNs);
+        if (ok && there == 2) ok = warp_wait(&bs[b + 1], done, kTcWaitNs);
         if (!ok) break;
         tc_fence_after();
         __syncwarp();
 #pragma unroll
         for (int c = 0; c < ROWS; c += 32) {
-          float z[32];
-          tmem_ld32(tl + b * ROWS + c, z);
+          float z[2][32];
+          tmem_ld32(tl + b * ROWS + c, z[0]);
+          tmem_ld32(tl + (b + 1) * ROWS + c, z[1]);
           if (c + 32 == ROWS) {
             tc_fence_before();
             mbar_arrive(&be[b]);
+            mbar_arrive(&be[b + 1]);
           }
           const float4 *st = s_stat + sl * (ROWS / 2) + c / 2;
           if (!special && live >= c + 32) {
 #pragma unroll
             for (int m = 0; m < 32; m += 2) {
               const float4 u = st[m / 2];
-              a0 = fmaf(exp2_fast(fmaf(z[m], A.scale, -u.x)), u.y, a0);
-              a1 = fmaf(exp2_fast(fmaf(z[m + 1], A.scale, -u.z)), u.w, a1);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                acc[h][0] = fmaf(exp2_fast(fmaf(z[h][m], A.scale, -u.x)), u.y, acc[h][0]);
+                acc[h][1] = fmaf(exp2_fast(fmaf(z[h][m + 1], A.scale, -u.z)), u.w, acc[h][1]);
+              }
             }
           } else {
             const uint32_t *see = s_see + sl * ROWS + c;
 #pragma unroll
-            for (int m = 0; m < 32; m += 2) {
-              const float4 u = st[m / 2];
-              const float w0 = exp2_fast(fmaf(z[m], A.scale, -u.x)), w1 = exp2_fast(fmaf(z[m + 1], A.scale, -u.z));
-              if (c + m < live && (d < 0 || (d < 32 && (see[m] >> d) & 1u))) a0 = fmaf(w0, u.y, a0);
-              if (c + m + 1 < live && (d < 0 || (d < 32 && (see[m + 1] >> d) & 1u))) a1 = fmaf(w1, u.w, a1);
+            for (int m = 0; m < 32; ++m) {
+              const float2 u = reinterpret_cast<const float2 *>(st)[m];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float w = exp2_fast(fmaf(z[h][m], A.scale, -u.x));
+                const bool sees = d[h] < 0 || (d[h] < 32 && (see[m] >> d[h]) & 1u);
+                if (c + m < live && sees) acc[h][m & 1] = fmaf(w, u.y, acc[h][m & 1]);
+              }
             }
           }
           __syncwarp();
         }
         if (!stay) mbar_arrive(&empty_q[sl]);
       }
-      if (!ok || pos >= L) continue;
-      if (pos >= A.S) flag_error(A.err, kErrIndex);
-      else if (d >= 0) scores[pos] = (unsigned)id < (unsigned)A.pages ? a0 + a1 : 0.f;
-      else if ((unsigned)id < (unsigned)A.pages) scores[pos] = old + (a0 + a1);
+      if (!ok) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (pos[h] >= L) continue;
+        const float w = acc[h][0] + acc[h][1];
+        if (pos[h] >= A.S) flag_error(A.err, kErrIndex);
+        else if (d[h] >= 0) scores[pos[h]] = (unsigned)id[h] < (unsigned)A.pages ? w : 0.f;
+        else if ((unsigned)id[h] < (unsigned)A.pages) scores[pos[h]] = old[h] + w;
+      }
     }
     if (!ok && lane == 0) flag_error(A.err, kErrTimeout);
   }
+  pdl_wait();
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 5) {
     tc_fence_after();
     tmem_dealloc(tbase, Lc::COLS);
   }
