@@ -27,7 +27,7 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveKeys = 32, kMoveHeads = 8;    // of a CTA: a row's offsets by a thread each
 static_assert(kMoveKeys * kMoveHeads == kMoveThreads, "a row a thread");
 constexpr uint32_t kHeld = 0xffffffffu;          // above every score
-constexpr int kStageMost = 40 * 1024;            // keys of a CTA in shared memory
+constexpr int kStageMost = 40 * 1024;            // scores of a CTA in shared memory
 
 struct EvictArgs {
   asf_kv_cache c;
@@ -40,7 +40,7 @@ struct EvictArgs {
   int S, S_out;
   int32_t *kept;                                 // [R][heads][keep]
   int keep, first, recent;
-  int staged;                                    // keys of a CTA that fit its shared memory
+  int staged;                                    // scores of a CTA that fit its shared memory
   int32_t *err;
 };
 
@@ -86,17 +86,22 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *part, uint3
 }
 
 // A cluster of CL CTAs is one kv head of one request, each of them a run of its
-// positions, kept in shared memory as keys where it fits.  Per digit: counts of the
-// keys that agree with the digits found so far, summed over distributed shared
-// memory by every CTA, and a scan from the largest value down.  Then each thread
-// walks a run of its own twice: how many stay, and where they go.
+// positions, whose scores it keeps in shared memory where they fit.  Per digit: counts
+// of the keys that agree with the digits found so far; each CTA adds up the cluster's
+// counts for its share of the digit's values over distributed shared memory, and all
+// of them look through the one share where the wanted count is reached.  Then each
+// warp walks a stretch of positions twice: how many stay, and where they go.
+// Latency bounds it (barriers, shared-memory round trips).
 template <int CL>
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(EvictArgs A) {
-  extern __shared__ uint32_t s_keys[];
-  __shared__ uint32_t s_hist[kBins], s_part[kSelThreads / 32], s_found[2], s_count[2];
+  constexpr int NW = kSelThreads / 32, SHARE = kBins / CL, PER = SHARE > kSelThreads ? SHARE / kSelThreads : 1;
+  extern __shared__ float s_score[];
+  __shared__ uint32_t s_hist[kBins], s_share[SHARE], s_part[NW], s_found[2], s_count[2];
+  __shared__ uint32_t s_more[NW], s_same[NW];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, rank = CL > 1 ? (int)blockIdx.x % CL : 0, unit = blockIdx.x / CL;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = CL > 1 ? (int)blockIdx.x % CL : 0, unit = blockIdx.x / CL;
   const int r = unit / A.c.heads, head = unit % A.c.heads;
   int n = ld_cg_i32(A.lens + r);
   const int cap = (int)min((int64_t)A.S, (int64_t)A.max_pages * A.c.page);
@@ -117,14 +122,23 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(EvictArgs A) {
     return;
   }
   const int run = (n + CL - 1) / CL, p0 = min(n, rank * run), mine = min(n, p0 + run) - p0;
-  auto fresh = [&](int i) {
-    const int p = p0 + i;
-    return p < A.first || p >= n - A.recent ? kHeld : order_of(__ldcg(scores + p));
-  };
   const bool staged = run <= A.staged;
-  if (staged)
-    for (int i = tid; i < mine; i += kSelThreads) s_keys[i] = fresh(i);
-  auto key = [&](int i) { return staged ? s_keys[i] : fresh(i); };
+  if (staged) {
+    constexpr int U = 8;                         // loads in flight
+    for (int i0 = tid; i0 < mine; i0 += U * kSelThreads) {
+      float v[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) v[k] = i0 + k * kSelThreads < mine ? __ldcg(scores + p0 + i0 + k * kSelThreads) : 0.f;
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (i0 + k * kSelThreads < mine) s_score[i0 + k * kSelThreads] = v[k];
+    }
+  }
+  auto score = [&](int i) { return staged ? s_score[i] : __ldcg(scores + p0 + i); };
+  auto key_of = [&](int i, float v) {
+    const int p = p0 + i;
+    return p < A.first || p >= n - A.recent ? kHeld : order_of(v);
+  };
 
   uint32_t want = (uint32_t)A.keep, prefix = 0;  // of the keys that agree with prefix, the want-th largest
   int shift = 21;
@@ -135,76 +149,116 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(EvictArgs A) {
     __syncthreads();
 #pragma unroll 4
     for (int i = tid; i < mine; i += kSelThreads) {
-      const uint32_t k = key(i);
+      const uint32_t k = key_of(i, score(i));
       if (digit == 0 || k >> upper == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
     }
-    if (CL > 1) cluster_barrier();
-    else __syncthreads();
-    // four bins a thread, from the largest down
-    constexpr int PER = kBins / kSelThreads;
-    uint32_t c[PER], sum = 0;
+    const uint32_t *counts = s_hist;             // of `share` * SHARE and the values after it
+    int share = 0;
+    uint32_t passed = 0;                         // keys above the share
+    if constexpr (CL > 1) {
+      static_assert(SHARE <= kSelThreads, "a value a thread");
+      cluster_barrier();
+      uint32_t c = 0, total;
+      if (tid < SHARE) {
+#pragma unroll
+        for (int q = 0; q < CL; ++q) c += ld_peer(&s_hist[rank * SHARE + tid], q);
+        s_share[tid] = c;
+      }
+      block_scan(c, s_part, total);
+      if (tid == 0) s_count[0] = total;
+      cluster_barrier();                         // the counts are read: they may be cleared
+      const uint32_t sum = lane < CL ? ld_peer(&s_count[0], lane) : 0;
+      uint32_t above = 0;
+#pragma unroll
+      for (int q = CL - 1; q >= 0; --q) {
+        const uint32_t u = __shfl_sync(0xffffffffu, sum, q);
+        if (above < want && above + u >= want) {
+          share = q;
+          passed = above;
+        }
+        above += u;
+      }
+      counts = s_share;
+    } else {
+      __syncthreads();
+    }
+    // PER values a thread, from the largest down
+    uint32_t c[PER], sum = 0, total;
 #pragma unroll
     for (int b = 0; b < PER; ++b) {
-      const int bin = kBins - 1 - (tid * PER + b);
-      c[b] = 0;
-      if (CL > 1) {
-#pragma unroll
-        for (int q = 0; q < CL; ++q) c[b] += ld_peer(&s_hist[bin], q);
-      } else {
-        c[b] = s_hist[bin];
-      }
+      const int value = SHARE - 1 - (tid * PER + b);
+      c[b] = value < 0 ? 0u : CL > 1 ? ld_peer(counts + max(value, 0), share) : counts[max(value, 0)];
       sum += c[b];
     }
-    uint32_t total;
-    uint32_t above = block_scan(sum, s_part, total);
+    uint32_t above = passed + block_scan(sum, s_part, total);
 #pragma unroll
     for (int b = 0; b < PER; ++b) {
       if (above < want && above + c[b] >= want) {
-        s_found[0] = kBins - 1 - (tid * PER + b);
+        s_found[0] = share * SHARE + SHARE - 1 - (tid * PER + b);
         s_found[1] = want - above;
       }
       above += c[b];
     }
-    if (CL > 1) cluster_barrier();               // counts are read before they are cleared
-    else __syncthreads();
+    __syncthreads();
     prefix = prefix << bits | s_found[0];
     want = s_found[1];
     shift -= digit == 1 ? 10 : 11;
-    __syncthreads();
   }
   // larger keys than prefix stay, and the first `want` of those equal to it
-  const int per = ((mine + kSelThreads - 1) / kSelThreads) | 1;          // odd: threads' runs begin in different banks
-  const int i0 = min(mine, tid * per), i1 = min(mine, i0 + per);
+  const int stretch = ((mine + NW - 1) / NW + 31) & ~31, i0 = warp * stretch, i1 = min(mine, i0 + stretch);
   uint32_t more = 0, same = 0;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key(i);
-    more += k > prefix;
-    same += k == prefix;
+  for (int i = i0; i < i1; i += 32) {
+    const uint32_t k = i + lane < i1 ? key_of(i + lane, score(i + lane)) : 0u;
+    more += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && k > prefix));
+    same += __popc(__ballot_sync(0xffffffffu, i + lane < i1 && k == prefix));
   }
-  uint32_t all_more, all_same;
-  uint32_t m = block_scan(more, s_part, all_more), e = block_scan(same, s_part, all_same);
-  if (CL > 1) {
+  if (lane == 0) {
+    s_more[warp] = more;
+    s_same[warp] = same;
+  }
+  __syncthreads();
+  uint32_t m = 0, e = 0, all_more = 0, all_same = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const uint32_t a = s_more[w], b = s_same[w];
+    if (w < warp) {
+      m += a;
+      e += b;
+    }
+    all_more += a;
+    all_same += b;
+  }
+  if constexpr (CL > 1) {
+    cluster_barrier();                           // the shares' sums have been read
     if (tid == 0) {
       s_count[0] = all_more;
       s_count[1] = all_same;
     }
     cluster_barrier();
-    for (int q = 0; q < rank; ++q) {
-      m += ld_peer(&s_count[0], q);
-      e += ld_peer(&s_count[1], q);
+    uint32_t a = 0, b = 0;
+    if (lane < rank) {
+      a = ld_peer(&s_count[0], lane);
+      b = ld_peer(&s_count[1], lane);
     }
-    cluster_barrier();                           // nobody leaves while its counts are read
+    m += __reduce_add_sync(0xffffffffu, a);
+    e += __reduce_add_sync(0xffffffffu, b);
   }
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key(i);
-    if (k > prefix || (k == prefix && e < want)) {
-      const uint32_t to = m + min(e, want);
-      kept[to] = p0 + i;
-      scores_out[to] = __ldcg(scores + p0 + i);
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = i0; i < i1; i += 32) {
+    const bool in = i + lane < i1;
+    const float v = in ? score(i + lane) : 0.f;
+    const uint32_t k = in ? key_of(i + lane, v) : 0u;
+    const uint32_t bm = __ballot_sync(0xffffffffu, in && k > prefix), be = __ballot_sync(0xffffffffu, in && k == prefix);
+    const uint32_t mm = m + __popc(bm & below), ee = e + __popc(be & below);
+    if (in && (k > prefix || (k == prefix && ee < want))) {
+      const uint32_t to = mm + min(ee, want);
+      kept[to] = p0 + i + lane;
+      scores_out[to] = v;
     }
-    m += k > prefix;
-    e += k == prefix;
+    m += __popc(bm);
+    e += __popc(be);
   }
+  if constexpr (CL > 1) cluster_barrier();       // nobody leaves while its counts are read
 }
 
 // The kept rows to their new places: offsets of 32 keys x 8 heads by a thread
