@@ -23,9 +23,13 @@ namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kBins = 2048;
+// Rows of a CTA, a row's places by a thread each.  4 requests of up to 65500 keys to 16384, us
+// of the call: 32 x 8 rows and four steps in flight 127, 16 x 8 117 (a shorter tail),
+// without the streaming hint on loads 110, with two steps in flight 107 (eight: 129).
 constexpr int kMoveThreads = 256;
-constexpr int kMoveKeys = 32, kMoveHeads = 8;    // of a CTA: a row's offsets by a thread each
-static_assert(kMoveKeys * kMoveHeads == kMoveThreads, "a row a thread");
+constexpr int kMoveKeys = 16, kMoveHeads = 8;
+constexpr int kMoveRows = kMoveKeys * kMoveHeads;
+static_assert(kMoveRows <= kMoveThreads, "a row a thread");
 constexpr uint32_t kHeld = 0xffffffffu;          // above every score
 constexpr int kStageMost = 40 * 1024;            // scores of a CTA in shared memory
 
@@ -51,15 +55,24 @@ __device__ __forceinline__ uint32_t order_of(float v) {
   return b >> 31 ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // a word of CTA `rank`'s shared memory, at the address of this CTA's p
 __device__ __forceinline__ uint32_t ld_peer(const uint32_t *p, int rank) {
   uint32_t at, v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
+}
+
+// adds to it
+__device__ __forceinline__ void add_peer(uint32_t *p, int rank, uint32_t v) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
 // exclusive sum over the CTA's threads, and the total; `part` holds a word per warp
@@ -87,16 +100,18 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *part, uint3
 
 // A cluster of CL CTAs is one kv head of one request, each of them a run of its
 // positions, whose scores it keeps in shared memory where they fit.  Per digit: counts
-// of the keys that agree with the digits found so far; each CTA adds up the cluster's
-// counts for its share of the digit's values over distributed shared memory, and all
-// of them look through the one share where the wanted count is reached.  Then each
-// warp walks a stretch of positions twice: how many stay, and where they go.
-// Latency bounds it (barriers, shared-memory round trips).
+// of the keys that agree with the digits found so far, which every CTA adds to the
+// CTAs that own a share of the digit's values (distributed shared memory), and a scan of
+// all of them from the largest value down.  Then each warp walks a stretch of positions
+// twice: how many stay, and where they go.  Latency bounds it, above all the barriers
+// of the cluster: five of them, a microsecond and more each (with nine, counts fetched and
+// shares' sums published, 26 us at 65500 keys).
 template <int CL>
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(EvictArgs A) {
-  constexpr int NW = kSelThreads / 32, SHARE = kBins / CL, PER = SHARE > kSelThreads ? SHARE / kSelThreads : 1;
+  constexpr int NW = kSelThreads / 32, SHARE = kBins / CL, PER = kBins / kSelThreads;
   extern __shared__ float s_score[];
-  __shared__ uint32_t s_hist[kBins], s_share[SHARE], s_part[NW], s_found[2], s_count[2];
+  __shared__ uint32_t s_hist[kBins], s_part[NW], s_found[2];
+  __shared__ uint32_t s_share[3][CL > 1 ? SHARE : 1], s_count[2];   // other CTAs add to these: a digit's counts, what is before this CTA
   __shared__ uint32_t s_more[NW], s_same[NW];
   pdl_wait();
   pdl_trigger();
@@ -120,6 +135,11 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(EvictArgs A) {
       scores_out[p] = scores[p];
     }
     return;
+  }
+  if constexpr (CL > 1) {
+    for (int i = tid; i < 3 * SHARE; i += kSelThreads) s_share[i / SHARE][i % SHARE] = 0;
+    if (tid < 2) s_count[tid] = 0;
+    cluster_arrive();
   }
   const int run = (n + CL - 1) / CL, p0 = min(n, rank * run), mine = min(n, p0 + run) - p0;
   const bool staged = run <= A.staged;
@@ -152,49 +172,28 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(EvictArgs A) {
       const uint32_t k = key_of(i, score(i));
       if (digit == 0 || k >> upper == prefix) atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
     }
-    const uint32_t *counts = s_hist;             // of `share` * SHARE and the values after it
-    int share = 0;
-    uint32_t passed = 0;                         // keys above the share
+    __syncthreads();
     if constexpr (CL > 1) {
-      static_assert(SHARE <= kSelThreads, "a value a thread");
-      cluster_barrier();
-      uint32_t c = 0, total;
-      if (tid < SHARE) {
-#pragma unroll
-        for (int q = 0; q < CL; ++q) c += ld_peer(&s_hist[rank * SHARE + tid], q);
-        s_share[tid] = c;
-      }
-      block_scan(c, s_part, total);
-      if (tid == 0) s_count[0] = total;
-      cluster_barrier();                         // the counts are read: they may be cleared
-      const uint32_t sum = lane < CL ? ld_peer(&s_count[0], lane) : 0;
-      uint32_t above = 0;
-#pragma unroll
-      for (int q = CL - 1; q >= 0; --q) {
-        const uint32_t u = __shfl_sync(0xffffffffu, sum, q);
-        if (above < want && above + u >= want) {
-          share = q;
-          passed = above;
-        }
-        above += u;
-      }
-      counts = s_share;
-    } else {
-      __syncthreads();
+      if (digit == 0) cluster_wait();            // every CTA's shares are clear
+      for (int i = tid; i < kBins; i += kSelThreads)
+        if (s_hist[i]) add_peer(&s_share[digit][i % SHARE], i / SHARE, s_hist[i]);
+      cluster_arrive();
+      cluster_wait();
     }
     // PER values a thread, from the largest down
     uint32_t c[PER], sum = 0, total;
 #pragma unroll
     for (int b = 0; b < PER; ++b) {
-      const int value = SHARE - 1 - (tid * PER + b);
-      c[b] = value < 0 ? 0u : CL > 1 ? ld_peer(counts + max(value, 0), share) : counts[max(value, 0)];
-      sum += c[b];
+      const int value = kBins - 1 - (tid * PER + b);
+      c[b] = CL > 1 ? ld_peer(&s_share[digit][value % SHARE], value / SHARE) : s_hist[value];
     }
-    uint32_t above = passed + block_scan(sum, s_part, total);
+#pragma unroll
+    for (int b = 0; b < PER; ++b) sum += c[b];
+    uint32_t above = block_scan(sum, s_part, total);
 #pragma unroll
     for (int b = 0; b < PER; ++b) {
       if (above < want && above + c[b] >= want) {
-        s_found[0] = share * SHARE + SHARE - 1 - (tid * PER + b);
+        s_found[0] = kBins - 1 - (tid * PER + b);
         s_found[1] = want - above;
       }
       above += c[b];
@@ -229,19 +228,14 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(EvictArgs A) {
     all_same += b;
   }
   if constexpr (CL > 1) {
-    cluster_barrier();                           // the shares' sums have been read
-    if (tid == 0) {
-      s_count[0] = all_more;
-      s_count[1] = all_same;
+    if (tid > rank && tid < CL) {
+      add_peer(&s_count[0], tid, all_more);
+      add_peer(&s_count[1], tid, all_same);
     }
-    cluster_barrier();
-    uint32_t a = 0, b = 0;
-    if (lane < rank) {
-      a = ld_peer(&s_count[0], lane);
-      b = ld_peer(&s_count[1], lane);
-    }
-    m += __reduce_add_sync(0xffffffffu, a);
-    e += __reduce_add_sync(0xffffffffu, b);
+    cluster_arrive();
+    cluster_wait();                              // nothing reaches into another CTA from here on
+    m += s_count[0];
+    e += s_count[1];
   }
   const uint32_t below = (1u << lane) - 1u;
   for (int i = i0; i < i1; i += 32) {
@@ -258,21 +252,20 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(EvictArgs A) {
     m += __popc(bm);
     e += __popc(be);
   }
-  if constexpr (CL > 1) cluster_barrier();       // nobody leaves while its counts are read
 }
 
-// The kept rows to their new places: offsets of 32 keys x 8 heads by a thread
-// each, then 16 bytes of keys and of values a thread at a time.
+// The kept rows to their new places: a row's two places by a thread each, then 16
+// bytes of keys and of values a thread at a time.  HBM bounds it: 402 MB in 80 us.
 __global__ void __launch_bounds__(kMoveThreads) k_evict_move(EvictArgs A) {
-  __shared__ int64_t s_from[kMoveThreads], s_to[kMoveThreads];
+  __shared__ int64_t s_from[kMoveRows], s_to[kMoveRows];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, r = blockIdx.z, j0 = blockIdx.x * kMoveKeys, h0 = blockIdx.y * kMoveHeads;
   const int stay = ld_cg_i32(A.lens_out + r), page = A.c.page;
   if (j0 >= stay) return;
   const int heads = min(kMoveHeads, A.c.heads - h0), keys = min(kMoveKeys, stay - j0);
-  {
-    const int j = j0 + (tid & 31), h = tid >> 5;
+  if (tid < kMoveRows) {
+    const int j = j0 + tid % kMoveKeys, h = tid / kMoveKeys;
     int64_t from = -1, to = -1;
     if (h < heads && j < stay) {
       const int p = ld_cg_i32(A.kept + ((int64_t)r * A.c.heads + h0 + h) * A.keep + j);
@@ -286,7 +279,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_move(EvictArgs A) {
         flag_error(A.err, kErrIndex);
       }
     }
-    const int at = (tid & 31) * heads + h;       // a key's heads side by side
+    const int at = tid % kMoveKeys * heads + h;    // a key's heads side by side
     if (h < heads) {
       s_from[at] = from;
       s_to[at] = to;
@@ -297,7 +290,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_move(EvictArgs A) {
   const int lanes = kMoveThreads / ch;           // rows at a time
   const int c = tid % ch;
   __half *k = static_cast<__half *>(A.c.k), *v = static_cast<__half *>(A.c.v);
-  constexpr int U = 4;
+  constexpr int U = 2;
   for (int row = tid / ch; row < rows; row += lanes * U) {
     uint4 a[U], b[U];
     int64_t to[U];
@@ -306,8 +299,8 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_move(EvictArgs A) {
       const int at = row + i * lanes;
       to[i] = at < rows && tid < lanes * ch ? s_to[at] : -1;
       if (to[i] >= 0) {
-        a[i] = __ldcs(reinterpret_cast<const uint4 *>(k + s_from[at]) + c);
-        b[i] = __ldcs(reinterpret_cast<const uint4 *>(v + s_from[at]) + c);
+        a[i] = __ldcg(reinterpret_cast<const uint4 *>(k + s_from[at]) + c);
+        b[i] = __ldcg(reinterpret_cast<const uint4 *>(v + s_from[at]) + c);
       }
     }
 #pragma unroll
