@@ -23,8 +23,12 @@ namespace {
 
 constexpr int kDownThreads = 256;
 constexpr int kUpThreads = 128;
-constexpr int kUpRows = 128;           // rows of y that a CTA takes
-constexpr int kAlong = 8;              // tokens at a time
+constexpr int kAlong = 4;              // tokens at a time
+// Eight ranks of a row are a lane's; `lpr` lanes are a row's, and each has `up_steps` rows.
+template <typename T>
+__host__ __device__ constexpr int up_steps() { return sizeof(T) == 2 ? 8 : 4; }
+template <typename T>
+__host__ __device__ constexpr int up_rows(int lpr) { return kUpThreads / lpr * up_steps<T>(); }
 
 struct LoraArgs {
   int adapters, rank, k, rows, B;
@@ -104,11 +108,11 @@ __device__ __forceinline__ void down_rows(const LoraArgs &A, int a, int row0, ui
   float acc[RW * NB];
 #pragma unroll
   for (int i = 0; i < RW * NB; ++i) acc[i] = 0.f;
-#pragma unroll 2
+#pragma unroll(NB == 1 ? 4 : 2)
   for (int i = tid * E; i < A.k; i += kDownThreads * E) {
     uint4 wv[RW], xv[NB];
 #pragma unroll
-    for (int r = 0; r < RW; ++r) wv[r] = __ldg(reinterpret_cast<const uint4 *>(w + (int64_t)r * A.k + i));
+    for (int r = 0; r < RW; ++r) wv[r] = __ldcg(reinterpret_cast<const uint4 *>(w + (int64_t)r * A.k + i));
 #pragma unroll
     for (int b = 0; b < NB; ++b) xv[b] = __ldcg(reinterpret_cast<const uint4 *>(x + (int64_t)tok[b] * A.k + i));
 #pragma unroll
@@ -125,7 +129,7 @@ __device__ __forceinline__ void down_rows(const LoraArgs &A, int a, int row0, ui
     float sum = 0.f;
 #pragma unroll
     for (int q = 0; q < kDownThreads / 32; ++q) sum += s_red[q * N + tid];
-    const float s = A.scale ? __ldg(A.scale + a) : 1.f;
+    const float s = A.scale ? __ldcg(A.scale + a) : 1.f;
     int t = tok[0];
 #pragma unroll
     for (int b = 1; b < NB; ++b) t = tid % NB == b ? tok[b] : t;
@@ -135,41 +139,57 @@ __device__ __forceinline__ void down_rows(const LoraArgs &A, int a, int row0, ui
 
 // h = s A x: a CTA is RW rows of the adapter that its token leads, over all of k.
 template <typename T, int RW>
-__global__ void __launch_bounds__(kDownThreads) k_lora_down(LoraArgs A) {
-  __shared__ float s_red[kDownThreads / 32 * 32];
-  pdl_wait();
+__global__ void __launch_bounds__(kDownThreads, 2) k_lora_down(LoraArgs A) {
+  __shared__ float s_red[kDownThreads / 32 * RW * kAlong];
   pdl_trigger();
   int a;
   uint32_t set = led_by(A, blockIdx.y, a);
-  if (!set || a < 0) return;
   const int row0 = blockIdx.x * RW;    // rank is a multiple of 8
-  while (set) {
+  while (set && a >= 0) {
     const int left = __popc(set);
-    if (left > 4) down_rows<T, RW, 8>(A, a, row0, set, s_red);
-    else if (left > 2) down_rows<T, RW, 4>(A, a, row0, set, s_red);
+    if (left > 2) down_rows<T, RW, 4>(A, a, row0, set, s_red);
     else if (left > 1) down_rows<T, RW, 2>(A, a, row0, set, s_red);
     else down_rows<T, RW, 1>(A, a, row0, set, s_red);
   }
+  pdl_wait();
 }
 
+// eight values as they were read
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8]);
+struct Eight;
 template <>
-__device__ __forceinline__ void load8<__half>(const __half *p, float (&v)[8]) {
-  Vec<__half>::to_float(__ldg(reinterpret_cast<const uint4 *>(p)), v);
-}
+struct Eight<__half> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __half *p) { u = __ldcg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void to(float (&v)[8]) const { Vec<__half>::to_float(u, v); }
+};
 template <>
-__device__ __forceinline__ void load8<float>(const float *p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = __ldcg(reinterpret_cast<const float4 *>(p));
+    b = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
+  }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void to(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+__device__ __forceinline__ void put(const LoraArgs &A, int64_t at, float v) {
+  if (A.relu) v = v > 0.f ? v : (v != v ? v : 0.f);
+  if (A.y16) static_cast<__half *>(A.y)[at] = __float2half_rn(v);
+  else static_cast<float *>(A.y)[at] = v;
 }
 
 template <typename T, int NB>
-__device__ __forceinline__ void up_rows(const LoraArgs &A, int a, int row0, int lpr, uint32_t &set, float *s_out) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ __forceinline__ void up_tokens(const LoraArgs &A, const Eight<T> (&w)[up_steps<T>()], int row0, int lpr, uint32_t &set,
+                                          float *s_out) {
+  const int tid = threadIdx.x, rows = up_rows<T>(lpr);
   int tok[NB];
   const int n = take<NB>(set, tok);
-  const int part = lane & (lpr - 1), per = 32 / lpr;                   // rows a warp has at a time
+  const int part = tid & (lpr - 1);
   const bool in = part * 8 < A.rank;
   float h[NB][8];
 #pragma unroll
@@ -180,15 +200,11 @@ __device__ __forceinline__ void up_rows(const LoraArgs &A, int a, int row0, int 
                           : make_float4(0.f, 0.f, 0.f, 0.f);
       h[b][e] = u.x; h[b][e + 1] = u.y; h[b][e + 2] = u.z; h[b][e + 3] = u.w;
     }
-  const T *w = static_cast<const T *>(A.Bm) + (int64_t)a * A.rows * A.rank + part * 8;
   __syncthreads();                     // s_out has been read
-#pragma unroll 4
-  for (int i = warp * 32 + lane / lpr; i < warp * 32 + 32; i += per) {
-    const int row = row0 + i;
-    float v[8], acc[NB];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    if (in && row < A.rows) load8<T>(w + (int64_t)row * A.rank, v);
+  for (int i = 0; i < up_steps<T>(); ++i) {
+    float v[8], acc[NB];
+    w[i].to(v);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       acc[b] = 0.f;
@@ -200,53 +216,56 @@ __device__ __forceinline__ void up_rows(const LoraArgs &A, int a, int row0, int 
       for (int b = 0; b < NB; ++b) acc[b] += __shfl_xor_sync(0xffffffffu, acc[b], o);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      if (part == (b & (lpr - 1))) s_out[b * kUpRows + i] = acc[b];
+      if (part == (b & (lpr - 1))) s_out[b * rows + i * (kUpThreads / lpr) + tid / lpr] = acc[b];
   }
   __syncthreads();
-  const int row = row0 + tid;
-  if (row < A.rows)
+  for (int i = tid; i < rows && row0 + i < A.rows; i += kUpThreads)
 #pragma unroll
     for (int b = 0; b < NB; ++b)
       if (b < n) {
-        const int64_t at = (int64_t)tok[b] * A.rows + row;
-        float v = __ldcg(A.base + at) + s_out[b * kUpRows + tid];
-        if (A.relu) v = v > 0.f ? v : (v != v ? v : 0.f);
-        if (A.y16) static_cast<__half *>(A.y)[at] = __float2half_rn(v);
-        else static_cast<float *>(A.y)[at] = v;
+        const int64_t at = (int64_t)tok[b] * A.rows + row0 + i;
+        put(A, at, __ldcg(A.base + at) + s_out[b * rows + i]);
       }
 }
 
-// y = act(base + B h): a CTA is 128 rows of the adapter that its token leads; lanes
-// lie side by side along a row of B, eight ranks each, so that a warp reads whole
-// rows one after the other, and the tokens' sums go through shared memory to come
-// out row by row.
+// y = act(base + B h): a CTA is 16 KB of the adapter that its token leads, all of it in
+// flight at once and kept for all of its tokens; lanes lie side by side along a row, eight
+// ranks each, and the tokens' sums go through shared memory to come out row by row.
 template <typename T>
-__global__ void __launch_bounds__(kUpThreads) k_lora_up(LoraArgs A, int lpr) {
-  __shared__ float s_out[kAlong * kUpRows];
-  pdl_wait();
+__global__ void __launch_bounds__(kUpThreads, 5) k_lora_up(LoraArgs A, int lpr) {
+  extern __shared__ float s_out[];     // [kAlong][rows of the CTA]
   pdl_trigger();
   int a;
   uint32_t set = led_by(A, blockIdx.y, a);
-  if (!set) return;
-  const int row0 = blockIdx.x * kUpRows;
-  if (a < 0) {                         // no adapter: the activation and the rounding are left to do
-    const int row = row0 + threadIdx.x;
-    if (row >= A.rows || (static_cast<const void *>(A.base) == A.y && !A.relu)) return;
-    for (; set; set &= set - 1) {
-      const int64_t at = (int64_t)(__ffs(set) - 1) * A.rows + row;
-      float v = __ldcg(A.base + at);
-      if (A.relu) v = v > 0.f ? v : (v != v ? v : 0.f);
-      if (A.y16) static_cast<__half *>(A.y)[at] = __float2half_rn(v);
-      else static_cast<float *>(A.y)[at] = v;
-    }
+  const int tid = threadIdx.x, rows = up_rows<T>(lpr), row0 = blockIdx.x * rows, part = tid & (lpr - 1);
+  if (!set) {
+    pdl_wait();
     return;
   }
+  if (a < 0) {                         // no adapter: the activation and the rounding are left to do
+    pdl_wait();
+    if (static_cast<const void *>(A.base) == A.y && !A.relu) return;
+    for (; set; set &= set - 1)
+      for (int i = tid; i < rows && row0 + i < A.rows; i += kUpThreads) {
+        const int64_t at = (int64_t)(__ffs(set) - 1) * A.rows + row0 + i;
+        put(A, at, __ldcg(A.base + at));
+      }
+    return;
+  }
+  Eight<T> w[up_steps<T>()];
+  const T *from = static_cast<const T *>(A.Bm) + (int64_t)a * A.rows * A.rank + part * 8;
+#pragma unroll
+  for (int i = 0; i < up_steps<T>(); ++i) {
+    const int row = row0 + i * (kUpThreads / lpr) + tid / lpr;
+    w[i].clear();
+    if (part * 8 < A.rank && row < A.rows) w[i].load(from + (int64_t)row * A.rank);
+  }
+  pdl_wait();
   while (set) {
     const int left = __popc(set);
-    if (left > 4) up_rows<T, 8>(A, a, row0, lpr, set, s_out);
-    else if (left > 2) up_rows<T, 4>(A, a, row0, lpr, set, s_out);
-    else if (left > 1) up_rows<T, 2>(A, a, row0, lpr, set, s_out);
-    else up_rows<T, 1>(A, a, row0, lpr, set, s_out);
+    if (left > 2) up_tokens<T, 4>(A, w, row0, lpr, set, s_out);
+    else if (left > 1) up_tokens<T, 2>(A, w, row0, lpr, set, s_out);
+    else up_tokens<T, 1>(A, w, row0, lpr, set, s_out);
   }
 }
 
@@ -322,9 +341,11 @@ asf_status asf_w4_matmul_lora(const asf_w4_matrix *mat, const asf_lora *lora, co
   if (e != cudaSuccess) return ASF_ERR_CUDA;
   int lpr = 1;
   while (lpr * 8 < a.rank) lpr *= 2;
-  const dim3 grid((a.rows + kUpRows - 1) / kUpRows, B);
-  e = xdtype == ASF_F16 ? launch(k_lora_up<__half>, grid, dim3(kUpThreads), 0, st, a, lpr)
-                        : launch(k_lora_up<float>, grid, dim3(kUpThreads), 0, st, a, lpr);
+  const int tile = xdtype == ASF_F16 ? up_rows<__half>(lpr) : up_rows<float>(lpr);
+  const dim3 grid((unsigned)(((int64_t)a.rows + tile - 1) / tile), B);
+  const size_t smem = (size_t)kAlong * tile * 4;
+  e = xdtype == ASF_F16 ? launch(k_lora_up<__half>, grid, dim3(kUpThreads), smem, st, a, lpr)
+                        : launch(k_lora_up<float>, grid, dim3(kUpThreads), smem, st, a, lpr);
   return cuda_status(e);
 }
 
