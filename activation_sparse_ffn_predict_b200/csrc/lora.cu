@@ -21,14 +21,14 @@ using namespace asf;
 
 namespace {
 
-constexpr int kDownThreads = 256;
+constexpr int kDownThreads = 128;
 constexpr int kUpThreads = 128;
+constexpr int kUpCtas = 3;             // of an SM
+constexpr int kUpStages = 4, kUpStage = 16 * 1024;
+constexpr int kUpRows = 256;           // of a stage at most
 constexpr int kAlong = 4;              // tokens at a time
-// Eight ranks of a row are a lane's; `lpr` lanes are a row's, and each has `up_steps` rows.
-template <typename T>
-__host__ __device__ constexpr int up_steps() { return sizeof(T) == 2 ? 8 : 4; }
-template <typename T>
-__host__ __device__ constexpr int up_rows(int lpr) { return kUpThreads / lpr * up_steps<T>(); }
+constexpr uint64_t kUpWaitNs = 200ull * 1000 * 1000;   // bound on any mbarrier wait
+constexpr size_t kUpSmem = (size_t)kUpStages * kUpStage + 2 * kAlong * kUpRows * 4;
 
 struct LoraArgs {
   int adapters, rank, k, rows, B;
@@ -108,7 +108,7 @@ __device__ __forceinline__ void down_rows(const LoraArgs &A, int a, int row0, ui
   float acc[RW * NB];
 #pragma unroll
   for (int i = 0; i < RW * NB; ++i) acc[i] = 0.f;
-#pragma unroll(NB == 1 ? 4 : 2)
+#pragma unroll(RW * NB == 1 ? 4 : NB == 1 ? 2 : 1)
   for (int i = tid * E; i < A.k; i += kDownThreads * E) {
     uint4 wv[RW], xv[NB];
 #pragma unroll
@@ -139,7 +139,7 @@ __device__ __forceinline__ void down_rows(const LoraArgs &A, int a, int row0, ui
 
 // h = s A x: a CTA is RW rows of the adapter that its token leads, over all of k.
 template <typename T, int RW>
-__global__ void __launch_bounds__(kDownThreads, 2) k_lora_down(LoraArgs A) {
+__global__ void __launch_bounds__(kDownThreads, 8) k_lora_down(LoraArgs A) {
   __shared__ float s_red[kDownThreads / 32 * RW * kAlong];
   pdl_trigger();
   int a;
@@ -154,41 +154,31 @@ __global__ void __launch_bounds__(kDownThreads, 2) k_lora_down(LoraArgs A) {
   pdl_wait();
 }
 
-// eight values as they were read
-template <typename T>
-struct Eight;
-template <>
-struct Eight<__half> {
-  uint4 u;
-  __device__ __forceinline__ void load(const __half *p) { u = __ldcg(reinterpret_cast<const uint4 *>(p)); }
-  __device__ __forceinline__ void clear() { u = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void to(float (&v)[8]) const { Vec<__half>::to_float(u, v); }
-};
-template <>
-struct Eight<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float *p) {
-    a = __ldcg(reinterpret_cast<const float4 *>(p));
-    b = __ldcg(reinterpret_cast<const float4 *>(p) + 1);
-  }
-  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void to(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-};
-
 __device__ __forceinline__ void put(const LoraArgs &A, int64_t at, float v) {
   if (A.relu) v = v > 0.f ? v : (v != v ? v : 0.f);
   if (A.y16) static_cast<__half *>(A.y)[at] = __float2half_rn(v);
   else static_cast<float *>(A.y)[at] = v;
 }
+__device__ __forceinline__ void eight(const __half *p, float (&v)[8]) {
+  Vec<__half>::to_float(*reinterpret_cast<const uint4 *>(p), v);
+}
+__device__ __forceinline__ void eight(const float *p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
 
+// NB tokens over `rows` rows of B in shared memory; lpr lanes a row, eight ranks each
 template <typename T, int NB>
-__device__ __forceinline__ void up_tokens(const LoraArgs &A, const Eight<T> (&w)[up_steps<T>()], int row0, int lpr, uint32_t &set,
-                                          float *s_out) {
-  const int tid = threadIdx.x, rows = up_rows<T>(lpr);
+__device__ __forceinline__ void up_tokens(const LoraArgs &A, const T *w, int row0, int rows, int lpr, uint32_t &set, float *s_out) {
+  const int tid = threadIdx.x;
   int tok[NB];
   const int n = take<NB>(set, tok);
+  float base[kUpRows / kUpThreads][NB];            // on their way while the sums are made
+#pragma unroll
+  for (int q = 0; q < kUpRows / kUpThreads; ++q)
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      base[q][b] = tid + q * kUpThreads < rows && b < n ? __ldcg(A.base + (int64_t)tok[b] * A.rows + row0 + tid + q * kUpThreads) : 0.f;
   const int part = tid & (lpr - 1);
   const bool in = part * 8 < A.rank;
   float h[NB][8];
@@ -196,15 +186,17 @@ __device__ __forceinline__ void up_tokens(const LoraArgs &A, const Eight<T> (&w)
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int e = 0; e < 8; e += 4) {
-      const float4 u = in ? __ldcg(reinterpret_cast<const float4 *>(A.h + (int64_t)tok[b] * A.rank + part * 8 + e))
+      const float4 u = in ? *reinterpret_cast<const float4 *>(A.h + (int64_t)tok[b] * A.rank + part * 8 + e)
                           : make_float4(0.f, 0.f, 0.f, 0.f);
       h[b][e] = u.x; h[b][e + 1] = u.y; h[b][e + 2] = u.z; h[b][e + 3] = u.w;
     }
-  __syncthreads();                     // s_out has been read
-#pragma unroll
-  for (int i = 0; i < up_steps<T>(); ++i) {
+#pragma unroll 4
+  for (int row = tid / lpr; row < kUpRows; row += kUpThreads / lpr) {
+    if (row - tid / lpr >= rows) break;            // the same for all lanes
     float v[8], acc[NB];
-    w[i].to(v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    if (in && row < rows) eight(w + row * A.rank + part * 8, v);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       acc[b] = 0.f;
@@ -216,57 +208,106 @@ __device__ __forceinline__ void up_tokens(const LoraArgs &A, const Eight<T> (&w)
       for (int b = 0; b < NB; ++b) acc[b] += __shfl_xor_sync(0xffffffffu, acc[b], o);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      if (part == (b & (lpr - 1))) s_out[b * rows + i * (kUpThreads / lpr) + tid / lpr] = acc[b];
+      if (part == (b & (lpr - 1)) && row < kUpRows) s_out[b * kUpRows + row] = acc[b];
   }
   __syncthreads();
-  for (int i = tid; i < rows && row0 + i < A.rows; i += kUpThreads)
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-      if (b < n) {
-        const int64_t at = (int64_t)tok[b] * A.rows + row0 + i;
-        put(A, at, __ldcg(A.base + at) + s_out[b * rows + i]);
-      }
+  for (int q = 0; q < kUpRows / kUpThreads; ++q)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int i = tid + q * kUpThreads;
+      if (i < rows && b < n) put(A, (int64_t)tok[b] * A.rows + row0 + i, base[q][b] + s_out[b * kUpRows + i]);
+    }
 }
 
-// y = act(base + B h): a CTA is 16 KB of the adapter that its token leads, all of it in
-// flight at once and kept for all of its tokens; lanes lie side by side along a row, eight
-// ranks each, and the tokens' sums go through shared memory to come out row by row.
+// y = act(base + B h).  The (adapter in use, tile of its rows) pairs are dealt out in one
+// run of equal lengths per CTA, which streams its tiles, whole runs of memory, through a
+// ring of bulk copies; the first of them are issued before the wait.  Lanes lie side by
+// side along a row, and the tokens' sums go through shared memory to come out row by row.
 template <typename T>
-__global__ void __launch_bounds__(kUpThreads, 5) k_lora_up(LoraArgs A, int lpr) {
-  extern __shared__ float s_out[];     // [kAlong][rows of the CTA]
+__global__ void __launch_bounds__(kUpThreads, kUpCtas) k_lora_up(LoraArgs A, int lpr, int tile) {
+  extern __shared__ __align__(128) unsigned char sm[];
+  __shared__ uint64_t full[kUpStages];
+  __shared__ int s_adapter[32];
+  __shared__ uint32_t s_set[32];
   pdl_trigger();
-  int a;
-  uint32_t set = led_by(A, blockIdx.y, a);
-  const int tid = threadIdx.x, rows = up_rows<T>(lpr), row0 = blockIdx.x * rows, part = tid & (lpr - 1);
-  if (!set) {
-    pdl_wait();
-    return;
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kUpStages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
   }
-  if (a < 0) {                         // no adapter: the activation and the rounding are left to do
-    pdl_wait();
-    if (static_cast<const void *>(A.base) == A.y && !A.relu) return;
-    for (; set; set &= set - 1)
-      for (int i = tid; i < rows && row0 + i < A.rows; i += kUpThreads) {
-        const int64_t at = (int64_t)(__ffs(set) - 1) * A.rows + row0 + i;
+  int w = -1;
+  if (lane < A.B) w = ld_cg_i32(A.which + lane);
+  if (w >= A.adapters) {
+    if (blockIdx.x == 0) flag_error(A.err, kErrIndex);
+    w = -1;
+  }
+  w = max(w, -1);
+  const uint32_t same = __match_any_sync(0xffffffffu, w), tokens = A.B >= 32 ? 0xffffffffu : (1u << A.B) - 1u;
+  const bool leads = w >= 0 && __ffs(same) - 1 == lane;
+  const uint32_t leaders = __ballot_sync(0xffffffffu, leads), none = __ballot_sync(0xffffffffu, w < 0) & tokens;
+  if (tid < 32 && leads) {
+    const int at = __popc(leaders & ((1u << lane) - 1u));
+    s_adapter[at] = w;
+    s_set[at] = same;
+  }
+  __syncthreads();
+  const int tiles = (A.rows - 1) / tile + 1;
+  const int64_t total = (int64_t)__popc(leaders) * tiles, u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+  const int n = (int)(u1 - u0);
+  int lead = (int)(u0 / tiles), t = (int)(u0 - (int64_t)lead * tiles);   // of the copies, then of the sums
+  int next_lead = lead, next_t = t;
+  auto copy = [&](int i) {             // thread 0: pair i of the run
+    const int rows = min(tile, A.rows - next_t * tile);
+    const uint32_t bytes = (uint32_t)(rows * A.rank * (int)sizeof(T));
+    mbar_arrive_expect_tx(&full[i % kUpStages], bytes);
+    bulk_g2s(sm + (i % kUpStages) * kUpStage,
+             static_cast<const T *>(A.Bm) + ((int64_t)s_adapter[next_lead] * A.rows + (int64_t)next_t * tile) * A.rank, bytes,
+             &full[i % kUpStages]);
+    if (++next_t == tiles) {
+      next_t = 0;
+      ++next_lead;
+    }
+  };
+  if (tid == 0)
+    for (int i = 0; i < min(n, kUpStages); ++i) copy(i);
+  pdl_wait();
+  float *s_out = reinterpret_cast<float *>(sm + kUpStages * kUpStage);
+  int flip = 0;                        // of the two halves of s_out: one barrier between a use and the next but one
+  bool ok = true;
+  for (int i = 0; i < n && ok; ++i) {
+    ok = mbar_wait(&full[i % kUpStages], (uint32_t)(i / kUpStages) & 1u, kUpWaitNs);
+    ok = __syncthreads_and(ok);
+    if (!ok) {
+      if (tid == 0) {
+        flag_error(A.err, kErrTimeout);
+        // what is on its way lands before the shared memory is given back
+        for (int e = i; e < min(n, i + kUpStages); ++e) mbar_wait(&full[e % kUpStages], (uint32_t)(e / kUpStages) & 1u, kUpWaitNs);
+      }
+      break;
+    }
+    const T *rows_of_b = reinterpret_cast<const T *>(sm + (i % kUpStages) * kUpStage);
+    const int row0 = t * tile, rows = min(tile, A.rows - row0);
+    for (uint32_t set = s_set[lead]; set; flip ^= 1) {
+      float *out = s_out + flip * kAlong * kUpRows;
+      const int left = __popc(set);
+      if (left > 2) up_tokens<T, 4>(A, rows_of_b, row0, rows, lpr, set, out);
+      else if (left > 1) up_tokens<T, 2>(A, rows_of_b, row0, rows, lpr, set, out);
+      else up_tokens<T, 1>(A, rows_of_b, row0, rows, lpr, set, out);
+    }
+    if (tid == 0 && i + kUpStages < n) copy(i + kUpStages);              // the stage's last reads are before the last barrier
+    if (++t == tiles) {
+      t = 0;
+      ++lead;
+    }
+  }
+  // tokens without an adapter: the activation and the rounding are left to do
+  if (none && (A.relu || static_cast<const void *>(A.base) != A.y))
+    for (int64_t row = (int64_t)blockIdx.x * kUpThreads + tid; row < A.rows; row += (int64_t)gridDim.x * kUpThreads)
+      for (uint32_t set = none; set; set &= set - 1) {
+        const int64_t at = (int64_t)(__ffs(set) - 1) * A.rows + row;
         put(A, at, __ldcg(A.base + at));
       }
-    return;
-  }
-  Eight<T> w[up_steps<T>()];
-  const T *from = static_cast<const T *>(A.Bm) + (int64_t)a * A.rows * A.rank + part * 8;
-#pragma unroll
-  for (int i = 0; i < up_steps<T>(); ++i) {
-    const int row = row0 + i * (kUpThreads / lpr) + tid / lpr;
-    w[i].clear();
-    if (part * 8 < A.rank && row < A.rows) w[i].load(from + (int64_t)row * A.rank);
-  }
-  pdl_wait();
-  while (set) {
-    const int left = __popc(set);
-    if (left > 2) up_tokens<T, 4>(A, w, row0, lpr, set, s_out);
-    else if (left > 1) up_tokens<T, 2>(A, w, row0, lpr, set, s_out);
-    else up_tokens<T, 1>(A, w, row0, lpr, set, s_out);
-  }
 }
 
 // ------------------------------------------------------------------ host --
@@ -341,11 +382,13 @@ asf_status asf_w4_matmul_lora(const asf_w4_matrix *mat, const asf_lora *lora, co
   if (e != cudaSuccess) return ASF_ERR_CUDA;
   int lpr = 1;
   while (lpr * 8 < a.rank) lpr *= 2;
-  const int tile = xdtype == ASF_F16 ? up_rows<__half>(lpr) : up_rows<float>(lpr);
-  const dim3 grid((unsigned)(((int64_t)a.rows + tile - 1) / tile), B);
-  const size_t smem = (size_t)kAlong * tile * 4;
-  e = xdtype == ASF_F16 ? launch(k_lora_up<__half>, grid, dim3(kUpThreads), smem, st, a, lpr)
-                        : launch(k_lora_up<float>, grid, dim3(kUpThreads), smem, st, a, lpr);
+  // 16 KB a tile, or as much as leaves an SM one
+  const int64_t even = ((int64_t)a.rows * std::min(B, a.adapters) / sm_count() + 31) / 32 * 32;
+  const int tile = (int)std::min<int64_t>({kUpRows, kUpStage / (a.rank * (xdtype == ASF_F16 ? 2 : 4)), std::max<int64_t>(32, even)});
+  const int64_t pairs = ((int64_t)a.rows + tile - 1) / tile * std::min(B, a.adapters);
+  const dim3 grid((unsigned)std::min<int64_t>(std::max<int64_t>(pairs, 1), (int64_t)kUpCtas * sm_count()));
+  e = xdtype == ASF_F16 ? launch(k_lora_up<__half>, grid, dim3(kUpThreads), kUpSmem, st, a, lpr, tile)
+                        : launch(k_lora_up<float>, grid, dim3(kUpThreads), kUpSmem, st, a, lpr, tile);
   return cuda_status(e);
 }
 
