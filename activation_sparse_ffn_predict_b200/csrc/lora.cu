@@ -28,7 +28,6 @@ constexpr int kUpStages = 4, kUpStage = 16 * 1024;
 constexpr int kUpRows = 256;           // of a stage at most
 constexpr int kAlong = 4;              // tokens at a time
 constexpr uint64_t kUpWaitNs = 200ull * 1000 * 1000;   // bound on any mbarrier wait
-constexpr size_t kUpSmem = (size_t)kUpStages * kUpStage + 2 * kAlong * kUpRows * 4;
 
 struct LoraArgs {
   int adapters, rank, k, rows, B;
@@ -167,65 +166,55 @@ __device__ __forceinline__ void eight(const float *p, float (&v)[8]) {
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// NB tokens over `rows` rows of B in shared memory; lpr lanes a row, eight ranks each
+// NB of the leader's tokens, from its token number `from` on, over `rows` rows of B in
+// shared memory, a thread a row.  s_h: [token][2][rank / 2], the first four values of each
+// eight ranks and the last four.  A thread begins with its own eight ranks, so that eight
+// neighbours' 16 bytes of rows that lie a multiple of 128 bytes apart are in different banks.
 template <typename T, int NB>
-__device__ __forceinline__ void up_tokens(const LoraArgs &A, const T *w, int row0, int rows, int lpr, uint32_t &set, float *s_out) {
-  const int tid = threadIdx.x;
+__device__ __forceinline__ void up_tokens(const LoraArgs &A, const T *w, int row0, int rows, const float *s_h, uint32_t &set) {
   int tok[NB];
-  const int n = take<NB>(set, tok);
-  float base[kUpRows / kUpThreads][NB];            // on their way while the sums are made
-#pragma unroll
-  for (int q = 0; q < kUpRows / kUpThreads; ++q)
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-      base[q][b] = tid + q * kUpThreads < rows && b < n ? __ldcg(A.base + (int64_t)tok[b] * A.rows + row0 + tid + q * kUpThreads) : 0.f;
-  const int part = tid & (lpr - 1);
-  const bool in = part * 8 < A.rank;
-  float h[NB][8];
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      const float4 u = in ? *reinterpret_cast<const float4 *>(A.h + (int64_t)tok[b] * A.rank + part * 8 + e)
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-      h[b][e] = u.x; h[b][e + 1] = u.y; h[b][e + 2] = u.z; h[b][e + 3] = u.w;
-    }
-#pragma unroll 4
-  for (int row = tid / lpr; row < kUpRows; row += kUpThreads / lpr) {
-    if (row - tid / lpr >= rows) break;            // the same for all lanes
-    float v[8], acc[NB];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    if (in && row < rows) eight(w + row * A.rank + part * 8, v);
+  const int n = take<NB>(set, tok), eights = A.rank / 8;
+  const int g = eights & -eights, rot = (threadIdx.x & 7) * min(g, 8) >> 3;
+  for (int row = threadIdx.x; row < rows; row += kUpThreads) {
+    float base[NB], acc[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
+      base[b] = b < n ? __ldcg(A.base + (int64_t)tok[b] * A.rows + row0 + row) : 0.f;   // on its way while the sum is made
       acc[b] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[b] = fmaf(v[e], h[b][e], acc[b]);
     }
-    for (int o = lpr / 2; o > 0; o >>= 1)
+    const T *wr = w + row * A.rank;
+    int c = rot;
+#pragma unroll 4
+    for (int i = 0; i < eights; ++i) {
+      float v[8];
+      eight(wr + c * 8, v);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) acc[b] += __shfl_xor_sync(0xffffffffu, acc[b], o);
+      for (int b = 0; b < NB; ++b) {
+        const float *h = s_h + (b < n ? b : 0) * A.rank + c * 4;
+        const float4 p = *reinterpret_cast<const float4 *>(h), q = *reinterpret_cast<const float4 *>(h + A.rank / 2);
+        float d = v[0] * p.x;
+        d = fmaf(v[1], p.y, d);
+        d = fmaf(v[2], p.z, d);
+        d = fmaf(v[3], p.w, d);
+        d = fmaf(v[4], q.x, d);
+        d = fmaf(v[5], q.y, d);
+        d = fmaf(v[6], q.z, d);
+        d = fmaf(v[7], q.w, d);
+        acc[b] += d;
+      }
+      if (++c == eights) c = 0;
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      if (part == (b & (lpr - 1)) && row < kUpRows) s_out[b * kUpRows + row] = acc[b];
+      if (b < n) put(A, (int64_t)tok[b] * A.rows + row0 + row, base[b] + acc[b]);
   }
-  __syncthreads();
-#pragma unroll
-  for (int q = 0; q < kUpRows / kUpThreads; ++q)
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int i = tid + q * kUpThreads;
-      if (i < rows && b < n) put(A, (int64_t)tok[b] * A.rows + row0 + i, base[q][b] + s_out[b * kUpRows + i]);
-    }
 }
 
 // y = act(base + B h).  The (adapter in use, tile of its rows) pairs are dealt out in one
 // run of equal lengths per CTA, which streams its tiles, whole runs of memory, through a
-// ring of bulk copies; the first of them are issued before the wait.  Lanes lie side by
-// side along a row, and the tokens' sums go through shared memory to come out row by row.
+// ring of bulk copies; the first of them are issued before the wait.
 template <typename T>
-__global__ void __launch_bounds__(kUpThreads, kUpCtas) k_lora_up(LoraArgs A, int lpr, int tile) {
+__global__ void __launch_bounds__(kUpThreads, kUpCtas) k_lora_up(LoraArgs A, int tile) {
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ uint64_t full[kUpStages];
   __shared__ int s_adapter[32];
@@ -272,10 +261,20 @@ __global__ void __launch_bounds__(kUpThreads, kUpCtas) k_lora_up(LoraArgs A, int
   if (tid == 0)
     for (int i = 0; i < min(n, kUpStages); ++i) copy(i);
   pdl_wait();
-  float *s_out = reinterpret_cast<float *>(sm + kUpStages * kUpStage);
-  int flip = 0;                        // of the two halves of s_out: one barrier between a use and the next but one
+  float *s_h = reinterpret_cast<float *>(sm + kUpStages * kUpStage);   // of the tokens that `there` leads
+  int there = -1;
   bool ok = true;
   for (int i = 0; i < n && ok; ++i) {
+    uint32_t set = s_set[lead];
+    if (lead != there) {
+      const int quads = A.rank / 4, all = __popc(set) * quads;
+      for (int j = tid; j < all; j += kUpThreads) {
+        const int b = j / quads, q = j - b * quads, tok = __fns(set, 0, b + 1);
+        *reinterpret_cast<float4 *>(s_h + b * A.rank + (q & 1) * (A.rank / 2) + (q >> 1) * 4) =
+            __ldcg(reinterpret_cast<const float4 *>(A.h + (int64_t)tok * A.rank) + q);
+      }
+      there = lead;
+    }
     ok = mbar_wait(&full[i % kUpStages], (uint32_t)(i / kUpStages) & 1u, kUpWaitNs);
     ok = __syncthreads_and(ok);
     if (!ok) {
@@ -288,14 +287,14 @@ __global__ void __launch_bounds__(kUpThreads, kUpCtas) k_lora_up(LoraArgs A, int
     }
     const T *rows_of_b = reinterpret_cast<const T *>(sm + (i % kUpStages) * kUpStage);
     const int row0 = t * tile, rows = min(tile, A.rows - row0);
-    for (uint32_t set = s_set[lead]; set; flip ^= 1) {
-      float *out = s_out + flip * kAlong * kUpRows;
+    for (const float *h = s_h; set; h += kAlong * A.rank) {
       const int left = __popc(set);
-      if (left > 2) up_tokens<T, 4>(A, rows_of_b, row0, rows, lpr, set, out);
-      else if (left > 1) up_tokens<T, 2>(A, rows_of_b, row0, rows, lpr, set, out);
-      else up_tokens<T, 1>(A, rows_of_b, row0, rows, lpr, set, out);
+      if (left > 2) up_tokens<T, 4>(A, rows_of_b, row0, rows, h, set);
+      else if (left > 1) up_tokens<T, 2>(A, rows_of_b, row0, rows, h, set);
+      else up_tokens<T, 1>(A, rows_of_b, row0, rows, h, set);
     }
-    if (tid == 0 && i + kUpStages < n) copy(i + kUpStages);              // the stage's last reads are before the last barrier
+    __syncthreads();                   // the stage and the values of h have been read
+    if (tid == 0 && i + kUpStages < n) copy(i + kUpStages);
     if (++t == tiles) {
       t = 0;
       ++lead;
@@ -380,15 +379,14 @@ asf_status asf_w4_matmul_lora(const asf_w4_matrix *mat, const asf_lora *lora, co
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = xdtype == ASF_F16 ? run_down<__half>(a, st) : run_down<float>(a, st);
   if (e != cudaSuccess) return ASF_ERR_CUDA;
-  int lpr = 1;
-  while (lpr * 8 < a.rank) lpr *= 2;
   // 16 KB a tile, or as much as leaves an SM one
   const int64_t even = ((int64_t)a.rows * std::min(B, a.adapters) / sm_count() + 31) / 32 * 32;
   const int tile = (int)std::min<int64_t>({kUpRows, kUpStage / (a.rank * (xdtype == ASF_F16 ? 2 : 4)), std::max<int64_t>(32, even)});
   const int64_t pairs = ((int64_t)a.rows + tile - 1) / tile * std::min(B, a.adapters);
   const dim3 grid((unsigned)std::min<int64_t>(std::max<int64_t>(pairs, 1), (int64_t)kUpCtas * sm_count()));
-  e = xdtype == ASF_F16 ? launch(k_lora_up<__half>, grid, dim3(kUpThreads), kUpSmem, st, a, lpr, tile)
-                        : launch(k_lora_up<float>, grid, dim3(kUpThreads), kUpSmem, st, a, lpr, tile);
+  const size_t smem = (size_t)kUpStages * kUpStage + (size_t)B * a.rank * 4;
+  e = xdtype == ASF_F16 ? launch(k_lora_up<__half>, grid, dim3(kUpThreads), smem, st, a, tile)
+                        : launch(k_lora_up<float>, grid, dim3(kUpThreads), smem, st, a, tile);
   return cuda_status(e);
 }
 
