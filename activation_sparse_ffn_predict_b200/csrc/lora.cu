@@ -107,7 +107,7 @@ __device__ __forceinline__ void down_rows(const LoraArgs &A, int a, int row0, ui
   float acc[RW * NB];
 #pragma unroll
   for (int i = 0; i < RW * NB; ++i) acc[i] = 0.f;
-#pragma unroll(RW * NB == 1 ? 4 : NB == 1 ? 2 : 1)
+#pragma unroll(NB == 1 ? 4 : NB == 2 && RW == 4 ? 2 : NB == 2 ? 4 : RW == 4 ? 2 : 1)
   for (int i = tid * E; i < A.k; i += kDownThreads * E) {
     uint4 wv[RW], xv[NB];
 #pragma unroll
@@ -138,7 +138,7 @@ __device__ __forceinline__ void down_rows(const LoraArgs &A, int a, int row0, ui
 
 // h = s A x: a CTA is RW rows of the adapter that its token leads, over all of k.
 template <typename T, int RW>
-__global__ void __launch_bounds__(kDownThreads, 8) k_lora_down(LoraArgs A) {
+__global__ void __launch_bounds__(kDownThreads, RW == 1 ? 8 : 4) k_lora_down(LoraArgs A) {
   __shared__ float s_red[kDownThreads / 32 * RW * kAlong];
   pdl_trigger();
   int a;
