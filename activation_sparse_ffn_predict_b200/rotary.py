@@ -52,16 +52,18 @@ class Rotary:
         self._ref = ctypes.byref(self.desc)
 
 
-def _rows(t: torch.Tensor, name: str, device, dtype):
-    """Address of [T, heads, head_dim] whose heads are contiguous, and its strides (never read for a dimension of one)."""
+def _rows(t: torch.Tensor, name: str, device, dtype, of):
+    """Address of a tensor of the shape `of`, [T, heads, head_dim] with its last dimension contiguous, and its
+    token and head strides (never read for a dimension of one)."""
     if not isinstance(t, torch.Tensor) or t.get_device() != device.index:
         raise ValueError(f"{name} must be a tensor on {device}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    st, of = t.stride(), t.shape
-    if st[2] != 1 and of[2] != 1:
+    token, head, one = t.stride()
+    T, heads, D = of
+    if one != 1 and D != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t.data_ptr(), st[0] if of[0] > 1 else of[1] * of[2], st[1] if of[1] > 1 else of[2]
+    return t.data_ptr(), token if T > 1 else heads * D, head if heads > 1 else D
 
 
 def asf_rotary_apply(rot: Rotary, x: torch.Tensor, pos: torch.Tensor, y: torch.Tensor, stream=None) -> None:
@@ -71,14 +73,17 @@ def asf_rotary_apply(rot: Rotary, x: torch.Tensor, pos: torch.Tensor, y: torch.T
     of = x.shape
     if len(of) != 3 or of[2] != rot.head_dim or y.shape != of:
         raise ValueError("x and y must be [T, heads, head_dim]")
-    if x.dtype not in _DT:
+    dt = x.dtype
+    code = _DT.get(dt)
+    if code is None:
         raise ValueError("x must be float16 or float32")
-    if pos.shape != of[:1]:
+    n = pos.shape
+    if len(n) != 1 or n[0] != of[0]:
         raise ValueError("pos must be [T]")
     dev = rot.device
-    xp, xt, xh = _rows(x, "x", dev, x.dtype)
-    yp, yt, yh = _rows(y, "y", dev, x.dtype)
-    _invoke("asf_rotary_apply", dev, stream, rot._ref, xp, _DT[x.dtype], of[0], of[1], xt, xh,
+    xp, xt, xh = _rows(x, "x", dev, dt, of)
+    yp, yt, yh = _rows(y, "y", dev, dt, of)
+    _invoke("asf_rotary_apply", dev, stream, rot._ref, xp, code, of[0], of[1], xt, xh,
             _arg(pos, "pos", dev, torch.int32), yp, yt, yh)
 
 
@@ -93,18 +98,17 @@ def asf_rotary_append(rot: Rotary, cache: KVCache, table: torch.Tensor, lens: to
         raise ValueError("q and q_out must be [T, q_heads, head_dim]")
     if len(kv) != 3 or kv[0] != of[0] or kv[1] != cache.heads or kv[2] != cache.head_dim or v.shape != kv:
         raise ValueError("k and v must be [T, heads, head_dim]")
-    if pos.shape != of[:1]:
+    n = pos.shape
+    if len(n) != 1 or n[0] != of[0]:
         raise ValueError("pos must be [T]")
-    dev, f16 = cache.device, torch.float16
-    if rot.device != dev:
+    dev, f16, D = cache.device, torch.float16, cache.head_dim
+    if rot.device.index != dev.index:
         raise ValueError(f"the rotary table must be on {dev}")
     req = _requests(cache, table, lens, begin)
-    ptrs = []
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        p, token, head = _rows(t, name, dev, f16)
-        if head != cache.head_dim:
-            raise ValueError(f"{name}'s heads must be contiguous")
-        ptrs.append((p, token))
-    (qp, qs), (kp, ks), (vp, vs) = ptrs
+    qp, qs, qh = _rows(q, "q", dev, f16, of)
+    kp, ks, kh = _rows(k, "k", dev, f16, kv)
+    vp, vs, vh = _rows(v, "v", dev, f16, kv)
+    if qh != D or kh != D or vh != D:
+        raise ValueError("the heads of q, k and v must be contiguous")
     _invoke("asf_rotary_append", dev, stream, rot._ref, cache._ref, *req, of[0], _arg(pos, "pos", dev, torch.int32), of[1],
             qp, qs, _arg(q_out, "q_out", dev, f16), kp, ks, vp, vs, ws.on(dev), ws.nbytes)

@@ -139,11 +139,11 @@ def asf_w4_dequantize(mat: W4Matrix, dst: torch.Tensor, stream=None) -> None:
 
 
 def _product(mat: W4Matrix, x, y, bias, relu):
-    xt, yt, of = _DT.get(x.dtype), _DT.get(y.dtype), x.shape
+    xt, yt, of, to = _DT.get(x.dtype), _DT.get(y.dtype), x.shape, y.shape
     if xt is None or len(of) != 2 or of[1] != mat.k:
         raise ValueError("x must be [B, k], float16 or float32")
     B = of[0]
-    if yt is None or y.shape != (B, mat.rows):
+    if yt is None or len(to) != 2 or to[0] != B or to[1] != mat.rows:
         raise ValueError("y must be [B, rows], float16 or float32")
     dev = mat.device
     bp = None
@@ -164,10 +164,10 @@ def asf_w4_matmul_lora(mat: W4Matrix, lora: LoraSet, which: torch.Tensor, x: tor
                        bias: Optional[torch.Tensor] = None, relu: bool = False, stream=None) -> None:
     """asf_w4_matmul with each token's own adapter beside it: which int32 [B], negative for none; x in the
     adapters' dtype.  ws: Workspace.for_w4(mat, B, lora=lora)."""
-    args = _product(mat, x, y, bias, relu)
-    if which.shape != x.shape[:1]:
+    args, n = _product(mat, x, y, bias, relu), which.shape
+    if len(n) != 1 or n[0] != args[2]:
         raise ValueError("which must be [B]")
-    if lora.device != mat.device or x.dtype is not lora.dtype:
+    if lora.device.index != mat.device.index or x.dtype is not lora.dtype:
         raise ValueError(f"the adapters must be on {mat.device} and in x's dtype")
     _invoke("asf_w4_matmul_lora", mat.device, stream, mat._ref, lora._ref, _arg(which, "which", mat.device, torch.int32),
             *args, ws.on(mat.device), ws.nbytes)
