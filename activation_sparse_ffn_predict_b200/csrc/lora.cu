@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kDownThreads = 128;
 constexpr int kUpThreads = 128;
-constexpr int kUpCtas = 3;             // of an SM
+constexpr int kUpCtas = 3;             // of an SM, where its shared memory holds them
 constexpr int kUpStages = 4, kUpStage = 16 * 1024;
 constexpr int kUpRows = 256;           // of a stage at most
 constexpr int kAlong = 4;              // tokens at a time
@@ -383,8 +383,9 @@ asf_status asf_w4_matmul_lora(const asf_w4_matrix *mat, const asf_lora *lora, co
   const int64_t even = ((int64_t)a.rows * std::min(B, a.adapters) / sm_count() + 31) / 32 * 32;
   const int tile = (int)std::min<int64_t>({kUpRows, kUpStage / (a.rank * (xdtype == ASF_F16 ? 2 : 4)), std::max<int64_t>(32, even)});
   const int64_t pairs = ((int64_t)a.rows + tile - 1) / tile * std::min(B, a.adapters);
-  const dim3 grid((unsigned)std::min<int64_t>(std::max<int64_t>(pairs, 1), (int64_t)kUpCtas * sm_count()));
   const size_t smem = (size_t)kUpStages * kUpStage + (size_t)B * a.rank * 4;
+  const int ctas = smem <= 75 * 1024 ? kUpCtas : 2;                      // as many as an SM's shared memory holds
+  const dim3 grid((unsigned)std::min<int64_t>(std::max<int64_t>(pairs, 1), (int64_t)ctas * sm_count()));
   e = xdtype == ASF_F16 ? launch(k_lora_up<__half>, grid, dim3(kUpThreads), smem, st, a, tile)
                         : launch(k_lora_up<float>, grid, dim3(kUpThreads), smem, st, a, tile);
   return cuda_status(e);

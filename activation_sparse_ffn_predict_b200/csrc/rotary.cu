@@ -332,7 +332,7 @@ asf_status asf_rotary_apply(const asf_rotary *rot, const void *x, asf_dtype dtyp
   a.hs = (int)std::min<int64_t>(heads, std::max<int64_t>(1, kRotThreads * (chunks < wave ? 1 : kItems) / per));
   if (a.hs == heads)
     a.tb = (int)std::max<int64_t>(1, std::min<int64_t>({8, (int64_t)kRotThreads * kItems / (heads * per), chunks / wave}));
-  const dim3 grid((unsigned)((T + a.tb - 1) / a.tb), (unsigned)((heads + a.hs - 1) / a.hs));
+  const dim3 grid((unsigned)(((int64_t)T + a.tb - 1) / a.tb), (unsigned)((heads + a.hs - 1) / a.hs));
   const size_t smem = (size_t)a.tb * half * sizeof(float2);
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
