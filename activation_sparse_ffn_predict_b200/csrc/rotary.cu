@@ -51,18 +51,59 @@ __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
 __device__ __forceinline__ void from_f(float v, float &to) { to = v; }
 __device__ __forceinline__ void from_f(float v, __half &to) { to = __float2half_rn(v); }
 
-// VEC pairs of a head: halves are `half` columns apart, neighbours side by side.
+// Columns of an access to what passes: as many as VEC pairs have, 16 bytes at most.
+template <typename T, int VEC>
+__host__ __device__ constexpr int pass_columns() { return 2 * VEC * sizeof(T) <= 16 ? 2 * VEC : VEC; }
+
+// VEC pairs of a head: halves are `half` columns apart, neighbours side by side (one
+// access where they are 16 bytes at most).
 template <typename T, int VEC, bool PAIRS>
 struct Pairs {
   Pack<T, VEC> a, b;
+  static constexpr int kPass = pass_columns<T, VEC>();
+  static constexpr bool kOne = PAIRS && kPass == 2 * VEC;
   __device__ __forceinline__ static int second(int j, int half) { return PAIRS ? 2 * j * VEC + VEC : half + j * VEC; }
   __device__ __forceinline__ void load(const T *row, int j, int half) {
-    a = *reinterpret_cast<const Pack<T, VEC> *>(row + (PAIRS ? 2 : 1) * j * VEC);
-    b = *reinterpret_cast<const Pack<T, VEC> *>(row + second(j, half));
+    if constexpr (kOne) {
+      load_pass(row + 2 * j * VEC);
+    } else {
+      a = *reinterpret_cast<const Pack<T, VEC> *>(row + (PAIRS ? 2 : 1) * j * VEC);
+      b = *reinterpret_cast<const Pack<T, VEC> *>(row + second(j, half));
+    }
   }
   __device__ __forceinline__ void store(T *row, int j, int half) const {
-    *reinterpret_cast<Pack<T, VEC> *>(row + (PAIRS ? 2 : 1) * j * VEC) = a;
-    *reinterpret_cast<Pack<T, VEC> *>(row + second(j, half)) = b;
+    if constexpr (kOne) {
+      store_pass(row + 2 * j * VEC);
+    } else {
+      *reinterpret_cast<Pack<T, VEC> *>(row + (PAIRS ? 2 : 1) * j * VEC) = a;
+      *reinterpret_cast<Pack<T, VEC> *>(row + second(j, half)) = b;
+    }
+  }
+  // kPass columns, as they are
+  __device__ __forceinline__ void load_pass(const T *p) {
+    if constexpr (kPass == VEC) {
+      a = *reinterpret_cast<const Pack<T, VEC> *>(p);
+    } else {
+      const Pack<T, kPass> u = *reinterpret_cast<const Pack<T, kPass> *>(p);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        a.v[i] = u.v[i];
+        b.v[i] = u.v[VEC + i];
+      }
+    }
+  }
+  __device__ __forceinline__ void store_pass(T *p) const {
+    if constexpr (kPass == VEC) {
+      *reinterpret_cast<Pack<T, VEC> *>(p) = a;
+    } else {
+      Pack<T, kPass> u;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        u.v[i] = a.v[i];
+        u.v[VEC + i] = b.v[i];
+      }
+      *reinterpret_cast<Pack<T, kPass> *>(p) = u;
+    }
   }
   // cs[i]: cos and sin of the i-th pair
   __device__ __forceinline__ void turn(const float2 *cs) {
@@ -107,7 +148,8 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary(RotArgs A) {
   pdl_trigger();
   const int t0 = blockIdx.x * A.tb, nt = min(A.tb, A.T - t0);
   const int h0 = blockIdx.y * A.hs, nh = min(A.hs, A.heads - h0);
-  const int turned = A.half / VEC, per = turned + (A.copy ? (A.D - 2 * A.half) / VEC : 0);
+  constexpr int kPass = pass_columns<T, VEC>();
+  const int turned = A.half / VEC, per = turned + (A.copy ? (A.D - 2 * A.half) / kPass : 0);
   const int lanes = min(per, kRotThreads), step = kRotThreads / lanes, rows = nt * nh;
   const int row0 = threadIdx.x / lanes, c0 = threadIdx.x - row0 * lanes;
   const T *x = static_cast<const T *>(A.x) + t0 * A.xt + h0 * A.xh;
@@ -117,7 +159,7 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary(RotArgs A) {
   for (int c = c0; c < per; c += lanes) {              // c0 < lanes <= per: every thread is here once at least
     int t = row0 / nh, h = row0 - t * nh, row = row0 < step ? row0 : rows;
     const bool turns = c < turned;
-    const int at = 2 * A.half + (c - turned) * VEC;
+    const int at = 2 * A.half + (c - turned) * kPass;
     do {
       Pairs<T, VEC, PAIRS> v[kAhead];
       int64_t to[kAhead];
@@ -130,7 +172,7 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary(RotArgs A) {
           tok[i] = t;
           const T *from = x + (t * A.xt + h * A.xh);
           if (turns) v[i].load(from, c, A.half);
-          else v[i].a = *reinterpret_cast<const Pack<T, VEC> *>(from + at);
+          else v[i].load_pass(from + at);
         }
         row += step;
         h += dh;
@@ -155,7 +197,7 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary(RotArgs A) {
           v[i].turn(s_cs + tok[i] * A.half + c * VEC);
           v[i].store(y + to[i], c, A.half);
         } else {
-          *reinterpret_cast<Pack<T, VEC> *>(y + to[i] + at) = v[i].a;
+          v[i].store_pass(y + to[i] + at);
         }
       }
     } while (row < rows);
@@ -176,14 +218,14 @@ struct RotAppendArgs {
   int32_t *err;
 };
 
-// A thread takes VEC pairs, or VEC columns that pass, of a token's query or key
+// A thread takes VEC pairs, or as many columns that pass, of a token's query or key
 // head, or 16 bytes of its value head.  Latency bounds it: positions and ranges,
 // then the table, then the store.
 template <int VEC, bool PAIRS>
 __global__ void __launch_bounds__(128) k_rotary_append(RotAppendArgs A) {
   pdl_wait();
   pdl_trigger();
-  const int D = A.c.head_dim, turned = A.half / VEC, per = turned + (D - 2 * A.half) / VEC;
+  const int D = A.c.head_dim, turned = A.half / VEC, kPass = pass_columns<__half, VEC>(), per = turned + (D - 2 * A.half) / kPass;
   const int qk = (A.q_heads + A.c.heads) * per, each = qk + A.c.heads * (D / 8), total = A.T * each;
   const int i = blockIdx.x * blockDim.x + threadIdx.x, at = min(i, total - 1);
   const int tok = at / each, in = at - tok * each;
@@ -196,11 +238,11 @@ __global__ void __launch_bounds__(128) k_rotary_append(RotAppendArgs A) {
   const __half *from = (value ? A.v + tok * A.vt : query ? A.q + tok * A.qt : A.k + tok * A.kt) + (int64_t)head * D;
   Pairs<__half, VEC, PAIRS> x;
   uint4 whole = make_uint4(0, 0, 0, 0);
-  const int col = value ? c * 8 : 2 * A.half + (c - turned) * VEC;
+  const int col = value ? c * 8 : 2 * A.half + (c - turned) * kPass;
   const bool turns = !value && c < turned;
   if (value) whole = *reinterpret_cast<const uint4 *>(from + col);
   else if (turns) x.load(from, c, A.half);
-  else x.a = *reinterpret_cast<const Pack<__half, VEC> *>(from + col);
+  else x.load_pass(from + col);
   const Place w = place_of(A.lens, A.begin, A.R, A.T, tok, A.err, i == 0);
   if (i >= total || w.r < 0) return;   // behind the last range: nothing is written
   __half *to = A.qo + ((int64_t)tok * A.q_heads + head) * D;
@@ -225,7 +267,7 @@ __global__ void __launch_bounds__(128) k_rotary_append(RotAppendArgs A) {
     x.turn(cs);
     x.store(to, c, A.half);
   } else {
-    *reinterpret_cast<Pack<__half, VEC> *>(to + col) = x.a;
+    x.store_pass(to + col);
   }
 }
 
@@ -327,7 +369,8 @@ asf_status asf_rotary_apply(const asf_rotary *rot, const void *x, asf_dtype dtyp
   const int half = rot->rot_dim / 2, vec = pairs_of(half, per16);
   RotArgs a{x, y, x_token_stride, x_head_stride, y_token_stride, y_head_stride, T, heads, D, half, rot->turns, rot->scale,
             pos, 1, heads, !in_place};
-  const int64_t per = half / vec + (in_place ? 0 : (D - 2 * half) / vec);
+  const int pass = 2 * vec <= per16 ? 2 * vec : vec;
+  const int64_t per = half / vec + (in_place ? 0 : (D - 2 * half) / pass);
   const int64_t chunks = (int64_t)T * heads * per, wave = (int64_t)sm_count() * 2048 * 2;
   a.hs = (int)std::min<int64_t>(heads, std::max<int64_t>(1, kRotThreads * (chunks < wave ? 1 : kItems) / per));
   if (a.hs == heads)
@@ -376,7 +419,7 @@ asf_status asf_rotary_append(const asf_rotary *rot, const asf_kv_cache *cache, c
                   static_cast<const __half *>(q), static_cast<const __half *>(k), static_cast<const __half *>(v),
                   q_stride, k_stride, v_stride, static_cast<__half *>(q_out), &static_cast<Header *>(ws)->err};
   const int vec = pairs_of(a.half, 4);
-  const int64_t items = T * ((q_heads + cache->heads) * (int64_t)(a.half / vec + (D - 2 * a.half) / vec) + cache->heads * (D / 8));
+  const int64_t items = T * ((q_heads + cache->heads) * (int64_t)(a.half / vec + (D - 2 * a.half) / (2 * vec)) + cache->heads * (D / 8));
   if (items > INT32_MAX) return ASF_ERR_UNSUPPORTED;
   cudaStream_t st = (cudaStream_t)stream;
   return cuda_status(vec == 4   ? run_append<4>(a, rot->layout, items, st)
