@@ -2,7 +2,7 @@
 // (include/asffn.h, "Rotary positions").
 //
 //   asf_rotary_frequencies, asf_rotary_turns   host
-//   asf_rotary_apply                           k_rotary
+//   asf_rotary_apply                           k_rotary, k_rotary_odd
 //   asf_rotary_append                          k_rotary_append
 //
 // Mathematics.  Pair j of a head at position p turns by p f_j radians,
@@ -27,10 +27,11 @@ using namespace asf;
 namespace {
 
 constexpr int kRotThreads = 128;
-// Chunks that a thread has in flight: where they are 16 bytes, the threads of an SM are
-// enough with one (8192 tokens x 72 heads of 128 columns in fp16, us with 4, 2 and 1: 79, 60, 57).
-template <typename T, int VEC>
-__host__ __device__ constexpr int ahead() { return VEC * sizeof(T) == 16 ? 1 : 4; }
+// Places of a head that a thread has in flight, of 32 bytes (halves) or 16 (pairs): more are
+// slower, the threads of an SM are enough (8192 tokens x 72 heads of 128 columns in fp16,
+// halves, us with 4, 2 and 1: 79, 60, 57).
+constexpr int kAheadHalf = 1, kAheadPairs = 2;
+static_assert(ASF_MAX_ROTARY_DIM / 4 <= kRotThreads, "a head's places are a CTA's");
 constexpr int kItems = 9;              // chunks of a thread where there is work for every SM
 
 __device__ __forceinline__ float2 cos_sin(int pos, uint64_t turns, float mul) {
@@ -55,7 +56,7 @@ __device__ __forceinline__ void from_f(float v, __half &to) { to = __float2half_
 template <typename T, int VEC>
 __host__ __device__ constexpr int pass_columns() { return 2 * VEC * sizeof(T) <= 16 ? 2 * VEC : VEC; }
 
-// VEC pairs of a head: halves are `half` columns apart, neighbours side by side (one
+// (k_rotary_append) VEC pairs of a head: halves are `half` columns apart, neighbours side by side (one
 // access where they are 16 bytes at most).
 template <typename T, int VEC, bool PAIRS>
 struct Pairs {
@@ -135,72 +136,144 @@ struct RotArgs {
   bool copy;                           // the columns from rot_dim on, too
 };
 
+template <typename T>
+using Chunk = Pack<T, 16 / (int)sizeof(T)>;
+
+// cosines and sines of the CTA's tokens
+__device__ __forceinline__ void all_angles(const RotArgs &A, int t0, int nt, float2 *cs) {
+  for (int i = threadIdx.x; i < nt * A.half; i += kRotThreads) {
+    const int k = i / A.half;
+    cs[i] = cos_sin(A.pos[t0 + k], A.turns[i - k * A.half], A.mul);
+  }
+  __syncthreads();
+}
+
 // A CTA takes tb tokens and hs of their heads: each token's cosines and sines
 // are computed once a CTA, into shared memory, while the first chunks are on
 // their way; then a thread keeps one place in a head, and steps from head to head.
+// A place is 16 bytes of neighbours (those behind rot_dim keep their bits), or 16 of
+// each half where the halves are whole 16 bytes; k_rotary_odd takes the others.
 // HBM bounds it on long prompts: 8192 tokens x 72 heads of 128 columns in fp16, 302 MB
 // in 57 us, 5.3 TB/s.
-template <typename T, int VEC, bool PAIRS>
+template <typename T, bool PAIRS>
 __global__ void __launch_bounds__(kRotThreads) k_rotary(RotArgs A) {
-  constexpr int kAhead = ahead<T, VEC>();
+  constexpr int U = 16 / (int)sizeof(T), kAhead = PAIRS ? kAheadPairs : kAheadHalf;
   extern __shared__ float2 s_cs[];     // [tb][half]
   pdl_wait();
   pdl_trigger();
   const int t0 = blockIdx.x * A.tb, nt = min(A.tb, A.T - t0);
   const int h0 = blockIdx.y * A.hs, nh = min(A.hs, A.heads - h0);
-  constexpr int kPass = pass_columns<T, VEC>();
-  const int turned = A.half / VEC, per = turned + (A.copy ? (A.D - 2 * A.half) / kPass : 0);
-  const int lanes = min(per, kRotThreads), step = kRotThreads / lanes, rows = nt * nh;
-  const int row0 = threadIdx.x / lanes, c0 = threadIdx.x - row0 * lanes;
-  const T *x = static_cast<const T *>(A.x) + t0 * A.xt + h0 * A.xh;
-  T *y = static_cast<T *>(A.y) + t0 * A.yt + h0 * A.yh;
+  const int turned = PAIRS ? (2 * A.half + U - 1) / U : A.half / U;
+  const int per = !A.copy ? turned : PAIRS ? A.D / U : turned + (A.D - 2 * A.half) / U;   // at most kRotThreads
+  const int step = kRotThreads / per, rows = nt * nh;
+  const int row0 = threadIdx.x / per, c = threadIdx.x - row0 * per;
+  const bool turns = c < turned;
+  const int at = PAIRS || turns ? c * U : 2 * A.half + (c - turned) * U;
+  const T *x = static_cast<const T *>(A.x) + t0 * A.xt + h0 * A.xh + at;
+  T *y = static_cast<T *>(A.y) + t0 * A.yt + h0 * A.yh + at;
   const int dt = step / nh, dh = step - dt * nh;
+  int t = row0 / nh, h = row0 - t * nh, row = row0 < step ? row0 : rows;
   bool fresh = true;
-  for (int c = c0; c < per; c += lanes) {              // c0 < lanes <= per: every thread is here once at least
-    int t = row0 / nh, h = row0 - t * nh, row = row0 < step ? row0 : rows;
-    const bool turns = c < turned;
-    const int at = 2 * A.half + (c - turned) * kPass;
-    do {
-      Pairs<T, VEC, PAIRS> v[kAhead];
-      int64_t to[kAhead];
-      int tok[kAhead];
+  do {
+    Chunk<T> a[kAhead], b[PAIRS ? 1 : kAhead];
+    int64_t to[kAhead];
+    int tok[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        to[i] = -1;
-        if (row < rows) {
-          to[i] = t * A.yt + h * A.yh;
-          tok[i] = t;
-          const T *from = x + (t * A.xt + h * A.xh);
-          if (turns) v[i].load(from, c, A.half);
-          else v[i].load_pass(from + at);
-        }
-        row += step;
-        h += dh;
-        t += dt;
-        if (h >= nh) {
-          h -= nh;
-          ++t;
-        }
+    for (int i = 0; i < kAhead; ++i) {
+      to[i] = -1;
+      if (row < rows) {
+        to[i] = t * A.yt + h * A.yh;
+        tok[i] = t;
+        const T *from = x + (t * A.xt + h * A.xh);
+        a[i] = *reinterpret_cast<const Chunk<T> *>(from);
+        if constexpr (!PAIRS)
+          if (turns) b[i] = *reinterpret_cast<const Chunk<T> *>(from + A.half);
       }
-      if (fresh) {
-        for (int i = threadIdx.x; i < nt * A.half; i += kRotThreads) {
-          const int k = i / A.half;
-          s_cs[i] = cos_sin(A.pos[t0 + k], A.turns[i - k * A.half], A.mul);
-        }
-        __syncthreads();
-        fresh = false;
+      row += step;
+      h += dh;
+      t += dt;
+      if (h >= nh) {
+        h -= nh;
+        ++t;
       }
+    }
+    if (fresh) all_angles(A, t0, nt, s_cs);        // every thread is here once at least
+    fresh = false;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (to[i] < 0) continue;
-        if (turns) {
-          v[i].turn(s_cs + tok[i] * A.half + c * VEC);
-          v[i].store(y + to[i], c, A.half);
-        } else {
-          v[i].store_pass(y + to[i] + at);
+    for (int i = 0; i < kAhead; ++i) {
+      if (to[i] < 0) continue;
+      if (turns) {
+        const float2 *cs = s_cs + tok[i] * A.half + (PAIRS ? c * (U / 2) : c * U);
+#pragma unroll
+        for (int j = 0; j < (PAIRS ? U / 2 : U); ++j) {
+          if (PAIRS && c * (U / 2) + j >= A.half) break;
+          T &u = a[i].v[PAIRS ? 2 * j : j], &w = PAIRS ? a[i].v[(2 * j + 1) % U] : b[PAIRS ? 0 : i].v[j];
+          const float fu = to_f(u), fw = to_f(w), cv = cs[j].x, sv = cs[j].y;
+          from_f(fmaf(fu, cv, -(fw * sv)), u);
+          from_f(fmaf(fw, cv, fu * sv), w);
         }
+        if constexpr (!PAIRS) *reinterpret_cast<Chunk<T> *>(y + to[i] + A.half) = b[i];
       }
-    } while (row < rows);
+      *reinterpret_cast<Chunk<T> *>(y + to[i]) = a[i];
+    }
+  } while (row < rows);
+}
+
+// Halves that are not whole 16 bytes: a thread has 16 bytes of a head, and finds the
+// other halves of its pairs in shared memory, where the CTA lays out a group of heads
+// (two buffers: a barrier a group), the next group's chunk in flight meanwhile.
+// 8192 tokens x 72 heads, 126 of 128 columns in fp16: ODD_US us (a pair a thread in 2-byte
+// accesses 171).
+template <typename T>
+__global__ void __launch_bounds__(kRotThreads) k_rotary_odd(RotArgs A) {
+  constexpr int U = 16 / (int)sizeof(T);
+  extern __shared__ float2 s_cs[];     // [tb][half]
+  __shared__ Chunk<T> s_row[2][kRotThreads];
+  pdl_wait();
+  pdl_trigger();
+  const int t0 = blockIdx.x * A.tb, nt = min(A.tb, A.T - t0);
+  const int h0 = blockIdx.y * A.hs, nh = min(A.hs, A.heads - h0);
+  const int per = A.copy ? A.D / U : (2 * A.half + U - 1) / U;           // at most kRotThreads
+  const int step = kRotThreads / per, rows = nt * nh;
+  const int row0 = threadIdx.x / per, c = threadIdx.x - row0 * per;
+  const T *x = static_cast<const T *>(A.x) + t0 * A.xt + h0 * A.xh + c * U;
+  T *y = static_cast<T *>(A.y) + t0 * A.yt + h0 * A.yh + c * U;
+  const int dt = step / nh, dh = step - dt * nh;
+  int t = row0 / nh, h = row0 - t * nh;
+  auto load = [&](int row) {
+    Chunk<T> v;
+    if (row < rows && row0 < step) v = *reinterpret_cast<const Chunk<T> *>(x + (t * A.xt + h * A.xh));
+    return v;
+  };
+  Chunk<T> now = load(row0);
+  all_angles(A, t0, nt, s_cs);
+  for (int first = 0, buf = 0; first < rows; first += step, buf ^= 1) {
+    const bool there = first + row0 < rows && row0 < step;
+    const int tok = t;
+    const int64_t to = t * A.yt + h * A.yh;
+    s_row[buf][threadIdx.x] = now;
+    Chunk<T> v = now;
+    h += dh;
+    t += dt;
+    if (h >= nh) {
+      h -= nh;
+      ++t;
+    }
+    now = load(first + step + row0);
+    __syncthreads();
+    if (!there) continue;
+    const T *own = reinterpret_cast<const T *>(s_row[buf] + row0 * per);
+    const float2 *cs = s_cs + tok * A.half;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int col = c * U + j;
+      if (col >= 2 * A.half) break;
+      const bool upper = col >= A.half;
+      const float2 p = cs[upper ? col - A.half : col];
+      const float fu = to_f(v.v[j]), fw = to_f(own[upper ? col - A.half : col + A.half]) * p.y;
+      from_f(upper ? fmaf(fu, p.x, fw) : fmaf(fu, p.x, -fw), v.v[j]);
+    }
+    *reinterpret_cast<Chunk<T> *>(y + to) = v;
   }
 }
 
@@ -295,10 +368,11 @@ bool apart(int T, int heads, int64_t ts, int64_t hs, int D) {
          (heads == 1 || T == 1 || ts >= (heads - 1) * hs + D || hs >= (T - 1) * ts + D);
 }
 
-template <typename T, int VEC>
+template <typename T>
 cudaError_t run_rotary(const RotArgs &a, int layout, dim3 grid, size_t smem, cudaStream_t st) {
-  return layout == ASF_ROTARY_PAIRS ? launch(k_rotary<T, VEC, true>, grid, dim3(kRotThreads), smem, st, a)
-                                    : launch(k_rotary<T, VEC, false>, grid, dim3(kRotThreads), smem, st, a);
+  return layout == ASF_ROTARY_PAIRS          ? launch(k_rotary<T, true>, grid, dim3(kRotThreads), smem, st, a)
+         : a.half % (16 / (int)sizeof(T)) == 0 ? launch(k_rotary<T, false>, grid, dim3(kRotThreads), smem, st, a)
+                                               : launch(k_rotary_odd<T>, grid, dim3(kRotThreads), smem, st, a);
 }
 template <int VEC>
 cudaError_t run_append(const RotAppendArgs &a, int layout, int64_t items, cudaStream_t st) {
@@ -366,11 +440,12 @@ asf_status asf_rotary_apply(const asf_rotary *rot, const void *x, asf_dtype dtyp
   if (!in_place && overlap(x, (size_t)extent(T, heads, x_token_stride, x_head_stride, D) * size, y,
                            (size_t)extent(T, heads, y_token_stride, y_head_stride, D) * size))
     return ASF_ERR_INVALID_ARG;
-  const int half = rot->rot_dim / 2, vec = pairs_of(half, per16);
+  const int half = rot->rot_dim / 2;
   RotArgs a{x, y, x_token_stride, x_head_stride, y_token_stride, y_head_stride, T, heads, D, half, rot->turns, rot->scale,
             pos, 1, heads, !in_place};
-  const int pass = 2 * vec <= per16 ? 2 * vec : vec;
-  const int64_t per = half / vec + (in_place ? 0 : (D - 2 * half) / pass);
+  // places of a head: ASF_MAX_ROTARY_DIM / 4 = kRotThreads at most
+  const bool wide = rot->layout == ASF_ROTARY_HALF && half % per16 == 0;
+  const int64_t per = wide ? half / per16 + (in_place ? 0 : (D - 2 * half) / per16) : in_place ? (2 * half + per16 - 1) / per16 : D / per16;
   const int64_t chunks = (int64_t)T * heads * per, wave = (int64_t)sm_count() * 2048 * 2;
   a.hs = (int)std::min<int64_t>(heads, std::max<int64_t>(1, kRotThreads * (chunks < wave ? 1 : kItems) / per));
   if (a.hs == heads)
@@ -378,17 +453,8 @@ asf_status asf_rotary_apply(const asf_rotary *rot, const void *x, asf_dtype dtyp
   const dim3 grid((unsigned)(((int64_t)T + a.tb - 1) / a.tb), (unsigned)((heads + a.hs - 1) / a.hs));
   const size_t smem = (size_t)a.tb * half * sizeof(float2);
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e;
-  if (dtype == ASF_F16)
-    e = vec == 8   ? run_rotary<__half, 8>(a, rot->layout, grid, smem, st)
-        : vec == 4 ? run_rotary<__half, 4>(a, rot->layout, grid, smem, st)
-        : vec == 2 ? run_rotary<__half, 2>(a, rot->layout, grid, smem, st)
-                   : run_rotary<__half, 1>(a, rot->layout, grid, smem, st);
-  else
-    e = vec == 4   ? run_rotary<float, 4>(a, rot->layout, grid, smem, st)
-        : vec == 2 ? run_rotary<float, 2>(a, rot->layout, grid, smem, st)
-                   : run_rotary<float, 1>(a, rot->layout, grid, smem, st);
-  return cuda_status(e);
+  return cuda_status(dtype == ASF_F16 ? run_rotary<__half>(a, rot->layout, grid, smem, st)
+                                      : run_rotary<float>(a, rot->layout, grid, smem, st));
 }
 
 asf_status asf_rotary_append(const asf_rotary *rot, const asf_kv_cache *cache, const int32_t *table, int32_t max_pages,
