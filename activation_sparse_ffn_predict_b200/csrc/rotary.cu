@@ -139,11 +139,19 @@ struct RotArgs {
 template <typename T>
 using Chunk = Pack<T, 16 / (int)sizeof(T)>;
 
+// Where a token's pair is, among its cosines and sines: those of every P-th pair side
+// by side, since neighbouring threads read pairs P apart (together in different banks;
+// two neighbouring pairs are 16 bytes in any case).
+template <int P>
+__host__ __device__ constexpr int pitch(int half) { return (half + P - 1) / P; }
+template <int P>
+__device__ __forceinline__ int place_in(int half, int pair) { return P > 2 ? pair % P * pitch<P>(half) + pair / P : pair; }
 // cosines and sines of the CTA's tokens
+template <int P>
 __device__ __forceinline__ void all_angles(const RotArgs &A, int t0, int nt, float2 *cs) {
   for (int i = threadIdx.x; i < nt * A.half; i += kRotThreads) {
-    const int k = i / A.half;
-    cs[i] = cos_sin(A.pos[t0 + k], A.turns[i - k * A.half], A.mul);
+    const int k = i / A.half, j = i - k * A.half;
+    cs[k * P * pitch<P>(A.half) + place_in<P>(A.half, j)] = cos_sin(A.pos[t0 + k], A.turns[j], A.mul);
   }
   __syncthreads();
 }
@@ -154,11 +162,11 @@ __device__ __forceinline__ void all_angles(const RotArgs &A, int t0, int nt, flo
 // A place is 16 bytes of neighbours (those behind rot_dim keep their bits), or 16 of
 // each half where the halves are whole 16 bytes; k_rotary_odd takes the others.
 // HBM bounds it on long prompts: 8192 tokens x 72 heads of 128 columns in fp16, 302 MB
-// in 57 us, 5.3 TB/s.
+// in 55 us, 5.5 TB/s.
 template <typename T, bool PAIRS>
 __global__ void __launch_bounds__(kRotThreads) k_rotary(RotArgs A) {
-  constexpr int U = 16 / (int)sizeof(T), kAhead = PAIRS ? kAheadPairs : kAheadHalf;
-  extern __shared__ float2 s_cs[];     // [tb][half]
+  constexpr int U = 16 / (int)sizeof(T), kAhead = PAIRS ? kAheadPairs : kAheadHalf, P = PAIRS ? U / 2 : U;   // pairs of a place
+  extern __shared__ float2 s_cs[];     // [tb][P][pitch]
   pdl_wait();
   pdl_trigger();
   const int t0 = blockIdx.x * A.tb, nt = min(A.tb, A.T - t0);
@@ -197,18 +205,19 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary(RotArgs A) {
         ++t;
       }
     }
-    if (fresh) all_angles(A, t0, nt, s_cs);        // every thread is here once at least
+    if (fresh) all_angles<P>(A, t0, nt, s_cs);     // every thread is here once at least
     fresh = false;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (to[i] < 0) continue;
       if (turns) {
-        const float2 *cs = s_cs + tok[i] * A.half + (PAIRS ? c * (U / 2) : c * U);
+        const int apart = P > 2 ? pitch<P>(A.half) : 1;
+        const float2 *cs = s_cs + tok[i] * P * pitch<P>(A.half) + (P > 2 ? c : c * P);
 #pragma unroll
-        for (int j = 0; j < (PAIRS ? U / 2 : U); ++j) {
-          if (PAIRS && c * (U / 2) + j >= A.half) break;
+        for (int j = 0; j < P; ++j) {
+          if (PAIRS && c * P + j >= A.half) break;
           T &u = a[i].v[PAIRS ? 2 * j : j], &w = PAIRS ? a[i].v[(2 * j + 1) % U] : b[PAIRS ? 0 : i].v[j];
-          const float fu = to_f(u), fw = to_f(w), cv = cs[j].x, sv = cs[j].y;
+          const float fu = to_f(u), fw = to_f(w), cv = cs[j * apart].x, sv = cs[j * apart].y;
           from_f(fmaf(fu, cv, -(fw * sv)), u);
           from_f(fmaf(fw, cv, fu * sv), w);
         }
@@ -222,12 +231,12 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary(RotArgs A) {
 // Halves that are not whole 16 bytes: a thread has 16 bytes of a head, and finds the
 // other halves of its pairs in shared memory, where the CTA lays out a group of heads
 // (two buffers: a barrier a group), the next group's chunk in flight meanwhile.
-// 8192 tokens x 72 heads, 126 of 128 columns in fp16: ODD_US us (a pair a thread in 2-byte
+// 8192 tokens x 72 heads, 126 of 128 columns in fp16: 82 us (a pair a thread in 2-byte
 // accesses 171).
 template <typename T>
 __global__ void __launch_bounds__(kRotThreads) k_rotary_odd(RotArgs A) {
   constexpr int U = 16 / (int)sizeof(T);
-  extern __shared__ float2 s_cs[];     // [tb][half]
+  extern __shared__ float2 s_cs[];     // [tb][U][pitch]
   __shared__ Chunk<T> s_row[2][kRotThreads];
   pdl_wait();
   pdl_trigger();
@@ -246,7 +255,7 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary_odd(RotArgs A) {
     return v;
   };
   Chunk<T> now = load(row0);
-  all_angles(A, t0, nt, s_cs);
+  all_angles<U>(A, t0, nt, s_cs);
   for (int first = 0, buf = 0; first < rows; first += step, buf ^= 1) {
     const bool there = first + row0 < rows && row0 < step;
     const int tok = t;
@@ -263,13 +272,14 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary_odd(RotArgs A) {
     __syncthreads();
     if (!there) continue;
     const T *own = reinterpret_cast<const T *>(s_row[buf] + row0 * per);
-    const float2 *cs = s_cs + tok * A.half;
+    const float2 *cs = s_cs + tok * U * pitch<U>(A.half);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int col = c * U + j;
       if (col >= 2 * A.half) break;
       const bool upper = col >= A.half;
-      const float2 p = cs[upper ? col - A.half : col];
+      const int pair = upper ? col - A.half : col;
+      const float2 p = cs[place_in<U>(A.half, pair)];
       const float fu = to_f(v.v[j]), fw = to_f(own[upper ? col - A.half : col + A.half]) * p.y;
       from_f(upper ? fmaf(fu, p.x, fw) : fmaf(fu, p.x, -fw), v.v[j]);
     }
@@ -451,7 +461,7 @@ asf_status asf_rotary_apply(const asf_rotary *rot, const void *x, asf_dtype dtyp
   if (a.hs == heads)
     a.tb = (int)std::max<int64_t>(1, std::min<int64_t>({8, (int64_t)kRotThreads * kItems / (heads * per), chunks / wave}));
   const dim3 grid((unsigned)(((int64_t)T + a.tb - 1) / a.tb), (unsigned)((heads + a.hs - 1) / a.hs));
-  const size_t smem = (size_t)a.tb * half * sizeof(float2);
+  const size_t smem = (size_t)a.tb * (half + per16) * sizeof(float2);     // pitches round up
   cudaStream_t st = (cudaStream_t)stream;
   return cuda_status(dtype == ASF_F16 ? run_rotary<__half>(a, rot->layout, grid, smem, st)
                                       : run_rotary<float>(a, rot->layout, grid, smem, st));
