@@ -153,20 +153,21 @@ __global__ void __launch_bounds__(128) k_tree_score(AttnArgs A) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   bool bad;
   const Req q = req_lane(A, 16, lane, bad);                              // bad requests have been flagged
-  int end = q.n ? q.nkt * A.hkv : 0;                                     // this request's tiles, all heads
-  const int own = end;
+  int64_t end = q.n ? (int64_t)q.nkt * A.hkv : 0;                        // this request's tiles, all heads
+  const int64_t own = end;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, end, o);
+    const int64_t v = __shfl_up_sync(0xffffffffu, end, o);
     if (lane >= o) end += v;
   }
-  const int total = __shfl_sync(0xffffffffu, end, 31);
-  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+  const int64_t total = __shfl_sync(0xffffffffu, end, 31);
+  for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
     const int req = __popc(__ballot_sync(0xffffffffu, end <= u));
-    const int in = u - __shfl_sync(0xffffffffu, end - own, req), nkt = __shfl_sync(0xffffffffu, q.nkt, req);
+    const int64_t in = u - __shfl_sync(0xffffffffu, end - own, req);
+    const int nkt = __shfl_sync(0xffffffffu, q.nkt, req);
     const int t0 = __shfl_sync(0xffffffffu, q.t0, req), n = __shfl_sync(0xffffffffu, q.n, req);
     const int len = __shfl_sync(0xffffffffu, q.len, req), L = __shfl_sync(0xffffffffu, q.L, req);
-    const int head = in / nkt, pos0 = (in - head * nkt) * kTile, rows = n * A.grp;
+    const int head = (int)(in / nkt), pos0 = (int)(in - (int64_t)head * nkt) * kTile, rows = n * A.grp;
     if (tid < kTile) {
       const int pos = pos0 + tid;
       int64_t off = -1;
