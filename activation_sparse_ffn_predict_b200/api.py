@@ -40,13 +40,21 @@ def _stream(stream) -> ctypes.c_void_p:
 
 def _arg(t: torch.Tensor, name: str, device, dtype=None) -> int:
     """Address of a contiguous tensor on ``device``."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device.index:    # -1: not on a GPU
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if dtype is not None and t.dtype is not dtype:
+    return _ptr(t, name, device.index, t.dtype if dtype is None and isinstance(t, torch.Tensor) else dtype)
+
+
+def _ptr(t: torch.Tensor, name: str, index: int, dtype) -> int:
+    """Address of a contiguous tensor of that dtype on CUDA device ``index``."""
+    try:
+        if t.get_device() == index and t.dtype is dtype and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:           # -1: not on a GPU
+        raise ValueError(f"{name} must be a tensor on cuda:{index}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (

@@ -9,7 +9,9 @@ from typing import Optional
 import torch
 
 from . import _lib as L
-from .api import Workspace, _arg, _invoke
+from .api import Workspace, _invoke, _ptr
+
+_I32, _F16, _F32 = torch.int32, torch.float16, torch.float32
 
 
 class KVCache:
@@ -24,7 +26,7 @@ class KVCache:
                 raise ValueError(f"{name} must not be empty, and its last dimension contiguous")
         if k.shape != v.shape or k.stride() != v.stride() or k.device != v.device:
             raise ValueError("k and v must have one shape, layout and device")
-        self.k, self.v, self.device = k, v, k.device
+        self.k, self.v, self.device, self.index = k, v, k.device, k.device.index
         self.pages, self.page, self.heads, self.head_dim = (int(n) for n in k.shape)
         self.desc = L.asf_kv_cache(self.pages, self.page, self.heads, self.head_dim, k.data_ptr(), v.data_ptr(),
                                    # the stride of a dimension of one is never used, and torch's can be anything
@@ -39,14 +41,13 @@ class KVCache:
 
 
 def _requests(cache: KVCache, table, lens, begin):
-    dev, of, n, b = cache.device, table.shape, lens.shape, begin.shape    # each shape read once: a tenth of a microsecond
+    on, of, n, b = cache.index, table.shape, lens.shape, begin.shape    # each shape read once: a tenth of a microsecond
     if len(of) != 2 or len(n) != 1 or n[0] != of[0]:
         raise ValueError("table must be [R, max_pages] and lens [R]")
     R, max_pages = of
     if len(b) != 1 or b[0] != R + 1:
         raise ValueError("begin must be [R + 1]")
-    return (_arg(table, "table", dev, torch.int32), max_pages, R, _arg(lens, "lens", dev, torch.int32),
-            _arg(begin, "begin", dev, torch.int32))
+    return _ptr(table, "table", on, _I32), max_pages, R, _ptr(lens, "lens", on, _I32), _ptr(begin, "begin", on, _I32)
 
 
 def asf_kv_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin: torch.Tensor, k: torch.Tensor,
@@ -59,7 +60,7 @@ def asf_kv_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin
         raise ValueError("k and v must be [T, heads, head_dim]")
     dev = cache.device
     req = _requests(cache, table, lens, begin)
-    kp, vp = _arg(k, "k", dev, torch.float16), _arg(v, "v", dev, torch.float16)
+    kp, vp = _ptr(k, "k", dev.index, _F16), _ptr(v, "v", dev.index, _F16)
     _invoke("asf_kv_append", dev, stream, cache._ref, *req, of[0], kp, vp, ws.on(dev), ws.nbytes)
 
 
@@ -70,10 +71,10 @@ def _attend(cache: KVCache, table, lens, begin, q, anc, o, ws, scale):
     n = anc.shape
     if len(n) != 1 or n[0] != of[0]:
         raise ValueError("anc must be [T]")
-    dev = cache.device
+    on = cache.index
     req = _requests(cache, table, lens, begin)
-    qp, op = _arg(q, "q", dev, torch.float16), _arg(o, "o", dev, torch.float16)
-    ap = _arg(anc, "anc", dev, torch.int32)
+    qp, op = _ptr(q, "q", on, _F16), _ptr(o, "o", on, _F16)
+    ap = _ptr(anc, "anc", on, _I32)
     return (cache._ref, *req, of[0], of[1], qp, ap, cache.head_dim ** -0.5 if scale is None else scale, op)
 
 
@@ -99,7 +100,7 @@ def asf_tree_attention_scored(cache: KVCache, table: torch.Tensor, lens: torch.T
     of = scores.shape
     if len(of) != 3 or of[0] != lens.shape[0] or of[1] != cache.heads:
         raise ValueError("scores must be [R, heads, S]")
-    sp = _arg(scores, "scores", cache.device, torch.float32)
+    sp = _ptr(scores, "scores", cache.index, _F32)
     _invoke("asf_tree_attention_scored", cache.device, stream, *args, sp, of[2], ws.on(cache.device), ws.nbytes)
 
 
@@ -111,19 +112,18 @@ def asf_kv_evict(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, scores
 
     lens_out int32 [R], kept int32 [R, heads, keep] (the old positions) and scores_out fp32 [R, heads,
     >= keep] are written as far as keys are kept."""
-    dev, of, n, old, new = cache.device, scores.shape, lens.shape, table.shape, table_out.shape
+    on, of, n, old, new = cache.index, scores.shape, lens.shape, table.shape, table_out.shape
     R = n[0] if len(n) == 1 else -1
     if len(old) != 2 or len(new) != 2 or old[0] != R or new[0] != R:
         raise ValueError("table and table_out must be [R, max_pages], lens [R]")
     if len(of) != 3 or of[0] != R or of[1] != cache.heads:
         raise ValueError("scores must be [R, heads, S]")
-    if lens_out.shape != n or kept.shape != (R, cache.heads, keep):
+    to, sel = scores_out.shape, kept.shape
+    if lens_out.shape != n or len(sel) != 3 or sel[0] != R or sel[1] != cache.heads or sel[2] != keep:
         raise ValueError("lens_out must be [R] and kept [R, heads, keep]")
-    to = scores_out.shape
     if len(to) != 3 or to[0] != R or to[1] != cache.heads:
         raise ValueError("scores_out must be [R, heads, S_out]")
-    i32, f32 = torch.int32, torch.float32
-    _invoke("asf_kv_evict", dev, stream, cache._ref, _arg(table, "table", dev, i32), old[1], R,
-            _arg(lens, "lens", dev, i32), _arg(scores, "scores", dev, f32), of[2], int(keep), int(first), int(recent),
-            _arg(table_out, "table_out", dev, i32), new[1], _arg(lens_out, "lens_out", dev, i32),
-            _arg(scores_out, "scores_out", dev, f32), to[2], _arg(kept, "kept", dev, i32), ws.on(dev), ws.nbytes)
+    _invoke("asf_kv_evict", cache.device, stream, cache._ref, _ptr(table, "table", on, _I32), old[1], R,
+            _ptr(lens, "lens", on, _I32), _ptr(scores, "scores", on, _F32), of[2], int(keep), int(first), int(recent),
+            _ptr(table_out, "table_out", on, _I32), new[1], _ptr(lens_out, "lens_out", on, _I32),
+            _ptr(scores_out, "scores_out", on, _F32), to[2], _ptr(kept, "kept", on, _I32), ws.on(cache.device), ws.nbytes)

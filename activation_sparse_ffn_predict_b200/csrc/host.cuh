@@ -114,6 +114,9 @@ inline asf_status check_ws(void *ws, size_t ws_bytes, size_t need) {
   return ASF_OK;
 }
 
+// workspace of asf_w4_matmul for exactly B tokens (w4.cu); 0 for a matrix that it refuses
+size_t w4_product_bytes(const asf_w4_matrix *mat, int B);
+
 inline asf_status cuda_status(cudaError_t e) { return e == cudaSuccess ? ASF_OK : ASF_ERR_CUDA; }
 
 // cuTensorMapEncodeTiled, from the driver through the runtime (no link to the

@@ -347,7 +347,7 @@ asf_status asf_w4_matmul_lora(const asf_w4_matrix *mat, const asf_lora *lora, co
     return ASF_ERR_INVALID_ARG;
   if ((ydtype != ASF_F16 && ydtype != ASF_F32) || xdtype != lora->dtype) return ASF_ERR_UNSUPPORTED;
   if (!al4(which) || !al16(x) || (reinterpret_cast<uintptr_t>(y) & (ydtype == ASF_F16 ? 1u : 3u))) return ASF_ERR_MISALIGNED;
-  const size_t plain = r256(asf_w4_workspace_bytes(mat, nullptr, B));
+  const size_t plain = r256(w4_product_bytes(mat, B));                  // at most what the workspace was sized with
   if (plain) {
     s = check_ws(ws, ws_bytes, plain + lora_scratch(lora, B));
     if (s != ASF_OK) return s;

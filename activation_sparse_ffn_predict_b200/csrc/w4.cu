@@ -1456,6 +1456,12 @@ cudaError_t run_down(const DownArgs &a, cudaStream_t st) {
 
 }  // namespace
 
+namespace asf {
+size_t w4_product_bytes(const asf_w4_matrix *mat, int B) {
+  return check_w4(mat) == ASF_OK ? kHeaderBytes + dot_part_bytes(ceil_div(mat->rows, 16), mat->k, mat->group, B) : 0;
+}
+}  // namespace asf
+
 extern "C" {
 
 int64_t asf_w4_row_bytes(int32_t k, int32_t group) {

@@ -8,8 +8,8 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib as L
-from .api import _DT, Workspace, _arg, _invoke, check
-from .attention import KVCache, _requests
+from .api import _DT, Workspace, _invoke, _ptr, check
+from .attention import _F16, _I32, KVCache, _requests
 
 _LAYOUT = {"half": L.ASF_ROTARY_HALF, "pairs": L.ASF_ROTARY_PAIRS}
 _SCALING = {"none": L.ASF_ROTARY_PLAIN, "linear": L.ASF_ROTARY_LINEAR, "ntk": L.ASF_ROTARY_NTK, "yarn": L.ASF_ROTARY_YARN}
@@ -45,18 +45,18 @@ class Rotary:
         self.frequencies, self.scale = list(freq), float(mul.value if scale is None else scale)
         signed = [t - (1 << 64) if t >> 63 else t for t in turns]
         self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
-        self.device = self.turns.device
+        self.device, self.index = self.turns.device, self.turns.device.index
         if self.device.type != "cuda":
             raise ValueError("device must be a CUDA device")
         self.desc = L.asf_rotary(self.head_dim, rot_dim, _LAYOUT[layout], self.scale, self.turns.data_ptr())
         self._ref = ctypes.byref(self.desc)
 
 
-def _rows(t: torch.Tensor, name: str, device, dtype, of):
-    """Address of a tensor of the shape `of`, [T, heads, head_dim] with its last dimension contiguous, and its
-    token and head strides (never read for a dimension of one)."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device.index:
-        raise ValueError(f"{name} must be a tensor on {device}")
+def _rows(t: torch.Tensor, name: str, index: int, dtype, of):
+    """Address of a tensor of the shape `of`, [T, heads, head_dim] with its last dimension contiguous, on CUDA
+    device `index`, and its token and head strides (never read for a dimension of one)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be a tensor on cuda:{index}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
     token, head, one = t.stride()
@@ -80,11 +80,11 @@ def asf_rotary_apply(rot: Rotary, x: torch.Tensor, pos: torch.Tensor, y: torch.T
     n = pos.shape
     if len(n) != 1 or n[0] != of[0]:
         raise ValueError("pos must be [T]")
-    dev = rot.device
-    xp, xt, xh = _rows(x, "x", dev, dt, of)
-    yp, yt, yh = _rows(y, "y", dev, dt, of)
-    _invoke("asf_rotary_apply", dev, stream, rot._ref, xp, code, of[0], of[1], xt, xh,
-            _arg(pos, "pos", dev, torch.int32), yp, yt, yh)
+    on = rot.index
+    xp, xt, xh = _rows(x, "x", on, dt, of)
+    yp, yt, yh = _rows(y, "y", on, dt, of)
+    _invoke("asf_rotary_apply", rot.device, stream, rot._ref, xp, code, of[0], of[1], xt, xh,
+            _ptr(pos, "pos", on, _I32), yp, yt, yh)
 
 
 def asf_rotary_append(rot: Rotary, cache: KVCache, table: torch.Tensor, lens: torch.Tensor, begin: torch.Tensor,
@@ -101,14 +101,14 @@ def asf_rotary_append(rot: Rotary, cache: KVCache, table: torch.Tensor, lens: to
     n = pos.shape
     if len(n) != 1 or n[0] != of[0]:
         raise ValueError("pos must be [T]")
-    dev, f16, D = cache.device, torch.float16, cache.head_dim
-    if rot.device.index != dev.index:
+    dev, on, D = cache.device, cache.index, cache.head_dim
+    if rot.index != on:
         raise ValueError(f"the rotary table must be on {dev}")
     req = _requests(cache, table, lens, begin)
-    qp, qs, qh = _rows(q, "q", dev, f16, of)
-    kp, ks, kh = _rows(k, "k", dev, f16, kv)
-    vp, vs, vh = _rows(v, "v", dev, f16, kv)
+    qp, qs, qh = _rows(q, "q", on, _F16, of)
+    kp, ks, kh = _rows(k, "k", on, _F16, kv)
+    vp, vs, vh = _rows(v, "v", on, _F16, kv)
     if qh != D or kh != D or vh != D:
         raise ValueError("the heads of q, k and v must be contiguous")
-    _invoke("asf_rotary_append", dev, stream, rot._ref, cache._ref, *req, of[0], _arg(pos, "pos", dev, torch.int32), of[1],
-            qp, qs, _arg(q_out, "q_out", dev, f16), kp, ks, vp, vs, ws.on(dev), ws.nbytes)
+    _invoke("asf_rotary_append", dev, stream, rot._ref, cache._ref, *req, of[0], _ptr(pos, "pos", on, _I32), of[1],
+            qp, qs, _ptr(q_out, "q_out", on, _F16), kp, ks, vp, vs, ws.on(dev), ws.nbytes)

@@ -8,7 +8,7 @@ from typing import Optional
 import torch
 
 from . import _lib as L
-from .api import _ACT, _DT, Workspace, _arg, _invoke
+from .api import _ACT, _DT, Workspace, _arg, _invoke, _ptr
 
 
 def asf_w4_row_bytes(k: int, group: int) -> int:
@@ -139,19 +139,19 @@ def asf_w4_dequantize(mat: W4Matrix, dst: torch.Tensor, stream=None) -> None:
 
 
 def _product(mat: W4Matrix, x, y, bias, relu):
-    xt, yt, of, to = _DT.get(x.dtype), _DT.get(y.dtype), x.shape, y.shape
+    xd, yd, of, to = x.dtype, y.dtype, x.shape, y.shape
+    xt, yt = _DT.get(xd), _DT.get(yd)
     if xt is None or len(of) != 2 or of[1] != mat.k:
         raise ValueError("x must be [B, k], float16 or float32")
     B = of[0]
     if yt is None or len(to) != 2 or to[0] != B or to[1] != mat.rows:
         raise ValueError("y must be [B, rows], float16 or float32")
-    dev = mat.device
-    bp = None
+    on, bp = mat.device.index, None
     if bias is not None:
         if bias.shape != (mat.rows,):
             raise ValueError("bias must be [rows]")
-        bp = _arg(bias, "bias", dev, torch.float32)
-    return _arg(x, "x", dev), xt, B, bp, int(bool(relu)), _arg(y, "y", dev), yt
+        bp = _ptr(bias, "bias", on, torch.float32)
+    return _ptr(x, "x", on, xd), xt, B, bp, int(bool(relu)), _ptr(y, "y", on, yd), yt
 
 
 def asf_w4_matmul(mat: W4Matrix, x: torch.Tensor, y: torch.Tensor, ws: Workspace,
@@ -169,7 +169,7 @@ def asf_w4_matmul_lora(mat: W4Matrix, lora: LoraSet, which: torch.Tensor, x: tor
         raise ValueError("which must be [B]")
     if lora.device.index != mat.device.index or x.dtype is not lora.dtype:
         raise ValueError(f"the adapters must be on {mat.device} and in x's dtype")
-    _invoke("asf_w4_matmul_lora", mat.device, stream, mat._ref, lora._ref, _arg(which, "which", mat.device, torch.int32),
+    _invoke("asf_w4_matmul_lora", mat.device, stream, mat._ref, lora._ref, _ptr(which, "which", mat.device.index, torch.int32),
             *args, ws.on(mat.device), ws.nbytes)
 
 
