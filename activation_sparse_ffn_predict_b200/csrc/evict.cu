@@ -342,11 +342,26 @@ asf_status asf_kv_evict(const asf_kv_cache *cache, const int32_t *table, int32_t
               keep, first, recent, 0, &static_cast<Header *>(ws)->err};
   cudaStream_t st = (cudaStream_t)stream;
   const int most = (int)std::min<int64_t>(S, (int64_t)max_pages * cache->page), units = R * cache->heads;
-  const int cl = most > 4096 ? 8 : 1;
+  // A cluster per kv head as large as leaves every CTA an SM, or half of one where its run is
+  // long (tables of requests of different lengths leave some CTAs idle), and in any case so
+  // large that its shared memory holds the scores.  us of the call, keeping 200 keys, with 8, 4, 2
+  // and 1 CTAs: 8 heads x 4000 keys 13.9, 14.1, 15.5, 12.9; 20000 keys 16.7, 19.6, 26.2,
+  // 34.2; 32 heads x 20000 27.0, 21.9, 26.5, 34.4; 64 heads x 10000 43.2, 26.0, 20.8, 22.9;
+  // 128 heads x 10000 76.8, 44.3, 28.5, 24.5; 32 heads x 65500 keys 37.9 and 37.0 (8 and 4), and
+  // with a request in two of them short 104 and 113.
+  int cl = 1;
+  for (; cl < 8 && most > 4096; cl *= 2) {
+    const int run = (most + cl - 1) / cl, room = sm_count() * (run > 12 * 1024 ? 2 : 1);
+    if (units * cl * 2 > room && run <= kStageMost) break;
+  }
   a.staged = std::min((most + cl - 1) / cl, kStageMost);
-  const size_t smem = (size_t)a.staged * 4;
-  cudaError_t e = cl == 8 ? launch_clusters(k_evict_select<8>, dim3(units * 8), dim3(kSelThreads), smem, st, 8, a)
-                          : launch(k_evict_select<1>, dim3(units), dim3(kSelThreads), smem, st, a);
+  // Beside the static part (21 KB at most) more than 48 KB have to be asked for, which a launch does from 40 KB on.
+  const size_t keys = (size_t)a.staged * 4, smem = keys <= 24 * 1024 ? keys : std::max<size_t>(keys, 41 * 1024);
+  const dim3 ctas(units * cl), block(kSelThreads);
+  const cudaError_t e = cl == 8   ? launch_clusters(k_evict_select<8>, ctas, block, smem, st, 8, a)
+                        : cl == 4 ? launch_clusters(k_evict_select<4>, ctas, block, smem, st, 4, a)
+                        : cl == 2 ? launch_clusters(k_evict_select<2>, ctas, block, smem, st, 2, a)
+                                  : launch(k_evict_select<1>, ctas, block, smem, st, a);
   if (e != cudaSuccess) return ASF_ERR_CUDA;
   const int last = std::min(keep, most);
   const dim3 grid((last + kMoveKeys - 1) / kMoveKeys, (cache->heads + kMoveHeads - 1) / kMoveHeads, R);

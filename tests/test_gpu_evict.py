@@ -76,7 +76,10 @@ class Case:
     ([500], 100, dict(first=60, recent=40)), ([4000], 1000, dict(hkv=5, first=4, recent=256)), ([4096], 7, {}), ([4097], 4096, {}),
     ([5000, 300, 4999], 2048, dict(hkv=9, D=64, page=64, first=4, recent=100)), ([9001], 4000, dict(hkv=1, D=24, page=7, S=9500)),
     ([513, 512, 511], 256, dict(hkv=2, spare=50)), (list(range(0, 320, 10)), 100, dict(hkv=8, D=8, page=5)),
-    ([20000], 19999, dict(hkv=1, D=8, page=256)), ([8191], 1, dict(hkv=2, D=8, page=64, S=8192))])
+    ([20000], 19999, dict(hkv=1, D=8, page=256)), ([8191], 1, dict(hkv=2, D=8, page=64, S=8192)),
+    # clusters of 4, 2 and 1 CTAs, as many as leave each an SM; 2 where one CTA does not hold the scores
+    ([5000, 4097, 30], 700, dict(hkv=9, D=8, page=64)), ([4500] * 3, 100, dict(hkv=20, D=8, page=64, first=1, recent=9)),
+    ([4200, 4097], 1000, dict(hkv=50, D=8, page=64)), ([45000, 100], 3, dict(hkv=80, D=8, page=512)), ([5000], 4999, dict(hkv=37, D=8, page=32))])
 def test_against_the_definition(lens, keep, kw):
     c = Case(lens, keep, seed=sum(lens) + keep, **kw)
     c.check(c.run())
@@ -88,6 +91,14 @@ def test_against_the_definition(lens, keep, kw):
     [3e38, -3e38, 2.0, -2.0, 1e-38, np.nan, np.inf]])
 def test_ties_and_unusual_scores(n, keep, values):
     c = Case([n], keep, hkv=3, first=3, recent=5, seed=n, values=values)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("n,hkv", [(66000, 1), (74000, 1), (78000, 2), (81900, 1), (100000, 1), (12200, 60), (13400, 60), (20000, 60), (24600, 20),
+                                   (41000, 20), (6100, 100), (6200, 100), (10200, 100)])
+def test_shared_memory_of_every_size(n, hkv):
+    """Around the sizes from which a kernel has to ask for its shared memory."""
+    c = Case([n], 700, hkv=hkv, D=8, page=512, first=4, recent=64, seed=n)
     c.check(c.run())
 
 
