@@ -136,7 +136,10 @@ __device__ __forceinline__ void down_rows(const LoraArgs &A, int a, int row0, ui
   }
 }
 
-// h = s A x: a CTA is RW rows of the adapter that its token leads, over all of k.
+// h = s A x: a CTA is RW rows of the adapter that its token leads, over all of k.  Four
+// rows where those are a CTA an SM (x is read once for them), else one, in few registers, so
+// that it finds room beside a product that leaves some (k_w4_dot).  24 adapters of rank 64 over
+// 8192 columns, 25 MB: 12 us alone, 2.0 TB/s: the loads of 2.6 CTAs an SM in flight.
 template <typename T, int RW>
 __global__ void __launch_bounds__(kDownThreads, RW == 1 ? 8 : 4) k_lora_down(LoraArgs A) {
   __shared__ float s_red[kDownThreads / 32 * RW * kAlong];
@@ -212,7 +215,9 @@ __device__ __forceinline__ void up_tokens(const LoraArgs &A, const T *w, int row
 
 // y = act(base + B h).  The (adapter in use, tile of its rows) pairs are dealt out in one
 // run of equal lengths per CTA, which streams its tiles, whole runs of memory, through a
-// ring of bulk copies; the first of them are issued before the wait.
+// ring of bulk copies; the first of them are issued before the wait.  24 adapters of rank
+// 64 over 28672 rows, 88 MB: 24 us alone, 3.7 TB/s; with the product and k_lora_down 77
+// (lanes along a row of B, whose sums meet by shuffles: 99; fewer tiles in flight: 82).
 template <typename T>
 __global__ void __launch_bounds__(kUpThreads, kUpCtas) k_lora_up(LoraArgs A, int tile) {
   extern __shared__ __align__(128) unsigned char sm[];
