@@ -95,7 +95,8 @@ class AttentionStage:
         """Between steps, with scored: every request's layers and kv heads keep `keep` keys (asf_kv_evict) on the pages
         of `table` int32 [R, pages], which are then the stage's.  Returns the kept positions int32 [layers, R, heads, keep].
 
-        The stage's table, lens and scores go over to what is left, in place, so that a captured stack runs on."""
+        The stage's table, lens and scores go over to what is left, in place, so that a captured stack runs on.  Past
+        `table`'s columns its own then lists no page (-1): the old ones are the caller's again."""
         if self.scores is None:
             raise ValueError("eviction goes by the scores of a scored stage")
         n, R, heads, S = self.scores.shape
@@ -108,6 +109,7 @@ class AttentionStage:
                          recent=recent)
             self.scores[l].copy_(scores)
         self.table[:, :table.shape[1]].copy_(table)
+        self.table[:, table.shape[1]:].fill_(-1)
         self.lens.copy_(lens)
         return kept
 

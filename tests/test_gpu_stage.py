@@ -76,7 +76,7 @@ def test_steps_and_an_eviction(hkv, grp, D, page, R, T):
         scores[l].copy_(out)
     kept = stage.evict(keep, fresh, first=2, recent=20)
     assert torch.equal(kept, want) and torch.equal(stage.lens, lens) and lens.max() == keep
-    assert torch.equal(stage.table[:, :8], fresh) and torch.equal(stage.scores, scores)
+    assert torch.equal(stage.table[:, :8], fresh) and bool((stage.table[:, 8:] == -1).all()) and torch.equal(stage.scores, scores)
     st.step()                                                # the captured step goes on over what is left
     by_hand()
     assert st.read_error() == 0
