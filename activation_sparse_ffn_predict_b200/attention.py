@@ -94,7 +94,8 @@ def asf_tree_attention_scored(cache: KVCache, table: torch.Tensor, lens: torch.T
                               scale: Optional[float] = None, stream=None) -> None:
     """asf_tree_attention that adds to scores fp32 [R, heads, S] the weight that each cached key received.
 
-    S covers the positions seen; the call's own tokens' positions are set instead.  ws:
+    Every token of the call counts: those of a verified tree go through it by themselves, drafts through
+    asf_tree_attention.  S covers the positions seen; the call's own tokens' positions are set instead.  ws:
     Workspace.for_attention(..., scored_pages=the table's width)."""
     args = _attend(cache, table, lens, begin, q, anc, o, ws, scale)
     of = scores.shape

@@ -33,12 +33,15 @@ class AttentionStage:
 
     rotary: q and k are turned by the tokens' positions, which the caller fills
     in pos [B].  scored: scores[l] [R, heads, max_pages * page] adds up the weight
-    that each cached key receives, for evict().  adapters: adapters[l] beside
-    out[l]; the caller fills which [B] (-1, none, at first)."""
+    that each cached key receives, for evict(); every token of a step counts, so
+    all of them stay.  Where steps hold drafted tokens of which some may be
+    rejected, drafts (with scored) leaves the step unscored, and accept() counts
+    those that stay.  adapters: adapters[l] beside out[l]; the caller fills
+    which [B] (-1, none, at first)."""
 
     def __init__(self, caches: Sequence[KVCache], q_heads: int, requests: int, max_pages: int, batch: int,
                  out: Optional[Sequence[W4Matrix]] = None, rotary: Optional[Rotary] = None, scored: bool = False,
-                 adapters: Optional[Sequence[LoraSet]] = None):
+                 adapters: Optional[Sequence[LoraSet]] = None, drafts: bool = False):
         c0, n = caches[0], len(caches)
         if any((c.heads, c.head_dim, c.page, c.device) != (c0.heads, c0.head_dim, c0.page, c0.device) for c in caches):
             raise ValueError("the layers' caches must have one head layout, page size and device")
@@ -50,7 +53,9 @@ class AttentionStage:
         if adapters is not None and (out is None or len(adapters) != n or any(
                 (a.k, a.rows, a.dtype) != (m.k, m.rows, torch.float16) for a, m in zip(adapters, out))):
             raise ValueError("one set of float16 adapters per projection, of its shape")
-        self.rotary, self.adapters = rotary, adapters
+        if drafts and not scored:
+            raise ValueError("drafts says how a scored stage counts")
+        self.rotary, self.adapters, self.drafts = rotary, adapters, bool(drafts)
         self.caches, self.out, self.R, self.max_pages = list(caches), out, int(requests), int(max_pages)
         half = lambda *s: torch.zeros(*s, dtype=torch.float16, device=c0.device)  # noqa: E731
         ints = lambda *s: torch.zeros(*s, dtype=torch.int32, device=c0.device)  # noqa: E731
@@ -72,7 +77,8 @@ class AttentionStage:
         sms = torch.cuda.get_device_properties(c.device).multi_processor_count
         split = _attention_splits(self.max_pages * c.page, c.heads, c.head_dim, self.q.shape[2] // c.heads, self.R,
                                   self.q.shape[1], sms)
-        return 2 + int(split) + int(self.scores is not None) + int(self.out is not None) + 2 * int(self.adapters is not None)
+        scores = self.scores is not None and not self.drafts
+        return 2 + int(split) + int(scores) + int(self.out is not None) + 2 * int(self.adapters is not None)
 
     def enqueue(self, l: int, x: torch.Tensor, stream=None) -> None:
         o = self.o if self.out is not None else x.view(self.o.shape)
@@ -82,7 +88,7 @@ class AttentionStage:
             q = self.q_turned
         else:
             asf_kv_append(cache, *req, self.k[l], self.v[l], self.ws, stream)
-        if self.scores is not None:
+        if self.scores is not None and not self.drafts:
             asf_tree_attention_scored(cache, *req, q, self.anc, o, self.scores[l], self.ws, stream=stream)
         else:
             asf_tree_attention(cache, *req, q, self.anc, o, self.ws, stream=stream)
@@ -90,6 +96,38 @@ class AttentionStage:
             asf_w4_matmul_lora(self.out[l], self.adapters[l], self.which, o.view(x.shape[0], -1), x, self.ws_out, stream=stream)
         elif self.out is not None:
             asf_w4_matmul(self.out[l], o.view(x.shape[0], -1), x, self.ws_out, stream=stream)
+
+    def accept(self, accepted: Sequence[Sequence[int]]) -> None:
+        """After a step of drafts is verified: accepted[r] are the places in the step of request r's tokens that stay, in
+        their order; each has seen the ones before it.  They are appended again from lens on, their weights go into
+        scores as if they had been decoded one by one, and lens grows by them.  The others leave nothing in scores.
+
+        Reads begin on the host, so it waits for what is enqueued."""
+        if not self.drafts:
+            raise ValueError("tokens are accepted by a stage of drafts")
+        begin = self.begin.tolist()
+        if len(accepted) != self.R or any(len(set(a)) != len(a) or any(not begin[r] <= t < begin[r + 1] for t in a)
+                                          for r, a in enumerate(accepted)):
+            raise ValueError("accepted must list each request's own tokens of the step, each once")
+        which, first, anc = [int(t) for a in accepted for t in a], [0], []
+        for a in accepted:
+            t0 = first[-1]
+            first.append(t0 + len(a))
+            anc += [(1 << (t + 1)) - (1 << t0) for t in range(t0, first[-1])]
+        if not which:
+            return
+        dev = self.lens.device
+        which, first = torch.tensor(which, device=dev), torch.tensor(first, dtype=torch.int32, device=dev)
+        anc = torch.tensor([m - (1 << 32) if m >> 31 else m for m in anc], dtype=torch.int32, device=dev)
+        for l, cache in enumerate(self.caches):
+            q, k, v = (t[l].index_select(0, which) for t in (self.q, self.k, self.v))
+            req = (cache, self.table, self.lens, first)
+            if self.rotary is not None:
+                asf_rotary_append(self.rotary, *req, self.pos.index_select(0, which), q, q, k, v, self.ws)
+            else:
+                asf_kv_append(*req, k, v, self.ws)
+            asf_tree_attention_scored(*req, q, anc, torch.empty_like(q), self.scores[l], self.ws)
+        self.lens.add_(first[1:] - first[:-1])
 
     def evict(self, keep: int, table: torch.Tensor, first: int = 0, recent: int = 0) -> torch.Tensor:
         """Between steps, with scored: every request's layers and kv heads keep `keep` keys (asf_kv_evict) on the pages

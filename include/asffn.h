@@ -420,7 +420,11 @@ ASF_API asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *
  * scores (device fp32 [R][heads][S], request by request, by position) gains, for every
  * key before lens[r], the sum over request r's tokens and the kv head's query heads of
  * softmax_p; the positions of the call's own tokens are set to their sums, whatever
- * was there (drafted tokens that were not accepted leave nothing behind).  Positions
+ * was there.  Every token of the call counts, and nothing takes its weight off again:
+ * the call is for tokens that stay.  Drafts are attended with asf_tree_attention; once
+ * their tree is verified, the accepted tokens, appended again, go through this call by
+ * themselves, lens as it was and each seeing those before it and itself, which leaves
+ * the scores of decoding them one by one and nothing of the other drafts.  Positions
  * from lens[r] + the request's tokens on, and requests without tokens, stay as they
  * are.  S has to cover the positions seen: those from S on are skipped and flagged.
  * scores is apart from q and o.  o is asf_tree_attention's, bit for bit. */

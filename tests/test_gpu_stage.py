@@ -1,8 +1,10 @@
 """The attention stage with rotary positions, scores and adapters, captured with its layers: every stage has the
 bits of the single calls, before an eviction and after it."""
+import numpy as np
 import pytest
 import torch
 
+from oracle import attention as O
 from tests.gpu_util import ensure_built
 
 import activation_sparse_ffn_predict_b200 as A
@@ -95,3 +97,90 @@ def test_stage_refuses_what_does_not_fit():
                 lambda: A.AttentionStage(*args, outs, scored=True).evict(65, torch.zeros(1, 4, dtype=torch.int32, device="cuda"))):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("hkv,grp,D,page,turned", [(2, 4, 64, 16, True), (1, 16, 80, 20, True), (3, 8, 128, 64, False)])
+def test_drafts_leave_only_what_was_accepted(hkv, grp, D, page, turned):
+    """Trees are drafted, some of their tokens accepted: cache and scores are those of decoding the accepted ones, against
+    the definition (the tolerance of a key's score is that of tests/test_gpu_scored.py, a rounding more for each
+    step that adds to it) and against single calls."""
+    ensure_built()
+    layers, width, R, T, hq = 2, 12, 2, 8, hkv * grp
+    caches, outs, _, ffns = _model(layers, T, hkv, grp, D, page, R * width, adapters=False)
+    twins = [A.KVCache(c.k.clone(), c.v.clone()) for c in caches]
+    rot = A.Rotary(D, D // 2) if turned else None
+    stage = A.AttentionStage(caches, hq, R, width, T, outs, rotary=rot, scored=True, drafts=True)
+    st = A.LayerStack([], ffns, T, mode="dense", attention=stage)
+    stage.table.copy_(torch.randperm(R * width).int().view(R, width))
+    lens, old = [90, 41], torch.rand(stage.scores.shape, device="cuda") * 0.01
+    stage.lens.copy_(torch.tensor(lens))
+    stage.scores.copy_(old)
+    st.capture()
+    assert st.kernel_nodes() == st.launches_per_step()
+    # (tokens of each request, their parents: -1 the prefix) and what is accepted of them
+    trees = [(([-1, 0, 0, 2, 2], [-1, 0, 0]), ([0, 2, 4], [5, 7])), (([-1, -1, 1, 2], [-1, 0, 1, 2]), ([1, 2], [])),
+             (([-1], [-1, -1, 1, 2, 2, 0, 0]), ([0], [2, 3, 5]))]
+    want, err, step = old.cpu().double().numpy(), np.zeros(old.shape), 0
+    table = stage.table.cpu().numpy()
+    for parents, accepted in trees:
+        begin, anc, depth = [0], [], []
+        for tree in parents:
+            t0 = begin[-1]
+            for i, p in enumerate(tree):
+                anc.append((anc[t0 + p] if p >= 0 else 0) | 1 << (t0 + i))
+                depth.append(depth[t0 + p] + 1 if p >= 0 else 0)
+            begin.append(t0 + len(tree))
+        stage.begin.copy_(torch.tensor(begin))
+        stage.anc.copy_(torch.tensor(anc))
+        stage.pos.copy_(torch.tensor([lens[t >= begin[1]] + d for t, d in enumerate(depth)])) if turned else None
+        stage.q.normal_(), stage.k.normal_(), stage.v.normal_()
+        before = stage.scores.clone()
+        st.step()
+        assert torch.equal(stage.scores, before)                             # drafts count for nothing
+        stage.accept(accepted)
+        for l in range(layers):
+            ws = A.Workspace.for_attention(twins[l], hq, R, 1)
+            for r in range(R):                                               # token by token
+                for i, t in enumerate(accepted[r]):
+                    one = lambda x: x[l, t:t + 1].contiguous()  # noqa: E731
+                    at = [torch.tensor(v, dtype=torch.int32, device="cuda") for v in (lens, [0, 1, 1] if r == 0 else [0, 0, 1])]
+                    at[0][r] += i
+                    q = one(stage.q)
+                    if turned:
+                        A.asf_rotary_append(rot, twins[l], stage.table, *at, stage.pos[t:t + 1], q, q, one(stage.k), one(stage.v), ws)
+                    else:
+                        A.asf_kv_append(twins[l], stage.table, *at, one(stage.k), one(stage.v), ws)
+                    want[l], more = O.received(twins[l].k.cpu().numpy(), table, at[0].tolist(), at[1].tolist(), q.cpu().numpy(),
+                                               np.array([1]), D ** -0.5, want[l])
+                    err[l] += more
+            assert A.asf_read_error(ws) == 0
+        lens = [n + len(a) for n, a in zip(lens, accepted)]
+        assert stage.lens.tolist() == lens
+        step += 1
+        got = stage.scores.cpu().double().numpy()
+        tol = 2 * 2.0 ** -23 * err + step * 2.0 ** -20 * np.abs(want) + 2.0 ** -100
+        for l in range(layers):
+            for r in range(R):
+                n = lens[r]
+                assert (np.abs(got - want) <= tol)[l, r, :, :n].all()
+                assert np.array_equal(got[l, r, :, n:], old[l, r, :, n:].cpu().numpy())
+                pg, sl = (x.tolist() for x in O.positions(table[r], page, n))
+                assert torch.equal(caches[l].k[pg, sl], twins[l].k[pg, sl]) and torch.equal(caches[l].v[pg, sl], twins[l].v[pg, sl])
+    assert st.read_error() == 0
+    st.release()
+
+
+def test_accept_refuses():
+    ensure_built()
+    caches, outs, _, _ = _model(1, 4, 2, 2, 64, 16, 8, adapters=False)
+    args = (caches, 4, 2, 4, 4, outs)
+    stage = A.AttentionStage(*args, scored=True, drafts=True)
+    stage.begin.copy_(torch.tensor([0, 2, 4]))
+    stage.table.copy_(torch.arange(8).int().view(2, 4))
+    for bad in (lambda: A.AttentionStage(*args, drafts=True), lambda: A.AttentionStage(*args, scored=True).accept([[0], [2]]),
+                lambda: stage.accept([[0]]), lambda: stage.accept([[0], [1]]), lambda: stage.accept([[0, 0], [2]]),
+                lambda: stage.accept([[-1], []]), lambda: stage.accept([[], [4]])):
+        with pytest.raises(ValueError):
+            bad()
+    stage.accept([[], []])
+    assert stage.lens.tolist() == [0, 0] and not stage.scores.any()
