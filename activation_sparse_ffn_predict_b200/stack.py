@@ -266,13 +266,21 @@ class LayerStack:
         return next((e for e in [asf_read_error(w, stream) for w in spaces if w is not None] if e), 0)
 
     def capture(self, warmup: int = 2) -> None:
-        s = torch.cuda.Stream()
-        s.wait_stream(torch.cuda.current_stream())
-        with torch.cuda.stream(s):
-            for _ in range(warmup):
-                self.enqueue()
-        torch.cuda.current_stream().wait_stream(s)
-        torch.cuda.synchronize()
+        """One step as a CUDA graph.  The `warmup` steps before it leave the attention stage's scores as they are."""
+        stage, s = self.attention, torch.cuda.Stream()
+        scores = stage.scores if stage is not None else None
+        if scores is not None:                        # every layer's go to the same place, which nobody reads
+            stage.scores = torch.zeros_like(scores[0]).expand_as(scores)
+        try:
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                for _ in range(warmup):
+                    self.enqueue()
+            torch.cuda.current_stream().wait_stream(s)
+            torch.cuda.synchronize()
+        finally:
+            if scores is not None:
+                stage.scores = scores
         g = torch.cuda.CUDAGraph(keep_graph=True)     # keeps the node list readable
         with torch.cuda.graph(g):
             self.enqueue()

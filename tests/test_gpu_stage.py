@@ -184,3 +184,27 @@ def test_accept_refuses():
             bad()
     stage.accept([[], []])
     assert stage.lens.tolist() == [0, 0] and not stage.scores.any()
+
+
+def test_capture_leaves_the_scores():
+    ensure_built()
+    caches, outs, _, ffns = _model(2, 2, 2, 2, 64, 16, 8, adapters=False)
+    stage = A.AttentionStage(caches, 4, 1, 8, 2, outs, scored=True)
+    st = A.LayerStack([], ffns, 2, mode="dense", attention=stage)
+    stage.table.copy_(torch.arange(8).int().view(1, 8))
+    stage.lens.fill_(100)
+    stage.begin.copy_(torch.tensor([0, 2]))
+    stage.anc.copy_(torch.tensor([1, 3]))
+    stage.q.normal_(), stage.k.normal_(), stage.v.normal_()
+    stage.scores.uniform_()
+    before, at = stage.scores.clone(), stage.scores.data_ptr()
+    for _ in range(2):                                       # the first time, and in the middle of decoding
+        st.capture()
+        assert torch.equal(stage.scores, before) and stage.scores.data_ptr() == at
+    st.step()
+    want = before.clone()
+    for l in range(2):
+        o, ws = torch.empty_like(stage.q[l]), A.Workspace.for_attention(caches[l], 4, 1, 2, scored_pages=8)
+        A.asf_tree_attention_scored(caches[l], stage.table, stage.lens, stage.begin, stage.q[l], stage.anc, o, want[l], ws)
+    assert torch.equal(stage.scores, want) and not torch.equal(want, before) and st.read_error() == 0
+    st.release()
