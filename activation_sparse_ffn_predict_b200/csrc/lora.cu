@@ -6,8 +6,8 @@
 // Mathematics.  y = act(W x + bias + s_a B_a (A_a x)) with a token's own adapter a:
 // h = s_a A_a x has `rank` values, kept in fp32, and so is W x, so that y is rounded
 // once.  Both steps read each adapter in use once: the first token of the call that
-// has it (its leader) takes all of its tokens along, eight at a time.  A token's sums
-// are added in the same order whoever comes along.
+// has it (its leader) takes all of its tokens along, four at a time.  A token's sums
+// are added in the same order whoever comes along, and however many.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -169,15 +169,17 @@ __device__ __forceinline__ void eight(const float *p, float (&v)[8]) {
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// NB of the leader's tokens, from its token number `from` on, over `rows` rows of B in
+// The next NB of the leader's tokens (`set`) over `rows` rows of B in
 // shared memory, a thread a row.  s_h: [token][2][rank / 2], the first four values of each
 // eight ranks and the last four.  A thread begins with its own eight ranks, so that eight
-// neighbours' 16 bytes of rows that lie a multiple of 128 bytes apart are in different banks.
+// neighbours' 16 bytes of rows that lie a multiple of 128 bytes apart are in different banks;
+// which they are goes by the row of the matrix, so that a row's sum has one order in every tiling.
 template <typename T, int NB>
 __device__ __forceinline__ void up_tokens(const LoraArgs &A, const T *w, int row0, int rows, const float *s_h, uint32_t &set) {
   int tok[NB];
   const int n = take<NB>(set, tok), eights = A.rank / 8;
-  const int g = eights & -eights, rot = (threadIdx.x & 7) * min(g, 8) >> 3;
+  const int g = eights & -eights, rot = ((row0 + threadIdx.x) & 7) * min(g, 8) >> 3;
+  static_assert(kUpThreads % 8 == 0, "a thread's rows begin alike");
   for (int row = threadIdx.x; row < rows; row += kUpThreads) {
     float base[NB], acc[NB];
 #pragma unroll

@@ -356,7 +356,8 @@ ASF_API size_t asf_w4_lora_workspace_bytes(const asf_w4_matrix *mat, const asf_l
  *          `adapters` on counts as none and is flagged
  * All else as for asf_w4_matmul, with x in the adapters' dtype.  Everything between x
  * and y is fp32, y is rounded once, and a token's result does not depend on the call's
- * other tokens, nor on their adapters. */
+ * other tokens, nor on their adapters; the adapter's share not on their number either
+ * (the product's sums are split by it). */
 ASF_API asf_status asf_w4_matmul_lora(const asf_w4_matrix *mat, const asf_lora *lora, const int32_t *which, const void *x,
                                       asf_dtype xdtype, int32_t batch, const float *bias, int32_t relu, void *y,
                                       asf_dtype ydtype, void *ws, size_t ws_bytes, asf_stream_t stream);

@@ -178,3 +178,17 @@ def test_binding_refuses():
         c.run()                                              # a workspace for the plain product alone
     with pytest.raises(A.AsfError):
         A.Workspace.for_w4(c.mat, 4, lora=other)
+
+
+@pytest.mark.parametrize("dt", ["f16", "f32"])
+@pytest.mark.parametrize("m,rank", [(4096, 48), (4096, 96), (1003, 80), (2000, 112), (4096, 240), (700, 64)])
+def test_the_adapters_share_does_not_depend_on_the_batch(m, rank, dt):
+    """Over weights of zero, so that the product is zero for every number of tokens: a token's bits alone, with another,
+    and as one of 8 and of 32, whose calls lay out rows of B in other tiles."""
+    c = Case(m, 256, 32, rank, 8, dt, 128, which=[b % 8 for b in range(32)], seed=11)
+    c.mat = A.W4Matrix.quantize(torch.zeros(m, 256, device="cuda"), 128)
+    want = c.run(bias=True)
+    x, which = c.x, c.which
+    for first, B in ((0, 1), (7, 1), (2, 2), (0, 8), (5, 8), (1, 31)):
+        c.B, c.x, c.which = B, x[first:first + B].contiguous(), which[first:first + B].contiguous()
+        assert torch.equal(c.run(bias=True), want[first:first + B]), (first, B)
