@@ -131,15 +131,16 @@ class AttentionStage:
 
     def evict(self, keep: int, table: torch.Tensor, first: int = 0, recent: int = 0) -> torch.Tensor:
         """Between steps, with scored: every request's layers and kv heads keep `keep` keys (asf_kv_evict) on the pages
-        of `table` int32 [R, pages], which are then the stage's.  Returns the kept positions int32 [layers, R, heads, keep].
+        of `table` int32 [R, pages], which have room for them and are then the stage's.  Returns the kept positions int32 [layers, R, heads, keep].
 
         The stage's table, lens and scores go over to what is left, in place, so that a captured stack runs on.  Past
         `table`'s columns its own then lists no page (-1): the old ones are the caller's again."""
         if self.scores is None:
             raise ValueError("eviction goes by the scores of a scored stage")
         n, R, heads, S = self.scores.shape
-        if table.dim() != 2 or table.shape[0] != R or table.shape[1] > self.max_pages or keep > S:
-            raise ValueError("table must be [R, pages] with at most the stage's pages, and keep fit its scores")
+        if table.dim() != 2 or table.shape[0] != R or table.shape[1] > self.max_pages or keep > S \
+                or table.shape[1] * self.caches[0].page < keep:
+            raise ValueError("table must be [R, pages] with at most the stage's pages, and keep fit them and its scores")
         kept = torch.zeros(n, R, heads, keep, dtype=torch.int32, device=self.scores.device)
         lens, scores = torch.empty_like(self.lens), torch.zeros_like(self.scores[0])
         for l, cache in enumerate(self.caches):

@@ -208,3 +208,20 @@ def test_capture_leaves_the_scores():
         A.asf_tree_attention_scored(caches[l], stage.table, stage.lens, stage.begin, stage.q[l], stage.anc, o, want[l], ws)
     assert torch.equal(stage.scores, want) and not torch.equal(want, before) and st.read_error() == 0
     st.release()
+
+
+def test_evict_refuses_a_table_that_keep_does_not_fit():
+    ensure_built()
+    caches, outs, _, _ = _model(2, 1, 2, 2, 64, 16, 12, adapters=False)
+    stage = A.AttentionStage(caches, 4, 1, 8, 1, outs, scored=True)
+    table = torch.arange(8).int().view(1, 8).cuda()
+    stage.table.copy_(table)
+    stage.lens.fill_(120)
+    stage.scores.uniform_()
+    scores, fresh = stage.scores.clone(), torch.arange(8, 12).int().view(1, 4).cuda()
+    for keep, pages in ((17, 1), (64, 3), (65, 4), (128, 4)):
+        with pytest.raises(ValueError):
+            stage.evict(keep, fresh[:, :pages].contiguous())
+        assert torch.equal(stage.table, table) and stage.lens.tolist() == [120] and torch.equal(stage.scores, scores)
+    stage.evict(64, fresh)                                   # exactly
+    assert stage.lens.tolist() == [64] and A.asf_read_error(stage.ws) == 0
