@@ -379,6 +379,32 @@ bool apart(int T, int heads, int64_t ts, int64_t hs, int D) {
          (heads == 1 || T == 1 || ts >= (heads - 1) * hs + D || hs >= (T - 1) * ts + D);
 }
 
+// f / 2 pi modulo 1 in units of 2^-64, rounded to the nearest: |f| < 2^100 is a whole number
+// below 2^53 times a power of two, 1 / 2 pi is taken to 192 bits, and their product is
+// exact, so that what is rounded is off by less than 2^-28 units.
+void turns_of(double f, uint64_t &out) {
+  static const uint64_t inv[3] = {0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull, 0x28be60db9391054aull};
+  int e;
+  const uint64_t whole = (uint64_t)std::ldexp(std::frexp(std::fabs(f), &e), 53);   // |f| = whole 2^(e - 53)
+  uint64_t p[4];                       // whole / 2 pi in units of 2^-192
+  unsigned __int128 carry = 0;
+  for (int i = 0; i < 3; ++i) {
+    carry += (unsigned __int128)whole * inv[i];
+    p[i] = (uint64_t)carry;
+    carry >>= 64;
+  }
+  p[3] = (uint64_t)carry;
+  auto bits = [&](int at) {            // 64 of them
+    const int w = at / 64, o = at % 64;
+    uint64_t v = w < 4 ? p[w] >> o : 0;
+    if (o && w + 1 < 4) v |= p[w + 1] << (64 - o);
+    return v;
+  };
+  const int from = 192 - 64 + 53 - e;  // of the unit; 81 at least
+  const uint64_t t = bits(from) + (bits(from - 1) & 1);
+  out = f < 0. ? 0 - t : t;
+}
+
 template <typename T>
 cudaError_t run_rotary(const RotArgs &a, int layout, dim3 grid, size_t smem, cudaStream_t st) {
   return layout == ASF_ROTARY_PAIRS          ? launch(k_rotary<T, true>, grid, dim3(kRotThreads), smem, st, a)
@@ -424,12 +450,8 @@ asf_status asf_rotary_frequencies(int32_t rot_dim, double base, int32_t scaling,
 asf_status asf_rotary_turns(const double *freq, int32_t n, uint64_t *turns_out) {
   if (!freq || !turns_out || n < 1) return ASF_ERR_INVALID_ARG;
   for (int i = 0; i < n; ++i)
-    if (!std::isfinite(freq[i])) return ASF_ERR_INVALID_ARG;
-  for (int i = 0; i < n; ++i) {
-    const long double t = (long double)freq[i] / (2.L * 3.14159265358979323846264338327950288L);
-    const long double whole = std::round((t - std::floor(t)) * 18446744073709551616.L);
-    turns_out[i] = whole >= 18446744073709551616.L ? 0ull : (uint64_t)whole;
-  }
+    if (!(std::fabs(freq[i]) < 0x1p100)) return ASF_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i) turns_of(freq[i], turns_out[i]);
   return ASF_OK;
 }
 

@@ -501,7 +501,7 @@ typedef struct {
 ASF_API asf_status asf_rotary_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor, double original,
                                           double *freq_out, float *scale_out);
 
-/* Host: freq [n] (any finite values, radians per position) as turns modulo 1, in
+/* Host: freq [n] (radians per position, below 2^100 in size) as turns modulo 1, in
  * units of 2^-64, rounded to the nearest. */
 ASF_API asf_status asf_rotary_turns(const double *freq, int32_t n, uint64_t *turns_out);
 

@@ -126,3 +126,23 @@ def test_append_refuses(lib):
         assert app(**kw) == L.ASF_ERR_MISALIGNED, kw
     for kw in (dict(qo=FAKE + 16), dict(qo=FAKE, qs=512), dict(q=4 * FAKE, qo=FAKE), dict(q=4 * FAKE, k=8 * FAKE, qo=FAKE + 32)):
         assert app(wsb=4096, **kw) == L.ASF_ERR_INVALID_ARG, kw
+
+
+def test_turns_are_rounded_once(lib):
+    """Half a unit off at most, whatever the size (2^-20 for what the 80 digits here and the 192 bits there leave)."""
+    rng = np.random.default_rng(3)
+    f = (rng.standard_normal(400) * 2.0 ** rng.integers(-80, 97, 400)).tolist()
+    f += [1.0, -1.0, 1e9, -1e9, 2.0 ** 53 + 2, 6.283185307179586, -6.283185307179586, 0.99, np.nextafter(2.0 ** 100, 0), 5e-324, -5e-324, 0.0]
+    out = (ctypes.c_uint64 * len(f))()
+    assert lib.asf_rotary_turns((ctypes.c_double * len(f))(*f), len(f), out) == L.ASF_OK
+    pi = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+    for x, got in zip(f, out):
+        t = Fraction(x) / (2 * pi)
+        off = abs(got - (t - math.floor(t)) * 2 ** 64)
+        assert min(off, 2 ** 64 - off) <= Fraction(1, 2) + Fraction(1, 2 ** 20), x
+
+
+@pytest.mark.parametrize("f", [2.0 ** 100, -(2.0 ** 100), 1e300, float("inf")])
+def test_turns_refuse_what_has_no_fraction_left(lib, f):
+    out = (ctypes.c_uint64 * 2)(7, 7)
+    assert lib.asf_rotary_turns((ctypes.c_double * 2)(1.0, f), 2, out) == L.ASF_ERR_INVALID_ARG and list(out) == [7, 7]
