@@ -20,6 +20,12 @@ inline asf_status check_cache(const asf_kv_cache *c) {
     return ASF_ERR_INVALID_ARG;
   return ASF_OK;
 }
+// whether bytes lie between the first and the last of the cache's keys, or of its values
+inline bool in_cache(const asf_kv_cache *c, const void *p, size_t bytes) {
+  const size_t span = 2 * ((size_t)(c->pages - 1) * c->page_stride + (size_t)(c->page - 1) * c->token_stride +
+                           (size_t)(c->heads - 1) * c->head_stride + c->head_dim);
+  return overlap(p, bytes, c->k, span) || overlap(p, bytes, c->v, span);
+}
 inline asf_status check_requests(const int32_t *table, int max_pages, int R, const int32_t *lens, const int32_t *begin, int T) {
   if (!table || !lens || !begin) return ASF_ERR_INVALID_ARG;
   if (max_pages < 1 || R < 1 || R > ASF_MAX_BATCH || T < 1 || T > ASF_MAX_BATCH) return ASF_ERR_INVALID_ARG;

@@ -512,7 +512,8 @@ asf_status asf_rotary_append(const asf_rotary *rot, const asf_kv_cache *cache, c
   const size_t out = (size_t)T * qw * 2;
   const bool in_place = q == q_out && (T == 1 || q_stride == qw);
   if (!in_place && overlap(q, ((size_t)(T - 1) * q_stride + qw) * 2, q_out, out)) return ASF_ERR_INVALID_ARG;
-  if (overlap(k, ((size_t)(T - 1) * k_stride + kw) * 2, q_out, out) || overlap(v, ((size_t)(T - 1) * v_stride + kw) * 2, q_out, out))
+  if (overlap(k, ((size_t)(T - 1) * k_stride + kw) * 2, q_out, out) ||
+      overlap(v, ((size_t)(T - 1) * v_stride + kw) * 2, q_out, out) || in_cache(cache, q_out, out))
     return ASF_ERR_INVALID_ARG;
   RotAppendArgs a{*cache, table, max_pages, R, T, lens, begin, pos, q_heads, rot->rot_dim / 2, rot->turns, rot->scale,
                   static_cast<const __half *>(q), static_cast<const __half *>(k), static_cast<const __half *>(v),

@@ -520,7 +520,8 @@ ASF_API asf_status asf_rotary_apply(const asf_rotary *rot, const void *x, asf_dt
  * (contiguous) becomes q turned.  q, k and v are fp16, their heads contiguous, their
  * tokens q_stride, k_stride and v_stride elements apart (multiples of 8, at least a
  * token's width): slices of one joint projection.  Tokens outside every range take no
- * part.  q_out may be q where q is contiguous, else it is apart from q, k, v and the cache.
+ * part.  q_out may be q where q is contiguous, else it is apart from q, k and v; and from
+ * the cache, from the first to the last byte of its keys and of its values.
  *   pos    device int32 [T], the tokens' positions: not lens[r] + i where tokens of a
  *          tree are alternatives, or where keys have been evicted
  * Everything else, and errors, as for asf_kv_append. */

@@ -146,3 +146,18 @@ def test_turns_are_rounded_once(lib):
 def test_turns_refuse_what_has_no_fraction_left(lib, f):
     out = (ctypes.c_uint64 * 2)(7, 7)
     assert lib.asf_rotary_turns((ctypes.c_double * 2)(1.0, f), 2, out) == L.ASF_ERR_INVALID_ARG and list(out) == [7, 7]
+
+
+def test_append_refuses_queries_over_the_cache(lib):
+    k, v = 16 * FAKE, 32 * FAKE
+    c = L.asf_kv_cache(10, 16, 2, 64, k, v, 2048, 128, 64)
+    last, out = (9 * 2048 + 15 * 128 + 64 + 64) * 2, 3 * 4 * 64 * 2
+
+    def app(qo, wsb=4096, q=FAKE):
+        return lib.asf_rotary_append(_rot(), ctypes.byref(c), FAKE, 4, 2, FAKE, FAKE, 3, FAKE, 4, q, 256, qo, 2 * FAKE, 128,
+                                     4 * FAKE, 128, FAKE, wsb, None)
+
+    for at in (k, v):
+        for qo in (at, at + last - 16, at - out + 16):
+            assert app(qo) == app(qo, q=qo) == L.ASF_ERR_INVALID_ARG
+    assert app(k + last, wsb=4095) == L.ASF_ERR_WORKSPACE
