@@ -334,10 +334,20 @@ asf_status asf_kv_evict(const asf_kv_cache *cache, const int32_t *table, int32_t
     return ASF_ERR_MISALIGNED;
   s = check_ws(ws, ws_bytes, kHeaderBytes);
   if (s != ASF_OK) return s;
-  const size_t rows = (size_t)R * cache->heads * 4, in = rows * S, out = rows * S_out, list = rows * keep;
-  if (overlap(scores, in, scores_out, out) || overlap(scores, in, kept, list) || overlap(scores_out, out, kept, list) ||
-      overlap(lens, (size_t)R * 4, lens_out, (size_t)R * 4))
-    return ASF_ERR_INVALID_ARG;
+  const size_t rows = (size_t)R * cache->heads * 4;
+  struct Range {
+    const void *p;
+    size_t bytes;
+  };
+  const Range in[] = {{table, (size_t)R * max_pages * 4}, {table_out, (size_t)R * max_pages_out * 4}, {lens, (size_t)R * 4}, {scores, rows * S}};
+  const Range out[] = {{lens_out, (size_t)R * 4}, {scores_out, rows * S_out}, {kept, rows * keep}};
+  for (int i = 0; i < 3; ++i) {
+    if (in_cache(cache, out[i].p, out[i].bytes)) return ASF_ERR_INVALID_ARG;
+    for (const Range &u : in)
+      if (overlap(u.p, u.bytes, out[i].p, out[i].bytes)) return ASF_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[j].p, out[j].bytes, out[i].p, out[i].bytes)) return ASF_ERR_INVALID_ARG;
+  }
   EvictArgs a{*cache, table, table_out, max_pages, max_pages_out, R, lens, lens_out, scores, scores_out, S, S_out, kept,
               keep, first, recent, 0, &static_cast<Header *>(ws)->err};
   cudaStream_t st = (cudaStream_t)stream;

@@ -455,7 +455,8 @@ ASF_API asf_status asf_tree_attention_scored(const asf_kv_cache *cache, const in
  *
  * Bad pages, lengths below 0 or past S or the table, and kept keys past table_out
  * are skipped, clamped and flagged as for asf_tree_attention.  ws: at least 4096
- * bytes, for the error word.  Outputs are apart from inputs and from one another. */
+ * bytes, for the error word.  Outputs are apart from inputs and from one another, from
+ * the cache as asf_rotary_append's. */
 ASF_API asf_status asf_kv_evict(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
                                 const int32_t *lens, const float *scores, int32_t S, int32_t keep, int32_t first,
                                 int32_t recent, const int32_t *table_out, int32_t max_pages_out, int32_t *lens_out,

@@ -36,3 +36,27 @@ def test_arguments_refused(lib):
                dict(lo=2 * FAKE + 4)):
         assert ev(wsb=4096, **kw) == L.ASF_ERR_INVALID_ARG, kw
     assert ev(cache=L.asf_kv_cache(10, 16, 2, 60, FAKE, FAKE, 2048, 128, 64)) == L.ASF_ERR_MISALIGNED
+
+
+def test_outputs_over_inputs_refused(lib):
+    """Each of lens_out, scores_out and kept at the first and the last word of every input, of the cache and of another output."""
+    R, heads, mp, mpo, S, So, keep = 2, 2, 4, 2, 64, 40, 32
+    c = L.asf_kv_cache(10, 16, heads, 64, 16 * FAKE, 32 * FAKE, 2048, 128, 64)
+    rows, span = R * heads * 4, (9 * 2048 + 15 * 128 + 64 + 64) * 2
+    place = dict(table=FAKE, lens=2 * FAKE, sc=3 * FAKE, to=4 * FAKE, lo=5 * FAKE, so=6 * FAKE, kept=7 * FAKE)
+    size = dict(table=R * mp * 4, lens=R * 4, sc=rows * S, to=R * mpo * 4, lo=R * 4, so=rows * So, kept=rows * keep)
+
+    def ev(wsb=4096, **kw):
+        p = dict(place, **kw)
+        return lib.asf_kv_evict(ctypes.byref(c), p["table"], mp, R, p["lens"], p["sc"], S, keep, 4, 8, p["to"], mpo, p["lo"], p["so"],
+                                So, p["kept"], 8 * FAKE, wsb, None)
+
+    assert ev(wsb=4095) == L.ASF_ERR_WORKSPACE
+    for out in ("lo", "so", "kept"):
+        for other in place:
+            if other != out:
+                for at in (place[other], place[other] + size[other] - 4, place[other] - size[out] + 4):
+                    assert ev(**{out: at}) == L.ASF_ERR_INVALID_ARG, (out, other)
+        for base in (16 * FAKE, 32 * FAKE):
+            for at in (base, base + span - 4, base - size[out] + 4):
+                assert ev(**{out: at}) == L.ASF_ERR_INVALID_ARG, (out, base)
