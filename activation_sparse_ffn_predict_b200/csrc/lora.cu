@@ -26,6 +26,10 @@ constexpr int kUpThreads = 128;
 constexpr int kUpCtas = 3;             // of an SM, where its shared memory holds them
 constexpr int kUpStages = 4, kUpStage = 16 * 1024;
 constexpr int kUpRows = 256;           // of a stage at most
+// Dynamic shared memory with which kUpCtas of them are on an SM: beside it each has its static part and 1 KB that
+// the system keeps (28672 x 8192, 22 tokens of as many adapters of rank 128, 75 KB: 99 us with two CTAs an SM,
+// 111 with three, of which the third waits).
+constexpr size_t kUpShared = 228 * 1024 / kUpCtas - 1024 - 512;
 constexpr int kAlong = 4;              // tokens at a time
 constexpr uint64_t kUpWaitNs = 200ull * 1000 * 1000;   // bound on any mbarrier wait
 
@@ -391,7 +395,7 @@ asf_status asf_w4_matmul_lora(const asf_w4_matrix *mat, const asf_lora *lora, co
   const int tile = (int)std::min<int64_t>({kUpRows, kUpStage / (a.rank * (xdtype == ASF_F16 ? 2 : 4)), std::max<int64_t>(32, even)});
   const int64_t pairs = ((int64_t)a.rows + tile - 1) / tile * std::min(B, a.adapters);
   const size_t smem = (size_t)kUpStages * kUpStage + (size_t)B * a.rank * 4;
-  const int ctas = smem <= 75 * 1024 ? kUpCtas : 2;                      // as many as an SM's shared memory holds
+  const int ctas = smem <= kUpShared ? kUpCtas : 2;                      // as many as an SM's shared memory holds
   const dim3 grid((unsigned)std::min<int64_t>(std::max<int64_t>(pairs, 1), (int64_t)ctas * sm_count()));
   e = xdtype == ASF_F16 ? launch(k_lora_up<__half>, grid, dim3(kUpThreads), smem, st, a, tile)
                         : launch(k_lora_up<float>, grid, dim3(kUpThreads), smem, st, a, tile);

@@ -192,3 +192,26 @@ def test_the_adapters_share_does_not_depend_on_the_batch(m, rank, dt):
     for first, B in ((0, 1), (7, 1), (2, 2), (0, 8), (5, 8), (1, 31)):
         c.B, c.x, c.which = B, x[first:first + B].contiguous(), which[first:first + B].contiguous()
         assert torch.equal(c.run(bias=True), want[first:first + B]), (first, B)
+
+
+@pytest.mark.parametrize("B,rank", [(8, 64), (21, 128), (22, 128), (32, 88), (32, 96), (32, 256)])
+def test_the_up_steps_grid_is_resident_at_once(B, rank):
+    """Its CTAs take equal runs, so one that waits for another to end would double the time."""
+    from cuda.bindings import driver as cu
+    c = Case(20000, 64, B, rank, B, group=64, which=list(range(B)), seed=13)
+    c.run()
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g):
+        y = c.run()
+    graph = cu.CUgraph(init_value=g.raw_cuda_graph())
+    nodes = cu.cuGraphGetNodes(graph, cu.cuGraphGetNodes(graph, 0)[2])[1]
+    kernels = [n for n in nodes if cu.cuGraphNodeGetType(n)[1] == cu.CUgraphNodeType.CU_GRAPH_NODE_TYPE_KERNEL]
+    up = [p for p in (cu.cuGraphKernelNodeGetParams(n)[1] for n in kernels) if p.sharedMemBytes == 4 * 16384 + B * rank * 4]
+    assert len(up) == 1
+    dev = torch.cuda.get_device_properties(0)
+    each = up[0].sharedMemBytes + 1024 + (4 * 8 + 2 * 32 * 4)          # its own static part, and the system's
+    assert -(-up[0].gridDimX // dev.multi_processor_count) * each <= dev.shared_memory_per_multiprocessor
+    g.instantiate()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, c.run())
