@@ -52,68 +52,53 @@ __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
 __device__ __forceinline__ void from_f(float v, float &to) { to = v; }
 __device__ __forceinline__ void from_f(float v, __half &to) { to = __float2half_rn(v); }
 
-// Columns of an access to what passes: as many as VEC pairs have, 16 bytes at most.
-template <typename T, int VEC>
-__host__ __device__ constexpr int pass_columns() { return 2 * VEC * sizeof(T) <= 16 ? 2 * VEC : VEC; }
-
-// (k_rotary_append) VEC pairs of a head: halves are `half` columns apart, neighbours side by side (one
-// access where they are 16 bytes at most).
-template <typename T, int VEC, bool PAIRS>
+// (k_rotary_append) VEC pairs of a head, 4 at most: halves are `half` columns apart, neighbours side by side in one access.
+template <int VEC, bool PAIRS>
 struct Pairs {
-  Pack<T, VEC> a, b;
-  static constexpr int kPass = pass_columns<T, VEC>();
-  static constexpr bool kOne = PAIRS && kPass == 2 * VEC;
-  __device__ __forceinline__ static int second(int j, int half) { return PAIRS ? 2 * j * VEC + VEC : half + j * VEC; }
-  __device__ __forceinline__ void load(const T *row, int j, int half) {
-    if constexpr (kOne) {
-      load_pass(row + 2 * j * VEC);
+  static constexpr int kPass = 2 * VEC;            // columns of an access to what passes
+  Pack<__half, VEC> a, b;
+  __device__ __forceinline__ void load(const __half *row, int j, int half) {
+    if constexpr (PAIRS) {
+      load_pass(row + j * kPass);
     } else {
-      a = *reinterpret_cast<const Pack<T, VEC> *>(row + (PAIRS ? 2 : 1) * j * VEC);
-      b = *reinterpret_cast<const Pack<T, VEC> *>(row + second(j, half));
+      a = *reinterpret_cast<const Pack<__half, VEC> *>(row + j * VEC);
+      b = *reinterpret_cast<const Pack<__half, VEC> *>(row + half + j * VEC);
     }
   }
-  __device__ __forceinline__ void store(T *row, int j, int half) const {
-    if constexpr (kOne) {
-      store_pass(row + 2 * j * VEC);
+  __device__ __forceinline__ void store(__half *row, int j, int half) const {
+    if constexpr (PAIRS) {
+      store_pass(row + j * kPass);
     } else {
-      *reinterpret_cast<Pack<T, VEC> *>(row + (PAIRS ? 2 : 1) * j * VEC) = a;
-      *reinterpret_cast<Pack<T, VEC> *>(row + second(j, half)) = b;
+      *reinterpret_cast<Pack<__half, VEC> *>(row + j * VEC) = a;
+      *reinterpret_cast<Pack<__half, VEC> *>(row + half + j * VEC) = b;
     }
   }
   // kPass columns, as they are
-  __device__ __forceinline__ void load_pass(const T *p) {
-    if constexpr (kPass == VEC) {
-      a = *reinterpret_cast<const Pack<T, VEC> *>(p);
-    } else {
-      const Pack<T, kPass> u = *reinterpret_cast<const Pack<T, kPass> *>(p);
+  __device__ __forceinline__ void load_pass(const __half *p) {
+    const Pack<__half, kPass> u = *reinterpret_cast<const Pack<__half, kPass> *>(p);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        a.v[i] = u.v[i];
-        b.v[i] = u.v[VEC + i];
-      }
+    for (int i = 0; i < VEC; ++i) {
+      a.v[i] = u.v[i];
+      b.v[i] = u.v[VEC + i];
     }
   }
-  __device__ __forceinline__ void store_pass(T *p) const {
-    if constexpr (kPass == VEC) {
-      *reinterpret_cast<Pack<T, VEC> *>(p) = a;
-    } else {
-      Pack<T, kPass> u;
+  __device__ __forceinline__ void store_pass(__half *p) const {
+    Pack<__half, kPass> u;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        u.v[i] = a.v[i];
-        u.v[VEC + i] = b.v[i];
-      }
-      *reinterpret_cast<Pack<T, kPass> *>(p) = u;
+    for (int i = 0; i < VEC; ++i) {
+      u.v[i] = a.v[i];
+      u.v[VEC + i] = b.v[i];
     }
+    *reinterpret_cast<Pack<__half, kPass> *>(p) = u;
   }
   // cs[i]: cos and sin of the i-th pair
   __device__ __forceinline__ void turn(const float2 *cs) {
-    Pack<T, VEC> x = a, y = b;
+    const Pack<__half, VEC> x = a, y = b;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       // element 2i and 2i + 1 of the 2 VEC where neighbours are paired
-      T &u = PAIRS ? (2 * i < VEC ? a.v[(2 * i) % VEC] : b.v[(2 * i) % VEC]) : a.v[i];
-      T &w = PAIRS ? (2 * i + 1 < VEC ? a.v[(2 * i + 1) % VEC] : b.v[(2 * i + 1) % VEC]) : b.v[i];
+      __half &u = PAIRS ? (2 * i < VEC ? a.v[(2 * i) % VEC] : b.v[(2 * i) % VEC]) : a.v[i];
+      __half &w = PAIRS ? (2 * i + 1 < VEC ? a.v[(2 * i + 1) % VEC] : b.v[(2 * i + 1) % VEC]) : b.v[i];
       const float fu = to_f(PAIRS ? (2 * i < VEC ? x.v[(2 * i) % VEC] : y.v[(2 * i) % VEC]) : x.v[i]);
       const float fw = to_f(PAIRS ? (2 * i + 1 < VEC ? x.v[(2 * i + 1) % VEC] : y.v[(2 * i + 1) % VEC]) : y.v[i]);
       const float c = cs[i].x, s = cs[i].y;
@@ -309,7 +294,7 @@ template <int VEC, bool PAIRS>
 __global__ void __launch_bounds__(128) k_rotary_append(RotAppendArgs A) {
   pdl_wait();
   pdl_trigger();
-  const int D = A.c.head_dim, turned = A.half / VEC, kPass = pass_columns<__half, VEC>(), per = turned + (D - 2 * A.half) / kPass;
+  const int D = A.c.head_dim, turned = A.half / VEC, kPass = 2 * VEC, per = turned + (D - 2 * A.half) / kPass;
   const int qk = (A.q_heads + A.c.heads) * per, each = qk + A.c.heads * (D / 8), total = A.T * each;
   const int i = blockIdx.x * blockDim.x + threadIdx.x, at = min(i, total - 1);
   const int tok = at / each, in = at - tok * each;
@@ -320,7 +305,7 @@ __global__ void __launch_bounds__(128) k_rotary_append(RotAppendArgs A) {
   const bool query = !value && head < A.q_heads;
   if (!value && !query) head -= A.q_heads;
   const __half *from = (value ? A.v + tok * A.vt : query ? A.q + tok * A.qt : A.k + tok * A.kt) + (int64_t)head * D;
-  Pairs<__half, VEC, PAIRS> x;
+  Pairs<VEC, PAIRS> x;
   uint4 whole = make_uint4(0, 0, 0, 0);
   const int col = value ? c * 8 : 2 * A.half + (c - turned) * kPass;
   const bool turns = !value && c < turned;
