@@ -40,7 +40,12 @@ def _stream(stream) -> ctypes.c_void_p:
 
 def _arg(t: torch.Tensor, name: str, device, dtype=None) -> int:
     """Address of a contiguous tensor on ``device``."""
-    return _ptr(t, name, device.index, t.dtype if dtype is None and isinstance(t, torch.Tensor) else dtype)
+    try:
+        if t.get_device() == device.index and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(t, name, device.index, t.dtype if dtype is None and isinstance(t, torch.Tensor) else dtype)   # raises
 
 
 def _ptr(t: torch.Tensor, name: str, index: int, dtype) -> int:
