@@ -1182,7 +1182,10 @@ cudaError_t run_attn_any(const AttnArgs &a, int wm, int units, cudaStream_t st) 
 }
 
 // Rows' references and sums, and their scores: of k_tree_attn's calls, and up to
-// kKeptScores bytes (a table may be far wider than its requests are long).
+// kKeptScores bytes.  That bounds the workspace, whose size goes by the table's width; it is not where
+// the two forms meet, keeping is faster at every length.  8 requests, 64 query heads, us with scores kept and, in a
+// table for 262208 keys that are past the bound, with the keys read again (pages of 64 by tcgen05, of 20 by
+// mma.sync): 1000 keys each 21.4, 25.8 and 34.8, 4000 keys 41.2, 52.3 and 83.0, 16000 keys 119, 150 and 286.
 constexpr int64_t kKeptScores = 512 << 20;
 int64_t kept_scores(const asf_kv_cache *c, int q_heads, int R, int T, int max_pages) {
   const int64_t zs = ((int64_t)max_pages * c->page + kTile - 1) / kTile * kTile, all = zs * T * q_heads * 4;
@@ -1263,9 +1266,10 @@ asf_status tree_attention(const asf_kv_cache *cache, const int32_t *table, int32
   cudaError_t e = attn_dp(cache) == 64 ? run_attn_any<64>(a, wm, units, st) : run_attn_any<128>(a, wm, units, st);
   a.mt = 16 * wm;
   // The sum of kept scores need not wait for the merge where requests have few splits
-  // to join.  us of the call behind the merge, and beside it: 8 requests of up to 1000 keys
-  // 20.0 and 18.4, 4000 keys 28.0 and 26.7, one of 4000 keys 26.7 and 24.6; 8 of up to
-  // 16000 keys 60.5 and 62.1.
+  // to join.  us of the call behind the merge, and beside it: 8 requests of 1000 keys each
+  // 22.9 and 21.3, 4000 keys 41.8 and 41.2, 8000 keys 68.0 and 68.0, 12000 keys 91.2 and 91.9, 16000 keys 118.5 and
+  // 120.0; a single one of 4000 keys 17.0 and 15.8, 8000 keys 19.1 and 18.0 (which would gain as much, 1.5 us, at 16000 keys,
+  // 27.1 and 25.3, and 32000; what the host does not know is how long the requests of a wide table are).
   a.beside = a.z && keys > (int64_t)whole * kTile && keys <= 8192;
   if (e == cudaSuccess && scores) e = run_scores(a, st);
   return cuda_status(e);

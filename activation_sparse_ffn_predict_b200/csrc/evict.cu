@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(EvictArgs A) {
 }
 
 // The kept rows to their new places: a row's two places by a thread each, then 16
-// bytes of keys and of values a thread at a time.  HBM bounds it: 402 MB in 80 us.
+// bytes of keys and of values a thread at a time.  HBM bounds it: 402 MB in 71 us, 5.7 TB/s.
 __global__ void __launch_bounds__(kMoveThreads) k_evict_move(EvictArgs A) {
   __shared__ int64_t s_from[kMoveRows], s_to[kMoveRows];
   pdl_wait();

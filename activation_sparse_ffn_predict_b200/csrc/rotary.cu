@@ -32,7 +32,11 @@ constexpr int kRotThreads = 128;
 // halves, us with 4, 2 and 1: 79, 60, 57).
 constexpr int kAheadHalf = 1, kAheadPairs = 2;
 static_assert(ASF_MAX_ROTARY_DIM / 4 <= kRotThreads, "a head's places are a CTA's");
-constexpr int kItems = 9;              // chunks of a thread where there is work for every SM
+// Chunks of a thread where there is work for every SM: more share the cosines, fewer leave more
+// CTAs to hide loads.  8192 tokens, us with 3, 6, 9 and 18: 72 heads of 128 in halves 54.2, 53.5, 55.0,
+// 61.0, 40 heads 31.0, 31.6, 32.8, 34.9, 128 heads 93.0, 92.1, 93.0, 98.0; 72 heads in pairs 68.3, 63.3, 61.0, 65.3,
+// 126 of 128 columns in halves 103, 91, 81, 78, 24 of 96 columns 96, 81, 71, 65.
+constexpr int kItems = 9;
 
 __device__ __forceinline__ float2 cos_sin(int pos, uint64_t turns, float mul) {
   const uint64_t phase = (uint64_t)(int64_t)pos * turns;
@@ -216,8 +220,9 @@ __global__ void __launch_bounds__(kRotThreads) k_rotary(RotArgs A) {
 // Halves that are not whole 16 bytes: a thread has 16 bytes of a head, and finds the
 // other halves of its pairs in shared memory, where the CTA lays out a group of heads
 // (two buffers: a barrier a group), the next group's chunk in flight meanwhile.
-// 8192 tokens x 72 heads, 126 of 128 columns in fp16: 82 us (a pair a thread in 2-byte
-// accesses 171).
+// 8192 tokens x 72 heads, 126 of 128 columns in fp16: 81 us (a pair a thread in 2-byte
+// accesses 171), 24 of 96 columns 71: 3.7 and 3.2 TB/s, the barrier a group of heads and two reads of shared
+// memory a pair.
 template <typename T>
 __global__ void __launch_bounds__(kRotThreads) k_rotary_odd(RotArgs A) {
   constexpr int U = 16 / (int)sizeof(T);

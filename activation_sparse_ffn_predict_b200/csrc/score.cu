@@ -144,7 +144,9 @@ __global__ void __launch_bounds__(kSumThreads) k_score_sum(AttnArgs A) {
 
 // ------------------------------------- keys again, any page size: mma.sync --
 // For pages that TMA does not take in whole tiles.  A tile of 64 keys is multiplied with
-// all of the request's rows, 16 at a time, a warp every fourth group of them.
+// all of the request's rows, 16 at a time, a warp every fourth group of them.  16 tokens x 64 heads over 65500 keys
+// in pages of 20: 302 us with the attention, 82 without (in pages of 64, k_score_tc, 97): the exponentials and
+// one tile in flight a CTA, whose loads nothing overlaps.
 template <int DP>
 __global__ void __launch_bounds__(128) k_tree_score(AttnArgs A) {
   constexpr int CH = DP / 8;

@@ -428,7 +428,10 @@ ASF_API asf_status asf_tree_attention(const asf_kv_cache *cache, const int32_t *
  * the scores of decoding them one by one and nothing of the other drafts.  Positions
  * from lens[r] + the request's tokens on, and requests without tokens, stay as they
  * are.  S has to cover the positions seen: those from S on are skipped and flagged.
- * scores is apart from q and o.  o is asf_tree_attention's, bit for bit. */
+ * scores is apart from q and o.  o is asf_tree_attention's, bit for bit.
+ * The workspace may hold every row's scores, 4 bytes for each token, query head and
+ * position that the table has room for, up to 512 MB; it is needed during the call
+ * alone, so that calls one after the other share it. */
 ASF_API size_t asf_attention_scored_workspace_bytes(const asf_kv_cache *cache, int32_t q_heads, int32_t R, int32_t T,
                                                     int32_t max_pages);
 ASF_API asf_status asf_tree_attention_scored(const asf_kv_cache *cache, const int32_t *table, int32_t max_pages, int32_t R,
