@@ -225,3 +225,29 @@ def test_evict_refuses_a_table_that_keep_does_not_fit():
         assert torch.equal(stage.table, table) and stage.lens.tolist() == [120] and torch.equal(stage.scores, scores)
     stage.evict(64, fresh)                                   # exactly
     assert stage.lens.tolist() == [64] and A.asf_read_error(stage.ws) == 0
+
+
+def test_accepting_a_whole_chain_is_a_scored_step():
+    """32 tokens (the last one's mask is the sign bit): the same call, so the same bits."""
+    ensure_built()
+    T, D, page = 32, 64, 16
+    caches, outs, _, ffns = _model(2, T, 2, 4, D, page, 16, adapters=False)
+    twins = [A.KVCache(c.k.clone(), c.v.clone()) for c in caches]
+    stages = [A.AttentionStage(c, 8, 2, 8, T, outs, scored=True, drafts=d) for c, d in ((caches, False), (twins, True))]
+    fill = [torch.randn_like(t) for t in (stages[0].q, stages[0].k, stages[0].v)]
+    for s in stages:
+        s.table.copy_(torch.arange(16).int().view(2, 8))
+        s.lens.copy_(torch.tensor([50, 7]))
+        s.begin.copy_(torch.tensor([0, 11, 32]))
+        s.anc.copy_(torch.tensor([(2 << t) - (1 << (0 if t < 11 else 11)) for t in range(T)]))
+        for to, t in zip((s.q, s.k, s.v), fill):
+            to.copy_(t)
+        st = A.LayerStack([], ffns, T, mode="dense", attention=s)
+        st.step()
+        if s.drafts:
+            s.accept([range(11), range(11, 32)])
+            assert s.lens.tolist() == [61, 28]
+        assert st.read_error() == 0
+    assert torch.equal(stages[0].scores, stages[1].scores) and stages[0].scores.any()
+    for a, b in zip(caches, twins):
+        assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
