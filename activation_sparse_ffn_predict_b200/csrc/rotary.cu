@@ -38,10 +38,9 @@ static_assert(ASF_MAX_ROTARY_DIM / 4 <= kRotThreads, "a head's places are a CTA'
 // 126 of 128 columns in halves 103, 91, 81, 78, 24 of 96 columns 96, 81, 71, 65.
 constexpr int kItems = 9;
 
-// The fraction of a turn is rounded to fp32 as it is.  Without its nearest quarter turn, or with what the rounding leaves
-// put back by a step of the derivative, fp32 heads would be a third nearer to the definition (3.7e-8 of their norm; half of it
-// is the output's own rounding); either takes 8 registers more where pairs are in flight, 8192 tokens x 72 heads in
-// pairs 60.3 -> 65.4 us.
+// The fraction of a turn is rounded to fp32 as it is: fp32 heads come out 3.7e-8 of their norm from the definition
+// (2.9e-8 with the angle in 64 bits).  Rounding only what is left of the nearest quarter turn, or a step of the derivative
+// for what the rounding leaves, takes 8 registers more where pairs are in flight: 8192 tokens x 72 heads 60.3 -> 65.4 us.
 __device__ __forceinline__ float2 cos_sin(int pos, uint64_t turns, float mul) {
   const uint64_t phase = (uint64_t)(int64_t)pos * turns;
   const int half_turns = (int)(uint32_t)((phase + 0x80000000ull) >> 32);     // of 2^-31
