@@ -1187,7 +1187,7 @@ cudaError_t run_attn_any(const AttnArgs &a, int wm, int units, cudaStream_t st) 
 // table past the bound, with the keys read again (pages of 64 by tcgen05, of 20 by mma.sync): 8 rows a kv head,
 // 1000 keys each 21.4, 25.8 and 34.8, 4000 keys 41.2, 52.3 and 83.0, 16000 keys 119, 150 and 286; 16 rows, 4000 keys 49.4 and
 // 54.5, 16000 keys 138 and 152; 32 rows, 4000 keys 59.6 and 55.5, 16000 keys 177 and 162 (heads of 64: 138 and 121).
-// So from some 24 rows on, in pages that TMA takes, reading again would be the faster one; it is chosen past 32.
+// Somewhere between 16 and 32 rows, in pages that TMA takes, reading again becomes the faster one; it is chosen past 32.
 constexpr int64_t kKeptScores = 512 << 20;
 int64_t kept_scores(const asf_kv_cache *c, int q_heads, int R, int T, int max_pages) {
   const int64_t zs = ((int64_t)max_pages * c->page + kTile - 1) / kTile * kTile, all = zs * T * q_heads * 4;

@@ -131,7 +131,8 @@ class AttentionStage:
 
     def evict(self, keep: int, table: torch.Tensor, first: int = 0, recent: int = 0) -> torch.Tensor:
         """Between steps, with scored: every request's layers and kv heads keep `keep` keys (asf_kv_evict) on the pages
-        of `table` int32 [R, pages], which have room for them and are then the stage's.  Returns the kept positions int32 [layers, R, heads, keep].
+        of `table` int32 [R, pages], which have room for them and are then the stage's.  Returns the kept positions
+        int32 [layers, R, heads, keep].
 
         The stage's table, lens and scores go over to what is left, in place, so that a captured stack runs on.  Past
         `table`'s columns its own then lists no page (-1): the old ones are the caller's again."""
@@ -270,11 +271,11 @@ class LayerStack:
         """One step as a CUDA graph.  The `warmup` steps before it leave the attention stage's scores as they are."""
         stage, s = self.attention, torch.cuda.Stream()
         scores = stage.scores if stage is not None else None
-        if scores is not None:                        # every layer's go to the same place, which nobody reads
-            stage.scores = torch.zeros_like(scores[0]).expand_as(scores)
+        s.wait_stream(torch.cuda.current_stream())
         try:
-            s.wait_stream(torch.cuda.current_stream())
             with torch.cuda.stream(s):
+                if scores is not None:                # every layer's go to the same place, which nobody reads
+                    stage.scores = torch.zeros_like(scores[0]).expand_as(scores)
                 for _ in range(warmup):
                     self.enqueue()
             torch.cuda.current_stream().wait_stream(s)
